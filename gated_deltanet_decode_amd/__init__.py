@@ -23,6 +23,9 @@ __all__ = [
     "tree_tables", "block_verify", "block_verify_ut", "block_commit", "block_commit_prepared", "state_signature", "snapshot", "restore", "prefill_chunked",
     "self_check_workspace_bytes", "self_check", "SELF_CHECK_PERTURB", "tree_verify_ut_noalloc",
     "NOALLOC_SCRATCH_BYTES",
+    "SsmDims", "ssm_dims", "ssm_conv_channels", "ssm_state_bytes", "ssm_conv_tail_bytes", "ssm_decode_token",
+    "ssm_prefill_workspace_bytes", "ssm_prefill", "SSM_MAX_TOKENS",
+    "beam_select_workspace_bytes", "beam_select", "beam_reorder", "MAX_BEAMS", "MAX_BEAM_SELECT",
     "LIB_PATH", "MAX_TREE_NODES", "MAX_TREE_DEPTH", "PREFILL_CHUNK", "PREFILL_SEGMENT", "F32", "BF16",
 ]
 
@@ -35,6 +38,9 @@ PREFILL_SEGMENT = 4096   # tokens per group of prefill launches; the workspace s
 F32, BF16 = 0, 1
 SELF_CHECK_PERTURB = 1
 NOALLOC_SCRATCH_BYTES = 16 << 20
+SSM_MAX_TOKENS = 1 << 22
+MAX_BEAMS = 32
+MAX_BEAM_SELECT = 64
 _STATUS_TREE = 5
 
 if not os.path.exists(LIB_PATH):
@@ -61,7 +67,27 @@ def dims(batch, num_k_heads, num_v_heads, head_k_dim, head_v_dim, conv_width=4, 
                 BF16 if act in ("bf16", BF16, torch.bfloat16) else F32)
 
 
+class SsmDims(C.Structure):
+    """A selective state space layer (gdn_ssm_dims)."""
+    _fields_ = [(n, C.c_int32) for n in ("batch", "num_heads", "num_groups", "head_dim", "state_dim", "conv_width",
+                                         "act_dtype")]
+
+    @property
+    def C(self) -> int:
+        return self.num_heads * self.head_dim + 2 * self.num_groups * self.state_dim
+
+    @property
+    def act_torch(self):
+        return torch.bfloat16 if self.act_dtype == BF16 else torch.float32
+
+
+def ssm_dims(batch, num_heads, num_groups, head_dim, state_dim, conv_width=4, act="bf16") -> SsmDims:
+    return SsmDims(batch, num_heads, num_groups, head_dim, state_dim, conv_width,
+                   BF16 if act in ("bf16", BF16, torch.bfloat16) else F32)
+
+
 _P = C.c_void_p
+_M = C.POINTER(SsmDims)
 _D = C.POINTER(Dims)
 _I = C.c_int32
 _sig = {
@@ -95,6 +121,16 @@ _sig = {
     "gdn_self_check_workspace_bytes": ([_D], C.c_size_t),
     "gdn_self_check": ([_D, C.c_uint32, _I, _P, C.c_size_t, _P, _P], C.c_int),
     "gdn_tree_verify_ut_noalloc": ([_D, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P], C.c_int),
+    "gdn_ssm_conv_channels": ([_M], C.c_size_t),
+    "gdn_ssm_state_bytes": ([_M], C.c_size_t),
+    "gdn_ssm_conv_tail_bytes": ([_M], C.c_size_t),
+    "gdn_ssm_decode_token": ([_M] + [_P] * 13, C.c_int),
+    "gdn_ssm_prefill_workspace_bytes": ([_M, _I], C.c_size_t),
+    "gdn_ssm_prefill": ([_M, _P, _P, _P, _P, _I] + [_P] * 10 + [C.c_size_t, _P], C.c_int),
+    "gdn_beam_select_workspace_bytes": ([_I] * 4, C.c_size_t),
+    "gdn_beam_select": ([_I, _I, _I, C.c_int64, _I, _P, _P, _P, _I, _I, _P, _P, _P, _P, C.c_size_t, _P], C.c_int),
+    "gdn_beam_reorder": ([_D, _I, _P, _P, _P, _P, _P], C.c_int),
+    "gdn_ssm_beam_reorder": ([_M, _I, _P, _P, _P, _P, _P], C.c_int),
 }
 for _name, (_args, _res) in _sig.items():
     _f = getattr(_lib, _name)
@@ -430,3 +466,120 @@ def tree_verify_ut_noalloc(d: Dims, state, tail, w, parent, x, a, b, o, status=N
                                            _t(o, "o", torch.float32, B * n * Hv * dv),
                                            _opt(status, "tree_status", torch.int32, B), _stream(stream)),
            "gdn_tree_verify_ut_noalloc")
+
+
+# ------------------------------------------------ selective state space layers
+
+def _on_current(*tensors) -> None:
+    """A launch goes to the current device: refuse tensors of another one."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.device.index != here:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
+
+
+def ssm_conv_channels(d: SsmDims) -> int:
+    return _lib.gdn_ssm_conv_channels(C.byref(d))
+
+
+def ssm_state_bytes(d: SsmDims) -> int:
+    return _lib.gdn_ssm_state_bytes(C.byref(d))
+
+
+def ssm_conv_tail_bytes(d: SsmDims) -> int:
+    return _lib.gdn_ssm_conv_tail_bytes(C.byref(d))
+
+
+def ssm_decode_token(d: SsmDims, state, tail_in, tail_out, w, x, dt, A, y, conv_bias=None, dt_bias=None, D=None,
+                     z=None, stream=None) -> None:
+    """One token of a selective state space layer: x [B][C], dt [B][H], y and z [B][H][P];
+    the tail goes from tail_in to tail_out."""
+    B, H, P, N, Cc, act = d.batch, d.num_heads, d.head_dim, d.state_dim, d.C, d.act_torch
+    _on_current(state, tail_in, tail_out, w, x, dt, A, y, conv_bias, dt_bias, D, z)
+    _check(_lib.gdn_ssm_decode_token(C.byref(d), _t(state, "state", torch.float32, B * H * P * N),
+                                     _t(tail_in, "conv_tail_in", act, B * Cc * 4),
+                                     _t(tail_out, "conv_tail_out", act, B * Cc * 4), _t(w, "conv_w", act, Cc * 4),
+                                     _opt(conv_bias, "conv_bias", act, Cc), _t(x, "x", act, B * Cc),
+                                     _t(dt, "dt", torch.float32, B * H), _opt(dt_bias, "dt_bias", torch.float32, H),
+                                     _t(A, "A", torch.float32, H), _opt(D, "D", torch.float32, H),
+                                     _opt(z, "z", act, B * H * P), _t(y, "y", act, B * H * P), _stream(stream)),
+           "gdn_ssm_decode_token")
+
+
+def ssm_prefill_workspace_bytes(d: SsmDims, T: int) -> int:
+    return _lib.gdn_ssm_prefill_workspace_bytes(C.byref(d), T)
+
+
+def ssm_prefill(d: SsmDims, state, tail, w, x, dt, A, y, workspace, conv_bias=None, dt_bias=None, D=None, z=None,
+                lengths=None, status=None, stream=None) -> None:
+    """Prompts of a selective state space layer: x [B][T][C], dt [B][T][H], y and z [B][T][H][P];
+    state and tail in place.  lengths [B] (int32, device): tokens of each sequence, None for T.
+    workspace: a device byte tensor of at least ssm_prefill_workspace_bytes(d, T) bytes."""
+    B, H, P, N, Cc, act = d.batch, d.num_heads, d.head_dim, d.state_dim, d.C, d.act_torch
+    if x.numel() % (B * Cc) or not x.numel():
+        raise ValueError("x must be [B][T][C]")
+    T = x.numel() // (B * Cc)
+    _on_current(state, tail, w, x, dt, A, y, workspace, conv_bias, dt_bias, D, z, lengths, status)
+    ptr, nbytes = _blob(workspace, ssm_prefill_workspace_bytes(d, T), "workspace")
+    _check(_lib.gdn_ssm_prefill(C.byref(d), _t(state, "state", torch.float32, B * H * P * N),
+                                _t(tail, "conv_tail", act, B * Cc * 4), _t(w, "conv_w", act, Cc * 4),
+                                _opt(conv_bias, "conv_bias", act, Cc), T, _t(x, "x", act, B * T * Cc),
+                                _t(dt, "dt", torch.float32, B * T * H), _opt(dt_bias, "dt_bias", torch.float32, H),
+                                _t(A, "A", torch.float32, H), _opt(D, "D", torch.float32, H),
+                                _opt(z, "z", act, B * T * H * P), _opt(lengths, "lengths", torch.int32, B),
+                                _t(y, "y", act, B * T * H * P), _opt(status, "status", torch.int32, B), ptr, nbytes,
+                                _stream(stream)), "gdn_ssm_prefill")
+
+
+# ------------------------------------------------ beam search over recurrent states
+
+def beam_select_workspace_bytes(batch: int, beams: int, vocab: int, select: int) -> int:
+    return _lib.gdn_beam_select_workspace_bytes(batch, beams, vocab, select)
+
+
+def beam_select(logits, scores, out_scores, parent, token, workspace, finished=None, eos=0, stream=None) -> None:
+    """The S best continuations of each sequence's K beams: logits [B][K][V] (bf16 or fp32; the
+    rows may be a slice of wider ones), scores [B][K]; out_scores, parent, token [B][S].
+    finished [B][K] (bool): beams that have ended, whose one candidate is eos at their own score."""
+    if not isinstance(logits, torch.Tensor) or logits.device.type != "cuda" or logits.dim() != 3:
+        raise ValueError("logits must be a device tensor [B][K][V]")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    B, K, V = logits.shape
+    if V == 0 or B == 0 or K == 0:
+        raise ValueError("logits must not be empty")
+    # strides of dimensions of one entry say nothing
+    pitch = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
+    if (V > 1 and logits.stride(2) != 1) or (K > 1 and B > 1 and logits.stride(0) != K * pitch) or pitch < V:
+        raise ValueError("logits must have contiguous entries and rows at one pitch of at least V")
+    if not isinstance(out_scores, torch.Tensor) or out_scores.numel() % B:
+        raise ValueError("out_scores must be [B][S]")
+    S = out_scores.numel() // B
+    _on_current(logits, scores, out_scores, parent, token, workspace, finished)
+    ptr, nbytes = _blob(workspace, beam_select_workspace_bytes(B, K, V, S), "workspace")
+    if finished is not None and finished.dtype == torch.uint8:
+        fin = _t(finished, "finished", torch.uint8, B * K)
+    else:
+        fin = _opt(finished, "finished", torch.bool, B * K)
+    _check(_lib.gdn_beam_select(B, K, V, pitch, BF16 if logits.dtype == torch.bfloat16 else F32, logits.data_ptr(),
+                                _t(scores, "scores", torch.float32, B * K), fin, eos, S,
+                                _t(out_scores, "out_scores", torch.float32, B * S),
+                                _t(parent, "parent", torch.int32, B * S), _t(token, "token", torch.int32, B * S), ptr,
+                                nbytes, _stream(stream)), "gdn_beam_select")
+
+
+def beam_reorder(d, state, tail, parent, status=None, stream=None) -> None:
+    """Move the beams' states and conv tails in place: parent [groups][beams] (int32), groups * beams
+    == d.batch; sequence g*beams + k takes what g*beams + parent[g][k] had.  d: Dims or SsmDims."""
+    if not isinstance(parent, torch.Tensor) or parent.dim() != 2 or parent.numel() != d.batch:
+        raise ValueError("parent must be [groups][beams] with groups * beams == batch")
+    groups, beams = parent.shape
+    _on_current(state, tail, parent, status)
+    if isinstance(d, SsmDims):
+        name, n = "gdn_ssm_beam_reorder", d.num_heads * d.head_dim * d.state_dim
+    else:
+        name, n = "gdn_beam_reorder", d.num_v_heads * d.head_v_dim * d.head_k_dim
+    _check(getattr(_lib, name)(C.byref(d), beams, _t(state, "state", torch.float32, d.batch * n),
+                               _t(tail, "conv_tail", d.act_torch, d.batch * d.C * 4),
+                               _t(parent, "parent", torch.int32, d.batch), _opt(status, "status", torch.int32, groups),
+                               _stream(stream)), name)

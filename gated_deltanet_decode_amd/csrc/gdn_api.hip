@@ -74,6 +74,39 @@ gdn_status tree_verify_args(const gdn_dims* d, gdn::Geo& g, std::initializer_lis
     return aligned16(workspace) ? GDN_OK : GDN_ERR_ALIGN;
 }
 
+gdn_status check_ssm_dims(const gdn_ssm_dims* d, gdn::SsmGeo& g) {
+    if (!d)
+        return GDN_ERR_NULL;
+    if (d->act_dtype != GDN_F32 && d->act_dtype != GDN_BF16)
+        return GDN_ERR_DTYPE;
+    if (d->batch < 1 || d->num_heads < 1 || d->num_groups < 1 || d->num_heads % d->num_groups != 0 ||
+        (d->head_dim != 32 && d->head_dim != 64 && d->head_dim != 128) ||
+        (d->state_dim != 32 && d->state_dim != 64 && d->state_dim != 128 && d->state_dim != 256) ||
+        d->conv_width != 4)
+        return GDN_ERR_SHAPE;
+    const int64_t C = static_cast<int64_t>(d->num_heads) * d->head_dim + 2ll * d->num_groups * d->state_dim;
+    if (C > (1ll << 24) || static_cast<int64_t>(d->batch) * d->num_heads > (1ll << 24))
+        return GDN_ERR_SHAPE;
+    g = {d->batch, d->num_heads, d->num_groups, d->head_dim, d->state_dim, static_cast<int>(C),
+         d->act_dtype == GDN_BF16};
+    return GDN_OK;
+}
+
+size_t ssm_tail_bytes(const gdn::SsmGeo& g) { return static_cast<size_t>(g.B) * g.C * 4 * (g.bf16 ? 2 : 4); }
+
+gdn_status aligned_or_null(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (!aligned16(p))
+            return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+
+bool beam_sizes_ok(int32_t batch, int32_t beams, int32_t vocab, int32_t select) {
+    return batch >= 1 && beams >= 1 && beams <= GDN_MAX_BEAMS && vocab >= 1 &&
+           static_cast<int64_t>(beams) * vocab < (1ll << 31) && select >= 1 && select <= GDN_MAX_BEAM_SELECT &&
+           select <= static_cast<int64_t>(beams) * vocab && static_cast<int64_t>(batch) * beams <= (1ll << 20);
+}
+
 }  // namespace
 
 extern "C" {
@@ -498,6 +531,137 @@ gdn_status gdn_tree_verify_ut_noalloc(const gdn_dims* d, const float* state_ckpt
         return GDN_ERR_HIP;
     return launched(gdn::launch_tree_verify_ut(g, state_ckpt, conv_tail, conv_w, n_nodes, parent, x, a, b, o,
                                                tree_status, ws, as_stream(stream)));
+}
+
+size_t gdn_ssm_conv_channels(const gdn_ssm_dims* d) {
+    gdn::SsmGeo g;
+    return check_ssm_dims(d, g) == GDN_OK ? static_cast<size_t>(g.C) : 0;
+}
+
+size_t gdn_ssm_state_bytes(const gdn_ssm_dims* d) {
+    gdn::SsmGeo g;
+    return check_ssm_dims(d, g) == GDN_OK ? static_cast<size_t>(g.B) * g.H * g.P * g.N * sizeof(float) : 0;
+}
+
+size_t gdn_ssm_conv_tail_bytes(const gdn_ssm_dims* d) {
+    gdn::SsmGeo g;
+    return check_ssm_dims(d, g) == GDN_OK ? ssm_tail_bytes(g) : 0;
+}
+
+gdn_status gdn_ssm_decode_token(const gdn_ssm_dims* d, float* state, const void* conv_tail_in, void* conv_tail_out,
+                                const void* conv_w, const void* conv_bias, const void* x, const float* dt,
+                                const float* dt_bias, const float* A, const float* D, const void* z, void* y,
+                                void* stream) {
+    gdn::SsmGeo g;
+    gdn_status st = check_ssm_dims(d, g);
+    if (st == GDN_OK)
+        st = ptrs_ok({state, conv_tail_in, conv_tail_out, conv_w, x, dt, A, y});
+    if (st == GDN_OK)
+        st = aligned_or_null({conv_bias, dt_bias, D, z});
+    if (st != GDN_OK)
+        return st;
+    const uintptr_t ti = reinterpret_cast<uintptr_t>(conv_tail_in), to = reinterpret_cast<uintptr_t>(conv_tail_out);
+    if (ti < to + ssm_tail_bytes(g) && to < ti + ssm_tail_bytes(g))
+        return GDN_ERR_ALIAS;
+    const gdn::SsmArgs a{state, conv_tail_in, conv_w, conv_bias, conv_tail_out, x, dt, dt_bias, A, D, z, y};
+    return launched(gdn::launch_ssm_token(g, a, as_stream(stream)));
+}
+
+size_t gdn_ssm_prefill_workspace_bytes(const gdn_ssm_dims* d, int32_t T) {
+    gdn::SsmGeo g;
+    if (check_ssm_dims(d, g) != GDN_OK || T < 1 || T > GDN_SSM_MAX_TOKENS)
+        return 0;
+    return gdn::ssm_prefill_ws_bytes(g, T);
+}
+
+gdn_status gdn_ssm_prefill(const gdn_ssm_dims* d, float* state, void* conv_tail, const void* conv_w,
+                           const void* conv_bias, int32_t T, const void* x, const float* dt, const float* dt_bias,
+                           const float* A, const float* D, const void* z, const int32_t* lengths, void* y,
+                           int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+    gdn::SsmGeo g;
+    gdn_status st = check_ssm_dims(d, g);
+    if (st == GDN_OK && (T < 1 || T > GDN_SSM_MAX_TOKENS))
+        st = GDN_ERR_SHAPE;
+    if (st == GDN_OK)
+        st = ptrs_ok({state, conv_tail, conv_w, x, dt, A, y});
+    if (st == GDN_OK)
+        st = aligned_or_null({conv_bias, dt_bias, D, z, lengths, status});
+    if (st != GDN_OK)
+        return st;
+    if (!workspace || workspace_bytes < gdn::ssm_prefill_ws_bytes(g, T))
+        return GDN_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return GDN_ERR_ALIGN;
+    const gdn::SsmArgs a{state, conv_tail, conv_w, conv_bias, conv_tail, x, dt, dt_bias, A, D, z, y};
+    return launched(gdn::launch_ssm_prefill(g, a, T, lengths, status, workspace, as_stream(stream)));
+}
+
+size_t gdn_beam_select_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t select) {
+    return beam_sizes_ok(batch, beams, vocab, select) ? gdn::beam_select_ws_bytes(batch, beams, vocab, select) : 0;
+}
+
+gdn_status gdn_beam_select(int32_t batch, int32_t beams, int32_t vocab, int64_t vocab_pitch, int32_t act_dtype,
+                           const void* logits, const float* scores, const uint8_t* finished, int32_t eos,
+                           int32_t select, float* out_scores, int32_t* parent, int32_t* token, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    if (act_dtype != GDN_F32 && act_dtype != GDN_BF16)
+        return GDN_ERR_DTYPE;
+    // a pitch of 2^40 elements is far beyond any memory and keeps every offset within 64 bits
+    if (!beam_sizes_ok(batch, beams, vocab, select) || vocab_pitch < vocab || vocab_pitch > (1ll << 40))
+        return GDN_ERR_SHAPE;
+    if (!logits)
+        return GDN_ERR_NULL;
+    gdn_status st = ptrs_ok({scores, out_scores, parent, token});
+    if (st == GDN_OK && ((reinterpret_cast<uintptr_t>(logits) & (act_dtype == GDN_BF16 ? 1u : 3u)) ||
+                         !aligned16(finished)))
+        st = GDN_ERR_ALIGN;
+    if (st == GDN_OK && finished && (eos < 0 || eos >= vocab))
+        st = GDN_ERR_INDEX;
+    if (st != GDN_OK)
+        return st;
+    if (!workspace || workspace_bytes < gdn::beam_select_ws_bytes(batch, beams, vocab, select))
+        return GDN_ERR_WORKSPACE;
+    if (!aligned16(workspace))
+        return GDN_ERR_ALIGN;
+    const gdn::BeamGeo g{batch, beams, vocab, select, vocab_pitch, act_dtype == GDN_BF16};
+    return launched(gdn::launch_beam_select(g, logits, scores, finished, eos, out_scores, parent, token, workspace,
+                                            as_stream(stream)));
+}
+
+static gdn_status beam_reorder(int32_t batch, int32_t beams, int64_t state_bytes, int64_t tail_bytes, float* state,
+                               void* conv_tail, const int32_t* parent, int32_t* status, void* stream) {
+    if (beams < 1 || beams > GDN_MAX_BEAMS || batch % beams != 0)
+        return GDN_ERR_SHAPE;
+    // one workgroup per 4 KB of a sequence and group
+    if ((state_bytes + tail_bytes) / 4096 * (batch / beams) >= (1ll << 30))
+        return GDN_ERR_SHAPE;
+    gdn_status st = ptrs_ok({state, conv_tail, parent});
+    if (st == GDN_OK)
+        st = aligned_or_null({status});
+    if (st != GDN_OK)
+        return st;
+    return launched(gdn::launch_beam_reorder(batch / beams, beams, state_bytes, tail_bytes, state, conv_tail, parent,
+                                             status, as_stream(stream)));
+}
+
+gdn_status gdn_beam_reorder(const gdn_dims* d, int32_t beams, float* state, void* conv_tail, const int32_t* parent,
+                            int32_t* status, void* stream) {
+    gdn::Geo g;
+    const gdn_status st = check_dims(d, g);
+    if (st != GDN_OK)
+        return st;
+    return beam_reorder(g.B, beams, static_cast<int64_t>(g.Hv) * g.D * g.D * 4,
+                        static_cast<int64_t>(g.C) * 4 * (g.bf16 ? 2 : 4), state, conv_tail, parent, status, stream);
+}
+
+gdn_status gdn_ssm_beam_reorder(const gdn_ssm_dims* d, int32_t beams, float* state, void* conv_tail,
+                                const int32_t* parent, int32_t* status, void* stream) {
+    gdn::SsmGeo g;
+    const gdn_status st = check_ssm_dims(d, g);
+    if (st != GDN_OK)
+        return st;
+    return beam_reorder(g.B, beams, static_cast<int64_t>(g.H) * g.P * g.N * 4,
+                        static_cast<int64_t>(g.C) * 4 * (g.bf16 ? 2 : 4), state, conv_tail, parent, status, stream);
 }
 
 }  // extern "C"

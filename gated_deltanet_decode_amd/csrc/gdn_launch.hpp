@@ -45,6 +45,40 @@ size_t prefill_workspace_bytes(const Geo& g, int T);
 hipError_t launch_prefill(const Geo& g, float* S, void* tail, const void* w, int T, const void* x, const float* a,
                           const float* b, float* o, void* ws, hipStream_t s);
 
+// Selective state space layers: C = H*P + 2*G*N conv channels, state [B][H][P][N].
+struct SsmGeo {
+    int B, H, G, P, N, C;
+    bool bf16;
+};
+// Operands of a call; the pointers marked optional may be null.
+struct SsmArgs {
+    float* state;
+    const void *tail_in, *w, *bias;      // bias optional
+    void* tail_out;                      // prefill: the tail in place (== tail_in)
+    const void* x;
+    const float *dt, *dt_bias, *A, *D;   // dt_bias, D optional
+    const void* z;                       // optional
+    void* y;
+};
+hipError_t launch_ssm_token(const SsmGeo& g, const SsmArgs& a, hipStream_t s);
+size_t ssm_prefill_ws_bytes(const SsmGeo& g, int T);
+// lengths, status optional (i32 [B]).
+hipError_t launch_ssm_prefill(const SsmGeo& g, const SsmArgs& a, int T, const int32_t* lengths, int32_t* status,
+                              void* ws, hipStream_t s);
+
+// Beam search: rows of `vocab` logits at a pitch of `pitch` elements.
+struct BeamGeo {
+    int B, K, V, S;
+    int64_t pitch;
+    bool bf16;
+};
+size_t beam_select_ws_bytes(int B, int K, int V, int S);
+hipError_t launch_beam_select(const BeamGeo& g, const void* logits, const float* scores, const uint8_t* finished,
+                              int eos, float* out_scores, int32_t* parent, int32_t* token, void* ws, hipStream_t s);
+// Sequences of state_bytes + tail_bytes each (multiples of 16), groups of K.
+hipError_t launch_beam_reorder(int groups, int K, int64_t state_bytes, int64_t tail_bytes, void* state, void* tail,
+                               const int32_t* parent, int32_t* status, hipStream_t s);
+
 size_t self_check_ws_bytes(const Geo& g);
 hipError_t launch_self_check(const Geo& g, void* ws, uint32_t seed, int perturb, int32_t* result, hipStream_t s);
 // Device address of the library-held scratch array on the current device.

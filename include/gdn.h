@@ -466,6 +466,124 @@ gdn_status gdn_tree_verify_ut_noalloc(const gdn_dims* d, const float* state_ckpt
                                       const void* conv_w, int32_t n_nodes, const int32_t* parent, const void* x,
                                       const float* a, const float* b, float* o, int32_t* tree_status, void* stream);
 
+/*
+ * The selective state space layer -- the other recurrent mixer of hybrid
+ * models, with one decay per head.  Its state and conv tail have the layouts
+ * of the delta-rule layer; the conventions above (memory, errors, streams,
+ * concurrency) hold.  Per token and sequence, with C = H*P + 2*G*N conv
+ * channels (x of H heads | B of G groups | C of G groups); head h reads group
+ * h / (H/G):
+ *   tail   shifts left by one and takes the raw input as its newest entry
+ *   conv   u[c] = SiLU(bias[c] + sum_{j<4} w[c][j] * tail[c][j])
+ *   step   d = softplus(dt + dt_bias), decay = exp(d * min(A, 0)), per head
+ *   state  S <- decay*S + (d*x) B^T                       (P x N per head)
+ *   output y = S C + D*x, times SiLU(z) where z is given
+ * Types: state, dt, dt_bias, A and D are fp32; x, z, y, the conv tail, weights
+ * and bias have the activation type.  y is rounded once, on output.
+ * Supported shapes: head_dim in {32, 64, 128}; state_dim in {32, 64, 128,
+ * 256}; num_heads % num_groups == 0; conv_width == 4.
+ */
+typedef struct {
+    int32_t batch;      /* B: independent sequences */
+    int32_t num_heads;  /* H: state heads */
+    int32_t num_groups; /* G: groups of heads that share B and C */
+    int32_t head_dim;   /* P: rows of a head's state */
+    int32_t state_dim;  /* N: entries of a row */
+    int32_t conv_width; /* must be 4 */
+    int32_t act_dtype;  /* gdn_dtype of x, z, y, conv tail, weights and bias */
+} gdn_ssm_dims;
+
+size_t gdn_ssm_conv_channels(const gdn_ssm_dims* d);   /* C = H*P + 2*G*N */
+size_t gdn_ssm_state_bytes(const gdn_ssm_dims* d);     /* B*H*P*N*4 */
+size_t gdn_ssm_conv_tail_bytes(const gdn_ssm_dims* d); /* B*C*4*sizeof(act) */
+
+/*
+ * gdn_ssm_decode_token -- one token for every sequence, in one launch (the
+ * counterpart of gdn_decode_token).
+ *   state          f32 [B][H][P][N]  (in/out)
+ *   conv_tail_in   act [B][C][4]     last four raw inputs, oldest first (read)
+ *   conv_tail_out  act [B][C][4]     the same after this token (written); must not
+ *                                    overlap conv_tail_in (GDN_ERR_ALIAS)
+ *   conv_w act [C][4];  conv_bias act [C] or NULL (0)
+ *   x act [B][C];  dt f32 [B][H];  dt_bias f32 [H] or NULL (0);  A f32 [H]
+ *   D f32 [H] or NULL (0);  z act [B][H][P] or NULL (no gate)
+ *   y act [B][H][P]  (written)
+ */
+gdn_status gdn_ssm_decode_token(const gdn_ssm_dims* d, float* state, const void* conv_tail_in, void* conv_tail_out,
+                                const void* conv_w, const void* conv_bias, const void* x, const float* dt,
+                                const float* dt_bias, const float* A, const float* D, const void* z, void* y,
+                                void* stream);
+
+/*
+ * gdn_ssm_prefill -- up to T tokens per sequence from (state, tail); both
+ * continue exactly like decode afterwards.
+ *   state and conv_tail as above, both in place;  conv_w .. D as above
+ *   x act [B][T][C];  dt f32 [B][T][H];  z act [B][T][H][P] or NULL
+ *   lengths i32 [B] (device) or NULL: tokens of each sequence, 0..T (NULL: T).
+ *           Rows behind a sequence's end are not read into any result, and
+ *           their y is not written; length 0 leaves state and tail as they are.
+ *   y act [B][T][H][P]  (written up to each sequence's length)
+ *   status i32 [B] or NULL: per sequence GDN_OK, or GDN_ERR_INDEX when its
+ *           length is out of range (that sequence is untouched)
+ *   workspace device bytes >= gdn_ssm_prefill_workspace_bytes(d, T), 256-byte
+ *           aligned.  1 <= T <= GDN_SSM_MAX_TOKENS.
+ * State and fp32 outputs agree with the token-by-token call to fp32 rounding,
+ * bf16 outputs to the rounding of bf16.
+ */
+#define GDN_SSM_MAX_TOKENS (1 << 22)
+size_t gdn_ssm_prefill_workspace_bytes(const gdn_ssm_dims* d, int32_t T);
+gdn_status gdn_ssm_prefill(const gdn_ssm_dims* d, float* state, void* conv_tail, const void* conv_w,
+                           const void* conv_bias, int32_t T, const void* x, const float* dt, const float* dt_bias,
+                           const float* A, const float* D, const void* z, const int32_t* lengths, void* y,
+                           int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_beam_select -- beam search's selection over K beams and V vocabulary
+ * entries per sequence: the S best candidates by
+ *   scores[k] + logits[k][v] - log(sum_v' exp(logits[k][v'])),
+ * best first, equal values by the lowest k*V + v.
+ *   logits   act_dtype [B][K] rows of V at a pitch of vocab_pitch >= V elements
+ *            (the row of beam (b, k) starts at element (b*K + k)*vocab_pitch)
+ *   scores   f32 [B][K]: cumulative log probabilities; -inf for a beam that
+ *            does not exist (as all but one in the first step)
+ *   finished u8 [B][K] or NULL: nonzero for a beam that has ended; its one
+ *            candidate is (k, eos) at scores[k].  eos in 0..V-1 (not read
+ *            where finished is NULL)
+ *   out_scores f32 [B][S];  parent i32 [B][S] (the beam);  token i32 [B][S]
+ * A logit of -inf or NaN is masked (its candidate is -inf); +inf counts as the
+ * largest finite value.  A row of masked logits, and a score of -inf or NaN,
+ * make all of the beam's candidates -inf.  -inf candidates are ordered like
+ * any equal values, by the lowest index, where fewer than S others are left.
+ * 1 <= K <= GDN_MAX_BEAMS, 1 <= S <= min(GDN_MAX_BEAM_SELECT, K*V),
+ * K*V < 2^31, B*K <= 2^20 (GDN_ERR_SHAPE otherwise; GDN_ERR_INDEX for eos).
+ * logits may be aligned to its element size only; the other arrays and the
+ * workspace (gdn_beam_select_workspace_bytes) are 16-byte aligned.
+ */
+#define GDN_MAX_BEAMS 32
+#define GDN_MAX_BEAM_SELECT 64
+size_t gdn_beam_select_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t select);
+gdn_status gdn_beam_select(int32_t batch, int32_t beams, int32_t vocab, int64_t vocab_pitch, int32_t act_dtype,
+                           const void* logits, const float* scores, const uint8_t* finished, int32_t eos,
+                           int32_t select, float* out_scores, int32_t* parent, int32_t* token, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_beam_reorder / gdn_ssm_beam_reorder -- move the beams' recurrent states
+ * after a selection, in place: for every group b of `beams` consecutive
+ * sequences, sequence b*beams + k takes the state and tail that sequence
+ * b*beams + parent[b][k] had before the call, bit for bit.  Slots that keep
+ * their own are neither read (unless another takes them) nor written.
+ *   state, conv_tail  as in the decode calls (in/out); d->batch % beams == 0
+ *   parent i32 [batch/beams][beams]: 0..beams-1, repeats allowed
+ *   status i32 [batch/beams] or NULL: per group GDN_OK, or GDN_ERR_INDEX when
+ *          an entry is out of range (that group is untouched)
+ * 1 <= beams <= GDN_MAX_BEAMS (GDN_ERR_SHAPE otherwise).
+ */
+gdn_status gdn_beam_reorder(const gdn_dims* d, int32_t beams, float* state, void* conv_tail, const int32_t* parent,
+                            int32_t* status, void* stream);
+gdn_status gdn_ssm_beam_reorder(const gdn_ssm_dims* d, int32_t beams, float* state, void* conv_tail,
+                                const int32_t* parent, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
