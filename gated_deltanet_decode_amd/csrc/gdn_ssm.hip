@@ -286,9 +286,11 @@ static hipError_t walk_cfg(const SsmGeo& g, const SsmArgs& a, int T, const int32
 
 template <typename Act>
 static hipError_t prefill_act(const SsmGeo& g, const SsmArgs& a, int T, const int32_t* lengths, int32_t* status,
-                              hipStream_t s) {
+                              void* ws, hipStream_t s) {
     hipError_t e;
-    switch (g.N) {
+    if (T > kWalkTokens)
+        e = launch_ssm_chunked(g, a, T, lengths, ws, s);
+    else switch (g.N) {
         case 32: e = walk_cfg<32, Act>(g, a, T, lengths, s); break;
         case 64: e = walk_cfg<64, Act>(g, a, T, lengths, s); break;
         case 128: e = walk_cfg<128, Act>(g, a, T, lengths, s); break;
@@ -308,12 +310,12 @@ hipError_t launch_ssm_token(const SsmGeo& g, const SsmArgs& a, hipStream_t s) {
     return g.bf16 ? ssm::token_act<uint16_t>(g, a, s) : ssm::token_act<float>(g, a, s);
 }
 
-size_t ssm_prefill_ws_bytes(const SsmGeo&, int) { return 256; }
+size_t ssm_prefill_ws_bytes(const SsmGeo& g, int T) { return T > ssm::kWalkTokens ? ssm::chunked_ws_bytes(g, T) : 256; }
 
 hipError_t launch_ssm_prefill(const SsmGeo& g, const SsmArgs& a, int T, const int32_t* lengths, int32_t* status,
-                              void*, hipStream_t s) {
-    return g.bf16 ? ssm::prefill_act<uint16_t>(g, a, T, lengths, status, s)
-                  : ssm::prefill_act<float>(g, a, T, lengths, status, s);
+                              void* ws, hipStream_t s) {
+    return g.bf16 ? ssm::prefill_act<uint16_t>(g, a, T, lengths, status, ws, s)
+                  : ssm::prefill_act<float>(g, a, T, lengths, status, ws, s);
 }
 
 }  // namespace gdn

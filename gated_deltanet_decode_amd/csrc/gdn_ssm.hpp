@@ -56,5 +56,11 @@ struct Rows {
     __device__ static int key(int j, int r) { return j * 4 * LPR + 4 * r; }
 };
 
+// Prompts up to this length take the token walk.
+constexpr int kWalkTokens = 32;
+size_t chunked_ws_bytes(const SsmGeo& g, int T);
+hipError_t launch_ssm_chunked(const SsmGeo& g, const SsmArgs& a, int T, const int32_t* lengths, void* ws,
+                              hipStream_t s);
+
 }  // namespace ssm
 }  // namespace gdn
