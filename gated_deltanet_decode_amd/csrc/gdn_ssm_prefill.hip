@@ -10,6 +10,7 @@
 //
 //   prep   one workgroup per (sequence, chunk, group): conv and SiLU of the
 //          group's B and C channels, and G, once for all heads of the group.
+//   steps  one wave per (sequence, chunk, head): d and c.
 //   chunk  one wave per (sequence, head, 32 rows of the state, segment of
 //          chunks): the state stays transposed in accumulators (entries down,
 //          rows across) from chunk to chunk, and since a lane's accumulators
@@ -90,14 +91,18 @@ __device__ __forceinline__ void parts8(const float (&v)[8], h8& hi, h8& lo) {
         lo = hi = half8(v);
 }
 
-// The power of two that brings m into [2^TO, 2^(TO + 1)), at most 2^100; and the
+// The power of two that brings m into [2^TO, 2^(TO + 1)), at most 2^MOST; and the
 // exact inverse of such a power.
-template <int TO>
+template <int TO, int MOST>
 __device__ __forceinline__ float pow2_to(float m) {
     const int e = static_cast<int>(__float_as_uint(m) >> 23) & 255;
     const int f = 254 + TO - e;
-    return __uint_as_float(static_cast<uint32_t>(f < 227 ? f : 227) << 23);
+    return __uint_as_float(static_cast<uint32_t>(f < 127 + MOST ? f : 127 + MOST) << 23);
 }
+// Caps of the scales.  Values below 2^-38 (B, C of a token) or 2^-32 (X' of a
+// row) lose relative precision to the absolute 2^-64 of fp16 at that scale; in
+// return no product of scales leaves fp32's range.
+constexpr int kMostBC = 40, kMostX = 40, kMostS = 100;
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
 // What prep leaves for one (sequence, group, chunk), in fragments of 64 lanes x
@@ -107,8 +112,8 @@ __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float(
 template <int N, bool FINE>
 struct Shared {
     static constexpr int CF = 2 * (N / 16), BF = 4 * (N / 32), GF = 6;   // fragments of one part
-    static constexpr int kC = 0, kCl = CF, kB = FINE ? 2 * CF : CF, kBl = kB + BF, kG = kBl + BF, kGl = kG + GF;
-    static constexpr int kFrags = kG + (FINE ? 2 : 1) * GF;
+    static constexpr int kC = 0, kCl = CF, kG = FINE ? 2 * CF : CF, kGl = kG + GF, kB = kG + (FINE ? 2 : 1) * GF,
+                         kBl = kB + BF, kFrags = kBl + BF;
     static constexpr size_t kHalfs = static_cast<size_t>(kFrags) * 512 + 256;   // scales: 128 floats
     static __device__ int g_frag(int it, int ks) { return it == 0 ? ks : 2 + ks; }
 };
@@ -173,7 +178,7 @@ __global__ __launch_bounds__(512) void ssm_prep_kernel(const Act* __restrict__ x
         for (int k = 32; k >= 1; k >>= 1)
             m = fmaxf(m, __shfl_xor(m, k));
         if (lane == 0) {
-            const float s = pow2_to<2>(m);
+            const float s = pow2_to<2, kMostBC>(m);
             sc[r] = s;
             osc[r] = inverse_pow2(s);
         }
@@ -249,36 +254,117 @@ __device__ __forceinline__ double wave_scan(double v, int lane) {
     return v;
 }
 
+// Step sizes and summed decays of a chunk's tokens, one wave per (sequence,
+// chunk, head): d, then c as a high and a low fp32 part, 64 each.  c is summed
+// in fp64: what matters are differences of it, also where it is large.
+__global__ __launch_bounds__(256) void ssm_steps_kernel(const float* __restrict__ dt,
+                                                        const float* __restrict__ dt_bias,
+                                                        const float* __restrict__ A,
+                                                        const int32_t* __restrict__ lengths, int T, int H, int nc,
+                                                        int64_t waves, float* __restrict__ steps) {
+    const int lane = threadIdx.x & 63;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
+    if (id >= waves)
+        return;
+    const int h = static_cast<int>(id % H);
+    const int chunk = static_cast<int>(id / H % nc);
+    const int seq = static_cast<int>(id / H / nc);
+    const int len = lengths ? lengths[seq] : T;
+    if (len > T || chunk * Q >= len)
+        return;
+    const int t = chunk * Q + lane;
+    const float d = t < len ? step_size(dt[(static_cast<size_t>(seq) * T + t) * H + h] + (dt_bias ? dt_bias[h] : 0.0f))
+                            : 0.0f;
+    const double cum = wave_scan(static_cast<double>(d) * static_cast<double>(rate2(A[h])), lane);
+    const float high = static_cast<float>(cum);
+    float* o = steps + ((static_cast<size_t>(seq) * H + h) * nc + chunk) * (3 * Q);
+    o[lane] = d;
+    o[Q + lane] = high;
+    o[2 * Q + lane] = static_cast<float>(cum - static_cast<double>(high));
+}
+
 struct ChunkArgs {
     SsmArgs p;
     const int32_t* lengths;
     const _Float16* shared;   // prep's output
+    const float* steps;       // steps' output [B][H][nc][3][64]
     float* seg_state;         // [B][H][segments][P][N]
     float* seg_decay;         // [B][H][segments] log2 of the segment's decay
-    int T, B, H, G, P, C, nc, segs, chunks_per_seg;
+    int T, B, H, G, P, C, nc, segs, chunks_per_seg, by_xcd;
 };
 
+// A wave's tile of 64 tokens x 32 channels of x in LDS, and later of y in fp32,
+// 32 tokens at a time.  The pitch (40 elements) puts the two lane halves' rows,
+// four apart, into different banks.
+template <typename Act>
+struct Tile {
+    static constexpr int kUnit = 16 / sizeof(Act);     // channels per 16 bytes
+    static constexpr int kPerRow = 32 / kUnit;         // 16-byte units per row; also units per lane of 64 rows
+    static constexpr int kRowStep = 64 / kPerRow;      // rows between a lane's units
+    static constexpr int kPitch = 40;
+    static constexpr int kBytes = Q * kPitch * sizeof(Act);
+    static_assert(kBytes >= 32 * kPitch * 4, "half a tile of fp32 outputs fits");
+};
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+// Nothing moves across, and values loaded before are loaded again after: the
+// compiler would otherwise hoist whole phases' loads, or keep their values, and
+// run out of registers.
+__device__ __forceinline__ void phase() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The value is computed by here (the compiler may otherwise sink what computes
+// it past a phase and keep all its operands instead).
+__device__ __forceinline__ void pin(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void pin(h8& v) { asm volatile("" : "+v"(v)); }
+
+// Orders a wave's LDS accesses: what one lane wrote is there for the others.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// One workgroup per (sequence, head, segment), one wave per 32 rows of the
+// state.  With every row's operands in one scale, a chunk's outputs are a single
+// product over 64 + N terms, Y = [M . G | 2^c C] [X'; S0^T]; its left factor is
+// the head's, so each wave builds a part of it and leaves it in LDS for all (the
+// one thing that the waves share; all else is a wave's own).  x comes a chunk
+// ahead, in 16-byte loads through a tile in LDS, and y leaves the same way.
 // OUT: form the outputs.  EXACT: the state's products in two fp16 parts.  With
 // segments, OUT without EXACT serves bf16 outputs (the state comes from join).
 template <int N, typename Act, bool FINE, bool OUT, bool EXACT>
-__global__ __launch_bounds__(256) void ssm_chunk_kernel(ChunkArgs a) {
+__global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel(ChunkArgs a) {
     using Sh = Shared<N, FINE>;
     using Qd = Quad<Act>;
-    constexpr int NT = N / 32;
-    __shared__ __align__(16) float factors[4][6][Q];
+    using Tl = Tile<Act>;
+    constexpr int NT = N / 32, KS = N / 16;
+    constexpr int AF = Sh::GF + Sh::CF;   // fragments of the left factor (of one part)
+    constexpr int NF = OUT ? 6 : 2;
+    extern __shared__ __align__(16) char pool[];   // [waves][tile, factors], then the left factor
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hi = lane >> 5, c = lane & 31;
-    const int slices = a.P / 32;
-    int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + wave;
-    const int slice = static_cast<int>(id % slices);
-    id /= slices;
-    const int h = static_cast<int>(id % a.H);
-    id /= a.H;
-    const int seg = static_cast<int>(id % a.segs);
-    const int seq = static_cast<int>(id / a.segs);
-    if (seq >= a.B)
+    const int waves = a.P / 32;
+    // workgroup -> (sequence, segment, group), head of the group: all heads that
+    // read the same fragments on one XCD (workgroups go to the eight in turn)
+    const int rep = a.H / a.G;
+    int set, member;
+    if (a.by_xcd) {
+        set = blockIdx.x / 8 / rep * 8 + blockIdx.x % 8;
+        member = blockIdx.x / 8 % rep;
+    } else {
+        set = blockIdx.x / rep;
+        member = blockIdx.x % rep;
+    }
+    if (set >= a.B * a.segs * a.G)
         return;
+    const int g = set % a.G;
+    const int h = g * rep + member;
+    const int seg = set / a.G % a.segs;
+    const int seq = set / a.G / a.segs;
     const int len = a.lengths ? a.lengths[seq] : a.T;
     if (len < 1 || len > a.T)
         return;
@@ -289,32 +375,63 @@ __global__ __launch_bounds__(256) void ssm_chunk_kernel(ChunkArgs a) {
         return;
     const bool split = a.segs > 1;
 
-    const int g = h / (a.H / a.G);
-    const int chan = h * a.P + slice * 32 + c;   // this lane's state row, as an x channel
-    const Act* xs = static_cast<const Act*>(a.p.x) + static_cast<size_t>(seq) * a.T * a.C + chan;
-    const Act* tail = static_cast<const Act*>(a.p.tail_in) + (static_cast<size_t>(seq) * a.C + chan) * 4;
-    const float* dts = a.p.dt + static_cast<size_t>(seq) * a.T * a.H + h;
+    constexpr int kWaveBytes = Tl::kBytes + NF * Q * 4;
+    Act* xt = reinterpret_cast<Act*>(pool + wave * kWaveBytes);
+    float* yt = reinterpret_cast<float*>(pool + wave * kWaveBytes);
+    float* fF = reinterpret_cast<float*>(pool + wave * kWaveBytes + Tl::kBytes);   // d * 2^-s_B
+    float* fW = fF + Q;       // 2^(c_last - c)
+    float* fS = fF + 2 * Q;   // 2^-s_C
+    float* fK = fF + 3 * Q;   // D * 2^s_C
+    float* fH = fF + 4 * Q;   // c, high and low part
+    float* fL = fF + 5 * Q;
+    _Float16* L = reinterpret_cast<_Float16*>(pool + waves * kWaveBytes);
+
+    const int col0 = h * a.P + wave * 32;
+    const int chan = col0 + c;   // this lane's state row, as an x channel
+    const Act* xs = static_cast<const Act*>(a.p.x) + static_cast<size_t>(seq) * a.T * a.C;
     float wf[4];
     Qd::to_float(Qd::load(static_cast<const Act*>(a.p.w) + static_cast<size_t>(chan) * 4), wf);
     const float bf = a.p.bias ? widen(static_cast<const Act*>(a.p.bias)[chan]) : 0.0f;
-    const float dtb = a.p.dt_bias ? a.p.dt_bias[h] : 0.0f;
-    const double rate = static_cast<double>(rate2(a.p.A[h]));
     const float skip = a.p.D ? a.p.D[h] : 0.0f;
-    const size_t yrow = static_cast<size_t>(a.H) * a.P;
-    const size_t ybase = static_cast<size_t>(seq) * a.T * yrow + chan;
+    const size_t head = static_cast<size_t>(seq) * a.H + h;
+    const float* steps = a.steps + head * a.nc * (3 * Q);
+    const _Float16* shared0 = a.shared + (static_cast<size_t>(seq) * a.G + g) * a.nc * Sh::kHalfs;
 
-    float* fF = factors[wave][0];   // d * 2^-s_B
-    float* fW = factors[wave][1];   // 2^(c_last - c)
-    float* fE = factors[wave][2];   // 2^c
-    float* fS = factors[wave][3];   // 2^-s_C
-    float* fH = factors[wave][4];   // c, high and low part
-    float* fL = factors[wave][5];
+    // unit k of this lane: row urow + k * kRowStep, channels ucol ..
+    const int urow = lane / Tl::kPerRow, ucol = lane % Tl::kPerRow * Tl::kUnit;
+    u4 xu[Tl::kPerRow];
+    float st_d, st_h, st_l, st_b, st_c = 1.0f;   // the chunk's step, c, scales (one token per lane)
+    auto load_chunk = [&](int ch) {
+        // rows behind the sequence's end are the last row again; their step size is 0
+#pragma unroll
+        for (int k = 0; k < Tl::kPerRow; ++k) {
+            const int t = min(ch * Q + urow + k * Tl::kRowStep, len - 1);
+            xu[k] = *reinterpret_cast<const u4*>(xs + static_cast<size_t>(t) * a.C + col0 + ucol);
+        }
+        const float* st = steps + static_cast<size_t>(ch) * (3 * Q);
+        const float* sc = reinterpret_cast<const float*>(shared0 + ch * Sh::kHalfs + Sh::kFrags * 512);
+        st_d = st[lane];
+        st_h = st[Q + lane];
+        st_l = st[2 * Q + lane];
+        st_b = sc[lane];
+        if (OUT)
+            st_c = sc[Q + lane];
+    };
+
+    // the three inputs before the segment
+    Act before[3];
+    {
+        const typename Qd::raw tr = Qd::load(static_cast<const Act*>(a.p.tail_in) +
+                                             (static_cast<size_t>(seq) * a.C + chan) * 4);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            before[k] = ch0 == 0 ? Qd::elem(tr, k + 1) : xs[static_cast<size_t>(ch0 * Q - 3 + k) * a.C + chan];
+    }
 
     // the state, transposed: S[nt][v] is entry 32 nt + 8 (v / 4) + 4 hi + v % 4 of this lane's row, times `unit`
     f16v S[NT];
     float unit = 1.0f;
-    const size_t head = static_cast<size_t>(seq) * a.H + h;
-    const size_t row_off = static_cast<size_t>(slice * 32 + c) * N + 4 * hi;
+    const size_t row_off = static_cast<size_t>(wave * 32 + c) * N + 4 * hi;
     float* seg_row = a.seg_state + (head * a.segs + seg) * a.P * N + row_off;
     float* state_row = a.p.state + head * a.P * N + row_off;
     if (OUT) {
@@ -334,73 +451,105 @@ __global__ __launch_bounds__(256) void ssm_chunk_kernel(ChunkArgs a) {
         for (int nt = 0; nt < NT; ++nt)
             S[nt] = zero16();
     }
+    // One dword of each 128-byte line of the chunk's fragments, so that they are in
+    // this XCD's L2 when their chunk comes: all heads of a group ask for them at
+    // about the same time, and all would wait for the memory behind it.
+    constexpr int kFrom = OUT ? 0 : Sh::kB, kTo = EXACT ? Sh::kFrags : Sh::kBl;
+    constexpr int kLines = (kTo - kFrom) * 8;
+    constexpr int kTouch = (kLines + 63) / 64;
+    uint32_t touched[kTouch];
+    auto touch = [&](int ch) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(shared0 + ch * Sh::kHalfs + kFrom * 512);
+#pragma unroll
+        for (int k = 0; k < kTouch; ++k)
+            if ((k * waves + wave) * 64 < kLines)   // kLines is a multiple of 32
+                touched[k] = p[min((k * waves + wave) * 64 + lane, kLines - 1) * 32];
+    };
+#pragma unroll
+    for (int k = 0; k < kTouch; ++k)
+        touched[k] = 0;
+    load_chunk(ch0);
+
+    // B's fragments of a k-step, loaded ahead of their products
+    constexpr int kAhead = OUT ? 1 : 2, kRing = kAhead + 1;
+    h8 bh_[kRing][NT], bl_[kRing][NT];
+    auto load_b = [&](const _Float16* sh, int ks) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            bh_[ks % kRing][nt] = ld_frag(sh, Sh::kB + nt * 4 + ks, lane);
+            if (EXACT)
+                bl_[ks % kRing][nt] = ld_frag(sh, Sh::kBl + nt * 4 + ks, lane);
+        }
+    };
 
     double seg_sum = 0.0;
     for (int ch = ch0; ch < ch1; ++ch) {
         const int t0 = ch * Q;
-        const _Float16* sh = a.shared + ((static_cast<size_t>(seq) * a.G + g) * a.nc + ch) * Sh::kHalfs;
-        const float* scales = reinterpret_cast<const float*>(sh + Sh::kFrags * 512);
-        // x, with the three tokens before each run of four
-        float xr[8][7];
-        if (t0 > 0 && t0 + Q <= len) {
-            const Act* p = xs + static_cast<size_t>(t0 + 4 * hi) * a.C;
+        const _Float16* sh = shared0 + ch * Sh::kHalfs;
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
+        for (int k = 0; k < kTouch; ++k)
+            asm volatile("" ::"v"(touched[k]));
+        touch(min(ch + 1, ch1 - 1));
+        // x into the tile, the chunk's factors beside it
 #pragma unroll
-                for (int e = 0; e < 7; ++e)
-                    xr[r][e] = widen(p[static_cast<int64_t>(8 * r + e - 3) * a.C]);
-        } else {
-            float tw[4];
-            Qd::to_float(Qd::load(tail), tw);
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-#pragma unroll
-                for (int e = 0; e < 7; ++e) {
-                    const int t = t0 + 8 * r + 4 * hi + e - 3;
-                    const float v = widen(xs[static_cast<size_t>(t < 0 ? 0 : t < len ? t : len - 1) * a.C]);
-                    xr[r][e] = t >= 0 ? (t < len ? v : 0.0f) : t == -1 ? tw[3] : t == -2 ? tw[2] : tw[1];
-                }
+        for (int k = 0; k < Tl::kPerRow; ++k)
+            *reinterpret_cast<u4*>(xt + (urow + k * Tl::kRowStep) * Tl::kPitch + ucol) = xu[k];
+        const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
+        const float total = th + tl;
+        seg_sum += static_cast<double>(th) + static_cast<double>(tl);
+        fF[lane] = st_d * st_b;
+        fW[lane] = __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
+        if (OUT) {
+            fS[lane] = st_c;
+            fK[lane] = skip * inverse_pow2(st_c);
+            fH[lane] = st_h;
+            fL[lane] = st_l;
         }
-        // the chunk's step sizes and decays, one token per lane
-        double total;
-        {
-            const int t = t0 + lane;
-            const float d = t < len ? step_size(dts[static_cast<size_t>(t) * a.H] + dtb) : 0.0f;
-            const double cum = wave_scan(static_cast<double>(d) * rate, lane);
-            total = __shfl(cum, 63);
-            fF[lane] = d * scales[lane];
-            fW[lane] = __builtin_amdgcn_exp2f(static_cast<float>(total - cum));
-            if (OUT) {
-                const float ch_ = static_cast<float>(cum);
-                fE[lane] = __builtin_amdgcn_exp2f(ch_);
-                fS[lane] = scales[Q + lane];
-                fH[lane] = ch_;
-                fL[lane] = static_cast<float>(cum - static_cast<double>(ch_));
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+        wave_sync();
+        if (!OUT) {
+            load_b(sh, 0);
+            load_b(sh, 1);
         }
-        const float decay = __builtin_amdgcn_exp2f(static_cast<float>(total));
-        seg_sum += total;
+        phase();
 
-        // conv; X' and the largest of it and of X'' in this row
-        float xc[32], xp[32];
+        // conv; the largest of X' and of X'' in this row
+        float xc[32];
         float m1 = 0.0f, m2 = 0.0f;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
+            float raw[7];
+#pragma unroll
+            for (int e = 0; e < 7; ++e) {
+                const int row = 8 * r + e - 3;
+                if (r == 0 && e < 3) {
+                    const Act v = xt[(row + 4) * Tl::kPitch + c];   // in the tile for the upper half
+                    raw[e] = widen(hi ? v : before[e]);
+                } else {
+                    raw[e] = widen(xt[(row + 4 * hi) * Tl::kPitch + c]);
+                }
+            }
             const float4 F = *reinterpret_cast<const float4*>(fF + 8 * r + 4 * hi);
             const float4 W = *reinterpret_cast<const float4*>(fW + 8 * r + 4 * hi);
             const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float win[4] = {xr[r][i], xr[r][i + 1], xr[r][i + 2], xr[r][i + 3]};
+                const float win[4] = {raw[i], raw[i + 1], raw[i + 2], raw[i + 3]};
                 const float v = conv_bias_silu(wf, win, bf);
                 xc[4 * r + i] = v;
-                xp[4 * r + i] = v * ff[i];
-                m1 = fmaxf(m1, fabsf(xp[4 * r + i]));
-                m2 = fmaxf(m2, fabsf(xp[4 * r + i] * ww[i]));
+                const float xp = v * ff[i];
+                m1 = fmaxf(m1, fabsf(xp));
+                m2 = fmaxf(m2, fabsf(xp * ww[i]));
+                pin(xc[4 * r + i]);
             }
+            pin(m1);
+            pin(m2);
+            if (r % 2)
+                phase();
         }
+#pragma unroll
+        for (int k = 0; k < 3; ++k)   // the tile's last three rows
+            before[k] = xt[(Q - 3 + k) * Tl::kPitch + c];
+        load_chunk(min(ch + 1, ch1 - 1));
         m1 = fmaxf(m1, __shfl_xor(m1, 32));
         m2 = fmaxf(m2, __shfl_xor(m2, 32));
         // the row's largest state entry
@@ -412,112 +561,209 @@ __global__ __launch_bounds__(256) void ssm_chunk_kernel(ChunkArgs a) {
                 ms = fmaxf(ms, fabsf(S[nt][v]));
         ms = fmaxf(ms, __shfl_xor(ms, 32));
         // a common unit of the state's part and the chunk's is kept small enough for both
-        const float room = fminf(pow2_to<60>(ms * inverse_pow2(unit)), unit * 0x1p60f);
+        const float state_max = ms * inverse_pow2(unit);
+        const float room = fminf(pow2_to<60, kMostS>(state_max), unit * 0x1p60f);
+        const float s2 = fminf(pow2_to<8, kMostS>(m2), room);   // the unit of S1
+        const float sx = pow2_to<8, kMostX>(fmaxf(m1, state_max));
+
+        // X'' and X' as fragments; Y starts from D x
+        h8 wh[4], wl[4], xh[4], xl[4];
+        f16v Y[2];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            float v[8], u[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float4 F = *reinterpret_cast<const float4*>(fF + 16 * ks + 8 * q + 4 * hi);
+                const float4 W = *reinterpret_cast<const float4*>(fW + 16 * ks + 8 * q + 4 * hi);
+                const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w};
+                float kk[4] = {};
+                if (OUT) {
+                    const float4 K = *reinterpret_cast<const float4*>(fK + 16 * ks + 8 * q + 4 * hi);
+                    kk[0] = K.x, kk[1] = K.y, kk[2] = K.z, kk[3] = K.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = xc[8 * ks + 4 * q + i];
+                    const float xp = x * ff[i];
+                    v[4 * q + i] = xp * (ww[i] * s2);
+                    if (OUT) {
+                        u[4 * q + i] = xp * sx;
+                        Y[ks / 2][8 * (ks % 2) + 4 * q + i] = (x * sx) * kk[i];
+                    }
+                }
+            }
+            parts8<EXACT>(v, wh[ks], wl[ks]);
+            pin(wh[ks]);
+            if (EXACT)
+                pin(wl[ks]);
+            if (OUT) {
+                parts8<FINE>(u, xh[ks], xl[ks]);
+                pin(xh[ks]);
+                if (FINE)
+                    pin(xl[ks]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float y = Y[ks / 2][8 * (ks % 2) + e];
+                    pin(y);
+                    Y[ks / 2][8 * (ks % 2) + e] = y;
+                }
+            }
+            phase();
+        }
 
         if (OUT) {
-            const float sx = fminf(pow2_to<8>(m1), room);
-            const float ss = pow2_to<8>(ms);   // on top of `unit`
-            f16v Y[2] = {zero16(), zero16()};
-            // C S0^T
+            // this wave's part of the left factor: M . G, then 2^c C; four fragments in flight
+            for (int f0 = wave; f0 < AF; f0 += 4 * waves) {
+                h8 fh[4], fl[4];
 #pragma unroll
-            for (int ks = 0; ks < N / 16; ++ks) {
+                for (int k = 0; k < 4; ++k) {
+                    const int f = min(f0 + k * waves, AF - 1);
+                    const int at = f < Sh::GF ? Sh::kG + f : Sh::kC + f - Sh::GF;
+                    fh[k] = ld_frag(sh, at, lane);
+                    if (FINE)
+                        fl[k] = ld_frag(sh, f < Sh::GF ? Sh::kGl + f : Sh::kCl + f - Sh::GF, lane);
+                }
+                phase();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int f = f0 + k * waves;
+                    if (f >= AF)
+                        break;
+                    h8 mh, ml;
+                    if (f < Sh::GF) {
+                        const int it = f >= 2, ks = it ? f - 2 : f;
+                        const float ci = fH[32 * it + c];
+                        const float li = FINE ? fL[32 * it + c] : 0.0f;
+                        float m[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int j = 16 * ks + kperm(hi, e);
+                            float arg = ci - fH[j];
+                            float gv = static_cast<float>(fh[k][e]);
+                            if (FINE) {
+                                arg += li - fL[j];
+                                gv += static_cast<float>(fl[k][e]);
+                            }
+                            m[e] = j <= 32 * it + c ? gv * __builtin_amdgcn_exp2f(arg) : 0.0f;
+                        }
+                        parts8<FINE>(m, mh, ml);
+                    } else {
+                        const int row = f - Sh::GF < KS ? c : 32 + c;
+                        const float e2 = __builtin_amdgcn_exp2f(fH[row] + fL[row]);
+                        if (FINE) {
+                            float m[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                m[e] = (static_cast<float>(fh[k][e]) + static_cast<float>(fl[k][e])) * e2;
+                            split8(m, mh, ml);
+                        } else {
+                            mh = fh[k] * static_cast<_Float16>(e2);
+                        }
+                    }
+                    st_frag(L, f, lane, mh);
+                    if (FINE)
+                        st_frag(L, AF + f, lane, ml);
+                }
+            }
+            phase();
+            __syncthreads();
+        }
+        // B's fragments and z come while the outputs are formed
+        const bool update = !OUT || !split || ch + 1 < ch1;
+        if (OUT && update)
+            load_b(sh, 0);
+        if (OUT) {
+            const float sscale = sx * inverse_pow2(unit);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] = S[ks / 2][8 * (ks % 2) + e] * ss;
+                    v[e] = S[ks / 2][8 * (ks % 2) + e] * sscale;
                 h8 bh, bl;
                 parts8<FINE>(v, bh, bl);
 #pragma unroll
                 for (int it = 0; it < 2; ++it) {
-                    const h8 ah = ld_frag(sh, Sh::kC + it * (N / 16) + ks, lane);
+                    const h8 ah = ld_frag(L, Sh::GF + it * KS + ks, lane);
                     Y[it] = mma(ah, bh, Y[it]);
                     if (FINE) {
                         Y[it] = mma(ah, bl, Y[it]);
-                        Y[it] = mma(ld_frag(sh, Sh::kCl + it * (N / 16) + ks, lane), bh, Y[it]);
+                        Y[it] = mma(ld_frag(L, AF + Sh::GF + it * KS + ks, lane), bh, Y[it]);
                     }
                 }
+                if (ks % 4 == 3)
+                    phase();
             }
-            const float ratio = sx * inverse_pow2(ss) * inverse_pow2(unit);
 #pragma unroll
-            for (int it = 0; it < 2; ++it)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 E = *reinterpret_cast<const float4*>(fE + 32 * it + 8 * q + 4 * hi);
-                    Y[it][4 * q] *= E.x * ratio;
-                    Y[it][4 * q + 1] *= E.y * ratio;
-                    Y[it][4 * q + 2] *= E.z * ratio;
-                    Y[it][4 * q + 3] *= E.w * ratio;
-                }
-            // (M . G) X'
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                float v[8], cj[8], lj[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[e] = xp[8 * ks + e] * sx;
-                    cj[e] = fH[16 * ks + kperm(hi, e)];
-                    if (FINE)
-                        lj[e] = fL[16 * ks + kperm(hi, e)];
-                }
-                h8 bh, bl;
-                parts8<FINE>(v, bh, bl);
+            for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
                 for (int it = ks / 2; it < 2; ++it) {
-                    const float ci = fH[32 * it + c];
-                    const float li = FINE ? fL[32 * it + c] : 0.0f;
-                    const h8 gh = ld_frag(sh, Sh::kG + Sh::g_frag(it, ks), lane);
-                    h8 gl = gh;
-                    if (FINE)
-                        gl = ld_frag(sh, Sh::kGl + Sh::g_frag(it, ks), lane);
-                    float m[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float arg = ci - cj[e];
-                        float gv = static_cast<float>(gh[e]);
-                        if (FINE) {
-                            arg += li - lj[e];
-                            gv += static_cast<float>(gl[e]);
-                        }
-                        m[e] = gv * __builtin_amdgcn_exp2f(arg);
-                        if (it == ks / 2)   // a block on the diagonal
-                            m[e] = 16 * ks + kperm(hi, e) <= 32 * it + c ? m[e] : 0.0f;
-                    }
-                    h8 mh, ml;
-                    parts8<FINE>(m, mh, ml);
-                    Y[it] = mma(mh, bh, Y[it]);
+                    const int f = Sh::g_frag(it, ks);
+                    const h8 ah = ld_frag(L, f, lane);
+                    Y[it] = mma(ah, xh[ks], Y[it]);
                     if (FINE) {
-                        Y[it] = mma(mh, bl, Y[it]);
-                        Y[it] = mma(ml, bh, Y[it]);
+                        Y[it] = mma(ah, xl[ks], Y[it]);
+                        Y[it] = mma(ld_frag(L, AF + f, lane), xh[ks], Y[it]);
                     }
                 }
-            }
             const float back = inverse_pow2(sx);
-            Act* yp = static_cast<Act*>(a.p.y) + ybase;
-            const Act* zp = static_cast<const Act*>(a.p.z) + (a.p.z ? ybase : 0);
+            const size_t yrow = static_cast<size_t>(a.H) * a.P;
+            const size_t y0 = (static_cast<size_t>(seq) * a.T + t0) * yrow + col0 + ucol;
 #pragma unroll
-            for (int it = 0; it < 2; ++it)
+            for (int it = 0; it < 2; ++it) {
+                constexpr int kHalf = Tl::kPerRow / 2;
+                union Unit {
+                    u4 raw;
+                    Act v[Tl::kUnit];
+                } zu[kHalf], yu;
+                if (a.p.z) {
+#pragma unroll
+                    for (int k = 0; k < kHalf; ++k) {
+                        const int r = min(32 * it + urow + k * Tl::kRowStep, len - 1 - t0);
+                        zu[k].raw = *reinterpret_cast<const u4*>(static_cast<const Act*>(a.p.z) + y0 + r * yrow);
+                    }
+                }
+                phase();
+                wave_sync();   // what was in the tile is read
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int tr = 32 * it + 8 * q + 4 * hi;
-                    const float4 Sc = *reinterpret_cast<const float4*>(fS + tr);
+                    const float4 Sc = *reinterpret_cast<const float4*>(fS + 32 * it + 8 * q + 4 * hi);
                     const float sc[4] = {Sc.x, Sc.y, Sc.z, Sc.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = t0 + tr + i;
-                        if (t < len) {
-                            float o = __builtin_fmaf(skip, xc[16 * it + 4 * q + i], Y[it][4 * q + i] * (sc[i] * back));
-                            if (a.p.z)
-                                o *= silu(widen(zp[static_cast<size_t>(t) * yrow]));
-                            narrow(o, yp[static_cast<size_t>(t) * yrow]);
-                        }
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        yt[(8 * q + 4 * hi + i) * Tl::kPitch + c] = Y[it][4 * q + i] * (sc[i] * back);
                 }
+                wave_sync();
+#pragma unroll
+                for (int k = 0; k < kHalf; ++k) {
+                    const int r = urow + k * Tl::kRowStep;
+                    float o[Tl::kUnit];
+#pragma unroll
+                    for (int q = 0; q < Tl::kUnit / 4; ++q) {
+                        const float4 v = *reinterpret_cast<const float4*>(yt + r * Tl::kPitch + ucol + 4 * q);
+                        o[4 * q] = v.x;
+                        o[4 * q + 1] = v.y;
+                        o[4 * q + 2] = v.z;
+                        o[4 * q + 3] = v.w;
+                    }
+                    if (a.p.z) {
+#pragma unroll
+                        for (int e = 0; e < Tl::kUnit; ++e)
+                            o[e] *= silu(widen(zu[k].v[e]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < Tl::kUnit; ++e)
+                        narrow(o[e], yu.v[e]);
+                    if (t0 + 32 * it + r < len)
+                        *reinterpret_cast<u4*>(static_cast<Act*>(a.p.y) + y0 + (32 * it + r) * yrow) = yu.raw;
+                }
+            }
         }
 
-        if (!OUT || !split || ch + 1 < ch1) {
-            // S1: the row's unit becomes that of X'' unless the state is too large for it
-            const float s2 = fminf(pow2_to<8>(m2), room);
-            const float keep = decay * (s2 * inverse_pow2(unit));
+        phase();
+        if (update) {
+            const float keep = __builtin_amdgcn_exp2f(total) * (s2 * inverse_pow2(unit));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -525,27 +771,24 @@ __global__ __launch_bounds__(256) void ssm_chunk_kernel(ChunkArgs a) {
                     S[nt][v] *= keep;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = xp[8 * ks + e] * (fW[16 * ks + kperm(hi, e)] * s2);
-                h8 bh, bl;
-                parts8<EXACT>(v, bh, bl);
+                if (ks + kAhead < 4)
+                    load_b(sh, ks + kAhead);
+                phase();
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const h8 ah = ld_frag(sh, Sh::kB + nt * 4 + ks, lane);
-                    S[nt] = mma(ah, bh, S[nt]);
+                    const h8 ah = bh_[ks % kRing][nt];
+                    S[nt] = mma(ah, wh[ks], S[nt]);
                     if (EXACT) {
-                        S[nt] = mma(ah, bl, S[nt]);
-                        S[nt] = mma(ld_frag(sh, Sh::kBl + nt * 4 + ks, lane), bh, S[nt]);
+                        S[nt] = mma(ah, wl[ks], S[nt]);
+                        S[nt] = mma(bl_[ks % kRing][nt], wh[ks], S[nt]);
                     }
                 }
             }
             unit = s2;
         }
-        // the factors are rewritten by the next chunk
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+        if (OUT)
+            __syncthreads();   // the left factor is rewritten by the next chunk
+        wave_sync();           // and so are tile and factors
     }
     if (OUT && split)
         return;   // join has written the state
@@ -557,7 +800,7 @@ __global__ __launch_bounds__(256) void ssm_chunk_kernel(ChunkArgs a) {
         for (int q = 0; q < 4; ++q)
             *reinterpret_cast<float4*>(to + 32 * nt + 8 * q) =
                 make_float4(S[nt][4 * q] * out, S[nt][4 * q + 1] * out, S[nt][4 * q + 2] * out, S[nt][4 * q + 3] * out);
-    if (split && slice == 0 && lane == 0)
+    if (split && wave == 0 && lane == 0)
         a.seg_decay[head * a.segs + seg] = static_cast<float>(seg_sum);
 }
 
@@ -618,10 +861,24 @@ size_t chunked_ws_bytes(const SsmGeo& g, int T) {
     int segs, per;
     segments(g, T, segs, per);
     const size_t nc = (T + Q - 1) / Q;
-    size_t n = up256(static_cast<size_t>(g.B) * g.G * nc * shared_halfs(g) * sizeof(_Float16));
+    size_t n = up256(static_cast<size_t>(g.B) * g.G * nc * shared_halfs(g) * sizeof(_Float16)) +
+               static_cast<size_t>(g.B) * g.H * nc * (3 * Q) * sizeof(float);
     if (segs > 1)
         n += up256(static_cast<size_t>(g.B) * g.H * segs * g.P * g.N * 4) + up256(static_cast<size_t>(g.B) * g.H * segs * 4);
     return n;
+}
+
+// A launch that may need more than 64 KB of LDS.
+static hipError_t launch_lds(void (*kernel)(ChunkArgs), dim3 grid, dim3 block, size_t lds, hipStream_t s,
+                             const ChunkArgs& a) {
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+        if (e != hipSuccess)
+            return e;
+    }
+    hipLaunchKernelGGL(kernel, grid, block, lds, s, a);
+    return hipGetLastError();
 }
 
 template <int N, typename Act, bool FINE>
@@ -633,6 +890,8 @@ static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const in
     char* base = static_cast<char*>(ws);
     _Float16* shared = reinterpret_cast<_Float16*>(base);
     base += up256(static_cast<size_t>(g.B) * g.G * nc * Shared<N, FINE>::kHalfs * sizeof(_Float16));
+    float* steps = reinterpret_cast<float*>(base);
+    base += static_cast<size_t>(g.B) * g.H * nc * (3 * Q) * sizeof(float);
     float* seg_state = reinterpret_cast<float*>(base);
     float* seg_decay = reinterpret_cast<float*>(base + up256(static_cast<size_t>(g.B) * g.H * segs * g.P * g.N * 4));
     constexpr size_t lds = (static_cast<size_t>(Q) * (2 * N + 1) + 2 * Q) * sizeof(float);
@@ -649,23 +908,33 @@ static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const in
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const ChunkArgs a{p, lengths, shared, seg_state, seg_decay, T, g.B, g.H, g.G, g.P, g.C, nc, segs, per};
-    const int64_t waves = static_cast<int64_t>(g.B) * g.H * (g.P / 32) * segs;
-    const dim3 grid(static_cast<unsigned>((waves + 3) / 4)), block(256);
-    if (segs == 1) {
-        hipLaunchKernelGGL((ssm_chunk_kernel<N, Act, FINE, true, true>), grid, block, 0, s, a);
-        return hipGetLastError();
-    }
-    hipLaunchKernelGGL((ssm_chunk_kernel<N, Act, FINE, false, true>), grid, block, 0, s, a);
+    const int64_t step_waves = static_cast<int64_t>(g.B) * g.H * nc;
+    hipLaunchKernelGGL(ssm_steps_kernel, dim3(static_cast<unsigned>((step_waves + 3) / 4)), dim3(256), 0, s, p.dt,
+                       p.dt_bias, p.A, lengths, T, g.H, nc, step_waves, steps);
     if ((e = hipGetLastError()) != hipSuccess)
+        return e;
+    // by XCD where the sets of heads come out even over the eight, or nearly
+    const int64_t sets = static_cast<int64_t>(g.B) * g.G * segs;
+    const bool by_xcd = sets % 8 == 0 || sets >= 64;
+    const ChunkArgs a{p,   lengths, shared, steps, seg_state, seg_decay, T,   g.B,
+                      g.H, g.G,     g.P,    g.C,   nc,        segs,      per, by_xcd};
+    const int waves = g.P / 32;
+    const int64_t wgs = (by_xcd ? (sets + 7) / 8 * 8 : sets) * (g.H / g.G);
+    const dim3 grid(static_cast<unsigned>(wgs)), block(64 * waves);
+    constexpr int kTile = Tile<Act>::kBytes;
+    const size_t lds_state = waves * (kTile + 2 * Q * 4);
+    const size_t lds_out = waves * (kTile + 6 * Q * 4) +
+                           (FINE ? 2 : 1) * (Shared<N, FINE>::GF + Shared<N, FINE>::CF) * 1024;
+    if (segs == 1)
+        return launch_lds(ssm_chunk_kernel<N, Act, FINE, true, true>, grid, block, lds_out, s, a);
+    if ((e = launch_lds(ssm_chunk_kernel<N, Act, FINE, false, true>, grid, block, lds_state, s, a)) != hipSuccess)
         return e;
     const int quads = g.P * N / 4;
     const int64_t threads = static_cast<int64_t>(g.B) * g.H * quads;
-    hipLaunchKernelGGL(ssm_join_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), block, 0, s, a, quads);
+    hipLaunchKernelGGL(ssm_join_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, a, quads);
     if ((e = hipGetLastError()) != hipSuccess)
         return e;
-    hipLaunchKernelGGL((ssm_chunk_kernel<N, Act, FINE, true, FINE>), grid, block, 0, s, a);
-    return hipGetLastError();
+    return launch_lds(ssm_chunk_kernel<N, Act, FINE, true, FINE>, grid, block, lds_out, s, a);
 }
 
 hipError_t launch_ssm_chunked(const SsmGeo& g, const SsmArgs& p, int T, const int32_t* lengths, void* ws,
