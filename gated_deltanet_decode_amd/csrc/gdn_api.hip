@@ -85,7 +85,8 @@ gdn_status check_ssm_dims(const gdn_ssm_dims* d, gdn::SsmGeo& g) {
         d->conv_width != 4)
         return GDN_ERR_SHAPE;
     const int64_t C = static_cast<int64_t>(d->num_heads) * d->head_dim + 2ll * d->num_groups * d->state_dim;
-    if (C > (1ll << 24) || static_cast<int64_t>(d->batch) * d->num_heads > (1ll << 24))
+    // A chunk of 64 rows is addressed by 32-bit byte offsets.
+    if (C > (1ll << 22) || static_cast<int64_t>(d->batch) * d->num_heads > (1ll << 24))
         return GDN_ERR_SHAPE;
     g = {d->batch, d->num_heads, d->num_groups, d->head_dim, d->state_dim, static_cast<int>(C),
          d->act_dtype == GDN_BF16};

@@ -289,8 +289,8 @@ static hipError_t prefill_act(const SsmGeo& g, const SsmArgs& a, int T, const in
                               void* ws, hipStream_t s) {
     hipError_t e;
     if (T > kWalkTokens)
-        e = launch_ssm_chunked(g, a, T, lengths, ws, s);
-    else switch (g.N) {
+        return launch_ssm_chunked(g, a, T, lengths, status, ws, s);
+    switch (g.N) {
         case 32: e = walk_cfg<32, Act>(g, a, T, lengths, s); break;
         case 64: e = walk_cfg<64, Act>(g, a, T, lengths, s); break;
         case 128: e = walk_cfg<128, Act>(g, a, T, lengths, s); break;

@@ -59,8 +59,8 @@ struct Rows {
 // Prompts up to this length take the token walk.
 constexpr int kWalkTokens = 32;
 size_t chunked_ws_bytes(const SsmGeo& g, int T);
-hipError_t launch_ssm_chunked(const SsmGeo& g, const SsmArgs& a, int T, const int32_t* lengths, void* ws,
-                              hipStream_t s);
+hipError_t launch_ssm_chunked(const SsmGeo& g, const SsmArgs& a, int T, const int32_t* lengths, int32_t* status,
+                              void* ws, hipStream_t s);
 
 }  // namespace ssm
 }  // namespace gdn

@@ -9,18 +9,18 @@
 // strong the decay.
 //
 //   prep   one workgroup per (sequence, chunk, group): conv and SiLU of the
-//          group's B and C channels, and G, once for all heads of the group.
-//   steps  one wave per (sequence, chunk, head): d and c.
+//          group's B and C channels, and G, once for all heads of the group;
+//          beside them the step sizes d and the sums c, per head.
 //   chunk  one wave per (sequence, head, 32 rows of the state, segment of
 //          chunks): the state stays transposed in accumulators (entries down,
 //          rows across) from chunk to chunk, and since a lane's accumulators
 //          of one product are its operand of the next (the fragment order
 //          below), no value passes between lanes.
 //   A prompt is cut into segments where there are too few (sequence, head)
-//   pairs to fill the chip: one pass forms each segment's own state from zero,
-//   `join` adds them up (the decay of a head is one number, so states combine
-//   by a scaled sum), and a second pass forms the outputs from the states that
-//   enter the segments.  The price is reading x twice.
+//   pairs to fill the chip: `state` forms each segment's own state from zero
+//   and leaves the convolved x behind, `join` adds the states up (the decay of
+//   a head is one number, so they combine by a scaled sum), and the output pass
+//   runs from the states that enter the segments.
 //
 // Precision.  fp16 matrix products with fp32 accumulation.  Every operand is
 // scaled by a power of two that keeps its largest value in range: B and C per
@@ -56,11 +56,17 @@ __device__ __forceinline__ f16v zero16() {
         z[v] = 0.0f;
     return z;
 }
+// A uniform base and a lane's 32-bit byte offset: one register of addresses
+// instead of two.
+template <typename T>
+__device__ __forceinline__ T& at(const void* base, uint32_t bytes) {
+    return *reinterpret_cast<T*>(const_cast<char*>(static_cast<const char*>(base)) + bytes);
+}
 __device__ __forceinline__ h8 ld_frag(const _Float16* m, int frag, int lane) {
-    return *reinterpret_cast<const h8*>(m + frag * 512 + lane * 8);
+    return at<const h8>(m + frag * 512, static_cast<uint32_t>(lane) * 16u);
 }
 __device__ __forceinline__ void st_frag(_Float16* m, int frag, int lane, h8 v) {
-    *reinterpret_cast<h8*>(m + frag * 512 + lane * 8) = v;
+    at<h8>(m + frag * 512, static_cast<uint32_t>(lane) * 16u) = v;
 }
 // v = hi + lo in fp16 (22 bits where v is well inside fp16's range).  The value
 // is pinned first: a product's rounding to fp16 may be fused into the multiply
@@ -71,7 +77,7 @@ __device__ __forceinline__ void split8(const float (&v)[8], h8& hi, h8& lo) {
         float x = v[e];
         asm("" : "+v"(x));
         hi[e] = static_cast<_Float16>(x);
-        lo[e] = static_cast<_Float16>(x - static_cast<float>(hi[e]));
+        lo[e] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(hi[e]), -1.0f, x));
     }
 }
 // One fp16 number per value.
@@ -99,16 +105,180 @@ __device__ __forceinline__ float pow2_to(float m) {
     const int f = 254 + TO - e;
     return __uint_as_float(static_cast<uint32_t>(f < 127 + MOST ? f : 127 + MOST) << 23);
 }
-// Caps of the scales.  Values below 2^-38 (B, C of a token) or 2^-32 (X' of a
-// row) lose relative precision to the absolute 2^-64 of fp16 at that scale; in
-// return no product of scales leaves fp32's range.
-constexpr int kMostBC = 40, kMostX = 40, kMostS = 100;
+// Caps of the scales.  A row of B, C, x, X' or X'' whose largest value is below
+// 2^-38 loses relative precision to fp16's absolute 2^-24 at that scale; in
+// return no product of scales and states leaves fp32's range.
+constexpr int kMostBC = 40, kMostX = 24, kMostF = 24, kMostW = 48, kMostS = 100;
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
+
+// Nothing moves across, and values loaded before are loaded again after: the
+// compiler would otherwise hoist whole phases' loads, or keep their values, and
+// run out of registers.
+__device__ __forceinline__ void phase() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+// The value is computed by here (the compiler may otherwise sink what computes
+// it past a phase and keep all its operands instead).
+__device__ __forceinline__ void pin(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void pin(h8& v) { asm volatile("" : "+v"(v)); }
+// Orders a wave's LDS accesses: what one lane wrote is there for the others.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// ------------------------------------------------------------ conv
+
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+
+// A wave's tile in LDS: 64 tokens x 32 channels of x after the four tokens
+// before them; later 32 tokens of y in fp32.  The pitch (40 elements) puts the
+// two lane halves' rows, four apart, into different banks.
+template <typename Act>
+struct Tile {
+    static constexpr int kUnit = 16 / sizeof(Act);     // channels per 16 bytes
+    static constexpr int kPerRow = 32 / kUnit;         // 16-byte units per row; also units per lane of 64 rows
+    static constexpr int kRowStep = 64 / kPerRow;      // rows between a lane's units
+    static constexpr int kPitch = 40;
+    static constexpr int kRows = Q + 4;
+    static constexpr int kBytes = kRows * kPitch * sizeof(Act);
+    static_assert(kBytes >= 32 * kPitch * 4, "half a tile of fp32 outputs fits");
+};
+
+// One channel's taps.  bf16 keeps them in pairs for the packed dot product (fp32
+// accumulation, within one rounding of the exact sum), in the two alignments
+// that a window can have against pairs of tokens; the taps that a pair has no
+// part in are zeros.
+template <typename Act>
+struct Taps;
+template <>
+struct Taps<uint16_t> {
+    uint32_t z0, w12, w3z, w01, w23;
+    float bias;
+    __device__ void load(const uint16_t* w, const uint16_t* b, int ch) {
+        const uint2 r = *reinterpret_cast<const uint2*>(w + static_cast<size_t>(ch) * 4);
+        w01 = r.x;
+        w23 = r.y;
+        z0 = r.x << 16;
+        w12 = (r.x >> 16) | (r.y << 16);
+        w3z = r.y >> 16;
+        bias = b ? widen(b[ch]) : 0.0f;
+    }
+};
+template <>
+struct Taps<float> {
+    float w[4];
+    float bias;
+    __device__ void load(const float* p, const float* b, int ch) {
+        const float4 r = *reinterpret_cast<const float4*>(p + static_cast<size_t>(ch) * 4);
+        w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+        bias = b ? b[ch] : 0.0f;
+    }
+};
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, a), __builtin_bit_cast(b2, b), c, false);
+}
+
+// SiLU(conv) of run r of this lane's channel: tokens 8 r + 4 hi .. + 3 of the tile.
+// bf16: the transposing LDS read gives a lane four tokens of its channel; the
+// lane supplies the address of four channels of one token.
+__device__ __forceinline__ void conv_run(const uint16_t* tile, const Taps<uint16_t>& k, int r, int lane, float (&out)[4]) {
+    typedef __attribute__((address_space(3))) s4* lds4;
+    const int row = (lane >> 5) * 4 + ((lane & 15) >> 2);
+    const uint16_t* p = tile + row * Tile<uint16_t>::kPitch + (lane & 16) + (lane & 3) * 4 + 8 * r * Tile<uint16_t>::kPitch;
+    const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p));
+    const uint2 b = __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * Tile<uint16_t>::kPitch)));
+    out[0] = silu(dot2(b.x, k.w3z, dot2(a.y, k.w12, dot2(a.x, k.z0, k.bias))));
+    out[1] = silu(dot2(b.x, k.w23, dot2(a.y, k.w01, k.bias)));
+    out[2] = silu(dot2(b.y, k.w3z, dot2(b.x, k.w12, dot2(a.y, k.z0, k.bias))));
+    out[3] = silu(dot2(b.y, k.w23, dot2(b.x, k.w01, k.bias)));
+}
+__device__ __forceinline__ void conv_run(const float* tile, const Taps<float>& k, int r, int lane, float (&out)[4]) {
+    const float* p = tile + ((lane >> 5) * 4 + 8 * r + 1) * Tile<float>::kPitch + (lane & 31);
+    float v[7];
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        v[e] = p[e * Tile<float>::kPitch];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float win[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+        out[i] = conv_bias_silu(k.w, win, k.bias);
+    }
+}
+
+// A wave's path of x from memory through its tile, a chunk at a time.
+template <typename Act>
+struct Stream {
+    using Tl = Tile<Act>;
+    Act* tile;
+    const Act* x;     // the sequence's rows, at the wave's first channel
+    int C, len, urow, ucol, lane;
+    u4 unit[Tl::kPerRow];
+    u4 keep;          // the tile's last four rows (lanes 0 .. 4 * kPerRow - 1)
+
+    __device__ void load(int t0) {   // rows behind the sequence's end are the last row again
+#pragma unroll
+        for (int k = 0; k < Tl::kPerRow; ++k) {
+            const int r = min(urow + k * Tl::kRowStep, len - 1 - t0);
+            unit[k] = at<const u4>(x + static_cast<size_t>(t0) * C,
+                                   static_cast<uint32_t>(r * C + ucol) * static_cast<uint32_t>(sizeof(Act)));
+        }
+    }
+    // the four rows before t0: of the sequence, or the conv tail of these channels
+    __device__ void begin(const Act* tail, int t0) {
+        if (t0 > 0) {
+            if (lane < 4 * Tl::kPerRow)
+                keep = *reinterpret_cast<const u4*>(x + static_cast<size_t>(t0 - 4 + lane / Tl::kPerRow) * C +
+                                                    lane % Tl::kPerRow * Tl::kUnit);
+        } else {
+            if (lane < 32) {
+                const typename Quad<Act>::raw r = Quad<Act>::load(tail + lane * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    tile[j * Tl::kPitch + lane] = Quad<Act>::elem(r, j);
+            }
+            wave_sync();
+            save(0);
+        }
+    }
+    __device__ void save(int row) {
+        if (lane < 4 * Tl::kPerRow)
+            keep = *reinterpret_cast<const u4*>(tile + (row + lane / Tl::kPerRow) * Tl::kPitch +
+                                                lane % Tl::kPerRow * Tl::kUnit);
+    }
+    __device__ void store() {
+        if (lane < 4 * Tl::kPerRow)
+            *reinterpret_cast<u4*>(tile + lane / Tl::kPerRow * Tl::kPitch + lane % Tl::kPerRow * Tl::kUnit) = keep;
+#pragma unroll
+        for (int k = 0; k < Tl::kPerRow; ++k)
+            *reinterpret_cast<u4*>(tile + (4 + urow + k * Tl::kRowStep) * Tl::kPitch + ucol) = unit[k];
+    }
+};
+template <typename Act>
+__device__ __forceinline__ Stream<Act> make_stream(Act* tile, const Act* x, int C, int len, int lane) {
+    Stream<Act> s;
+    s.tile = tile;
+    s.x = x;
+    s.C = C;
+    s.len = len;
+    s.lane = lane;
+    s.urow = lane / Tile<Act>::kPerRow;
+    s.ucol = lane % Tile<Act>::kPerRow * Tile<Act>::kUnit;
+    s.keep = u4{0, 0, 0, 0};
+    return s;
+}
+
+// ------------------------------------------------------------ prep
+
 // What prep leaves for one (sequence, group, chunk), in fragments of 64 lanes x
-// 8 fp16 (1 KB): C (rows: tokens, k: entries), B transposed (rows: entries, k:
-// tokens) and G (rows: tokens, k: tokens; the six k-steps at or below the
-// diagonal), each as hi and, where wanted, lo; then 2^-s per token of B and C.
+// 8 fp16 (1 KB): C (rows: tokens, k: entries), G (rows: tokens, k: tokens; the
+// six k-steps at or below the diagonal) and B transposed (rows: entries, k:
+// tokens), each as hi and, where wanted, lo; then 2^-s per token of B and C.
 template <int N, bool FINE>
 struct Shared {
     static constexpr int CF = 2 * (N / 16), BF = 4 * (N / 32), GF = 6;   // fragments of one part
@@ -118,114 +288,226 @@ struct Shared {
     static __device__ int g_frag(int it, int ks) { return it == 0 ? ks : 2 + ks; }
 };
 
-template <int N, typename Act, bool FINE>
-__global__ __launch_bounds__(512) void ssm_prep_kernel(const Act* __restrict__ x, const Act* __restrict__ tail,
-                                                       const Act* __restrict__ w, const Act* __restrict__ bias,
-                                                       const int32_t* __restrict__ lengths, int T, int H, int G, int P,
-                                                       int C, int nc, _Float16* __restrict__ out) {
-    using Sh = Shared<N, FINE>;
-    using Qd = Quad<Act>;
-    constexpr int PITCH = 2 * N + 1;
-    constexpr int SPLIT = 512 / (2 * N) > 0 ? 512 / (2 * N) : 1;   // threads per channel
-    constexpr int PER = Q / SPLIT;                                 // tokens per thread
-    extern __shared__ __align__(16) float lds[];                   // [Q][PITCH], then [2][Q] scales
-    float* sc = lds + Q * PITCH;
+struct ChunkArgs {
+    SsmArgs p;
+    const int32_t* lengths;
+    int32_t* status;
+    _Float16* shared;         // per (sequence, group, chunk): Shared<>
+    float* steps;             // [B][H][nc][3][64]: d, then c as a high and a low part
+    float* seg_state;         // [B][H][segments][P][N]
+    float* seg_decay;         // [B][H][segments] log2 of the segment's decay
+    char* conv;               // [B][H][nc][P / 32] convolved x (Conv<>)
+    int T, B, H, G, P, C, nc, segs, chunks_per_seg, by_xcd;
+};
 
-    const int chunk = blockIdx.x % nc;
-    const int g = (blockIdx.x / nc) % G;
-    const int seq = blockIdx.x / nc / G;
-    const int len = lengths ? lengths[seq] : T;
-    const int t0 = chunk * Q;
-    if (len > T || t0 >= len)
+// Largest of a 16-lane row's values, in all its lanes.
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, dpp_move<0xB1>(v));
+    v = fmaxf(v, dpp_move<0x4E>(v));
+    v = fmaxf(v, dpp_move<0x141>(v));
+    return fmaxf(v, dpp_move<0x140>(v));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = row_max(v);
+    const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
+    const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
+    const float c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32));
+    const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+    return fmaxf(fmaxf(a, b), fmaxf(c, d));
+}
+
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ double wave_scan(double v, int lane) {
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+        const double u = __shfl_up(v, k);
+        v += lane >= k ? u : 0.0;
+    }
+    return v;
+}
+
+constexpr int kStepHeads = 16;   // heads per workgroup of the step sizes
+
+// Step sizes and summed decays of a chunk's tokens.  c is summed in fp64: what
+// matters are differences of it, also where it is large.
+__device__ void steps_part(const ChunkArgs& a, int id, float* lds) {
+    const int hb = (a.H + kStepHeads - 1) / kStepHeads;
+    const int h0 = id % hb * kStepHeads;
+    const int chunk = id / hb % a.nc;
+    const int seq = id / hb / a.nc;
+    const int len = a.lengths ? a.lengths[seq] : a.T;
+    if (len > a.T || chunk * Q >= len)
         return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int heads = min(kStepHeads, a.H - h0);
+    for (int i = threadIdx.x; i < Q * kStepHeads; i += blockDim.x) {   // [token][head] -> [head][token]
+        const int t = chunk * Q + i / kStepHeads, k = i % kStepHeads;
+        lds[k * (Q + 1) + i / kStepHeads] =
+            t < len && k < heads ? a.p.dt[(static_cast<size_t>(seq) * a.T + t) * a.H + h0 + k] : 0.0f;
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 63;
+    for (int k = threadIdx.x >> 6; k < heads; k += blockDim.x >> 6) {
+        const int h = h0 + k;
+        const float d = chunk * Q + lane < len
+                            ? step_size(lds[k * (Q + 1) + lane] + (a.p.dt_bias ? a.p.dt_bias[h] : 0.0f)) : 0.0f;
+        const double cum = wave_scan(static_cast<double>(d) * static_cast<double>(rate2(a.p.A[h])), lane);
+        const float high = static_cast<float>(cum);
+        float* o = a.steps + ((static_cast<size_t>(seq) * a.H + h) * a.nc + chunk) * (3 * Q);
+        o[lane] = d;
+        o[Q + lane] = high;
+        o[2 * Q + lane] = static_cast<float>(cum - static_cast<double>(high));
+    }
+}
 
-    {
-        const int j = tid % (2 * N);
-        const int tb = tid / (2 * N) * PER;
-        const int ch = H * P + (j < N ? g * N + j : G * N + g * N + j - N);
-        const Act* xs = x + static_cast<size_t>(seq) * T * C + ch;
-        float wf[4], tw[4], win[4];
-        Qd::to_float(Qd::load(w + static_cast<size_t>(ch) * 4), wf);
-        Qd::to_float(Qd::load(tail + (static_cast<size_t>(seq) * C + ch) * 4), tw);
-        const float bf = bias ? widen(bias[ch]) : 0.0f;
-        win[0] = 0.0f;
-#pragma unroll
-        for (int k = 1; k < 4; ++k) {   // the three inputs before this thread's first
-            const int t = t0 + tb - 4 + k;
-            win[k] = t < 0 ? tw[k] : t < len ? widen(xs[static_cast<size_t>(t) * C]) : 0.0f;
-        }
-#pragma unroll 16
-        for (int i = 0; i < PER; ++i) {
-            const int t = t0 + tb + i;
-            win[0] = win[1];
-            win[1] = win[2];
-            win[2] = win[3];
-            win[3] = t < len ? widen(xs[static_cast<size_t>(t) * C]) : 0.0f;
-            lds[(tb + i) * PITCH + j] = t < len ? conv_bias_silu(wf, win, bf) : 0.0f;
-        }
+// One workgroup of N / 16 waves per (sequence, group, chunk): a wave convolves 32
+// of the group's 2 N channels.  B goes out straight from registers (a lane's
+// runs of four tokens are the fragments' k order); C and the rows that G is
+// formed from pass through LDS.
+template <int N, typename Act, bool FINE>
+__global__ __launch_bounds__(4 * N) void ssm_prep_kernel(ChunkArgs a, int prep_wgs) {
+    using Sh = Shared<N, FINE>;
+    constexpr int W = N / 16, KS = N / 16;
+    constexpr int kRowHalfs = Q * N;   // one part of B's or C's rows, in fragment order
+    extern __shared__ __align__(16) char pool[];
+    if (static_cast<int>(blockIdx.x) >= prep_wgs) {
+        steps_part(a, blockIdx.x - prep_wgs, reinterpret_cast<float*>(pool));
+        return;
     }
-    __syncthreads();
-    _Float16* o = out + ((static_cast<size_t>(seq) * G + g) * nc + chunk) * Sh::kHalfs;
-    float* osc = reinterpret_cast<float*>(o + Sh::kFrags * 512);
-    // each token's row of B and of C is brought to [4, 8): |G| <= 64 N stays in range
-    for (int r = wave; r < 2 * Q; r += 8) {
-        const float* row = lds + (r % Q) * PITCH + (r < Q ? 0 : N);
-        float m = 0.0f;
-        for (int n = lane; n < N; n += 64)
-            m = fmaxf(m, fabsf(row[n]));
-#pragma unroll
-        for (int k = 32; k >= 1; k >>= 1)
-            m = fmaxf(m, __shfl_xor(m, k));
-        if (lane == 0) {
-            const float s = pow2_to<2, kMostBC>(m);
-            sc[r] = s;
-            osc[r] = inverse_pow2(s);
-        }
-    }
-    __syncthreads();
+    const int chunk = blockIdx.x % a.nc;
+    const int g = blockIdx.x / a.nc % a.G;
+    const int seq = blockIdx.x / a.nc / a.G;
+    const int len = a.lengths ? a.lengths[seq] : a.T;
+    const int t0 = chunk * Q;
+    if (len > a.T || t0 >= len)
+        return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hi = lane >> 5, c = lane & 31;
-    // row fragment: token row, entries in k order
-    auto row_frag = [&](int tok, int off, int ks, float s, h8& fh, h8& fl) {
+    const int half = wave / (W / 2);   // 0: B, 1: C
+    const int nb = wave % (W / 2);     // 32-channel block
+    const int ch0 = a.H * a.P + half * a.G * N + g * N + nb * 32;
+
+    constexpr int kTiles = FINE ? 0 : W * Tile<Act>::kBytes;   // fp32 reads x directly
+    constexpr int kRows = (FINE ? 4 : 2) * kRowHalfs * 2;
+    _Float16* rows = reinterpret_cast<_Float16*>(pool);         // [B, C][hi, lo][fragments]; after the tiles' use
+    float* part = reinterpret_cast<float*>(pool + (kTiles > kRows ? kTiles : kRows));   // [wave][2][64]
+    float* sc = part + W * 2 * Q;                                                       // [B, C][64]
+
+    Taps<Act> taps;
+    taps.load(static_cast<const Act*>(a.p.w), static_cast<const Act*>(a.p.bias), ch0 + c);
+    const Act* xs = static_cast<const Act*>(a.p.x) + static_cast<size_t>(seq) * a.T * a.C + ch0;
+    const Act* tail = static_cast<const Act*>(a.p.tail_in) + (static_cast<size_t>(seq) * a.C + ch0) * 4;
+    float u[32];
+    if constexpr (FINE) {
+        float tw[4];
+        Quad<Act>::to_float(Quad<Act>::load(tail + c * 4), tw);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            float v[7];
+#pragma unroll
+            for (int e = 0; e < 7; ++e) {
+                const int t = t0 + 8 * r + 4 * hi + e - 3;
+                const float x = xs[static_cast<size_t>(max(0, min(t, len - 1))) * a.C + c];
+                v[e] = t >= 0 ? x : t == -1 ? tw[3] : t == -2 ? tw[2] : tw[1];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float win[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+                u[4 * r + i] = conv_bias_silu(taps.w, win, taps.bias);
+            }
+        }
+    } else {
+        Stream<Act> in = make_stream(reinterpret_cast<Act*>(pool + wave * Tile<Act>::kBytes), xs, a.C, len, lane);
+        in.load(t0);
+        in.begin(tail, t0);
+        in.store();
+        wave_sync();
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            float v[4];
+            conv_run(in.tile, taps, r, lane, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[4 * r + i] = v[i];
+        }
+    }
+    if (t0 + Q > len) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            u[k] = t0 + 8 * (k / 4) + 4 * hi + k % 4 < len ? u[k] : 0.0f;
+    }
+    // each token's row of B and of C is brought to [4, 8): |G| <= 64 N stays in range
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        float m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m[i] = row_max(fabsf(u[4 * r + i]));
+        if ((lane & 15) == 0)
+            *reinterpret_cast<float4*>(part + (wave * 2 + ((lane >> 4) & 1)) * Q + 8 * r + 4 * hi) =
+                make_float4(m[0], m[1], m[2], m[3]);
+    }
+    __syncthreads();
+    _Float16* o = a.shared + ((static_cast<size_t>(seq) * a.G + g) * a.nc + chunk) * Sh::kHalfs;
+    for (int i = threadIdx.x; i < 2 * Q; i += 4 * N) {
+        float m = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            m = fmaxf(m, part[(i / Q * W + k) * Q + i % Q]);
+        const float s = pow2_to<2, kMostBC>(m);
+        sc[i] = s;
+        reinterpret_cast<float*>(o + Sh::kFrags * 512)[i] = inverse_pow2(s);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = lds[tok * PITCH + off + 16 * ks + kperm(hi, e)] * s;
-        split8(v, fh, fl);
-    };
-    for (int f = wave; f < Sh::CF; f += 8) {
-        const int it = f / (N / 16), ks = f % (N / 16);
+        for (int q = 0; q < 2; ++q) {
+            const float4 s = *reinterpret_cast<const float4*>(sc + half * Q + 16 * ks + 8 * q + 4 * hi);
+            const float ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[4 * q + i] = u[8 * ks + 4 * q + i] * ss[i];
+        }
         h8 fh, fl;
-        row_frag(32 * it + c, N, ks, sc[Q + 32 * it + c], fh, fl);
-        st_frag(o, Sh::kC + f, lane, fh);
-        if (FINE)
-            st_frag(o, Sh::kCl + f, lane, fl);
-    }
-    for (int f = wave; f < Sh::BF; f += 8) {
-        const int nt = f / 4, ks = f % 4;
-        float v[8];
+        split8(v, fh, fl);
+        if (half == 0) {
+            st_frag(o, Sh::kB + nb * 4 + ks, lane, fh);
+            st_frag(o, Sh::kBl + nb * 4 + ks, lane, fl);
+        }
+        // entry n of token t in fragment order of the rows
+        const int n = nb * 32 + c;
+        const int at = (n / 16 * 64 + ((n >> 2) & 1) * 32) * 8 + ((n >> 3) & 1) * 4 + (n & 3);
+        _Float16* row = rows + half * (FINE ? 2 : 1) * kRowHalfs;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int t = 16 * ks + kperm(hi, e);
-            v[e] = lds[t * PITCH + 32 * nt + c] * sc[t];
+            const int pos = (t >> 5) * (KS * 512) + (t & 31) * 8 + at;
+            row[pos] = fh[e];
+            if (FINE)
+                row[kRowHalfs + pos] = fl[e];
         }
-        h8 fh, fl;
-        split8(v, fh, fl);
-        st_frag(o, Sh::kB + f, lane, fh);
-        st_frag(o, Sh::kBl + f, lane, fl);
+    }
+    __syncthreads();
+    const _Float16* Br = rows;
+    const _Float16* Cr = rows + (FINE ? 2 : 1) * kRowHalfs;
+    for (int f = wave; f < Sh::CF; f += W) {
+        st_frag(o, Sh::kC + f, lane, ld_frag(Cr, f, lane));
+        if (FINE)
+            st_frag(o, Sh::kCl + f, lane, ld_frag(Cr + kRowHalfs, f, lane));
     }
     // G transposed (rows j, columns i): its accumulators are the rows-i fragments
-    if (wave < 3) {
-        const int it = wave == 0 ? 0 : 1, jt = wave == 2 ? 1 : 0;
+    for (int tile = wave; tile < 3; tile += W) {
+        const int it = tile == 0 ? 0 : 1, jt = tile == 2 ? 1 : 0;
         f16v acc = zero16();
-        for (int ks = 0; ks < N / 16; ++ks) {
-            h8 bh, bl, ch, cl;
-            row_frag(32 * jt + c, 0, ks, sc[32 * jt + c], bh, bl);
-            row_frag(32 * it + c, N, ks, sc[Q + 32 * it + c], ch, cl);
+#pragma unroll 4
+        for (int ks = 0; ks < KS; ++ks) {
+            const h8 bh = ld_frag(Br, jt * KS + ks, lane), ch = ld_frag(Cr, it * KS + ks, lane);
             acc = mma(bh, ch, acc);
             if (FINE) {
-                acc = mma(bh, cl, acc);
-                acc = mma(bl, ch, acc);
+                acc = mma(bh, ld_frag(Cr + kRowHalfs, it * KS + ks, lane), acc);
+                acc = mma(ld_frag(Br + kRowHalfs, jt * KS + ks, lane), ch, acc);
             }
         }
 #pragma unroll
@@ -244,110 +526,30 @@ __global__ __launch_bounds__(512) void ssm_prep_kernel(const Act* __restrict__ x
     }
 }
 
-// Inclusive sum over the wave's lanes.
-__device__ __forceinline__ double wave_scan(double v, int lane) {
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-        const double u = __shfl_up(v, k);
-        v += lane >= k ? u : 0.0;
-    }
-    return v;
+template <int N, typename Act, bool FINE>
+constexpr size_t prep_lds() {
+    constexpr size_t tiles = FINE ? 0 : N / 16 * Tile<Act>::kBytes, rows = (FINE ? 4 : 2) * Q * N * 2;
+    constexpr size_t prep = (tiles > rows ? tiles : rows) + N / 16 * 2 * Q * 4 + 2 * Q * 4;
+    constexpr size_t steps = kStepHeads * (Q + 1) * 4;
+    return prep > steps ? prep : steps;
 }
 
-// Step sizes and summed decays of a chunk's tokens, one wave per (sequence,
-// chunk, head): d, then c as a high and a low fp32 part, 64 each.  c is summed
-// in fp64: what matters are differences of it, also where it is large.
-__global__ __launch_bounds__(256) void ssm_steps_kernel(const float* __restrict__ dt,
-                                                        const float* __restrict__ dt_bias,
-                                                        const float* __restrict__ A,
-                                                        const int32_t* __restrict__ lengths, int T, int H, int nc,
-                                                        int64_t waves, float* __restrict__ steps) {
-    const int lane = threadIdx.x & 63;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
-    if (id >= waves)
-        return;
-    const int h = static_cast<int>(id % H);
-    const int chunk = static_cast<int>(id / H % nc);
-    const int seq = static_cast<int>(id / H / nc);
-    const int len = lengths ? lengths[seq] : T;
-    if (len > T || chunk * Q >= len)
-        return;
-    const int t = chunk * Q + lane;
-    const float d = t < len ? step_size(dt[(static_cast<size_t>(seq) * T + t) * H + h] + (dt_bias ? dt_bias[h] : 0.0f))
-                            : 0.0f;
-    const double cum = wave_scan(static_cast<double>(d) * static_cast<double>(rate2(A[h])), lane);
-    const float high = static_cast<float>(cum);
-    float* o = steps + ((static_cast<size_t>(seq) * H + h) * nc + chunk) * (3 * Q);
-    o[lane] = d;
-    o[Q + lane] = high;
-    o[2 * Q + lane] = static_cast<float>(cum - static_cast<double>(high));
-}
+// ------------------------------------------------------------ chunks
 
-struct ChunkArgs {
-    SsmArgs p;
-    const int32_t* lengths;
-    const _Float16* shared;   // prep's output
-    const float* steps;       // steps' output [B][H][nc][3][64]
-    float* seg_state;         // [B][H][segments][P][N]
-    float* seg_decay;         // [B][H][segments] log2 of the segment's decay
-    int T, B, H, G, P, C, nc, segs, chunks_per_seg, by_xcd;
+// Convolved x of one (sequence, head, chunk, 32 rows), as the output pass takes
+// it.  bf16: four fragments in fp16 (k: tokens, columns: rows of the state), in a
+// scale per row that follows them.  fp32: the lane's 32 values, four at a time.
+template <bool FINE>
+struct Conv {
+    static constexpr size_t kBytes = FINE ? 64 * 32 * 4 : 4 * 1024 + 32 * 4;
 };
 
-// A wave's tile of 64 tokens x 32 channels of x in LDS, and later of y in fp32,
-// 32 tokens at a time.  The pitch (40 elements) puts the two lane halves' rows,
-// four apart, into different banks.
-template <typename Act>
-struct Tile {
-    static constexpr int kUnit = 16 / sizeof(Act);     // channels per 16 bytes
-    static constexpr int kPerRow = 32 / kUnit;         // 16-byte units per row; also units per lane of 64 rows
-    static constexpr int kRowStep = 64 / kPerRow;      // rows between a lane's units
-    static constexpr int kPitch = 40;
-    static constexpr int kBytes = Q * kPitch * sizeof(Act);
-    static_assert(kBytes >= 32 * kPitch * 4, "half a tile of fp32 outputs fits");
+// Which work is this workgroup's, and its place in memory; false: none.
+struct Place {
+    int g, h, seg, seq, len, ch0, ch1, last;
+    size_t head;
 };
-typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-
-// Nothing moves across, and values loaded before are loaded again after: the
-// compiler would otherwise hoist whole phases' loads, or keep their values, and
-// run out of registers.
-__device__ __forceinline__ void phase() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-// The value is computed by here (the compiler may otherwise sink what computes
-// it past a phase and keep all its operands instead).
-__device__ __forceinline__ void pin(float& v) { asm volatile("" : "+v"(v)); }
-__device__ __forceinline__ void pin(h8& v) { asm volatile("" : "+v"(v)); }
-
-// Orders a wave's LDS accesses: what one lane wrote is there for the others.
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
-// One workgroup per (sequence, head, segment), one wave per 32 rows of the
-// state.  With every row's operands in one scale, a chunk's outputs are a single
-// product over 64 + N terms, Y = [M . G | 2^c C] [X'; S0^T]; its left factor is
-// the head's, so each wave builds a part of it and leaves it in LDS for all (the
-// one thing that the waves share; all else is a wave's own).  x comes a chunk
-// ahead, in 16-byte loads through a tile in LDS, and y leaves the same way.
-// OUT: form the outputs.  EXACT: the state's products in two fp16 parts.  With
-// segments, OUT without EXACT serves bf16 outputs (the state comes from join).
-template <int N, typename Act, bool FINE, bool OUT, bool EXACT>
-__global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel(ChunkArgs a) {
-    using Sh = Shared<N, FINE>;
-    using Qd = Quad<Act>;
-    using Tl = Tile<Act>;
-    constexpr int NT = N / 32, KS = N / 16;
-    constexpr int AF = Sh::GF + Sh::CF;   // fragments of the left factor (of one part)
-    constexpr int NF = OUT ? 6 : 2;
-    extern __shared__ __align__(16) char pool[];   // [waves][tile, factors], then the left factor
-
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int hi = lane >> 5, c = lane & 31;
-    const int waves = a.P / 32;
+__device__ __forceinline__ bool place(const ChunkArgs& a, bool report, Place& w) {
     // workgroup -> (sequence, segment, group), head of the group: all heads that
     // read the same fragments on one XCD (workgroups go to the eight in turn)
     const int rep = a.H / a.G;
@@ -360,448 +562,461 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         member = blockIdx.x % rep;
     }
     if (set >= a.B * a.segs * a.G)
-        return;
-    const int g = set % a.G;
-    const int h = g * rep + member;
-    const int seg = set / a.G % a.segs;
-    const int seq = set / a.G / a.segs;
-    const int len = a.lengths ? a.lengths[seq] : a.T;
-    if (len < 1 || len > a.T)
-        return;
-    const int last = (len + Q - 1) / Q;
-    const int ch0 = seg * a.chunks_per_seg;
-    const int ch1 = ch0 + a.chunks_per_seg < last ? ch0 + a.chunks_per_seg : last;
-    if (ch0 >= ch1)
-        return;
-    const bool split = a.segs > 1;
+        return false;
+    w.g = set % a.G;
+    w.h = w.g * rep + member;
+    w.seg = set / a.G % a.segs;
+    w.seq = set / a.G / a.segs;
+    w.head = static_cast<size_t>(w.seq) * a.H + w.h;
+    w.len = a.lengths ? a.lengths[w.seq] : a.T;
+    const bool bad = w.len < 0 || w.len > a.T;
+    if (report && a.status && w.h == 0 && w.seg == 0 && threadIdx.x == 0)
+        a.status[w.seq] = bad ? GDN_ERR_INDEX : GDN_OK;
+    if (bad)
+        return false;
+    w.last = (w.len + Q - 1) / Q;
+    w.ch0 = w.seg * a.chunks_per_seg;
+    w.ch1 = min(w.ch0 + a.chunks_per_seg, w.last);
+    return w.ch0 < w.ch1;
+}
 
-    constexpr int kWaveBytes = Tl::kBytes + NF * Q * 4;
-    Act* xt = reinterpret_cast<Act*>(pool + wave * kWaveBytes);
-    float* yt = reinterpret_cast<float*>(pool + wave * kWaveBytes);
-    float* fF = reinterpret_cast<float*>(pool + wave * kWaveBytes + Tl::kBytes);   // d * 2^-s_B
-    float* fW = fF + Q;       // 2^(c_last - c)
-    float* fS = fF + 2 * Q;   // 2^-s_C
-    float* fK = fF + 3 * Q;   // D * 2^s_C
-    float* fH = fF + 4 * Q;   // c, high and low part
-    float* fL = fF + 5 * Q;
-    _Float16* L = reinterpret_cast<_Float16*>(pool + waves * kWaveBytes);
-
-    const int col0 = h * a.P + wave * 32;
-    const int chan = col0 + c;   // this lane's state row, as an x channel
-    const Act* xs = static_cast<const Act*>(a.p.x) + static_cast<size_t>(seq) * a.T * a.C;
-    float wf[4];
-    Qd::to_float(Qd::load(static_cast<const Act*>(a.p.w) + static_cast<size_t>(chan) * 4), wf);
-    const float bf = a.p.bias ? widen(static_cast<const Act*>(a.p.bias)[chan]) : 0.0f;
-    const float skip = a.p.D ? a.p.D[h] : 0.0f;
-    const size_t head = static_cast<size_t>(seq) * a.H + h;
-    const float* steps = a.steps + head * a.nc * (3 * Q);
-    const _Float16* shared0 = a.shared + (static_cast<size_t>(seq) * a.G + g) * a.nc * Sh::kHalfs;
-
-    // unit k of this lane: row urow + k * kRowStep, channels ucol ..
-    const int urow = lane / Tl::kPerRow, ucol = lane % Tl::kPerRow * Tl::kUnit;
-    u4 xu[Tl::kPerRow];
-    float st_d, st_h, st_l, st_b, st_c = 1.0f;   // the chunk's step, c, scales (one token per lane)
-    auto load_chunk = [&](int ch) {
-        // rows behind the sequence's end are the last row again; their step size is 0
+// The state, transposed: S[nt][v] is entry 32 nt + 8 (v / 4) + 4 hi + v % 4 of the
+// lane's row; `row` points at entry 4 hi.
+template <int NT>
+__device__ __forceinline__ void load_state(f16v (&S)[NT], const float* row) {
 #pragma unroll
-        for (int k = 0; k < Tl::kPerRow; ++k) {
-            const int t = min(ch * Q + urow + k * Tl::kRowStep, len - 1);
-            xu[k] = *reinterpret_cast<const u4*>(xs + static_cast<size_t>(t) * a.C + col0 + ucol);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 v = *reinterpret_cast<const float4*>(row + 32 * nt + 8 * q);
+            S[nt][4 * q] = v.x;
+            S[nt][4 * q + 1] = v.y;
+            S[nt][4 * q + 2] = v.z;
+            S[nt][4 * q + 3] = v.w;
         }
-        const float* st = steps + static_cast<size_t>(ch) * (3 * Q);
-        const float* sc = reinterpret_cast<const float*>(shared0 + ch * Sh::kHalfs + Sh::kFrags * 512);
-        st_d = st[lane];
-        st_h = st[Q + lane];
-        st_l = st[2 * Q + lane];
-        st_b = sc[lane];
-        if (OUT)
-            st_c = sc[Q + lane];
-    };
-
-    // the three inputs before the segment
-    Act before[3];
-    {
-        const typename Qd::raw tr = Qd::load(static_cast<const Act*>(a.p.tail_in) +
-                                             (static_cast<size_t>(seq) * a.C + chan) * 4);
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            before[k] = ch0 == 0 ? Qd::elem(tr, k + 1) : xs[static_cast<size_t>(ch0 * Q - 3 + k) * a.C + chan];
-    }
-
-    // the state, transposed: S[nt][v] is entry 32 nt + 8 (v / 4) + 4 hi + v % 4 of this lane's row, times `unit`
-    f16v S[NT];
-    float unit = 1.0f;
-    const size_t row_off = static_cast<size_t>(wave * 32 + c) * N + 4 * hi;
-    float* seg_row = a.seg_state + (head * a.segs + seg) * a.P * N + row_off;
-    float* state_row = a.p.state + head * a.P * N + row_off;
-    if (OUT) {
-        const float* from = split ? seg_row : state_row;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 v = *reinterpret_cast<const float4*>(from + 32 * nt + 8 * q);
-                S[nt][4 * q] = v.x;
-                S[nt][4 * q + 1] = v.y;
-                S[nt][4 * q + 2] = v.z;
-                S[nt][4 * q + 3] = v.w;
-            }
-    } else {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            S[nt] = zero16();
-    }
-    // One dword of each 128-byte line of the chunk's fragments, so that they are in
-    // this XCD's L2 when their chunk comes: all heads of a group ask for them at
-    // about the same time, and all would wait for the memory behind it.
-    constexpr int kFrom = OUT ? 0 : Sh::kB, kTo = EXACT ? Sh::kFrags : Sh::kBl;
-    constexpr int kLines = (kTo - kFrom) * 8;
-    constexpr int kTouch = (kLines + 63) / 64;
-    uint32_t touched[kTouch];
-    auto touch = [&](int ch) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(shared0 + ch * Sh::kHalfs + kFrom * 512);
-#pragma unroll
-        for (int k = 0; k < kTouch; ++k)
-            if ((k * waves + wave) * 64 < kLines)   // kLines is a multiple of 32
-                touched[k] = p[min((k * waves + wave) * 64 + lane, kLines - 1) * 32];
-    };
-#pragma unroll
-    for (int k = 0; k < kTouch; ++k)
-        touched[k] = 0;
-    load_chunk(ch0);
-
-    // B's fragments of a k-step, loaded ahead of their products
-    constexpr int kAhead = OUT ? 1 : 2, kRing = kAhead + 1;
-    h8 bh_[kRing][NT], bl_[kRing][NT];
-    auto load_b = [&](const _Float16* sh, int ks) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            bh_[ks % kRing][nt] = ld_frag(sh, Sh::kB + nt * 4 + ks, lane);
-            if (EXACT)
-                bl_[ks % kRing][nt] = ld_frag(sh, Sh::kBl + nt * 4 + ks, lane);
-        }
-    };
-
-    double seg_sum = 0.0;
-    for (int ch = ch0; ch < ch1; ++ch) {
-        const int t0 = ch * Q;
-        const _Float16* sh = shared0 + ch * Sh::kHalfs;
-#pragma unroll
-        for (int k = 0; k < kTouch; ++k)
-            asm volatile("" ::"v"(touched[k]));
-        touch(min(ch + 1, ch1 - 1));
-        // x into the tile, the chunk's factors beside it
-#pragma unroll
-        for (int k = 0; k < Tl::kPerRow; ++k)
-            *reinterpret_cast<u4*>(xt + (urow + k * Tl::kRowStep) * Tl::kPitch + ucol) = xu[k];
-        const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
-        const float total = th + tl;
-        seg_sum += static_cast<double>(th) + static_cast<double>(tl);
-        fF[lane] = st_d * st_b;
-        fW[lane] = __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
-        if (OUT) {
-            fS[lane] = st_c;
-            fK[lane] = skip * inverse_pow2(st_c);
-            fH[lane] = st_h;
-            fL[lane] = st_l;
-        }
-        wave_sync();
-        if (!OUT) {
-            load_b(sh, 0);
-            load_b(sh, 1);
-        }
-        phase();
-
-        // conv; the largest of X' and of X'' in this row
-        float xc[32];
-        float m1 = 0.0f, m2 = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            float raw[7];
-#pragma unroll
-            for (int e = 0; e < 7; ++e) {
-                const int row = 8 * r + e - 3;
-                if (r == 0 && e < 3) {
-                    const Act v = xt[(row + 4) * Tl::kPitch + c];   // in the tile for the upper half
-                    raw[e] = widen(hi ? v : before[e]);
-                } else {
-                    raw[e] = widen(xt[(row + 4 * hi) * Tl::kPitch + c]);
-                }
-            }
-            const float4 F = *reinterpret_cast<const float4*>(fF + 8 * r + 4 * hi);
-            const float4 W = *reinterpret_cast<const float4*>(fW + 8 * r + 4 * hi);
-            const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float win[4] = {raw[i], raw[i + 1], raw[i + 2], raw[i + 3]};
-                const float v = conv_bias_silu(wf, win, bf);
-                xc[4 * r + i] = v;
-                const float xp = v * ff[i];
-                m1 = fmaxf(m1, fabsf(xp));
-                m2 = fmaxf(m2, fabsf(xp * ww[i]));
-                pin(xc[4 * r + i]);
-            }
-            pin(m1);
-            pin(m2);
-            if (r % 2)
-                phase();
-        }
-#pragma unroll
-        for (int k = 0; k < 3; ++k)   // the tile's last three rows
-            before[k] = xt[(Q - 3 + k) * Tl::kPitch + c];
-        load_chunk(min(ch + 1, ch1 - 1));
-        m1 = fmaxf(m1, __shfl_xor(m1, 32));
-        m2 = fmaxf(m2, __shfl_xor(m2, 32));
-        // the row's largest state entry
-        float ms = 0.0f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int v = 0; v < 16; ++v)
-                ms = fmaxf(ms, fabsf(S[nt][v]));
-        ms = fmaxf(ms, __shfl_xor(ms, 32));
-        // a common unit of the state's part and the chunk's is kept small enough for both
-        const float state_max = ms * inverse_pow2(unit);
-        const float room = fminf(pow2_to<60, kMostS>(state_max), unit * 0x1p60f);
-        const float s2 = fminf(pow2_to<8, kMostS>(m2), room);   // the unit of S1
-        const float sx = pow2_to<8, kMostX>(fmaxf(m1, state_max));
-
-        // X'' and X' as fragments; Y starts from D x
-        h8 wh[4], wl[4], xh[4], xl[4];
-        f16v Y[2];
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            float v[8], u[8];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float4 F = *reinterpret_cast<const float4*>(fF + 16 * ks + 8 * q + 4 * hi);
-                const float4 W = *reinterpret_cast<const float4*>(fW + 16 * ks + 8 * q + 4 * hi);
-                const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w};
-                float kk[4] = {};
-                if (OUT) {
-                    const float4 K = *reinterpret_cast<const float4*>(fK + 16 * ks + 8 * q + 4 * hi);
-                    kk[0] = K.x, kk[1] = K.y, kk[2] = K.z, kk[3] = K.w;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = xc[8 * ks + 4 * q + i];
-                    const float xp = x * ff[i];
-                    v[4 * q + i] = xp * (ww[i] * s2);
-                    if (OUT) {
-                        u[4 * q + i] = xp * sx;
-                        Y[ks / 2][8 * (ks % 2) + 4 * q + i] = (x * sx) * kk[i];
-                    }
-                }
-            }
-            parts8<EXACT>(v, wh[ks], wl[ks]);
-            pin(wh[ks]);
-            if (EXACT)
-                pin(wl[ks]);
-            if (OUT) {
-                parts8<FINE>(u, xh[ks], xl[ks]);
-                pin(xh[ks]);
-                if (FINE)
-                    pin(xl[ks]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float y = Y[ks / 2][8 * (ks % 2) + e];
-                    pin(y);
-                    Y[ks / 2][8 * (ks % 2) + e] = y;
-                }
-            }
-            phase();
-        }
-
-        if (OUT) {
-            // this wave's part of the left factor: M . G, then 2^c C; four fragments in flight
-            for (int f0 = wave; f0 < AF; f0 += 4 * waves) {
-                h8 fh[4], fl[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int f = min(f0 + k * waves, AF - 1);
-                    const int at = f < Sh::GF ? Sh::kG + f : Sh::kC + f - Sh::GF;
-                    fh[k] = ld_frag(sh, at, lane);
-                    if (FINE)
-                        fl[k] = ld_frag(sh, f < Sh::GF ? Sh::kGl + f : Sh::kCl + f - Sh::GF, lane);
-                }
-                phase();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int f = f0 + k * waves;
-                    if (f >= AF)
-                        break;
-                    h8 mh, ml;
-                    if (f < Sh::GF) {
-                        const int it = f >= 2, ks = it ? f - 2 : f;
-                        const float ci = fH[32 * it + c];
-                        const float li = FINE ? fL[32 * it + c] : 0.0f;
-                        float m[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int j = 16 * ks + kperm(hi, e);
-                            float arg = ci - fH[j];
-                            float gv = static_cast<float>(fh[k][e]);
-                            if (FINE) {
-                                arg += li - fL[j];
-                                gv += static_cast<float>(fl[k][e]);
-                            }
-                            m[e] = j <= 32 * it + c ? gv * __builtin_amdgcn_exp2f(arg) : 0.0f;
-                        }
-                        parts8<FINE>(m, mh, ml);
-                    } else {
-                        const int row = f - Sh::GF < KS ? c : 32 + c;
-                        const float e2 = __builtin_amdgcn_exp2f(fH[row] + fL[row]);
-                        if (FINE) {
-                            float m[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                m[e] = (static_cast<float>(fh[k][e]) + static_cast<float>(fl[k][e])) * e2;
-                            split8(m, mh, ml);
-                        } else {
-                            mh = fh[k] * static_cast<_Float16>(e2);
-                        }
-                    }
-                    st_frag(L, f, lane, mh);
-                    if (FINE)
-                        st_frag(L, AF + f, lane, ml);
-                }
-            }
-            phase();
-            __syncthreads();
-        }
-        // B's fragments and z come while the outputs are formed
-        const bool update = !OUT || !split || ch + 1 < ch1;
-        if (OUT && update)
-            load_b(sh, 0);
-        if (OUT) {
-            const float sscale = sx * inverse_pow2(unit);
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = S[ks / 2][8 * (ks % 2) + e] * sscale;
-                h8 bh, bl;
-                parts8<FINE>(v, bh, bl);
-#pragma unroll
-                for (int it = 0; it < 2; ++it) {
-                    const h8 ah = ld_frag(L, Sh::GF + it * KS + ks, lane);
-                    Y[it] = mma(ah, bh, Y[it]);
-                    if (FINE) {
-                        Y[it] = mma(ah, bl, Y[it]);
-                        Y[it] = mma(ld_frag(L, AF + Sh::GF + it * KS + ks, lane), bh, Y[it]);
-                    }
-                }
-                if (ks % 4 == 3)
-                    phase();
-            }
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-                for (int it = ks / 2; it < 2; ++it) {
-                    const int f = Sh::g_frag(it, ks);
-                    const h8 ah = ld_frag(L, f, lane);
-                    Y[it] = mma(ah, xh[ks], Y[it]);
-                    if (FINE) {
-                        Y[it] = mma(ah, xl[ks], Y[it]);
-                        Y[it] = mma(ld_frag(L, AF + f, lane), xh[ks], Y[it]);
-                    }
-                }
-            const float back = inverse_pow2(sx);
-            const size_t yrow = static_cast<size_t>(a.H) * a.P;
-            const size_t y0 = (static_cast<size_t>(seq) * a.T + t0) * yrow + col0 + ucol;
-#pragma unroll
-            for (int it = 0; it < 2; ++it) {
-                constexpr int kHalf = Tl::kPerRow / 2;
-                union Unit {
-                    u4 raw;
-                    Act v[Tl::kUnit];
-                } zu[kHalf], yu;
-                if (a.p.z) {
-#pragma unroll
-                    for (int k = 0; k < kHalf; ++k) {
-                        const int r = min(32 * it + urow + k * Tl::kRowStep, len - 1 - t0);
-                        zu[k].raw = *reinterpret_cast<const u4*>(static_cast<const Act*>(a.p.z) + y0 + r * yrow);
-                    }
-                }
-                phase();
-                wave_sync();   // what was in the tile is read
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 Sc = *reinterpret_cast<const float4*>(fS + 32 * it + 8 * q + 4 * hi);
-                    const float sc[4] = {Sc.x, Sc.y, Sc.z, Sc.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        yt[(8 * q + 4 * hi + i) * Tl::kPitch + c] = Y[it][4 * q + i] * (sc[i] * back);
-                }
-                wave_sync();
-#pragma unroll
-                for (int k = 0; k < kHalf; ++k) {
-                    const int r = urow + k * Tl::kRowStep;
-                    float o[Tl::kUnit];
-#pragma unroll
-                    for (int q = 0; q < Tl::kUnit / 4; ++q) {
-                        const float4 v = *reinterpret_cast<const float4*>(yt + r * Tl::kPitch + ucol + 4 * q);
-                        o[4 * q] = v.x;
-                        o[4 * q + 1] = v.y;
-                        o[4 * q + 2] = v.z;
-                        o[4 * q + 3] = v.w;
-                    }
-                    if (a.p.z) {
-#pragma unroll
-                        for (int e = 0; e < Tl::kUnit; ++e)
-                            o[e] *= silu(widen(zu[k].v[e]));
-                    }
-#pragma unroll
-                    for (int e = 0; e < Tl::kUnit; ++e)
-                        narrow(o[e], yu.v[e]);
-                    if (t0 + 32 * it + r < len)
-                        *reinterpret_cast<u4*>(static_cast<Act*>(a.p.y) + y0 + (32 * it + r) * yrow) = yu.raw;
-                }
-            }
-        }
-
-        phase();
-        if (update) {
-            const float keep = __builtin_amdgcn_exp2f(total) * (s2 * inverse_pow2(unit));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int v = 0; v < 16; ++v)
-                    S[nt][v] *= keep;
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                if (ks + kAhead < 4)
-                    load_b(sh, ks + kAhead);
-                phase();
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const h8 ah = bh_[ks % kRing][nt];
-                    S[nt] = mma(ah, wh[ks], S[nt]);
-                    if (EXACT) {
-                        S[nt] = mma(ah, wl[ks], S[nt]);
-                        S[nt] = mma(bl_[ks % kRing][nt], wh[ks], S[nt]);
-                    }
-                }
-            }
-            unit = s2;
-        }
-        if (OUT)
-            __syncthreads();   // the left factor is rewritten by the next chunk
-        wave_sync();           // and so are tile and factors
-    }
-    if (OUT && split)
-        return;   // join has written the state
-    float* to = split ? seg_row : state_row;
-    const float out = inverse_pow2(unit);
+}
+template <int NT>
+__device__ __forceinline__ void store_state(const f16v (&S)[NT], float out, float* row) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4*>(to + 32 * nt + 8 * q) =
+            *reinterpret_cast<float4*>(row + 32 * nt + 8 * q) =
                 make_float4(S[nt][4 * q] * out, S[nt][4 * q + 1] * out, S[nt][4 * q + 2] * out, S[nt][4 * q + 3] * out);
-    if (split && wave == 0 && lane == 0)
-        a.seg_decay[head * a.segs + seg] = static_cast<float>(seg_sum);
+}
+template <int NT>
+__device__ __forceinline__ float state_max(const f16v (&S)[NT]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+            m = fmaxf(m, fabsf(S[nt][v]));
+    return fmaxf(m, __shfl_xor(m, 32));
+}
+
+// One dword of each 128-byte line of fragments [FROM, TO) of a chunk, so that
+// they are in this XCD's L2 when their chunk comes: all heads of a group ask for
+// them at about the same time, and all would wait for the memory behind it.
+template <int FROM, int TO>
+struct Touch {
+    static constexpr int kLines = (TO - FROM) * 8, kLoads = (kLines + 63) / 64;
+    uint32_t got[kLoads];
+    __device__ void start(const _Float16* sh, int wave, int waves, int lane) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            if ((k * waves + wave) * 64 < kLines)   // kLines is a multiple of 16
+                got[k] = at<const uint32_t>(sh + FROM * 512 + (k * waves + wave) * 4096,
+                                            static_cast<uint32_t>(min(lane, kLines - 1 - (k * waves + wave) * 64)) * 128u);
+    }
+    __device__ void finish() const {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            asm volatile("" ::"v"(got[k]));
+    }
+    __device__ void clear() {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            got[k] = 0;
+    }
+};
+
+// The head's left factor of a chunk, [M . G | 2^c C], into LDS: each wave builds
+// the fragments wave, wave + waves, ..., four in flight.  cH, cL: c per token.
+template <int N, bool FINE>
+__device__ __forceinline__ void left_factor(const _Float16* sh, _Float16* L, const float* cH, const float* cL,
+                                            int wave, int waves, int lane) {
+    using Sh = Shared<N, FINE>;
+    constexpr int AF = Sh::GF + Sh::CF, KS = N / 16;
+    const int hi = lane >> 5, c = lane & 31;
+    for (int f0 = wave; f0 < AF; f0 += 4 * waves) {
+        h8 fh[4], fl[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int f = min(f0 + k * waves, AF - 1);
+            fh[k] = ld_frag(sh, f < Sh::GF ? Sh::kG + f : Sh::kC + f - Sh::GF, lane);
+            if (FINE)
+                fl[k] = ld_frag(sh, f < Sh::GF ? Sh::kGl + f : Sh::kCl + f - Sh::GF, lane);
+        }
+        phase();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int f = f0 + k * waves;
+            if (f >= AF)
+                break;
+            h8 mh, ml;
+            if (f < Sh::GF) {
+                const int it = f >= 2, ks = it ? f - 2 : f;
+                const float ci = cH[32 * it + c];
+                const float li = FINE ? cL[32 * it + c] : 0.0f;
+                float m[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = 16 * ks + kperm(hi, e);
+                    float arg = ci - cH[j];
+                    float gv = static_cast<float>(fh[k][e]);
+                    if (FINE) {
+                        arg += li - cL[j];
+                        gv += static_cast<float>(fl[k][e]);
+                    }
+                    m[e] = j <= 32 * it + c ? gv * __builtin_amdgcn_exp2f(arg) : 0.0f;
+                }
+                parts8<FINE>(m, mh, ml);
+            } else {
+                const int row = f - Sh::GF < KS ? c : 32 + c;
+                const float e2 = __builtin_amdgcn_exp2f(cH[row] + cL[row]);
+                if (FINE) {
+                    float m[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        m[e] = (static_cast<float>(fh[k][e]) + static_cast<float>(fl[k][e])) * e2;
+                    split8(m, mh, ml);
+                } else {
+                    mh = fh[k] * static_cast<_Float16>(e2);
+                }
+            }
+            st_frag(L, f, lane, mh);
+            if (FINE)
+                st_frag(L, AF + f, lane, ml);
+        }
+    }
+}
+
+// Y += C' S0^T, the state scaled by `scale` into fp16.
+template <int N, bool FINE>
+__device__ __forceinline__ void state_product(f16v (&Y)[2], const f16v (&S)[N / 32], float scale, const _Float16* L,
+                                              int lane) {
+    using Sh = Shared<N, FINE>;
+    constexpr int AF = Sh::GF + Sh::CF, KS = N / 16;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = S[ks / 2][8 * (ks % 2) + e] * scale;
+        h8 bh, bl;
+        parts8<FINE>(v, bh, bl);
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+            const h8 ah = ld_frag(L, Sh::GF + it * KS + ks, lane);
+            Y[it] = mma(ah, bh, Y[it]);
+            if (FINE) {
+                Y[it] = mma(ah, bl, Y[it]);
+                Y[it] = mma(ld_frag(L, AF + Sh::GF + it * KS + ks, lane), bh, Y[it]);
+            }
+        }
+        if (ks % 4 == 3)
+            phase();
+    }
+}
+// Y += (M . G) X'
+template <int N, bool FINE>
+__device__ __forceinline__ void chunk_product(f16v (&Y)[2], const h8 (&xh)[4], const h8 (&xl)[4], const _Float16* L,
+                                              int lane) {
+    using Sh = Shared<N, FINE>;
+    constexpr int AF = Sh::GF + Sh::CF;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int it = ks / 2; it < 2; ++it) {
+            const int f = Sh::g_frag(it, ks);
+            const h8 ah = ld_frag(L, f, lane);
+            Y[it] = mma(ah, xh[ks], Y[it]);
+            if (FINE) {
+                Y[it] = mma(ah, xl[ks], Y[it]);
+                Y[it] = mma(ld_frag(L, AF + f, lane), xh[ks], Y[it]);
+            }
+        }
+}
+
+// Y * (rows' factors fS) * back, gated, to y: 32 tokens at a time through the
+// wave's tile, 16 bytes per store.  y and z point at the chunk's first token and
+// the wave's first channel.
+template <typename Act>
+__device__ __forceinline__ void store_y(const f16v (&Y)[2], const float* fS, float back, float* tile, Act* y,
+                                        const Act* z, int pitch, int rows, int lane) {
+    using Tl = Tile<Act>;
+    constexpr int kHalf = Tl::kPerRow / 2;
+    constexpr uint32_t kSize = sizeof(Act);
+    const int hi = lane >> 5, c = lane & 31;
+    const int urow = lane / Tl::kPerRow, ucol = lane % Tl::kPerRow * Tl::kUnit;
+    union Unit {
+        u4 raw;
+        Act v[Tl::kUnit];
+    };
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+        Unit zu[kHalf], yu;
+        if (z) {
+#pragma unroll
+            for (int k = 0; k < kHalf; ++k) {
+                const int r = min(32 * it + urow + k * Tl::kRowStep, rows - 1);
+                zu[k].raw = at<const u4>(z, static_cast<uint32_t>(r * pitch + ucol) * kSize);
+            }
+        }
+        phase();
+        wave_sync();   // what was in the tile is read
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 Sc = *reinterpret_cast<const float4*>(fS + 32 * it + 8 * q + 4 * hi);
+            const float sc[4] = {Sc.x, Sc.y, Sc.z, Sc.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tile[(8 * q + 4 * hi + i) * Tl::kPitch + c] = Y[it][4 * q + i] * (sc[i] * back);
+        }
+        wave_sync();
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k) {
+            const int r = urow + k * Tl::kRowStep;
+            float o[Tl::kUnit];
+#pragma unroll
+            for (int q = 0; q < Tl::kUnit / 4; ++q) {
+                const float4 v = *reinterpret_cast<const float4*>(tile + r * Tl::kPitch + ucol + 4 * q);
+                o[4 * q] = v.x;
+                o[4 * q + 1] = v.y;
+                o[4 * q + 2] = v.z;
+                o[4 * q + 3] = v.w;
+            }
+            if (z) {
+#pragma unroll
+                for (int e = 0; e < Tl::kUnit; ++e)
+                    o[e] *= silu(widen(zu[k].v[e]));
+            }
+#pragma unroll
+            for (int e = 0; e < Tl::kUnit; ++e)
+                narrow(o[e], yu.v[e]);
+            if (32 * it + r < rows)
+                at<u4>(y, static_cast<uint32_t>((32 * it + r) * pitch + ucol) * kSize) = yu.raw;
+        }
+    }
+}
+
+// The conv tails after the prompt, by the workgroups of its last chunk: a wave
+// its own channels, and the group's first head B's and C's.
+template <typename Act>
+__device__ void write_tails(const ChunkArgs& a, const Place& w, int col0, int N, int lane) {
+    auto put = [&](int ch) {
+        Act* tp = static_cast<Act*>(a.p.tail_out) + (static_cast<size_t>(w.seq) * a.C + ch) * 4;
+        const Act* xs = static_cast<const Act*>(a.p.x) + static_cast<size_t>(w.seq) * a.T * a.C + ch;
+        typename Quad<Act>::raw t = Quad<Act>::load(tp);
+#pragma unroll
+        for (int j = 4; j >= 1; --j)
+            if (w.len >= j)
+                t = Quad<Act>::push(t, xs[static_cast<size_t>(w.len - j) * a.C]);
+        Quad<Act>::store(tp, t);
+    };
+    if (lane < 32)
+        put(col0 + lane);
+    if (w.h % (a.H / a.G) == 0)
+        for (int i = threadIdx.x; i < 2 * N; i += blockDim.x)
+            put(a.H * a.P + (i < N ? 0 : a.G * N) + w.g * N + i % N);
+}
+
+// B's fragments, in slots of one k-step that are loaded ahead of their products:
+// the caller loads the first SLOTS k-steps, update() the others as slots come free.
+template <int N, bool FINE, bool EXACT, int SLOTS>
+struct BRing {
+    using Sh = Shared<N, FINE>;
+    static constexpr int NT = N / 32;
+    h8 h[SLOTS][NT], l[SLOTS][NT];
+    __device__ void load(const _Float16* sh, int ks, int lane) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            h[ks % SLOTS][nt] = ld_frag(sh, Sh::kB + nt * 4 + ks, lane);
+            if (EXACT)
+                l[ks % SLOTS][nt] = ld_frag(sh, Sh::kBl + nt * 4 + ks, lane);
+        }
+    }
+    // S = keep S + X''^T B
+    __device__ void update(f16v (&S)[NT], float keep, const h8 (&wh)[4], const h8 (&wl)[4], const _Float16* sh,
+                           int lane) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                S[nt][v] *= keep;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                S[nt] = mma(h[ks % SLOTS][nt], wh[ks], S[nt]);
+                if (EXACT) {
+                    S[nt] = mma(h[ks % SLOTS][nt], wl[ks], S[nt]);
+                    S[nt] = mma(l[ks % SLOTS][nt], wh[ks], S[nt]);
+                }
+            }
+            if (ks + SLOTS < 4) {
+                load(sh, ks + SLOTS, lane);
+                phase();
+            }
+        }
+    }
+};
+
+// Each segment's own state from zero, the state's products in two fp16 parts, and
+// the convolved x for the output pass.  One workgroup per (sequence, segment,
+// head), one wave per 32 rows of the state; the waves share nothing.
+template <int N, typename Act, bool FINE>
+__global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkArgs a) {
+    using Sh = Shared<N, FINE>;
+    using Tl = Tile<Act>;
+    constexpr int NT = N / 32;
+    extern __shared__ __align__(16) char pool[];   // [waves][tile, factors]
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hi = lane >> 5, c = lane & 31;
+    const int waves = a.P / 32;
+    Place w;
+    if (!place(a, false, w))
+        return;
+    const int col0 = w.h * a.P + wave * 32;
+    char* mine = pool + wave * (Tl::kBytes + Q * 4);
+    float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B * 2^(c_last - c)
+    const float* steps = a.steps + w.head * a.nc * (3 * Q);
+    const _Float16* shared0 = a.shared + (static_cast<size_t>(w.seq) * a.G + w.g) * a.nc * Sh::kHalfs;
+    char* conv = a.conv + (w.head * a.nc * waves + wave) * Conv<FINE>::kBytes;
+
+    Taps<Act> taps;
+    taps.load(static_cast<const Act*>(a.p.w), static_cast<const Act*>(a.p.bias), col0 + c);
+    Stream<Act> in = make_stream(reinterpret_cast<Act*>(mine),
+                                 static_cast<const Act*>(a.p.x) + static_cast<size_t>(w.seq) * a.T * a.C + col0, a.C,
+                                 w.len, lane);
+    float st_d, st_h, st_l, st_b;   // the chunk's step, c and scale (one token per lane)
+    auto load_steps = [&](int ch) {
+        const float* st = steps + static_cast<size_t>(ch) * (3 * Q);
+        st_d = st[lane];
+        st_h = st[Q + lane];
+        st_l = st[2 * Q + lane];
+        st_b = reinterpret_cast<const float*>(shared0 + ch * Sh::kHalfs + Sh::kFrags * 512)[lane];
+    };
+    Touch<Sh::kB, Sh::kFrags> touch;
+    constexpr int kSlots = N > 128 ? 1 : 2;
+    BRing<N, FINE, true, kSlots> B;
+    f16v S[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        S[nt] = zero16();
+    float unit = 1.0f;   // S holds the state times this
+    double seg_sum = 0.0;
+    touch.clear();
+    in.load(w.ch0 * Q);
+    load_steps(w.ch0);
+    in.begin(static_cast<const Act*>(a.p.tail_in) + (static_cast<size_t>(w.seq) * a.C + col0) * 4, w.ch0 * Q);
+
+    for (int ch = w.ch0; ch < w.ch1; ++ch) {
+        const _Float16* sh = shared0 + ch * Sh::kHalfs;
+        const int next = min(ch + 1, w.ch1 - 1);
+        touch.finish();
+        in.store();
+        const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
+        seg_sum += static_cast<double>(th) + static_cast<double>(tl);
+        fF[lane] = st_d * st_b * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
+        const float decay = __builtin_amdgcn_exp2f(th + tl);
+        wave_sync();
+        // loads and stores are counted in the order of issue, so the far ones go first and stores last: no wait for
+        // a near one is a wait for them
+        in.load(next * Q);
+        load_steps(next);
+        touch.start(shared0 + next * Sh::kHalfs, wave, waves, lane);
+        B.load(sh, 0, lane);
+        phase();
+
+        float xc[32];
+        float mx = 0.0f, mw = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            float v[4];
+            conv_run(in.tile, taps, r, lane, v);
+            const float4 F = *reinterpret_cast<const float4*>(fF + 8 * r + 4 * hi);
+            const float ff[4] = {F.x, F.y, F.z, F.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xc[4 * r + i] = v[i];
+                mx = fmaxf(mx, fabsf(v[i]));
+                mw = fmaxf(mw, fabsf(v[i] * ff[i]));
+                pin(xc[4 * r + i]);
+            }
+            pin(mx);
+            pin(mw);
+            if (r % 2)
+                phase();
+        }
+        in.save(Q);
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        mw = fmaxf(mw, __shfl_xor(mw, 32));
+
+        h8 wh[4], wl[4], xq[4];
+        const float s2 = fminf(pow2_to<8, kMostW>(mw), unit * 0x1p60f);
+        const float sx = pow2_to<8, kMostX>(mx);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            float v[8];
+            if (!FINE) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = xc[8 * ks + e] * sx;
+                xq[ks] = half8(v);
+                pin(xq[ks]);
+                phase();
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float4 F = *reinterpret_cast<const float4*>(fF + 16 * ks + 8 * q + 4 * hi);
+                const float ff[4] = {F.x, F.y, F.z, F.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[4 * q + i] = xc[8 * ks + 4 * q + i] * ff[i] * s2;
+            }
+            split8(v, wh[ks], wl[ks]);
+            pin(wh[ks]);
+            pin(wl[ks]);
+            phase();
+        }
+        if (kSlots > 1)
+            B.load(sh, 1, lane);
+        B.update(S, decay * (s2 * inverse_pow2(unit)), wh, wl, sh, lane);
+        unit = s2;
+        phase();
+        char* to = conv + static_cast<size_t>(ch) * waves * Conv<FINE>::kBytes;
+        if constexpr (FINE) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                reinterpret_cast<float4*>(to)[r * 64 + lane] =
+                    make_float4(xc[4 * r], xc[4 * r + 1], xc[4 * r + 2], xc[4 * r + 3]);
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                st_frag(reinterpret_cast<_Float16*>(to), ks, lane, xq[ks]);
+            if (lane < 32)
+                reinterpret_cast<float*>(to + 4096)[lane] = inverse_pow2(sx);
+        }
+        wave_sync();   // tile and factors are rewritten by the next chunk
+    }
+    touch.finish();
+    store_state(S, inverse_pow2(unit),
+                a.seg_state + (w.head * a.segs + w.seg) * a.P * N + static_cast<size_t>(wave * 32 + c) * N + 4 * hi);
+    if (wave == 0 && lane == 0)
+        a.seg_decay[w.head * a.segs + w.seg] = static_cast<float>(seg_sum);
 }
 
 // Each segment's own state becomes the state that enters it; the state itself
@@ -821,18 +1036,362 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(ChunkArgs a, int quads) {
     float4* sg = reinterpret_cast<float4*>(a.seg_state) + head * a.segs * quads + q;
     const float* dec = a.seg_decay + head * a.segs;
     float4 s = *st;
-    for (int k = 0; k < n; ++k) {
-        const float4 own = sg[static_cast<int64_t>(k) * quads];
-        sg[static_cast<int64_t>(k) * quads] = s;
-        const float d = __builtin_amdgcn_exp2f(dec[k]);
-        s = make_float4(__builtin_fmaf(d, s.x, own.x), __builtin_fmaf(d, s.y, own.y), __builtin_fmaf(d, s.z, own.z),
-                        __builtin_fmaf(d, s.w, own.w));
+    constexpr int U = 8;   // segments in flight
+    for (int k0 = 0; k0 < n; k0 += U) {
+        float4 own[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (k0 + k < n)
+                own[k] = sg[static_cast<int64_t>(k0 + k) * quads];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (k0 + k < n) {
+                sg[static_cast<int64_t>(k0 + k) * quads] = s;
+                const float d = __builtin_amdgcn_exp2f(dec[k0 + k]);
+                s = make_float4(__builtin_fmaf(d, s.x, own[k].x), __builtin_fmaf(d, s.y, own[k].y),
+                                __builtin_fmaf(d, s.z, own[k].z), __builtin_fmaf(d, s.w, own[k].w));
+            }
     }
     *st = s;
 }
 
+// The output pass over segments of bf16 activations, from the states that enter
+// them and the convolved x.  Its own state only serves outputs that are rounded
+// to bf16: one fp16 part each, and X' and X'' formed in packed fp16.  One
+// workgroup per (sequence, segment, head), one wave per 32 rows of the state; the
+// waves share the left factor.
+template <int N>
+__global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs a) {
+    using Act = uint16_t;
+    using Sh = Shared<N, false>;
+    using Tl = Tile<Act>;
+    constexpr int NT = N / 32;
+    constexpr int kWaveBytes = Tl::kBytes + 4 * Q * 4 + 2 * Q * 2;
+    extern __shared__ __align__(16) char pool[];   // [waves][tile, factors], then the left factor
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hi = lane >> 5, c = lane & 31;
+    const int waves = a.P / 32;
+    Place w;
+    if (!place(a, true, w))
+        return;
+    const int col0 = w.h * a.P + wave * 32;
+    char* mine = pool + wave * kWaveBytes;
+    float* yt = reinterpret_cast<float*>(mine);
+    float* fS = reinterpret_cast<float*>(mine + Tl::kBytes);   // 2^-s_C
+    float* fK = fS + Q;                                        // D * s_F * 2^s_C
+    float* fH = fS + 2 * Q;                                    // c, high and low part
+    float* fL = fS + 3 * Q;
+    _Float16* fF = reinterpret_cast<_Float16*>(fS + 4 * Q);    // d * 2^-s_B * s_F
+    _Float16* fW = fF + Q;                                     // 2^(c_last - c)
+    _Float16* L = reinterpret_cast<_Float16*>(pool + waves * kWaveBytes);
+    const float skip = a.p.D ? a.p.D[w.h] : 0.0f;
+    const float* steps = a.steps + w.head * a.nc * (3 * Q);
+    const _Float16* shared0 = a.shared + (static_cast<size_t>(w.seq) * a.G + w.g) * a.nc * Sh::kHalfs;
+    const char* conv = a.conv + (w.head * a.nc * waves + wave) * Conv<false>::kBytes;
+    const size_t yrow = static_cast<size_t>(a.H) * a.P;
+
+    float st_d, st_h, st_l, st_b, st_c, st_x;
+    h8 xq[4];
+    auto load_chunk = [&](int ch) {
+        const float* st = steps + static_cast<size_t>(ch) * (3 * Q);
+        st_d = st[lane];
+        st_h = st[Q + lane];
+        st_l = st[2 * Q + lane];
+        const float* sc = reinterpret_cast<const float*>(shared0 + ch * Sh::kHalfs + Sh::kFrags * 512);
+        st_b = sc[lane];
+        st_c = sc[Q + lane];
+        const char* from = conv + static_cast<size_t>(ch) * waves * Conv<false>::kBytes;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+            xq[ks] = ld_frag(reinterpret_cast<const _Float16*>(from), ks, lane);
+        st_x = reinterpret_cast<const float*>(from + 4096)[c];
+    };
+    Touch<0, Sh::kBl> touch;
+    BRing<N, false, false, 2> B;
+    f16v S[NT];
+    float unit = 1.0f;
+    touch.clear();
+    load_chunk(w.ch0);
+    load_state(S, a.seg_state + (w.head * a.segs + w.seg) * a.P * N + static_cast<size_t>(wave * 32 + c) * N + 4 * hi);
+
+    for (int ch = w.ch0; ch < w.ch1; ++ch) {
+        const _Float16* sh = shared0 + ch * Sh::kHalfs;
+        const int next = min(ch + 1, w.ch1 - 1);
+        touch.finish();
+        const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
+        const float F = st_d * st_b;
+        const float sF = pow2_to<0, kMostF>(wave_max(F));
+        const float cs = st_x;
+        fF[lane] = static_cast<_Float16>(F * sF);
+        fW[lane] = static_cast<_Float16>(__builtin_amdgcn_exp2f((th - st_h) + (tl - st_l)));
+        fS[lane] = st_c;
+        fK[lane] = skip * sF * inverse_pow2(st_c);
+        fH[lane] = st_h;
+        fL[lane] = st_l;
+        const float decay = __builtin_amdgcn_exp2f(th + tl);
+        wave_sync();
+        left_factor<N, false>(sh, L, fH, fL, wave, waves, lane);
+        phase();
+        // X', X'' in units of s_F / cs; x itself is taken up by Y below
+        const float ux = sF * inverse_pow2(cs);
+        h8 xh[4], wh[4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+            h8 f, g;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const h4 f4_ = *reinterpret_cast<const h4*>(fF + 16 * ks + 8 * q + 4 * hi);
+                const h4 g4_ = *reinterpret_cast<const h4*>(fW + 16 * ks + 8 * q + 4 * hi);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[4 * q + i] = f4_[i];
+                    g[4 * q + i] = g4_[i];
+                }
+            }
+            xh[ks] = xq[ks] * f;
+            wh[ks] = xh[ks] * g;
+            pin(xh[ks]);
+            pin(wh[ks]);
+        }
+        const float ss = pow2_to<8, kMostS>(state_max(S));   // on top of `unit`
+        phase();
+        B.load(sh, 0, lane);
+        B.load(sh, 1, lane);
+        phase();
+        touch.start(shared0 + next * Sh::kHalfs, wave, waves, lane);
+        phase();
+        __syncthreads();
+        f16v Y[2] = {zero16(), zero16()};
+        state_product<N, false>(Y, S, ss, L, lane);
+        // to X's unit, and D x
+        const float ratio = ux * (inverse_pow2(ss) * inverse_pow2(unit));
+#pragma unroll
+        for (int it = 0; it < 2; ++it)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 K = *reinterpret_cast<const float4*>(fK + 32 * it + 8 * q + 4 * hi);
+                const float kk[4] = {K.x, K.y, K.z, K.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float y = __builtin_fmaf(static_cast<float>(xq[2 * it + q / 2][4 * (q % 2) + i]), kk[i],
+                                             Y[it][4 * q + i] * ratio);
+                    pin(y);
+                    Y[it][4 * q + i] = y;
+                }
+            }
+        phase();
+        // loads are counted in the order of issue: the near ones first, so that no wait for them is one for the far
+        load_chunk(next);
+        phase();
+        chunk_product<N, false>(Y, xh, xh, L, lane);
+        const size_t y0 = (static_cast<size_t>(w.seq) * a.T + ch * Q) * yrow + col0;
+        phase();
+        if (ch + 1 < w.ch1) {
+            B.update(S, decay * (ux * inverse_pow2(unit)), wh, wh, sh, lane);
+            unit = ux;
+        }
+        phase();
+        store_y<Act>(Y, fS, inverse_pow2(ux), yt, static_cast<Act*>(a.p.y) + y0,
+                     a.p.z ? static_cast<const Act*>(a.p.z) + y0 : nullptr, static_cast<int>(yrow), w.len - ch * Q, lane);
+        __syncthreads();   // the left factor is rewritten by the next chunk
+        wave_sync();       // and so are tile and factors
+    }
+    touch.finish();
+    if (w.ch1 == w.last)
+        write_tails<Act>(a, w, col0, N, lane);
+}
+
+// The output pass that also carries the state (one segment), or takes the state
+// and the convolved x of segments in fp32.  One workgroup per (sequence, segment,
+// head), one wave per 32 rows of the state.  With every operand of a row in one
+// scale, a chunk's outputs are a single product over 64 + N terms,
+// Y = [M . G | 2^c C] [X'; S0^T]; the waves share its left factor.
+template <int N, typename Act, bool FINE, bool SPLIT>
+__global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel(ChunkArgs a) {
+    using Sh = Shared<N, FINE>;
+    using Tl = Tile<Act>;
+    constexpr int NT = N / 32;
+    constexpr int kWaveBytes = Tl::kBytes + 6 * Q * 4;
+    static_assert(FINE || !SPLIT, "bf16 segments are ssm_out_kernel's");
+    extern __shared__ __align__(16) char pool[];   // [waves][tile, factors], then the left factor
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hi = lane >> 5, c = lane & 31;
+    const int waves = a.P / 32;
+    Place w;
+    if (!place(a, true, w))
+        return;
+    const int col0 = w.h * a.P + wave * 32;
+    char* mine = pool + wave * kWaveBytes;
+    float* yt = reinterpret_cast<float*>(mine);
+    float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B
+    float* fW = fF + Q;                                        // 2^(c_last - c)
+    float* fS = fF + 2 * Q;                                    // 2^-s_C
+    float* fK = fF + 3 * Q;                                    // D * 2^s_C
+    float* fH = fF + 4 * Q;                                    // c, high and low part
+    float* fL = fF + 5 * Q;
+    _Float16* L = reinterpret_cast<_Float16*>(pool + waves * kWaveBytes);
+    const float skip = a.p.D ? a.p.D[w.h] : 0.0f;
+    const float* steps = a.steps + w.head * a.nc * (3 * Q);
+    const _Float16* shared0 = a.shared + (static_cast<size_t>(w.seq) * a.G + w.g) * a.nc * Sh::kHalfs;
+    const char* conv = a.conv + (w.head * a.nc * waves + wave) * Conv<FINE>::kBytes;
+    const size_t yrow = static_cast<size_t>(a.H) * a.P;
+
+    Taps<Act> taps;
+    taps.load(static_cast<const Act*>(a.p.w), static_cast<const Act*>(a.p.bias), col0 + c);
+    Stream<Act> in = make_stream(reinterpret_cast<Act*>(mine),
+                                 static_cast<const Act*>(a.p.x) + static_cast<size_t>(w.seq) * a.T * a.C + col0, a.C,
+                                 w.len, lane);
+    float st_d, st_h, st_l, st_b, st_c;
+    auto load_steps = [&](int ch) {
+        const float* st = steps + static_cast<size_t>(ch) * (3 * Q);
+        st_d = st[lane];
+        st_h = st[Q + lane];
+        st_l = st[2 * Q + lane];
+        const float* sc = reinterpret_cast<const float*>(shared0 + ch * Sh::kHalfs + Sh::kFrags * 512);
+        st_b = sc[lane];
+        st_c = sc[Q + lane];
+    };
+    Touch<0, Sh::kFrags> touch;
+    constexpr int kSlots = N > 128 ? 1 : 2;
+    BRing<N, FINE, true, kSlots> B;
+    f16v S[NT];
+    float unit = 1.0f;
+    const size_t row_off = static_cast<size_t>(wave * 32 + c) * N + 4 * hi;
+    float* state_row = SPLIT ? a.seg_state + (w.head * a.segs + w.seg) * a.P * N + row_off
+                             : a.p.state + w.head * a.P * N + row_off;
+    touch.clear();
+    load_steps(w.ch0);
+    if constexpr (!SPLIT) {
+        in.load(w.ch0 * Q);
+        in.begin(static_cast<const Act*>(a.p.tail_in) + (static_cast<size_t>(w.seq) * a.C + col0) * 4, w.ch0 * Q);
+    }
+    load_state(S, state_row);
+
+    for (int ch = w.ch0; ch < w.ch1; ++ch) {
+        const _Float16* sh = shared0 + ch * Sh::kHalfs;
+        const int next = min(ch + 1, w.ch1 - 1);
+        touch.finish();
+        if constexpr (!SPLIT)
+            in.store();
+        const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
+        fF[lane] = st_d * st_b;
+        fW[lane] = __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
+        fS[lane] = st_c;
+        fK[lane] = skip * inverse_pow2(st_c);
+        fH[lane] = st_h;
+        fL[lane] = st_l;
+        const float decay = __builtin_amdgcn_exp2f(th + tl);
+        wave_sync();
+        if constexpr (!SPLIT)
+            in.load(next * Q);
+        load_steps(next);
+        touch.start(shared0 + next * Sh::kHalfs, wave, waves, lane);
+
+        float xc[32];
+        float m1 = 0.0f, m2 = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            float v[4];
+            if constexpr (SPLIT) {
+                const float4 q = reinterpret_cast<const float4*>(
+                    conv + static_cast<size_t>(ch) * waves * Conv<FINE>::kBytes)[r * 64 + lane];
+                v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+            } else {
+                conv_run(in.tile, taps, r, lane, v);
+            }
+            const float4 F = *reinterpret_cast<const float4*>(fF + 8 * r + 4 * hi);
+            const float4 W = *reinterpret_cast<const float4*>(fW + 8 * r + 4 * hi);
+            const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xc[4 * r + i] = v[i];
+                const float xp = v[i] * ff[i];
+                m1 = fmaxf(m1, fabsf(xp));
+                m2 = fmaxf(m2, fabsf(xp * ww[i]));
+                pin(xc[4 * r + i]);
+            }
+            pin(m1);
+            pin(m2);
+            if (!SPLIT && r % 2)
+                phase();
+        }
+        if constexpr (!SPLIT)
+            in.save(Q);
+        m1 = fmaxf(m1, __shfl_xor(m1, 32));
+        m2 = fmaxf(m2, __shfl_xor(m2, 32));
+        const float ms = state_max(S) * inverse_pow2(unit);
+        const float s2 = fminf(pow2_to<8, kMostW>(m2), unit * 0x1p60f);   // the unit of the next state
+        const float sx = pow2_to<8, kMostX>(fmaxf(m1, ms));
+
+        // X'' and X' as fragments; Y starts from D x
+        h8 wh[4], wl[4], xh[4], xl[4];
+        f16v Y[2];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            float v[8], u[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float4 F = *reinterpret_cast<const float4*>(fF + 16 * ks + 8 * q + 4 * hi);
+                const float4 W = *reinterpret_cast<const float4*>(fW + 16 * ks + 8 * q + 4 * hi);
+                const float4 K = *reinterpret_cast<const float4*>(fK + 16 * ks + 8 * q + 4 * hi);
+                const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w}, kk[4] = {K.x, K.y, K.z, K.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = xc[8 * ks + 4 * q + i];
+                    const float xp = x * ff[i];
+                    v[4 * q + i] = xp * (ww[i] * s2);
+                    u[4 * q + i] = xp * sx;
+                    float y = (x * sx) * kk[i];
+                    pin(y);
+                    Y[ks / 2][8 * (ks % 2) + 4 * q + i] = y;
+                }
+            }
+            split8(v, wh[ks], wl[ks]);
+            parts8<FINE>(u, xh[ks], xl[ks]);
+            pin(wh[ks]);
+            pin(wl[ks]);
+            pin(xh[ks]);
+            if (FINE)
+                pin(xl[ks]);
+            phase();
+        }
+        left_factor<N, FINE>(sh, L, fH, fL, wave, waves, lane);
+        phase();
+        __syncthreads();
+        const bool update = !SPLIT || ch + 1 < w.ch1;
+        state_product<N, FINE>(Y, S, sx * inverse_pow2(unit), L, lane);
+        chunk_product<N, FINE>(Y, xh, xl, L, lane);
+        if (update) {
+#pragma unroll
+            for (int ks = 0; ks < kSlots; ++ks)
+                B.load(sh, ks, lane);
+        }
+        const size_t y0 = (static_cast<size_t>(w.seq) * a.T + ch * Q) * yrow + col0;
+        phase();
+        if (update) {
+            B.update(S, decay * (s2 * inverse_pow2(unit)), wh, wl, sh, lane);
+            unit = s2;
+        }
+        phase();
+        store_y<Act>(Y, fS, inverse_pow2(sx), yt, static_cast<Act*>(a.p.y) + y0,
+                     a.p.z ? static_cast<const Act*>(a.p.z) + y0 : nullptr, static_cast<int>(yrow), w.len - ch * Q, lane);
+        __syncthreads();   // the left factor is rewritten by the next chunk
+        wave_sync();       // and so are tile and factors
+    }
+    touch.finish();
+    if constexpr (!SPLIT)
+        store_state(S, inverse_pow2(unit), state_row);
+    if (w.ch1 == w.last)
+        write_tails<Act>(a, w, col0, N, lane);
+}
+
+// ------------------------------------------------------------ host
+
 // Segments: waves wanted, and chunks a segment has at least.
-constexpr int kWaves = 4096;
+constexpr int kWaves = 2048;
 constexpr int kSegChunks = 4;
 
 static void segments(const SsmGeo& g, int T, int& segs, int& per) {
@@ -845,6 +1404,8 @@ static void segments(const SsmGeo& g, int T, int& segs, int& per) {
     segs = (nc + per - 1) / per;
 }
 
+static size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
 static size_t shared_halfs(const SsmGeo& g) {
     const bool fine = !g.bf16;
     switch (g.N) {
@@ -855,99 +1416,104 @@ static size_t shared_halfs(const SsmGeo& g) {
     }
 }
 
-static size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
-
-size_t chunked_ws_bytes(const SsmGeo& g, int T) {
+// The workspace: fragments, steps, and with segments their states, decays and the convolved x.
+static size_t carve(const SsmGeo& g, int T, char* base, ChunkArgs* a) {
     int segs, per;
     segments(g, T, segs, per);
-    const size_t nc = (T + Q - 1) / Q;
-    size_t n = up256(static_cast<size_t>(g.B) * g.G * nc * shared_halfs(g) * sizeof(_Float16)) +
-               static_cast<size_t>(g.B) * g.H * nc * (3 * Q) * sizeof(float);
-    if (segs > 1)
-        n += up256(static_cast<size_t>(g.B) * g.H * segs * g.P * g.N * 4) + up256(static_cast<size_t>(g.B) * g.H * segs * 4);
+    const size_t nc = (T + Q - 1) / Q, BH = static_cast<size_t>(g.B) * g.H;
+    size_t n = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = n;
+        n += up256(bytes);
+        return base + at;
+    };
+    char* shared = take(static_cast<size_t>(g.B) * g.G * nc * shared_halfs(g) * sizeof(_Float16));
+    char* steps = take(BH * nc * (3 * Q) * sizeof(float));
+    char *state = nullptr, *decay = nullptr, *conv = nullptr;
+    if (segs > 1) {
+        state = take(BH * segs * g.P * g.N * sizeof(float));
+        decay = take(BH * segs * sizeof(float));
+        conv = take(BH * nc * (g.P / 32) * (g.bf16 ? Conv<false>::kBytes : Conv<true>::kBytes));
+    }
+    if (a) {
+        a->shared = reinterpret_cast<_Float16*>(shared);
+        a->steps = reinterpret_cast<float*>(steps);
+        a->seg_state = reinterpret_cast<float*>(state);
+        a->seg_decay = reinterpret_cast<float*>(decay);
+        a->conv = conv;
+        a->nc = static_cast<int>(nc);
+        a->segs = segs;
+        a->chunks_per_seg = per;
+    }
     return n;
 }
 
+size_t chunked_ws_bytes(const SsmGeo& g, int T) { return carve(g, T, nullptr, nullptr); }
+
 // A launch that may need more than 64 KB of LDS.
-static hipError_t launch_lds(void (*kernel)(ChunkArgs), dim3 grid, dim3 block, size_t lds, hipStream_t s,
-                             const ChunkArgs& a) {
+template <typename... Args>
+static hipError_t launch_lds(void (*kernel)(Args...), dim3 grid, dim3 block, size_t lds, hipStream_t s, Args... args) {
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL(kernel, grid, block, lds, s, a);
+    hipLaunchKernelGGL(kernel, grid, block, lds, s, args...);
     return hipGetLastError();
 }
 
 template <int N, typename Act, bool FINE>
-static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const int32_t* lengths, void* ws,
-                              hipStream_t s) {
-    int segs, per;
-    segments(g, T, segs, per);
-    const int nc = (T + Q - 1) / Q;
-    char* base = static_cast<char*>(ws);
-    _Float16* shared = reinterpret_cast<_Float16*>(base);
-    base += up256(static_cast<size_t>(g.B) * g.G * nc * Shared<N, FINE>::kHalfs * sizeof(_Float16));
-    float* steps = reinterpret_cast<float*>(base);
-    base += static_cast<size_t>(g.B) * g.H * nc * (3 * Q) * sizeof(float);
-    float* seg_state = reinterpret_cast<float*>(base);
-    float* seg_decay = reinterpret_cast<float*>(base + up256(static_cast<size_t>(g.B) * g.H * segs * g.P * g.N * 4));
-    constexpr size_t lds = (static_cast<size_t>(Q) * (2 * N + 1) + 2 * Q) * sizeof(float);
-    auto prep = ssm_prep_kernel<N, Act, FINE>;
-    if (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prep),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
-        if (e != hipSuccess)
-            return e;
-    }
-    hipLaunchKernelGGL(prep, dim3(static_cast<unsigned>(static_cast<int64_t>(g.B) * g.G * nc)), dim3(512), lds, s,
-                       static_cast<const Act*>(p.x), static_cast<const Act*>(p.tail_in), static_cast<const Act*>(p.w),
-                       static_cast<const Act*>(p.bias), lengths, T, g.H, g.G, g.P, g.C, nc, shared);
-    hipError_t e = hipGetLastError();
+static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const int32_t* lengths, int32_t* status,
+                              void* ws, hipStream_t s) {
+    ChunkArgs a{};
+    a.p = p;
+    a.lengths = lengths;
+    a.status = status;
+    a.T = T, a.B = g.B, a.H = g.H, a.G = g.G, a.P = g.P, a.C = g.C;
+    carve(g, T, static_cast<char*>(ws), &a);
+    // by XCD where the sets of heads come out even over the eight, or nearly
+    const int64_t sets = static_cast<int64_t>(g.B) * g.G * a.segs;
+    a.by_xcd = sets % 8 == 0 || sets >= 64;
+
+    const int prep_wgs = g.B * g.G * a.nc;
+    const int step_wgs = g.B * a.nc * ((g.H + kStepHeads - 1) / kStepHeads);
+    hipError_t e = launch_lds(ssm_prep_kernel<N, Act, FINE>, dim3(prep_wgs + step_wgs), dim3(4 * N),
+                              prep_lds<N, Act, FINE>(), s, a, prep_wgs);
     if (e != hipSuccess)
         return e;
-    const int64_t step_waves = static_cast<int64_t>(g.B) * g.H * nc;
-    hipLaunchKernelGGL(ssm_steps_kernel, dim3(static_cast<unsigned>((step_waves + 3) / 4)), dim3(256), 0, s, p.dt,
-                       p.dt_bias, p.A, lengths, T, g.H, nc, step_waves, steps);
-    if ((e = hipGetLastError()) != hipSuccess)
-        return e;
-    // by XCD where the sets of heads come out even over the eight, or nearly
-    const int64_t sets = static_cast<int64_t>(g.B) * g.G * segs;
-    const bool by_xcd = sets % 8 == 0 || sets >= 64;
-    const ChunkArgs a{p,   lengths, shared, steps, seg_state, seg_decay, T,   g.B,
-                      g.H, g.G,     g.P,    g.C,   nc,        segs,      per, by_xcd};
     const int waves = g.P / 32;
-    const int64_t wgs = (by_xcd ? (sets + 7) / 8 * 8 : sets) * (g.H / g.G);
+    const int64_t wgs = (a.by_xcd ? (sets + 7) / 8 * 8 : sets) * (g.H / g.G);
     const dim3 grid(static_cast<unsigned>(wgs)), block(64 * waves);
     constexpr int kTile = Tile<Act>::kBytes;
-    const size_t lds_state = waves * (kTile + 2 * Q * 4);
-    const size_t lds_out = waves * (kTile + 6 * Q * 4) +
-                           (FINE ? 2 : 1) * (Shared<N, FINE>::GF + Shared<N, FINE>::CF) * 1024;
-    if (segs == 1)
-        return launch_lds(ssm_chunk_kernel<N, Act, FINE, true, true>, grid, block, lds_out, s, a);
-    if ((e = launch_lds(ssm_chunk_kernel<N, Act, FINE, false, true>, grid, block, lds_state, s, a)) != hipSuccess)
+    constexpr int kLeft = (FINE ? 2 : 1) * (Shared<N, FINE>::GF + Shared<N, FINE>::CF) * 1024;
+    const size_t lds_chunk = waves * (kTile + 6 * Q * 4) + kLeft;
+    if (a.segs == 1)
+        return launch_lds(ssm_chunk_kernel<N, Act, FINE, false>, grid, block, lds_chunk, s, a);
+    if ((e = launch_lds(ssm_state_kernel<N, Act, FINE>, grid, block, waves * (kTile + Q * 4), s, a)) != hipSuccess)
         return e;
     const int quads = g.P * N / 4;
     const int64_t threads = static_cast<int64_t>(g.B) * g.H * quads;
     hipLaunchKernelGGL(ssm_join_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, a, quads);
     if ((e = hipGetLastError()) != hipSuccess)
         return e;
-    return launch_lds(ssm_chunk_kernel<N, Act, FINE, true, FINE>, grid, block, lds_out, s, a);
+    if constexpr (FINE)
+        return launch_lds(ssm_chunk_kernel<N, Act, true, true>, grid, block, lds_chunk, s, a);
+    else
+        return launch_lds(ssm_out_kernel<N>, grid, block, waves * (kTile + 4 * Q * 4 + 2 * Q * 2) + kLeft, s, a);
 }
 
-hipError_t launch_ssm_chunked(const SsmGeo& g, const SsmArgs& p, int T, const int32_t* lengths, void* ws,
-                              hipStream_t s) {
+hipError_t launch_ssm_chunked(const SsmGeo& g, const SsmArgs& p, int T, const int32_t* lengths, int32_t* status,
+                              void* ws, hipStream_t s) {
     switch (g.N) {
-        case 32: return g.bf16 ? chunked_cfg<32, uint16_t, false>(g, p, T, lengths, ws, s)
-                               : chunked_cfg<32, float, true>(g, p, T, lengths, ws, s);
-        case 64: return g.bf16 ? chunked_cfg<64, uint16_t, false>(g, p, T, lengths, ws, s)
-                               : chunked_cfg<64, float, true>(g, p, T, lengths, ws, s);
-        case 128: return g.bf16 ? chunked_cfg<128, uint16_t, false>(g, p, T, lengths, ws, s)
-                                : chunked_cfg<128, float, true>(g, p, T, lengths, ws, s);
-        default: return g.bf16 ? chunked_cfg<256, uint16_t, false>(g, p, T, lengths, ws, s)
-                               : chunked_cfg<256, float, true>(g, p, T, lengths, ws, s);
+        case 32: return g.bf16 ? chunked_cfg<32, uint16_t, false>(g, p, T, lengths, status, ws, s)
+                               : chunked_cfg<32, float, true>(g, p, T, lengths, status, ws, s);
+        case 64: return g.bf16 ? chunked_cfg<64, uint16_t, false>(g, p, T, lengths, status, ws, s)
+                               : chunked_cfg<64, float, true>(g, p, T, lengths, status, ws, s);
+        case 128: return g.bf16 ? chunked_cfg<128, uint16_t, false>(g, p, T, lengths, status, ws, s)
+                                : chunked_cfg<128, float, true>(g, p, T, lengths, status, ws, s);
+        default: return g.bf16 ? chunked_cfg<256, uint16_t, false>(g, p, T, lengths, status, ws, s)
+                               : chunked_cfg<256, float, true>(g, p, T, lengths, status, ws, s);
     }
 }
 
