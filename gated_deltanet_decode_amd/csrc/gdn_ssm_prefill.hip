@@ -857,13 +857,17 @@ struct BRing {
                 S[nt][v] *= keep;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
+            // parts outside, tiles inside: products of one accumulator do not follow one another
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NT; ++nt)
                 S[nt] = mma(h[ks % SLOTS][nt], wh[ks], S[nt]);
-                if (EXACT) {
+            if (EXACT) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
                     S[nt] = mma(h[ks % SLOTS][nt], wl[ks], S[nt]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
                     S[nt] = mma(l[ks % SLOTS][nt], wh[ks], S[nt]);
-                }
             }
             if (ks + SLOTS < 4) {
                 load(sh, ks + SLOTS, lane);

@@ -107,6 +107,30 @@ def test_first_step_and_finished_beams(V):
         check(lg, sc, S, finished=fin, eos=eos, bf16=True)
 
 
+def test_every_kind_of_nan_is_masked():
+    """Quiet and signalling NaNs of either sign, in both types."""
+    import gated_deltanet_decode_amd as gdn
+    r = np.random.default_rng(11)
+    V = 700
+    for bf16, bad in ((True, [0x7FC0, 0xFFC0, 0x7F81, 0xFF81, 0x7FFF, 0xFFFF]),
+                      (False, [0x7FC00000, 0xFFC00000, 0x7F800001, 0xFF800001, 0x7FFFFFFF, 0xFFFFFFFF])):
+        clean = sr.bf16_round(r.standard_normal((1, 2, V)))
+        masked = clean.copy()
+        masked[:, :, ::3] = np.nan
+        bits = (clean.view(np.uint32) >> 16).astype(np.uint16) if bf16 else clean.view(np.uint32).copy()
+        bits[:, :, ::3] = np.resize(np.array(bad, bits.dtype), bits[:, :, ::3].shape)
+        t = torch.from_numpy(bits.view(np.int16 if bf16 else np.int32)).cuda().view(
+            torch.bfloat16 if bf16 else torch.float32)
+        sc = np.array([[-0.5, -0.25]], np.float32)
+        val, par, tok = (torch.zeros(1, 9, device="cuda", dtype=d) for d in (torch.float32, torch.int32, torch.int32))
+        ws = torch.empty(gdn.beam_select_workspace_bytes(1, 2, V, 9), dtype=torch.uint8, device="cuda")
+        gdn.beam_select(t, torch.from_numpy(sc).cuda(), val, par, tok, ws)
+        torch.cuda.synchronize()
+        want = sr.select(masked, sc, 9)
+        assert np.array_equal(par.cpu().numpy(), want[1]) and np.array_equal(tok.cpu().numpy(), want[2])
+        assert np.allclose(val.cpu().numpy(), want[0], rtol=2.0 ** -23, atol=2.0 ** -18)
+
+
 def test_select_is_captured_and_replayed():
     import gated_deltanet_decode_amd as gdn
     r = np.random.default_rng(9)
