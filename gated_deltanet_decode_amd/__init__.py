@@ -469,13 +469,38 @@ def tree_verify_ut_noalloc(d: Dims, state, tail, w, parent, x, a, b, o, status=N
 
 
 # ------------------------------------------------ selective state space layers
+#
+# These calls are made once per layer and token, so their checks take one pass
+# of cheap queries per tensor; a tensor that fails them goes through _t, which
+# says what is wrong with it.
 
-def _on_current(*tensors) -> None:
-    """A launch goes to the current device: refuse tensors of another one."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.device.index != here:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle without a Stream object around it
+
+
+def _p(t, name, dtype, numel, dev):
+    """Address of a contiguous tensor of numel elements on device dev, the current one."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _t(t, name, dtype, numel)
+    raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+
+
+def _here(stream):
+    """(current device, stream handle); a launch goes to the current device."""
+    dev = torch.cuda.current_device()
+    if stream is not None:
+        return dev, _stream(stream)
+    return dev, _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _ws(workspace, need, dev):
+    ptr, nbytes = _blob(workspace, need, "workspace")
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, but the current device is cuda:{dev}")
+    return ptr, nbytes
 
 
 def ssm_conv_channels(d: SsmDims) -> int:
@@ -494,16 +519,20 @@ def ssm_decode_token(d: SsmDims, state, tail_in, tail_out, w, x, dt, A, y, conv_
                      z=None, stream=None) -> None:
     """One token of a selective state space layer: x [B][C], dt [B][H], y and z [B][H][P];
     the tail goes from tail_in to tail_out."""
-    B, H, P, N, Cc, act = d.batch, d.num_heads, d.head_dim, d.state_dim, d.C, d.act_torch
-    _on_current(state, tail_in, tail_out, w, x, dt, A, y, conv_bias, dt_bias, D, z)
-    _check(_lib.gdn_ssm_decode_token(C.byref(d), _t(state, "state", torch.float32, B * H * P * N),
-                                     _t(tail_in, "conv_tail_in", act, B * Cc * 4),
-                                     _t(tail_out, "conv_tail_out", act, B * Cc * 4), _t(w, "conv_w", act, Cc * 4),
-                                     _opt(conv_bias, "conv_bias", act, Cc), _t(x, "x", act, B * Cc),
-                                     _t(dt, "dt", torch.float32, B * H), _opt(dt_bias, "dt_bias", torch.float32, H),
-                                     _t(A, "A", torch.float32, H), _opt(D, "D", torch.float32, H),
-                                     _opt(z, "z", act, B * H * P), _t(y, "y", act, B * H * P), _stream(stream)),
-           "gdn_ssm_decode_token")
+    B, H, P, act = d.batch, d.num_heads, d.head_dim, torch.bfloat16 if d.act_dtype == BF16 else torch.float32
+    HP, f32 = H * P, torch.float32
+    Cc = HP + 2 * d.num_groups * d.state_dim
+    dev, s = _here(stream)
+    _check(_lib.gdn_ssm_decode_token(C.byref(d), _p(state, "state", f32, B * HP * d.state_dim, dev),
+                                     _p(tail_in, "conv_tail_in", act, B * Cc * 4, dev),
+                                     _p(tail_out, "conv_tail_out", act, B * Cc * 4, dev),
+                                     _p(w, "conv_w", act, Cc * 4, dev),
+                                     None if conv_bias is None else _p(conv_bias, "conv_bias", act, Cc, dev),
+                                     _p(x, "x", act, B * Cc, dev), _p(dt, "dt", f32, B * H, dev),
+                                     None if dt_bias is None else _p(dt_bias, "dt_bias", f32, H, dev),
+                                     _p(A, "A", f32, H, dev), None if D is None else _p(D, "D", f32, H, dev),
+                                     None if z is None else _p(z, "z", act, B * HP, dev), _p(y, "y", act, B * HP, dev),
+                                     s), "gdn_ssm_decode_token")
 
 
 def ssm_prefill_workspace_bytes(d: SsmDims, T: int) -> int:
@@ -515,20 +544,25 @@ def ssm_prefill(d: SsmDims, state, tail, w, x, dt, A, y, workspace, conv_bias=No
     """Prompts of a selective state space layer: x [B][T][C], dt [B][T][H], y and z [B][T][H][P];
     state and tail in place.  lengths [B] (int32, device): tokens of each sequence, None for T.
     workspace: a device byte tensor of at least ssm_prefill_workspace_bytes(d, T) bytes."""
-    B, H, P, N, Cc, act = d.batch, d.num_heads, d.head_dim, d.state_dim, d.C, d.act_torch
-    if x.numel() % (B * Cc) or not x.numel():
+    B, H, P, act = d.batch, d.num_heads, d.head_dim, torch.bfloat16 if d.act_dtype == BF16 else torch.float32
+    HP, f32 = H * P, torch.float32
+    Cc = HP + 2 * d.num_groups * d.state_dim
+    if not x.numel() or x.numel() % (B * Cc):
         raise ValueError("x must be [B][T][C]")
     T = x.numel() // (B * Cc)
-    _on_current(state, tail, w, x, dt, A, y, workspace, conv_bias, dt_bias, D, z, lengths, status)
-    ptr, nbytes = _blob(workspace, ssm_prefill_workspace_bytes(d, T), "workspace")
-    _check(_lib.gdn_ssm_prefill(C.byref(d), _t(state, "state", torch.float32, B * H * P * N),
-                                _t(tail, "conv_tail", act, B * Cc * 4), _t(w, "conv_w", act, Cc * 4),
-                                _opt(conv_bias, "conv_bias", act, Cc), T, _t(x, "x", act, B * T * Cc),
-                                _t(dt, "dt", torch.float32, B * T * H), _opt(dt_bias, "dt_bias", torch.float32, H),
-                                _t(A, "A", torch.float32, H), _opt(D, "D", torch.float32, H),
-                                _opt(z, "z", act, B * T * H * P), _opt(lengths, "lengths", torch.int32, B),
-                                _t(y, "y", act, B * T * H * P), _opt(status, "status", torch.int32, B), ptr, nbytes,
-                                _stream(stream)), "gdn_ssm_prefill")
+    dev, s = _here(stream)
+    ptr, nbytes = _ws(workspace, _lib.gdn_ssm_prefill_workspace_bytes(C.byref(d), T), dev)
+    _check(_lib.gdn_ssm_prefill(C.byref(d), _p(state, "state", f32, B * HP * d.state_dim, dev),
+                                _p(tail, "conv_tail", act, B * Cc * 4, dev), _p(w, "conv_w", act, Cc * 4, dev),
+                                None if conv_bias is None else _p(conv_bias, "conv_bias", act, Cc, dev), T,
+                                _p(x, "x", act, B * T * Cc, dev), _p(dt, "dt", f32, B * T * H, dev),
+                                None if dt_bias is None else _p(dt_bias, "dt_bias", f32, H, dev),
+                                _p(A, "A", f32, H, dev), None if D is None else _p(D, "D", f32, H, dev),
+                                None if z is None else _p(z, "z", act, B * T * HP, dev),
+                                None if lengths is None else _p(lengths, "lengths", torch.int32, B, dev),
+                                _p(y, "y", act, B * T * HP, dev),
+                                None if status is None else _p(status, "status", torch.int32, B, dev), ptr, nbytes, s),
+           "gdn_ssm_prefill")
 
 
 # ------------------------------------------------ beam search over recurrent states
@@ -543,29 +577,34 @@ def beam_select(logits, scores, out_scores, parent, token, workspace, finished=N
     finished [B][K] (bool): beams that have ended, whose one candidate is eos at their own score."""
     if not isinstance(logits, torch.Tensor) or logits.device.type != "cuda" or logits.dim() != 3:
         raise ValueError("logits must be a device tensor [B][K][V]")
-    if logits.dtype not in (torch.bfloat16, torch.float32):
+    if logits.dtype is torch.bfloat16:
+        act = BF16
+    elif logits.dtype is torch.float32:
+        act = F32
+    else:
         raise ValueError(f"logits must be bfloat16 or float32, got {logits.dtype}")
     B, K, V = logits.shape
     if V == 0 or B == 0 or K == 0:
         raise ValueError("logits must not be empty")
     # strides of dimensions of one entry say nothing
-    pitch = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
-    if (V > 1 and logits.stride(2) != 1) or (K > 1 and B > 1 and logits.stride(0) != K * pitch) or pitch < V:
+    sb, sk, sv = logits.stride()
+    pitch = sk if K > 1 else sb if B > 1 else V
+    if (V > 1 and sv != 1) or (K > 1 and B > 1 and sb != K * pitch) or pitch < V:
         raise ValueError("logits must have contiguous entries and rows at one pitch of at least V")
     if not isinstance(out_scores, torch.Tensor) or out_scores.numel() % B:
         raise ValueError("out_scores must be [B][S]")
     S = out_scores.numel() // B
-    _on_current(logits, scores, out_scores, parent, token, workspace, finished)
-    ptr, nbytes = _blob(workspace, beam_select_workspace_bytes(B, K, V, S), "workspace")
-    if finished is not None and finished.dtype == torch.uint8:
-        fin = _t(finished, "finished", torch.uint8, B * K)
-    else:
-        fin = _opt(finished, "finished", torch.bool, B * K)
-    _check(_lib.gdn_beam_select(B, K, V, pitch, BF16 if logits.dtype == torch.bfloat16 else F32, logits.data_ptr(),
-                                _t(scores, "scores", torch.float32, B * K), fin, eos, S,
-                                _t(out_scores, "out_scores", torch.float32, B * S),
-                                _t(parent, "parent", torch.int32, B * S), _t(token, "token", torch.int32, B * S), ptr,
-                                nbytes, _stream(stream)), "gdn_beam_select")
+    dev, s = _here(stream)
+    if logits.get_device() != dev:
+        raise ValueError(f"logits is on {logits.device}, but the current device is cuda:{dev}")
+    ptr, nbytes = _ws(workspace, _lib.gdn_beam_select_workspace_bytes(B, K, V, S), dev)
+    fin = None
+    if finished is not None:
+        fin = _p(finished, "finished", torch.uint8 if finished.dtype is torch.uint8 else torch.bool, B * K, dev)
+    _check(_lib.gdn_beam_select(B, K, V, pitch, act, logits.data_ptr(), _p(scores, "scores", torch.float32, B * K, dev),
+                                fin, eos, S, _p(out_scores, "out_scores", torch.float32, B * S, dev),
+                                _p(parent, "parent", torch.int32, B * S, dev),
+                                _p(token, "token", torch.int32, B * S, dev), ptr, nbytes, s), "gdn_beam_select")
 
 
 def beam_reorder(d, state, tail, parent, status=None, stream=None) -> None:
@@ -574,12 +613,11 @@ def beam_reorder(d, state, tail, parent, status=None, stream=None) -> None:
     if not isinstance(parent, torch.Tensor) or parent.dim() != 2 or parent.numel() != d.batch:
         raise ValueError("parent must be [groups][beams] with groups * beams == batch")
     groups, beams = parent.shape
-    _on_current(state, tail, parent, status)
+    dev, s = _here(stream)
     if isinstance(d, SsmDims):
-        name, n = "gdn_ssm_beam_reorder", d.num_heads * d.head_dim * d.state_dim
+        f, name, n = _lib.gdn_ssm_beam_reorder, "gdn_ssm_beam_reorder", d.num_heads * d.head_dim * d.state_dim
     else:
-        name, n = "gdn_beam_reorder", d.num_v_heads * d.head_v_dim * d.head_k_dim
-    _check(getattr(_lib, name)(C.byref(d), beams, _t(state, "state", torch.float32, d.batch * n),
-                               _t(tail, "conv_tail", d.act_torch, d.batch * d.C * 4),
-                               _t(parent, "parent", torch.int32, d.batch), _opt(status, "status", torch.int32, groups),
-                               _stream(stream)), name)
+        f, name, n = _lib.gdn_beam_reorder, "gdn_beam_reorder", d.num_v_heads * d.head_v_dim * d.head_k_dim
+    _check(f(C.byref(d), beams, _p(state, "state", torch.float32, d.batch * n, dev),
+             _p(tail, "conv_tail", d.act_torch, d.batch * d.C * 4, dev), _p(parent, "parent", torch.int32, d.batch, dev),
+             None if status is None else _p(status, "status", torch.int32, groups, dev), s), name)

@@ -134,10 +134,19 @@ static hipError_t token_cfg(const SsmGeo& g, const SsmArgs& a, hipStream_t s) {
 
 template <typename Act>
 static hipError_t token_act(const SsmGeo& g, const SsmArgs& a, hipStream_t s) {
+    // Once there are enough (sequence, head) pairs to fill the chip, more rows per
+    // workgroup share its conv.  At batch 64: N = 64 (64 heads of 64 rows) 35.1 us
+    // with 16 rows, 27.3 with 32, 25.3 with 64; N = 128 (48 heads of 128 rows) 70.8,
+    // 67.8 and 69.7 us; N = 256 47 us with any.  Few pairs want many workgroups
+    // instead (one sequence of 48 heads: 4.8 us with 16 rows).
+    const bool many = static_cast<int64_t>(g.B) * g.H >= 512;
     switch (g.N) {
         case 32: return token_cfg<32, 1, Act>(g, a, s);
-        case 64: return token_cfg<64, 1, Act>(g, a, s);
-        case 128: return token_cfg<128, 1, Act>(g, a, s);
+        case 64:
+            return !many       ? token_cfg<64, 1, Act>(g, a, s)
+                   : g.P == 32 ? token_cfg<64, 2, Act>(g, a, s)
+                               : token_cfg<64, 4, Act>(g, a, s);
+        case 128: return many ? token_cfg<128, 2, Act>(g, a, s) : token_cfg<128, 1, Act>(g, a, s);
         default: return token_cfg<256, 1, Act>(g, a, s);
     }
 }

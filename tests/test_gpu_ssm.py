@@ -87,6 +87,15 @@ def test_tokens(name, H, G, P, N, bf16, B):
     m.check(what=name)
 
 
+@pytest.mark.parametrize("P,N,H", [(32, 64, 40), (64, 64, 40), (128, 128, 33), (32, 128, 40), (64, 32, 40), (64, 256, 33)])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_tokens_of_many_heads(P, N, H, bf16):
+    """More (sequence, head) pairs than fill the chip: wider workgroups."""
+    m = Layer(sr.make(12, 16, 3, H, 1, P, N, bf16))
+    m.tokens(0, 3)
+    m.check()
+
+
 @pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 63, 64, 65, 200])
 @pytest.mark.parametrize("name,H,G,P,N,bf16", LAYERS, ids=IDS)
 def test_prefill(name, H, G, P, N, bf16, T):
