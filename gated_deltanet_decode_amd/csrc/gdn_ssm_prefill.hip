@@ -68,16 +68,24 @@ __device__ __forceinline__ h8 ld_frag(const _Float16* m, int frag, int lane) {
 __device__ __forceinline__ void st_frag(_Float16* m, int frag, int lane, h8 v) {
     at<h8>(m + frag * 512, static_cast<uint32_t>(lane) * 16u) = v;
 }
-// v = hi + lo in fp16 (22 bits where v is well inside fp16's range).  The value
-// is pinned first: a product's rounding to fp16 may be fused into the multiply
-// (one rounding), which now and then is not the fp16 that lo is the rest of.
+// v = hi + lo in fp16 (21 bits and more where v is well inside fp16's range): hi
+// is v cut to fp16, two at a time by one instruction, and lo the rest, formed by
+// the mixed multiply-add that reads an fp16 operand as it is (the factor -1 is
+// hidden, or the compiler makes a conversion and a subtraction of it).  Rounding
+// hi instead would not do with an ordinary conversion: the compiler may fuse the
+// product that v comes from into it, and hi is now and then not what lo is the
+// rest of.
 __device__ __forceinline__ void split8(const float (&v)[8], h8& hi, h8& lo) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    float minus = -1.0f;
+    asm("" : "+s"(minus));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float x = v[e];
-        asm("" : "+v"(x));
-        hi[e] = static_cast<_Float16>(x);
-        lo[e] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(hi[e]), -1.0f, x));
+    for (int e = 0; e < 8; e += 2) {
+        const h2 h = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_pkrtz(v[e], v[e + 1]));
+        hi[e] = h.x;
+        hi[e + 1] = h.y;
+        lo[e] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h.x), minus, v[e]));
+        lo[e + 1] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h.y), minus, v[e + 1]));
     }
 }
 // One fp16 number per value.
@@ -934,7 +942,10 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         in.store();
         const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
         seg_sum += static_cast<double>(th) + static_cast<double>(tl);
-        fF[lane] = st_d * st_b * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
+        // X'' = x F, F = d 2^-s_B 2^(c_last - c): x and F are scaled each for itself, so X'' is where x's scale puts it
+        const float F = st_d * st_b * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
+        const float sF = pow2_to<0, kMostF>(wave_max(F));
+        fF[lane] = F * sF;
         const float decay = __builtin_amdgcn_exp2f(th + tl);
         wave_sync();
         // loads and stores are counted in the order of issue, so the far ones go first and stores last: no wait for
@@ -946,42 +957,36 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         phase();
 
         float xc[32];
-        float mx = 0.0f, mw = 0.0f;
+        float mx = 0.0f;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             float v[4];
             conv_run(in.tile, taps, r, lane, v);
-            const float4 F = *reinterpret_cast<const float4*>(fF + 8 * r + 4 * hi);
-            const float ff[4] = {F.x, F.y, F.z, F.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 xc[4 * r + i] = v[i];
                 mx = fmaxf(mx, fabsf(v[i]));
-                mw = fmaxf(mw, fabsf(v[i] * ff[i]));
                 pin(xc[4 * r + i]);
             }
             pin(mx);
-            pin(mw);
             if (r % 2)
                 phase();
         }
         in.save(Q);
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        mw = fmaxf(mw, __shfl_xor(mw, 32));
 
         h8 wh[4], wl[4], xq[4];
-        const float s2 = fminf(pow2_to<8, kMostW>(mw), unit * 0x1p60f);
-        const float sx = pow2_to<8, kMostX>(mx);
+        const float sx = fminf(pow2_to<8, kMostX>(mx), unit * 0x1p40f);
+        const float s2 = sx * sF;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            float v[8];
-            if (!FINE) {
+            float v[8], u[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = xc[8 * ks + e] * sx;
-                xq[ks] = half8(v);
+            for (int e = 0; e < 8; ++e)
+                u[e] = xc[8 * ks + e] * sx;
+            if (!FINE) {
+                xq[ks] = half8(u);
                 pin(xq[ks]);
-                phase();
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -989,7 +994,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
                 const float ff[4] = {F.x, F.y, F.z, F.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[4 * q + i] = xc[8 * ks + 4 * q + i] * ff[i] * s2;
+                    v[4 * q + i] = u[4 * q + i] * ff[i];
             }
             split8(v, wh[ks], wl[ks]);
             pin(wh[ks]);
