@@ -623,32 +623,6 @@ __device__ __forceinline__ float state_max(const f16v (&S)[NT]) {
     return fmaxf(m, __shfl_xor(m, 32));
 }
 
-// One dword of each 128-byte line of fragments [FROM, TO) of a chunk, so that
-// they are in this XCD's L2 when their chunk comes: all heads of a group ask for
-// them at about the same time, and all would wait for the memory behind it.
-template <int FROM, int TO>
-struct Touch {
-    static constexpr int kLines = (TO - FROM) * 8, kLoads = (kLines + 63) / 64;
-    uint32_t got[kLoads];
-    __device__ void start(const _Float16* sh, int wave, int waves, int lane) {
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k)
-            if ((k * waves + wave) * 64 < kLines)   // kLines is a multiple of 16
-                got[k] = at<const uint32_t>(sh + FROM * 512 + (k * waves + wave) * 4096,
-                                            static_cast<uint32_t>(min(lane, kLines - 1 - (k * waves + wave) * 64)) * 128u);
-    }
-    __device__ void finish() const {
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k)
-            asm volatile("" ::"v"(got[k]));
-    }
-    __device__ void clear() {
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k)
-            got[k] = 0;
-    }
-};
-
 // The head's left factor of a chunk, [M . G | 2^c C], into LDS: each wave builds
 // the fragments wave, wave + waves, ..., four in flight.  cH, cL: c per token.
 template <int N, bool FINE>
@@ -921,7 +895,6 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         st_l = st[2 * Q + lane];
         st_b = reinterpret_cast<const float*>(shared0 + ch * Sh::kHalfs + Sh::kFrags * 512)[lane];
     };
-    Touch<Sh::kB, Sh::kFrags> touch;
     constexpr int kSlots = N > 128 ? 1 : 2;
     BRing<N, FINE, true, kSlots> B;
     f16v S[NT];
@@ -930,7 +903,6 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         S[nt] = zero16();
     float unit = 1.0f;   // S holds the state times this
     double seg_sum = 0.0;
-    touch.clear();
     in.load(w.ch0 * Q);
     load_steps(w.ch0);
     in.begin(static_cast<const Act*>(a.p.tail_in) + (static_cast<size_t>(w.seq) * a.C + col0) * 4, w.ch0 * Q);
@@ -938,7 +910,6 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
     for (int ch = w.ch0; ch < w.ch1; ++ch) {
         const _Float16* sh = shared0 + ch * Sh::kHalfs;
         const int next = min(ch + 1, w.ch1 - 1);
-        touch.finish();
         in.store();
         const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
         seg_sum += static_cast<double>(th) + static_cast<double>(tl);
@@ -952,7 +923,6 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         // a near one is a wait for them
         in.load(next * Q);
         load_steps(next);
-        touch.start(shared0 + next * Sh::kHalfs, wave, waves, lane);
         B.load(sh, 0, lane);
         phase();
 
@@ -1021,7 +991,6 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         }
         wave_sync();   // tile and factors are rewritten by the next chunk
     }
-    touch.finish();
     store_state(S, inverse_pow2(unit),
                 a.seg_state + (w.head * a.segs + w.seg) * a.P * N + static_cast<size_t>(wave * 32 + c) * N + 4 * hi);
     if (wave == 0 && lane == 0)
@@ -1116,18 +1085,15 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
             xq[ks] = ld_frag(reinterpret_cast<const _Float16*>(from), ks, lane);
         st_x = reinterpret_cast<const float*>(from + 4096)[c];
     };
-    Touch<0, Sh::kBl> touch;
     BRing<N, false, false, 2> B;
     f16v S[NT];
     float unit = 1.0f;
-    touch.clear();
     load_chunk(w.ch0);
     load_state(S, a.seg_state + (w.head * a.segs + w.seg) * a.P * N + static_cast<size_t>(wave * 32 + c) * N + 4 * hi);
 
     for (int ch = w.ch0; ch < w.ch1; ++ch) {
         const _Float16* sh = shared0 + ch * Sh::kHalfs;
         const int next = min(ch + 1, w.ch1 - 1);
-        touch.finish();
         const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
         const float F = st_d * st_b;
         const float sF = pow2_to<0, kMostF>(wave_max(F));
@@ -1169,7 +1135,6 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
         B.load(sh, 0, lane);
         B.load(sh, 1, lane);
         phase();
-        touch.start(shared0 + next * Sh::kHalfs, wave, waves, lane);
         phase();
         __syncthreads();
         f16v Y[2] = {zero16(), zero16()};
@@ -1207,7 +1172,6 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
         __syncthreads();   // the left factor is rewritten by the next chunk
         wave_sync();       // and so are tile and factors
     }
-    touch.finish();
     if (w.ch1 == w.last)
         write_tails<Act>(a, w, col0, N, lane);
 }
@@ -1263,7 +1227,6 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         st_b = sc[lane];
         st_c = sc[Q + lane];
     };
-    Touch<0, Sh::kFrags> touch;
     constexpr int kSlots = N > 128 ? 1 : 2;
     BRing<N, FINE, true, kSlots> B;
     f16v S[NT];
@@ -1271,7 +1234,6 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     const size_t row_off = static_cast<size_t>(wave * 32 + c) * N + 4 * hi;
     float* state_row = SPLIT ? a.seg_state + (w.head * a.segs + w.seg) * a.P * N + row_off
                              : a.p.state + w.head * a.P * N + row_off;
-    touch.clear();
     load_steps(w.ch0);
     if constexpr (!SPLIT) {
         in.load(w.ch0 * Q);
@@ -1282,7 +1244,6 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     for (int ch = w.ch0; ch < w.ch1; ++ch) {
         const _Float16* sh = shared0 + ch * Sh::kHalfs;
         const int next = min(ch + 1, w.ch1 - 1);
-        touch.finish();
         if constexpr (!SPLIT)
             in.store();
         const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
@@ -1297,7 +1258,6 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         if constexpr (!SPLIT)
             in.load(next * Q);
         load_steps(next);
-        touch.start(shared0 + next * Sh::kHalfs, wave, waves, lane);
 
         float xc[32];
         float m1 = 0.0f, m2 = 0.0f;
@@ -1390,7 +1350,6 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         __syncthreads();   // the left factor is rewritten by the next chunk
         wave_sync();       // and so are tile and factors
     }
-    touch.finish();
     if constexpr (!SPLIT)
         store_state(S, inverse_pow2(unit), state_row);
     if (w.ch1 == w.last)
@@ -1399,15 +1358,20 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
 
 // ------------------------------------------------------------ host
 
-// Segments: waves wanted, and chunks a segment has at least.
-constexpr int kWaves = 2048;
-constexpr int kSegChunks = 4;
-
-static void segments(const SsmGeo& g, int T, int& segs, int& per) {
+// Segments per sequence: as many as fill the chip once, which is two waves per
+// SIMD, or one where a wave needs more than 256 registers (N = 256, fp32).  One
+// 64-head prompt of 32,768 tokens: 540 us at 2,048 waves, 595 at 3,000, 605 at
+// 4,096; N = 256 (32 heads, 4,096 tokens) 106 us at 1,024 and 132 at 2,048.
+// Prompts of given lengths end at different times and take twice as many (eight
+// of up to 2,048 tokens: 362 against 390 us).  A segment has at least two chunks,
+// in fp32 one (64 heads, 512 tokens: 57 us with four, 45 with two, 49 with one;
+// fp32, 32 heads, 256 tokens: 57, 52 and 41 us).
+static void segments(const SsmGeo& g, int T, bool ragged, int& segs, int& per) {
     const int nc = (T + Q - 1) / Q;
     const int64_t waves = static_cast<int64_t>(g.B) * g.H * (g.P / 32);
-    const int64_t want = (kWaves + waves - 1) / waves;
-    const int most = std::max(1, nc / kSegChunks);
+    const int64_t fill = (g.N > 128 || !g.bf16 ? 1024 : 2048) * (ragged ? 2 : 1);
+    const int64_t want = (fill + waves - 1) / waves;
+    const int most = std::max(1, nc / (g.bf16 ? 2 : 1));
     segs = static_cast<int>(std::min<int64_t>(want, most));
     per = (nc + segs - 1) / segs;
     segs = (nc + per - 1) / per;
@@ -1426,9 +1390,9 @@ static size_t shared_halfs(const SsmGeo& g) {
 }
 
 // The workspace: fragments, steps, and with segments their states, decays and the convolved x.
-static size_t carve(const SsmGeo& g, int T, char* base, ChunkArgs* a) {
+static size_t carve(const SsmGeo& g, int T, bool ragged, char* base, ChunkArgs* a) {
     int segs, per;
-    segments(g, T, segs, per);
+    segments(g, T, ragged, segs, per);
     const size_t nc = (T + Q - 1) / Q, BH = static_cast<size_t>(g.B) * g.H;
     size_t n = 0;
     auto take = [&](size_t bytes) {
@@ -1457,7 +1421,9 @@ static size_t carve(const SsmGeo& g, int T, char* base, ChunkArgs* a) {
     return n;
 }
 
-size_t chunked_ws_bytes(const SsmGeo& g, int T) { return carve(g, T, nullptr, nullptr); }
+size_t chunked_ws_bytes(const SsmGeo& g, int T) {
+    return std::max(carve(g, T, false, nullptr, nullptr), carve(g, T, true, nullptr, nullptr));
+}
 
 // A launch that may need more than 64 KB of LDS.
 template <typename... Args>
@@ -1480,7 +1446,7 @@ static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const in
     a.lengths = lengths;
     a.status = status;
     a.T = T, a.B = g.B, a.H = g.H, a.G = g.G, a.P = g.P, a.C = g.C;
-    carve(g, T, static_cast<char*>(ws), &a);
+    carve(g, T, lengths != nullptr, static_cast<char*>(ws), &a);
     // by XCD where the sets of heads come out even over the eight, or nearly
     const int64_t sets = static_cast<int64_t>(g.B) * g.G * a.segs;
     a.by_xcd = sets % 8 == 0 || sets >= 64;
