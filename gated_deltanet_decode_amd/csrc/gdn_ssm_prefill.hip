@@ -624,65 +624,81 @@ __device__ __forceinline__ float state_max(const f16v (&S)[NT]) {
 }
 
 // The head's left factor of a chunk, [M . G | 2^c C], into LDS: each wave builds
-// the fragments wave, wave + waves, ..., four in flight.  cH, cL: c per token.
-template <int N, bool FINE>
-__device__ __forceinline__ void left_factor(const _Float16* sh, _Float16* L, const float* cH, const float* cL,
-                                            int wave, int waves, int lane) {
+// the fragments wave, wave + waves, ..., BATCH of them loaded at a time.  The
+// first batch is asked for well before it is needed (with four at a time, each
+// waited for, the left factor took 94 of the output pass's 290 us).
+template <int N, bool FINE, int BATCH>
+struct Left {
     using Sh = Shared<N, FINE>;
-    constexpr int AF = Sh::GF + Sh::CF, KS = N / 16;
-    const int hi = lane >> 5, c = lane & 31;
-    for (int f0 = wave; f0 < AF; f0 += 4 * waves) {
-        h8 fh[4], fl[4];
+    static constexpr int AF = Sh::GF + Sh::CF, KS = N / 16;
+    h8 fh[BATCH], fl[BATCH];
+
+    __device__ void load(const _Float16* sh, int f0, int waves, int lane) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int f = min(f0 + k * waves, AF - 1);
+        for (int k = 0; k < BATCH; ++k) {
+            const int f = min(f0 + k * waves, AF - 1);   // always something: a value kept from before costs registers
             fh[k] = ld_frag(sh, f < Sh::GF ? Sh::kG + f : Sh::kC + f - Sh::GF, lane);
             if (FINE)
                 fl[k] = ld_frag(sh, f < Sh::GF ? Sh::kGl + f : Sh::kCl + f - Sh::GF, lane);
         }
-        phase();
+    }
+    // cH, cL: c per token.  The first batch is loaded.
+    __device__ void build(const _Float16* sh, _Float16* L, const float* cH, const float* cL, int wave, int waves,
+                          int lane) {
+        const int hi = lane >> 5, c = lane & 31;
+        for (int f0 = wave; f0 < AF; f0 += BATCH * waves) {
+            if (f0 != wave)
+                load(sh, f0, waves, lane);
+            phase();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int f = f0 + k * waves;
-            if (f >= AF)
-                break;
-            h8 mh, ml;
-            if (f < Sh::GF) {
-                const int it = f >= 2, ks = it ? f - 2 : f;
-                const float ci = cH[32 * it + c];
-                const float li = FINE ? cL[32 * it + c] : 0.0f;
-                float m[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int j = 16 * ks + kperm(hi, e);
-                    float arg = ci - cH[j];
-                    float gv = static_cast<float>(fh[k][e]);
-                    if (FINE) {
-                        arg += li - cL[j];
-                        gv += static_cast<float>(fl[k][e]);
-                    }
-                    m[e] = j <= 32 * it + c ? gv * __builtin_amdgcn_exp2f(arg) : 0.0f;
-                }
-                parts8<FINE>(m, mh, ml);
-            } else {
-                const int row = f - Sh::GF < KS ? c : 32 + c;
-                const float e2 = __builtin_amdgcn_exp2f(cH[row] + cL[row]);
-                if (FINE) {
+            for (int k = 0; k < BATCH; ++k) {
+                const int f = f0 + k * waves;
+                if (f >= AF)
+                    break;
+                h8 mh, ml;
+                if (f < Sh::GF) {
+                    const int it = f >= 2, ks = it ? f - 2 : f;
+                    const float ci = cH[32 * it + c];
+                    const float li = FINE ? cL[32 * it + c] : 0.0f;
                     float m[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        m[e] = (static_cast<float>(fh[k][e]) + static_cast<float>(fl[k][e])) * e2;
-                    split8(m, mh, ml);
+                    for (int q = 0; q < 2; ++q) {
+                        const int j = 16 * ks + 8 * q + 4 * hi;
+                        const float4 cj = *reinterpret_cast<const float4*>(cH + j);
+                        const float4 lj = FINE ? *reinterpret_cast<const float4*>(cL + j) : float4{};
+                        const float cc[4] = {cj.x, cj.y, cj.z, cj.w}, ll[4] = {lj.x, lj.y, lj.z, lj.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float arg = ci - cc[e];
+                            float gv = static_cast<float>(fh[k][4 * q + e]);
+                            if (FINE) {
+                                arg += li - ll[e];
+                                gv += static_cast<float>(fl[k][4 * q + e]);
+                            }
+                            m[4 * q + e] = j + e <= 32 * it + c ? gv * __builtin_amdgcn_exp2f(arg) : 0.0f;
+                        }
+                    }
+                    parts8<FINE>(m, mh, ml);
                 } else {
-                    mh = fh[k] * static_cast<_Float16>(e2);
+                    const int row = f - Sh::GF < KS ? c : 32 + c;
+                    const float e2 = __builtin_amdgcn_exp2f(cH[row] + cL[row]);
+                    if (FINE) {
+                        float m[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            m[e] = (static_cast<float>(fh[k][e]) + static_cast<float>(fl[k][e])) * e2;
+                        split8(m, mh, ml);
+                    } else {
+                        mh = fh[k] * static_cast<_Float16>(e2);
+                    }
                 }
+                st_frag(L, f, lane, mh);
+                if (FINE)
+                    st_frag(L, AF + f, lane, ml);
             }
-            st_frag(L, f, lane, mh);
-            if (FINE)
-                st_frag(L, AF + f, lane, ml);
         }
     }
-}
+};
 
 // Y += C' S0^T, the state scaled by `scale` into fp16.
 template <int N, bool FINE>
@@ -1086,6 +1102,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
         st_x = reinterpret_cast<const float*>(from + 4096)[c];
     };
     BRing<N, false, false, 2> B;
+    Left<N, false, 12> left;
     f16v S[NT];
     float unit = 1.0f;
     load_chunk(w.ch0);
@@ -1094,6 +1111,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
     for (int ch = w.ch0; ch < w.ch1; ++ch) {
         const _Float16* sh = shared0 + ch * Sh::kHalfs;
         const int next = min(ch + 1, w.ch1 - 1);
+        left.load(sh, wave, waves, lane);
         const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
         const float F = st_d * st_b;
         const float sF = pow2_to<0, kMostF>(wave_max(F));
@@ -1106,8 +1124,6 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
         fL[lane] = st_l;
         const float decay = __builtin_amdgcn_exp2f(th + tl);
         wave_sync();
-        left_factor<N, false>(sh, L, fH, fL, wave, waves, lane);
-        phase();
         // X', X'' in units of s_F / cs; x itself is taken up by Y below
         const float ux = sF * inverse_pow2(cs);
         h8 xh[4], wh[4];
@@ -1130,6 +1146,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
             pin(xh[ks]);
             pin(wh[ks]);
         }
+        left.build(sh, L, fH, fL, wave, waves, lane);
         const float ss = pow2_to<8, kMostS>(state_max(S));   // on top of `unit`
         phase();
         B.load(sh, 0, lane);
@@ -1229,6 +1246,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     };
     constexpr int kSlots = N > 128 ? 1 : 2;
     BRing<N, FINE, true, kSlots> B;
+    Left<N, FINE, (FINE ? 4 : 8)> left;
     f16v S[NT];
     float unit = 1.0f;
     const size_t row_off = static_cast<size_t>(wave * 32 + c) * N + 4 * hi;
@@ -1295,6 +1313,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         const float s2 = fminf(pow2_to<8, kMostW>(m2), unit * 0x1p60f);   // the unit of the next state
         const float sx = pow2_to<8, kMostX>(fmaxf(m1, ms));
 
+        left.load(sh, wave, waves, lane);
         // X'' and X' as fragments; Y starts from D x
         h8 wh[4], wl[4], xh[4], xl[4];
         f16v Y[2];
@@ -1327,7 +1346,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
                 pin(xl[ks]);
             phase();
         }
-        left_factor<N, FINE>(sh, L, fH, fL, wave, waves, lane);
+        left.build(sh, L, fH, fL, wave, waves, lane);
         phase();
         __syncthreads();
         const bool update = !SPLIT || ch + 1 < w.ch1;
