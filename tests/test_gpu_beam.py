@@ -76,6 +76,19 @@ def test_every_order_and_ties(bf16):
 
 
 @pytest.mark.parametrize("bf16", [True, False])
+def test_long_spans_in_every_order(bf16):
+    """Rows enough for four long spans each: buffers fill and are cut again and again."""
+    B, K, V = 256, 4, 12000
+    r = np.random.default_rng(2)
+    for row in (np.linspace(-5, 5, V), np.linspace(5, -5, V), np.zeros(V) - 3, r.integers(0, 5, V) * 0.5):
+        lg = np.ascontiguousarray(np.broadcast_to(row, (B, K, V)), dtype=np.float32)
+        check(lg, -r.random((B, K)), 24, bf16=bf16)
+    lg = np.full((B, K, V), -INF, np.float32)              # all but a few tokens masked
+    lg[:, :, r.integers(0, V, 5)] = r.standard_normal(5)
+    check(lg, -r.random((B, K)), 12, bf16=bf16)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
 def test_masked_and_broken_logits(bf16):
     r = np.random.default_rng(5)
     V = 1030

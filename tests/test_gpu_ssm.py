@@ -104,6 +104,36 @@ def test_prefill(name, H, G, P, N, bf16, T):
     m.check(what=f"{name} T={T}")
 
 
+@pytest.mark.parametrize("T", [31, 32, 33, 129, 500])
+@pytest.mark.parametrize("H,G,P,N,bf16", [(4, 2, 32, 256, True), (2, 1, 128, 32, True), (6, 3, 64, 64, False),
+                                          (2, 2, 128, 128, False)])
+def test_prefill_around_its_forms(H, G, P, N, bf16, T):
+    """Lengths on both sides of the token walk's end, and with one and several segments."""
+    m = Layer(sr.make(220 + T, 2, T, H, G, P, N, bf16))
+    m.prefill()
+    m.check(what=f"T={T}")
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_prefill_of_a_batch_that_fills_the_chip(bf16):
+    """Enough sequences and heads for one segment of many chunks each, with ragged ends."""
+    i = sr.make(230, 16, 200, 64, 2, 64, 32, bf16)
+    m = Layer(i)
+    m.prefill()
+    m.check()
+    lengths = np.random.default_rng(1).integers(0, 201, 16).astype(np.int32)
+    m = Layer(i)
+    m.prefill(torch.from_numpy(lengths).cuda())
+    m.check(lengths)
+
+
+def test_prefill_of_sets_that_do_not_divide_by_the_xcds():
+    """3 sequences x 23 segments: 69 sets of heads over eight XCDs."""
+    m = Layer(sr.make(231, 3, 2944, 2, 1, 32, 32, True, gate=False))
+    m.prefill()
+    m.check()
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 def test_prefill_many_chunks(bf16):
     """Long enough for several segments of chunks per sequence, with an odd end."""
