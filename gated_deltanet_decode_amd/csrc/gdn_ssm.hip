@@ -297,7 +297,7 @@ template <typename Act>
 static hipError_t prefill_act(const SsmGeo& g, const SsmArgs& a, int T, const int32_t* lengths, int32_t* status,
                               void* ws, hipStream_t s) {
     hipError_t e;
-    if (T > kWalkTokens)
+    if (T > walk_tokens(g))
         return launch_ssm_chunked(g, a, T, lengths, status, ws, s);
     switch (g.N) {
         case 32: e = walk_cfg<32, Act>(g, a, T, lengths, s); break;
@@ -319,7 +319,7 @@ hipError_t launch_ssm_token(const SsmGeo& g, const SsmArgs& a, hipStream_t s) {
     return g.bf16 ? ssm::token_act<uint16_t>(g, a, s) : ssm::token_act<float>(g, a, s);
 }
 
-size_t ssm_prefill_ws_bytes(const SsmGeo& g, int T) { return T > ssm::kWalkTokens ? ssm::chunked_ws_bytes(g, T) : 256; }
+size_t ssm_prefill_ws_bytes(const SsmGeo& g, int T) { return T > ssm::walk_tokens(g) ? ssm::chunked_ws_bytes(g, T) : 256; }
 
 hipError_t launch_ssm_prefill(const SsmGeo& g, const SsmArgs& a, int T, const int32_t* lengths, int32_t* status,
                               void* ws, hipStream_t s) {

@@ -56,8 +56,12 @@ struct Rows {
     __device__ static int key(int j, int r) { return j * 4 * LPR + 4 * r; }
 };
 
-// Prompts up to this length take the token walk.
-constexpr int kWalkTokens = 32;
+// Prompts up to this length take the token walk, which costs about 0.5 us a token
+// (2 us where its workgroups no longer fit the chip at once) against 15 to 28 us
+// for a chunk of any length.  16 heads of 64 rows: 13.4 against 15.0 us at 16
+// tokens, 17.7 against 14.8 at 24; 8 x 64 heads: 26 against 26 us at 8 tokens, 43
+// against 26 at 16.
+inline int walk_tokens(const SsmGeo& g) { return static_cast<int64_t>(g.B) * g.H * g.P <= 16384 ? 16 : 8; }
 size_t chunked_ws_bytes(const SsmGeo& g, int T);
 hipError_t launch_ssm_chunked(const SsmGeo& g, const SsmArgs& a, int T, const int32_t* lengths, int32_t* status,
                               void* ws, hipStream_t s);

@@ -528,7 +528,8 @@ gdn_status gdn_ssm_decode_token(const gdn_ssm_dims* d, float* state, const void*
  *   workspace device bytes >= gdn_ssm_prefill_workspace_bytes(d, T), 256-byte
  *           aligned.  1 <= T <= GDN_SSM_MAX_TOKENS.
  * State and fp32 outputs agree with the token-by-token call to fp32 rounding,
- * bf16 outputs to the rounding of bf16.
+ * bf16 outputs to the rounding of bf16.  A NaN or infinity in a token's inputs
+ * may reach the outputs of every token of its chunk of 64, not only later ones.
  */
 #define GDN_SSM_MAX_TOKENS (1 << 22)
 size_t gdn_ssm_prefill_workspace_bytes(const gdn_ssm_dims* d, int32_t T);

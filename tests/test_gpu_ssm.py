@@ -104,7 +104,7 @@ def test_prefill(name, H, G, P, N, bf16, T):
     m.check(what=f"{name} T={T}")
 
 
-@pytest.mark.parametrize("T", [31, 32, 33, 129, 500])
+@pytest.mark.parametrize("T", [7, 8, 9, 15, 16, 17, 33, 129, 500])
 @pytest.mark.parametrize("H,G,P,N,bf16", [(4, 2, 32, 256, True), (2, 1, 128, 32, True), (6, 3, 64, 64, False),
                                           (2, 2, 128, 128, False)])
 def test_prefill_around_its_forms(H, G, P, N, bf16, T):
@@ -261,9 +261,10 @@ def test_repeats_are_bitwise_equal_and_two_streams_do_not_mix():
     e.check()
 
 
-def test_graph_of_prefill_and_tokens():
+@pytest.mark.parametrize("P,N,bf16", [(64, 128, True), (128, 256, False)])
+def test_graph_of_prefill_and_tokens(P, N, bf16):
     """One captured prefill and two tokens, replayed three times with eager resets in between."""
-    i = sr.make(84, 2, 200, 3, 1, 64, 128, True)
+    i = sr.make(84, 2, 200, 3, 1, P, N, bf16)
     m = Layer(i)
     ws = torch.empty(m.gdn.ssm_prefill_workspace_bytes(m.d, 200), dtype=torch.uint8, device="cuda")
     start = [m.state.clone(), m.tail.clone()]
