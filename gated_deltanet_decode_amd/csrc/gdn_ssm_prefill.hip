@@ -116,7 +116,7 @@ __device__ __forceinline__ float pow2_to(float m) {
 // Caps of the scales.  A row of B, C, x, X' or X'' whose largest value is below
 // 2^-38 loses relative precision to fp16's absolute 2^-24 at that scale; in
 // return no product of scales and states leaves fp32's range.
-constexpr int kMostBC = 40, kMostX = 24, kMostF = 24, kMostW = 48, kMostS = 100;
+constexpr int kMostBC = 40, kMostX = 24, kMostF = 24, kMostS = 100;
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
 
@@ -920,8 +920,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         st_l = st[2 * Q + lane];
         st_b = reinterpret_cast<const float*>(shared0 + ch * Sh::kHalfs + Sh::kFrags * 512)[lane];
     };
-    constexpr int kSlots = N > 128 ? 1 : 2;
-    BRing<N, FINE, true, kSlots> B;
+    BRing<N, FINE, true, 1> B;
     f16v S[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -996,8 +995,6 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
             pin(wl[ks]);
             phase();
         }
-        if (kSlots > 1)
-            B.load(sh, 1, lane);
         B.update(S, decay * (s2 * inverse_pow2(unit)), wh, wl, sh, lane);
         unit = s2;
         phase();
@@ -1225,10 +1222,10 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     const int col0 = w.h * a.P + wave * 32;
     char* mine = pool + wave * kWaveBytes;
     float* yt = reinterpret_cast<float*>(mine);
-    float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B
-    float* fW = fF + Q;                                        // 2^(c_last - c)
+    float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B * s_F
+    float* fW = fF + Q;                                        // the same times 2^(c_last - c)
     float* fS = fF + 2 * Q;                                    // 2^-s_C
-    float* fK = fF + 3 * Q;                                    // D * 2^s_C
+    float* fK = fF + 3 * Q;                                    // D * s_F * 2^s_C
     float* fH = fF + 4 * Q;                                    // c, high and low part
     float* fL = fF + 5 * Q;
     _Float16* L = reinterpret_cast<_Float16*>(pool + waves * kWaveBytes);
@@ -1274,10 +1271,12 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         if constexpr (!SPLIT)
             in.store();
         const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
-        fF[lane] = st_d * st_b;
-        fW[lane] = __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
+        const float sF = pow2_to<0, kMostF>(wave_max(st_d * st_b));
+        const float F = st_d * st_b * sF;
+        fF[lane] = F;
+        fW[lane] = F * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
         fS[lane] = st_c;
-        fK[lane] = skip * inverse_pow2(st_c);
+        fK[lane] = skip * sF * inverse_pow2(st_c);
         fH[lane] = st_h;
         fL[lane] = st_l;
         const float decay = __builtin_amdgcn_exp2f(th + tl);
@@ -1287,7 +1286,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         load_steps(next);
 
         float xc[32];
-        float m1 = 0.0f, m2 = 0.0f;
+        float mx = 0.0f;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             float v[4];
@@ -1298,37 +1297,32 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
             } else {
                 conv_run(in.tile, taps, r, lane, v);
             }
-            const float4 F = *reinterpret_cast<const float4*>(fF + 8 * r + 4 * hi);
-            const float4 W = *reinterpret_cast<const float4*>(fW + 8 * r + 4 * hi);
-            const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 xc[4 * r + i] = v[i];
-                const float xp = v[i] * ff[i];
-                m1 = fmaxf(m1, fabsf(xp));
-                m2 = fmaxf(m2, fabsf(xp * ww[i]));
+                mx = fmaxf(mx, fabsf(v[i]));
                 pin(xc[4 * r + i]);
             }
-            pin(m1);
-            pin(m2);
+            pin(mx);
             if (!SPLIT && r % 2)
                 phase();
         }
         if constexpr (!SPLIT)
             in.save(Q);
-        m1 = fmaxf(m1, __shfl_xor(m1, 32));
-        m2 = fmaxf(m2, __shfl_xor(m2, 32));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        // one scale for x, the state that enters and so all of the row: the state, up to a thousand times X', stays
+        // below 2^15 in it, and X' is the less exact the smaller it is beside the state
         const float ms = state_max(S) * inverse_pow2(unit);
-        const float s2 = fminf(pow2_to<8, kMostW>(m2), unit * 0x1p60f);   // the unit of the next state
-        const float sx = pow2_to<8, kMostX>(fmaxf(m1, ms));
+        const float sx = fminf(fminf(pow2_to<8, kMostX>(mx), pow2_to<14, kMostS>(ms) * inverse_pow2(sF)),
+                               unit * 0x1p40f);
+        const float u = sx * sF;   // the unit of X', X'', Y and the next state
 
-        left.load(sh, wave, waves, lane);
         // X'' and X' as fragments; Y starts from D x
         h8 wh[4], wl[4], xh[4], xl[4];
         f16v Y[2];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            float v[8], u[8];
+            float xw[8], xp[8];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const float4 F = *reinterpret_cast<const float4*>(fF + 16 * ks + 8 * q + 4 * hi);
@@ -1337,17 +1331,16 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
                 const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w}, kk[4] = {K.x, K.y, K.z, K.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float x = xc[8 * ks + 4 * q + i];
-                    const float xp = x * ff[i];
-                    v[4 * q + i] = xp * (ww[i] * s2);
-                    u[4 * q + i] = xp * sx;
-                    float y = (x * sx) * kk[i];
+                    const float x = xc[8 * ks + 4 * q + i] * sx;
+                    xw[4 * q + i] = x * ww[i];
+                    xp[4 * q + i] = x * ff[i];
+                    float y = x * kk[i];
                     pin(y);
                     Y[ks / 2][8 * (ks % 2) + 4 * q + i] = y;
                 }
             }
-            split8(v, wh[ks], wl[ks]);
-            parts8<FINE>(u, xh[ks], xl[ks]);
+            split8(xw, wh[ks], wl[ks]);
+            parts8<FINE>(xp, xh[ks], xl[ks]);
             pin(wh[ks]);
             pin(wl[ks]);
             pin(xh[ks]);
@@ -1355,11 +1348,12 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
                 pin(xl[ks]);
             phase();
         }
+        left.load(sh, wave, waves, lane);
         left.build(sh, L, fH, fL, wave, waves, lane);
         phase();
         __syncthreads();
         const bool update = !SPLIT || ch + 1 < w.ch1;
-        state_product<N, FINE>(Y, S, sx * inverse_pow2(unit), L, lane);
+        state_product<N, FINE>(Y, S, u * inverse_pow2(unit), L, lane);
         chunk_product<N, FINE>(Y, xh, xl, L, lane);
         if (update) {
 #pragma unroll
@@ -1369,11 +1363,11 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         const size_t y0 = (static_cast<size_t>(w.seq) * a.T + ch * Q) * yrow + col0;
         phase();
         if (update) {
-            B.update(S, decay * (s2 * inverse_pow2(unit)), wh, wl, sh, lane);
-            unit = s2;
+            B.update(S, decay * (u * inverse_pow2(unit)), wh, wl, sh, lane);
+            unit = u;
         }
         phase();
-        store_y<Act>(Y, fS, inverse_pow2(sx), yt, static_cast<Act*>(a.p.y) + y0,
+        store_y<Act>(Y, fS, inverse_pow2(u), yt, static_cast<Act*>(a.p.y) + y0,
                      a.p.z ? static_cast<const Act*>(a.p.z) + y0 : nullptr, static_cast<int>(yrow), w.len - ch * Q, lane);
         __syncthreads();   // the left factor is rewritten by the next chunk
         wave_sync();       // and so are tile and factors
