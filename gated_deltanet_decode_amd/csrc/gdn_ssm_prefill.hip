@@ -1250,8 +1250,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         st_b = sc[lane];
         st_c = sc[Q + lane];
     };
-    constexpr int kSlots = N > 128 ? 1 : 2;
-    BRing<N, FINE, true, kSlots> B;
+    BRing<N, FINE, true, 1> B;
     Left<N, FINE, (FINE ? 4 : 8)> left;
     f16v S[NT];
     float unit = 1.0f;
@@ -1355,11 +1354,8 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         const bool update = !SPLIT || ch + 1 < w.ch1;
         state_product<N, FINE>(Y, S, u * inverse_pow2(unit), L, lane);
         chunk_product<N, FINE>(Y, xh, xl, L, lane);
-        if (update) {
-#pragma unroll
-            for (int ks = 0; ks < kSlots; ++ks)
-                B.load(sh, ks, lane);
-        }
+        if (update)
+            B.load(sh, 0, lane);
         const size_t y0 = (static_cast<size_t>(w.seq) * a.T + ch * Q) * yrow + col0;
         phase();
         if (update) {
