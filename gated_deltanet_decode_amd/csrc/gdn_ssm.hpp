@@ -43,8 +43,8 @@ __device__ __forceinline__ float conv_bias_silu(const float w[4], const float wi
 // dt = softplus(raw + bias), without overflow on either side.
 __device__ __forceinline__ float step_size(float raw) { return fmaxf(raw, 0.0f) + log1pf(expf(-fabsf(raw))); }
 
-// log2 of the decay per unit step: A is taken as min(A, 0), so a decay never exceeds 1.
-__device__ __forceinline__ float rate2(float A) { return fminf(A, 0.0f) * kLog2e; }
+// log2 of the decay per unit step: A is taken as min(A, 0), so a decay never exceeds 1 (a NaN stays one).
+__device__ __forceinline__ float rate2(float A) { return (A > 0.0f ? 0.0f : A) * kLog2e; }
 
 // A state row of N entries over LPR consecutive lanes, NV float4 per lane.
 template <int N>

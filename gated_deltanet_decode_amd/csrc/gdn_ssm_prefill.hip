@@ -346,7 +346,10 @@ __device__ __forceinline__ double wave_scan(double v, int lane) {
 constexpr int kStepHeads = 16;   // heads per workgroup of the step sizes
 
 // Step sizes and summed decays of a chunk's tokens.  c is summed in fp64: what
-// matters are differences of it, also where it is large.
+// matters are differences of it, also where it is large.  A token's part of it
+// ends at -160, where the decay is 0 in fp32 whatever else is added, so that the
+// high part alone (all that bf16 outputs use) is within 2^-11 of c.
+constexpr float kLeastDecay = -160.0f;
 __device__ void steps_part(const ChunkArgs& a, int id, float* lds) {
     const int hb = (a.H + kStepHeads - 1) / kStepHeads;
     const int h0 = id % hb * kStepHeads;
@@ -367,7 +370,8 @@ __device__ void steps_part(const ChunkArgs& a, int id, float* lds) {
         const int h = h0 + k;
         const float d = chunk * Q + lane < len
                             ? step_size(lds[k * (Q + 1) + lane] + (a.p.dt_bias ? a.p.dt_bias[h] : 0.0f)) : 0.0f;
-        const double cum = wave_scan(static_cast<double>(d) * static_cast<double>(rate2(a.p.A[h])), lane);
+        const double part = static_cast<double>(d) * static_cast<double>(rate2(a.p.A[h]));
+        const double cum = wave_scan(part < kLeastDecay ? kLeastDecay : part, lane);
         const float high = static_cast<float>(cum);
         float* o = a.steps + ((static_cast<size_t>(seq) * a.H + h) * a.nc + chunk) * (3 * Q);
         o[lane] = d;

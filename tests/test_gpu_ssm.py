@@ -231,6 +231,39 @@ def test_step_sizes_at_the_ends_of_softplus():
     m.check()
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+def test_a_token_that_wipes_the_state(bf16):
+    """A step so long that the sums of decays grow past what their differences may be rounded by."""
+    i = sr.make(73, 1, 130, 2, 1, 64, 64, bf16, gate=False)
+    i["A"] = np.array([-8.0, -2.0], np.float32)
+    i["dt"][0, 5], i["dt"][0, 70] = 5e4, 3e4
+    m = Layer(i)
+    m.prefill()
+    m.check()
+
+
+@pytest.mark.parametrize("T", [1, 5, 100])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_a_broken_decay_shows(bf16, T):
+    """A NaN in A: that head's state and outputs are NaN, the other heads' as ever."""
+    i = sr.make(74, 1, T, 3, 1, 64, 64, bf16)
+    i["A"][1] = np.nan
+    y, state, _ = sr.run(i)
+    for by_token in (True, False):
+        m = Layer(i)
+        if by_token:
+            m.tokens(0, min(T, 5))
+        else:
+            m.prefill()
+        torch.cuda.synchronize()
+        n = min(T, 5) if by_token else T
+        assert torch.isnan(m.state[:, 1]).all() and torch.isnan(m.y[:, :n, 1]).all()
+        got = m.y.float().cpu().numpy()[:, :n, [0, 2]]
+        assert normwise(got, y[:, :n, [0, 2]]) < (TOL16 if bf16 else TOL32)
+        if not by_token:
+            assert normwise(m.state.cpu().numpy()[:, [0, 2]], state[:, [0, 2]]) < TOL32
+
+
 def test_a_sequence_does_not_depend_on_its_batch():
     """Bit for bit the same sequence alone in a batch of three copies (same grid rule per call)."""
     i = sr.make(81, 3, 100, 4, 1, 64, 128, True)
