@@ -594,6 +594,8 @@ def beam_select(logits, scores, out_scores, parent, token, workspace, finished=N
     if not isinstance(out_scores, torch.Tensor) or out_scores.numel() % B:
         raise ValueError("out_scores must be [B][S]")
     S = out_scores.numel() // B
+    if B * K >= 1 << 31 or K * V >= 1 << 31 or S >= 1 << 31:   # C's integers would wrap
+        raise GdnError(2, "gdn_beam_select")
     dev, s = _here(stream)
     if logits.get_device() != dev:
         raise ValueError(f"logits is on {logits.device}, but the current device is cuda:{dev}")

@@ -85,8 +85,8 @@ gdn_status check_ssm_dims(const gdn_ssm_dims* d, gdn::SsmGeo& g) {
         d->conv_width != 4)
         return GDN_ERR_SHAPE;
     const int64_t C = static_cast<int64_t>(d->num_heads) * d->head_dim + 2ll * d->num_groups * d->state_dim;
-    // A chunk of 64 rows is addressed by 32-bit byte offsets.
-    if (C > (1ll << 22) || static_cast<int64_t>(d->batch) * d->num_heads > (1ll << 24))
+    // A chunk of 64 rows is addressed by 32-bit byte offsets, and a launch counts 2^32 threads: 16 per state row.
+    if (C > (1ll << 22) || static_cast<int64_t>(d->batch) * d->num_heads * d->head_dim >= (1ll << 28))
         return GDN_ERR_SHAPE;
     g = {d->batch, d->num_heads, d->num_groups, d->head_dim, d->state_dim, static_cast<int>(C),
          d->act_dtype == GDN_BF16};
@@ -624,6 +624,11 @@ gdn_status gdn_beam_select(int32_t batch, int32_t beams, int32_t vocab, int64_t 
         return GDN_ERR_WORKSPACE;
     if (!aligned16(workspace))
         return GDN_ERR_ALIGN;
+    // in place a workgroup replaces the scores that it alone has read; any other overlap is a race
+    const uintptr_t si = reinterpret_cast<uintptr_t>(scores), so = reinterpret_cast<uintptr_t>(out_scores);
+    const uintptr_t in_bytes = 4ull * batch * beams, out_bytes = 4ull * batch * select;
+    if (si < so + out_bytes && so < si + in_bytes && !(si == so && select == beams))
+        return GDN_ERR_ALIAS;
     const gdn::BeamGeo g{batch, beams, vocab, select, vocab_pitch, act_dtype == GDN_BF16};
     return launched(gdn::launch_beam_select(g, logits, scores, finished, eos, out_scores, parent, token, workspace,
                                             as_stream(stream)));
@@ -633,8 +638,8 @@ static gdn_status beam_reorder(int32_t batch, int32_t beams, int64_t state_bytes
                                void* conv_tail, const int32_t* parent, int32_t* status, void* stream) {
     if (beams < 1 || beams > GDN_MAX_BEAMS || batch % beams != 0)
         return GDN_ERR_SHAPE;
-    // one workgroup per 4 KB of a sequence and group
-    if ((state_bytes + tail_bytes) / 4096 * (batch / beams) >= (1ll << 30))
+    // one workgroup per 4 KB of a sequence and group; a launch counts 2^32 threads
+    if ((state_bytes + tail_bytes + 4095) / 4096 * (batch / beams) >= (1ll << 24))
         return GDN_ERR_SHAPE;
     gdn_status st = ptrs_ok({state, conv_tail, parent});
     if (st == GDN_OK)

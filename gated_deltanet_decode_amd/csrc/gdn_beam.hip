@@ -392,8 +392,8 @@ constexpr int kMaxEntries = 8192;   // of one sequence, over beams and spans
 // that is its place.  R: entries per thread.
 template <int R>
 __global__ __launch_bounds__(64 * kJoinWaves) void beam_join_kernel(
-    const Part* __restrict__ sums, const uint2* __restrict__ keys, const float* __restrict__ scores,
-    const uint8_t* __restrict__ finished, int eos, int K, int V, int S, int spans, float* __restrict__ out_scores,
+    const Part* __restrict__ sums, const uint2* __restrict__ keys, const float* scores,
+    const uint8_t* __restrict__ finished, int eos, int K, int V, int S, int spans, float* out_scores,
     int32_t* __restrict__ parent, int32_t* __restrict__ token) {
     // A beam's entry of logit l has the value sc + ((l - m) - logs).
     struct Beam {

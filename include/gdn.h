@@ -481,7 +481,8 @@ gdn_status gdn_tree_verify_ut_noalloc(const gdn_dims* d, const float* state_ckpt
  * Types: state, dt, dt_bias, A and D are fp32; x, z, y, the conv tail, weights
  * and bias have the activation type.  y is rounded once, on output.
  * Supported shapes: head_dim in {32, 64, 128}; state_dim in {32, 64, 128,
- * 256}; num_heads % num_groups == 0; conv_width == 4.
+ * 256}; num_heads % num_groups == 0; conv_width == 4; C <= 2^22 and
+ * B*H*P < 2^28 (GDN_ERR_SHAPE otherwise).
  */
 typedef struct {
     int32_t batch;      /* B: independent sequences */
@@ -528,7 +529,8 @@ gdn_status gdn_ssm_decode_token(const gdn_ssm_dims* d, float* state, const void*
  *   workspace device bytes >= gdn_ssm_prefill_workspace_bytes(d, T), 256-byte
  *           aligned.  1 <= T <= GDN_SSM_MAX_TOKENS.
  * State and fp32 outputs agree with the token-by-token call to fp32 rounding,
- * bf16 outputs to the rounding of bf16.  A NaN or infinity in a token's inputs
+ * bf16 outputs to the rounding of bf16 (where step sizes within 64 tokens differ
+ * by more than 2^14, relative to a head's largest outputs there).  A NaN or infinity in a token's inputs
  * may reach the outputs of every token of its chunk of 64, not only later ones.
  */
 #define GDN_SSM_MAX_TOKENS (1 << 22)
@@ -557,6 +559,8 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_dims* d, float* state, void* conv_tail,
  * any equal values, by the lowest index, where fewer than S others are left.
  * 1 <= K <= GDN_MAX_BEAMS, 1 <= S <= min(GDN_MAX_BEAM_SELECT, K*V),
  * K*V < 2^31, B*K <= 2^20 (GDN_ERR_SHAPE otherwise; GDN_ERR_INDEX for eos).
+ * out_scores may be scores itself where S == K, and must not overlap it
+ * otherwise (GDN_ERR_ALIAS).
  * logits may be aligned to its element size only; the other arrays and the
  * workspace (gdn_beam_select_workspace_bytes) are 16-byte aligned.
  */
@@ -578,7 +582,8 @@ gdn_status gdn_beam_select(int32_t batch, int32_t beams, int32_t vocab, int64_t 
  *   parent i32 [batch/beams][beams]: 0..beams-1, repeats allowed
  *   status i32 [batch/beams] or NULL: per group GDN_OK, or GDN_ERR_INDEX when
  *          an entry is out of range (that group is untouched)
- * 1 <= beams <= GDN_MAX_BEAMS (GDN_ERR_SHAPE otherwise).
+ * 1 <= beams <= GDN_MAX_BEAMS; fewer than 2^24 pieces of 4 KB of a sequence's
+ * state and tail over all groups, 64 GB times beams (GDN_ERR_SHAPE otherwise).
  */
 gdn_status gdn_beam_reorder(const gdn_dims* d, int32_t beams, float* state, void* conv_tail, const int32_t* parent,
                             int32_t* status, void* stream);

@@ -127,6 +127,31 @@ def test_reorder_refusals(lib):  # noqa: F811
         assert f(None, 4, F, F, F, None, None) == 1
 
 
+def test_more_than_a_grid_holds(lib):  # noqa: F811
+    """States of more workgroups than a launch can count are refused, not cut short."""
+    lib.gdn_ssm_state_bytes.restype = C.c_size_t
+    for kw in (dict(batch=1 << 22, num_heads=1, num_groups=1, head_dim=64), dict(batch=1 << 15, num_heads=64,
+                                                                                  num_groups=1, head_dim=128)):
+        assert lib.gdn_ssm_state_bytes(C.byref(sd(state_dim=32, **kw))) == 0
+        kw["batch"] -= 1
+        assert lib.gdn_ssm_state_bytes(C.byref(sd(state_dim=32, **kw))) > 0
+    lib.gdn_ssm_beam_reorder.argtypes = [C.POINTER(SsmDims), C.c_int32] + [P] * 5
+    d = sd(batch=1 << 16, num_heads=32, num_groups=1, head_dim=64, state_dim=128)     # 64 GB and the tails
+    assert lib.gdn_ssm_beam_reorder(C.byref(d), 1, F, F, F, None, None) == 2
+    assert lib.gdn_ssm_beam_reorder(C.byref(d), 4, F, F, F + 4, None, None) == 4      # a quarter of the groups: only the pointer
+
+
+def test_scores_that_overlap(lib):  # noqa: F811
+    """out_scores may be scores itself where as many are selected as there are beams, and nothing else of it."""
+    lib.gdn_beam_select_workspace_bytes.restype = C.c_size_t
+    lib.gdn_beam_select.argtypes = ([C.c_int32] * 3 + [C.c_int64, C.c_int32, P, P, P, C.c_int32, C.c_int32]
+                                    + [P] * 4 + [C.c_size_t, P])
+    call = lambda S, o: lib.gdn_beam_select(8, 4, 1000, 1000, 1, F, F, None, 0, S, o, 0x100000, 0x200000, 0x300000,
+                                            1 << 30, None)
+    assert call(5, F) == 8 and call(3, F) == 8
+    assert call(4, F + 16) == 8 and call(4, F - 16) == 8 and call(4, F + 112) == 8
+
+
 def test_binding_refuses_host_tensors():
     import gated_deltanet_decode_amd as gdn
     with pytest.raises(ValueError, match="device tensor"):

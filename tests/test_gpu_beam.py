@@ -169,6 +169,36 @@ def test_select_is_captured_and_replayed():
         assert np.array_equal(par.cpu().numpy(), want[1]) and np.array_equal(tok.cpu().numpy(), want[2])
 
 
+def test_scores_in_place():
+    """With as many selected as there are beams the scores may be replaced where they are."""
+    import gated_deltanet_decode_amd as gdn
+    r = np.random.default_rng(31)
+    B, K, V = 6, 5, 3000
+    logits = r.standard_normal((B, K, V)).astype(np.float32)
+    scores = (-8 * r.random((B, K))).astype(np.float32)
+    want = gpu_select(logits, scores, K)
+    t, sc = torch.from_numpy(logits).cuda(), torch.from_numpy(scores).cuda()
+    par, tok = (torch.empty(B, K, dtype=torch.int32, device="cuda") for _ in range(2))
+    ws = torch.empty(gdn.beam_select_workspace_bytes(B, K, V, K), dtype=torch.uint8, device="cuda")
+    gdn.beam_select(t, sc, sc, par, tok, ws)
+    for a, b in zip(want, (sc, par, tok)):
+        assert np.array_equal(a, b.cpu().numpy())
+    with pytest.raises(RuntimeError):
+        gdn.beam_select(t, sc, sc.view(-1)[:B * 4].view(B, 4), par[:, :4].contiguous(), tok[:, :4].contiguous(), ws)
+
+
+def test_refuses_a_vocabulary_beyond_32_bits():
+    import gated_deltanet_decode_amd as gdn
+    V = (1 << 32) + 64
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 9 GB")
+    t = torch.empty(1, 1, V, dtype=torch.bfloat16, device="cuda")
+    sc, par = torch.zeros(1, 1, device="cuda"), torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    with pytest.raises((RuntimeError, ValueError)):
+        gdn.beam_select(t, sc, sc.clone(), par, par.clone(), ws)
+
+
 def test_select_refusals():
     import gated_deltanet_decode_amd as gdn
     lg = torch.zeros(2, 3, 100, device="cuda")
