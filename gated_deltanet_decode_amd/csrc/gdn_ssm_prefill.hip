@@ -30,6 +30,7 @@
 // matrix products, so that the state is as exact as one kept in fp32.  Outputs
 // that are rounded to bf16 take one fp16 number (11 bits against bf16's 8).
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn.h"
 #include "gdn_ssm.hpp"
@@ -570,10 +571,10 @@ struct Place {
     int g, h, seg, seq, len, ch0, ch1, last;
     size_t head;
 };
-__device__ __forceinline__ bool place(const ChunkArgs& a, bool report, Place& w) {
-    // workgroup -> (sequence, segment, group), head of the group: all heads that
+__device__ __forceinline__ bool place(const ChunkArgs& a, bool report, Place& w, int heads = 1, int head = 0) {
+    // workgroup -> (sequence, segment, group), heads of the group: all heads that
     // read the same fragments on one XCD (workgroups go to the eight in turn)
-    const int rep = a.H / a.G;
+    const int rep = a.H / a.G / heads;
     int set, member;
     if (a.by_xcd) {
         set = blockIdx.x / 8 / rep * 8 + blockIdx.x % 8;
@@ -585,7 +586,7 @@ __device__ __forceinline__ bool place(const ChunkArgs& a, bool report, Place& w)
     if (set >= a.B * a.segs * a.G)
         return false;
     w.g = set % a.G;
-    w.h = w.g * rep + member;
+    w.h = (w.g * rep + member) * heads + head;
     w.seg = set / a.G % a.segs;
     w.seq = set / a.G / a.segs;
     w.head = static_cast<size_t>(w.seq) * a.H + w.h;
@@ -636,6 +637,35 @@ __device__ __forceinline__ float state_max(const f16v (&S)[NT]) {
     return fmaxf(m, __shfl_xor(m, 32));
 }
 
+// Fragment f of M . G from G's; cH, cL: c per token.
+template <typename Sh, bool FINE>
+__device__ __forceinline__ void decayed_g(h8 gh, h8 gl, int f, const float* cH, const float* cL, int lane, h8& mh,
+                                          h8& ml) {
+    const int hi = lane >> 5, c = lane & 31;
+    const int it = f >= 2, ks = it ? f - 2 : f;
+    const float ci = cH[32 * it + c];
+    const float li = FINE ? cL[32 * it + c] : 0.0f;
+    float m[8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int j = 16 * ks + 8 * q + 4 * hi;
+        const float4 cj = *reinterpret_cast<const float4*>(cH + j);
+        const float4 lj = FINE ? *reinterpret_cast<const float4*>(cL + j) : float4{};
+        const float cc[4] = {cj.x, cj.y, cj.z, cj.w}, ll[4] = {lj.x, lj.y, lj.z, lj.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float arg = ci - cc[e];
+            float gv = static_cast<float>(gh[4 * q + e]);
+            if (FINE) {
+                arg += li - ll[e];
+                gv += static_cast<float>(gl[4 * q + e]);
+            }
+            m[4 * q + e] = j + e <= 32 * it + c ? gv * __builtin_amdgcn_exp2f(arg) : 0.0f;
+        }
+    }
+    parts8<FINE>(m, mh, ml);
+}
+
 // The head's left factor of a chunk, [M . G | 2^c C], into LDS: each wave builds
 // the fragments wave, wave + waves, ..., BATCH of them loaded at a time.  The
 // first batch is asked for well before it is needed (with four at a time, each
@@ -658,7 +688,7 @@ struct Left {
     // cH, cL: c per token.  The first batch is loaded.
     __device__ void build(const _Float16* sh, _Float16* L, const float* cH, const float* cL, int wave, int waves,
                           int lane) {
-        const int hi = lane >> 5, c = lane & 31;
+        const int c = lane & 31;
         for (int f0 = wave; f0 < AF; f0 += BATCH * waves) {
             if (f0 != wave)
                 load(sh, f0, waves, lane);
@@ -670,28 +700,7 @@ struct Left {
                     break;
                 h8 mh, ml;
                 if (f < Sh::GF) {
-                    const int it = f >= 2, ks = it ? f - 2 : f;
-                    const float ci = cH[32 * it + c];
-                    const float li = FINE ? cL[32 * it + c] : 0.0f;
-                    float m[8];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int j = 16 * ks + 8 * q + 4 * hi;
-                        const float4 cj = *reinterpret_cast<const float4*>(cH + j);
-                        const float4 lj = FINE ? *reinterpret_cast<const float4*>(cL + j) : float4{};
-                        const float cc[4] = {cj.x, cj.y, cj.z, cj.w}, ll[4] = {lj.x, lj.y, lj.z, lj.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float arg = ci - cc[e];
-                            float gv = static_cast<float>(fh[k][4 * q + e]);
-                            if (FINE) {
-                                arg += li - ll[e];
-                                gv += static_cast<float>(fl[k][4 * q + e]);
-                            }
-                            m[4 * q + e] = j + e <= 32 * it + c ? gv * __builtin_amdgcn_exp2f(arg) : 0.0f;
-                        }
-                    }
-                    parts8<FINE>(m, mh, ml);
+                    decayed_g<Sh, FINE>(fh[k], fl[k], f, cH, cL, lane, mh, ml);
                 } else {
                     const int row = f - Sh::GF < KS ? c : 32 + c;
                     const float e2 = __builtin_amdgcn_exp2f(cH[row] + cL[row]);
@@ -713,12 +722,11 @@ struct Left {
     }
 };
 
-// Y += C' S0^T, the state scaled by `scale` into fp16.
+// Y += C' S0^T, the state scaled by `scale` into fp16.  Ch, Cl: C's fragments.
 template <int N, bool FINE>
-__device__ __forceinline__ void state_product(f16v (&Y)[2], const f16v (&S)[N / 32], float scale, const _Float16* L,
-                                              int lane) {
-    using Sh = Shared<N, FINE>;
-    constexpr int AF = Sh::GF + Sh::CF, KS = N / 16;
+__device__ __forceinline__ void state_product(f16v (&Y)[2], const f16v (&S)[N / 32], float scale, const _Float16* Ch,
+                                              const _Float16* Cl, int lane) {
+    constexpr int KS = N / 16;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         float v[8];
@@ -729,11 +737,11 @@ __device__ __forceinline__ void state_product(f16v (&Y)[2], const f16v (&S)[N / 
         parts8<FINE>(v, bh, bl);
 #pragma unroll
         for (int it = 0; it < 2; ++it) {
-            const h8 ah = ld_frag(L, Sh::GF + it * KS + ks, lane);
+            const h8 ah = ld_frag(Ch, it * KS + ks, lane);
             Y[it] = mma(ah, bh, Y[it]);
             if (FINE) {
                 Y[it] = mma(ah, bl, Y[it]);
-                Y[it] = mma(ld_frag(L, AF + Sh::GF + it * KS + ks, lane), bh, Y[it]);
+                Y[it] = mma(ld_frag(Cl, it * KS + ks, lane), bh, Y[it]);
             }
         }
         if (ks % 4 == 3)
@@ -825,7 +833,8 @@ __device__ __forceinline__ void store_y(const f16v (&Y)[2], const float* fS, flo
 // The conv tails after the prompt, by the workgroups of its last chunk: a wave
 // its own channels, and the group's first head B's and C's.
 template <typename Act>
-__device__ void write_tails(const ChunkArgs& a, const Place& w, int col0, int N, int lane) {
+__device__ void write_tails(const ChunkArgs& a, const Place& w, int wave, int N, int lane) {
+    const int col0 = w.h * a.P + wave * 32;
     auto put = [&](int ch) {
         Act* tp = static_cast<Act*>(a.p.tail_out) + (static_cast<size_t>(w.seq) * a.C + ch) * 4;
         const Act* xs = static_cast<const Act*>(a.p.x) + static_cast<size_t>(w.seq) * a.T * a.C + ch;
@@ -839,7 +848,7 @@ __device__ void write_tails(const ChunkArgs& a, const Place& w, int col0, int N,
     if (lane < 32)
         put(col0 + lane);
     if (w.h % (a.H / a.G) == 0)
-        for (int i = threadIdx.x; i < 2 * N; i += blockDim.x)
+        for (int i = wave * 64 + lane; i < 2 * N; i += a.P * 2)
             put(a.H * a.P + (i < N ? 0 : a.G * N) + w.g * N + i % N);
 }
 
@@ -888,24 +897,78 @@ struct BRing {
     }
 };
 
+// The same fragments, loaded once by the four waves of a workgroup and passed on
+// through LDS.
+template <int N, bool FINE>
+struct BShare {
+    using Sh = Shared<N, FINE>;
+    static constexpr int NT = N / 32, PER = 2 * Sh::BF / 4;
+    static constexpr size_t kBytes = 2 * Sh::BF * 1024;
+    h8 r[PER];
+    __device__ void load(const _Float16* sh, int wave, int lane) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            r[k] = ld_frag(sh, Sh::kB + wave * PER + k, lane);
+    }
+    __device__ void store(_Float16* B, int wave, int lane) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            st_frag(B, wave * PER + k, lane, r[k]);
+    }
+    __device__ static void update(f16v (&S)[NT], float keep, const h8 (&wh)[4], const h8 (&wl)[4], const _Float16* B,
+                                  int lane) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                S[nt][v] *= keep;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            h8 h[NT], l[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                h[nt] = ld_frag(B, nt * 4 + ks, lane);
+                l[nt] = ld_frag(B, Sh::BF + nt * 4 + ks, lane);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                S[nt] = mma(h[nt], wh[ks], S[nt]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                S[nt] = mma(h[nt], wl[ks], S[nt]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                S[nt] = mma(l[nt], wh[ks], S[nt]);
+            phase();
+        }
+    }
+};
+
 // Each segment's own state from zero, the state's products in two fp16 parts, and
-// the convolved x for the output pass.  One workgroup per (sequence, segment,
-// head), one wave per 32 rows of the state; the waves share nothing.
-template <int N, typename Act, bool FINE>
+// the convolved x for the output pass.  One wave per 32 rows of the state; a
+// workgroup is one head's waves, which share nothing, or (SHARE) four waves of
+// heads of one group, which load B's fragments once for all: 230 -> 199 us at
+// 32,768 tokens of 64 heads, P = 64, N = 128, 537 MB in and out at 2.7 TB/s.  What
+// is left: the matrix products (41 us at the peak rate), conv, SiLU and the fp16
+// parts on the vector unit, and a chain of these per chunk that two waves per
+// SIMD only partly overlap.
+template <int N, typename Act, bool FINE, bool SHARE>
 __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkArgs a) {
     using Sh = Shared<N, FINE>;
     using Tl = Tile<Act>;
     constexpr int NT = N / 32;
-    extern __shared__ __align__(16) char pool[];   // [waves][tile, factors]
+    extern __shared__ __align__(16) char pool[];   // [waves][tile, factors], then B's fragments
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave_wg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hi = lane >> 5, c = lane & 31;
     const int waves = a.P / 32;
+    const int wave = SHARE ? wave_wg % waves : wave_wg;
     Place w;
-    if (!place(a, false, w))
+    if (!place(a, false, w, SHARE ? 4 / waves : 1, SHARE ? wave_wg / waves : 0))
         return;
     const int col0 = w.h * a.P + wave * 32;
-    char* mine = pool + wave * (Tl::kBytes + Q * 4);
+    char* mine = pool + wave_wg * (Tl::kBytes + Q * 4);
+    _Float16* Bs = reinterpret_cast<_Float16*>(pool + 4 * (Tl::kBytes + Q * 4));
     float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B * 2^(c_last - c)
     const float* steps = a.steps + w.head * a.nc * (3 * Q);
     const _Float16* shared0 = a.shared + (static_cast<size_t>(w.seq) * a.G + w.g) * a.nc * Sh::kHalfs;
@@ -924,7 +987,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         st_l = st[2 * Q + lane];
         st_b = reinterpret_cast<const float*>(shared0 + ch * Sh::kHalfs + Sh::kFrags * 512)[lane];
     };
-    BRing<N, FINE, true, 1> B;
+    std::conditional_t<SHARE, BShare<N, FINE>, BRing<N, FINE, true, 1>> B;
     f16v S[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -949,9 +1012,12 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         wave_sync();
         // loads and stores are counted in the order of issue, so the far ones go first and stores last: no wait for
         // a near one is a wait for them
+        if (SHARE)
+            B.load(sh, SHARE ? wave_wg : 0, lane);
         in.load(next * Q);
         load_steps(next);
-        B.load(sh, 0, lane);
+        if (!SHARE)
+            B.load(sh, 0, lane);
         phase();
 
         float xc[32];
@@ -999,7 +1065,14 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
             pin(wl[ks]);
             phase();
         }
-        B.update(S, decay * (s2 * inverse_pow2(unit)), wh, wl, sh, lane);
+        if constexpr (SHARE) {
+            __syncthreads();   // the last chunk's fragments are used
+            B.store(Bs, wave_wg, lane);
+            __syncthreads();
+            B.update(S, decay * (s2 * inverse_pow2(unit)), wh, wl, Bs, lane);
+        } else {
+            B.update(S, decay * (s2 * inverse_pow2(unit)), wh, wl, sh, lane);
+        }
         unit = s2;
         phase();
         char* to = conv + static_cast<size_t>(ch) * waves * Conv<FINE>::kBytes;
@@ -1059,36 +1132,84 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(ChunkArgs a, int quads) {
     *st = s;
 }
 
+// C's and B's fragments (the high parts) for the output pass: loaded once by the
+// waves of a workgroup and passed on through LDS, C first.
+template <int N>
+struct Common {
+    using Sh = Shared<N, false>;
+    static constexpr int NT = N / 32, kFrags = Sh::CF + Sh::BF, PER = kFrags / 4;   // PER: of a wave of four
+    h8 r[PER];
+    __device__ void load(const _Float16* sh, int f0, int step, int lane) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int f = min(f0 + k * step, kFrags - 1);
+            r[k] = ld_frag(sh, f < Sh::CF ? Sh::kC + f : Sh::kB + f - Sh::CF, lane);
+        }
+    }
+    // The first fragments are loaded; fewer than four waves take more than one turn.
+    __device__ void store(_Float16* to, const _Float16* sh, int wave, int waves, int lane) {
+        for (int f0 = wave; f0 < kFrags; f0 += PER * waves) {
+            if (f0 != wave)
+                load(sh, f0, waves, lane);
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+                st_frag(to, f0 + k * waves, lane, r[k]);
+        }
+    }
+    // S = keep S + X''^T B
+    __device__ static void update(f16v (&S)[NT], float keep, const h8 (&wh)[4], const _Float16* B, int lane) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                S[nt][v] *= keep;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                S[nt] = mma(ld_frag(B, nt * 4 + ks, lane), wh[ks], S[nt]);
+    }
+};
+
+// A wave's part of the output pass's LDS.
+constexpr size_t out_wave_bytes() { return Tile<uint16_t>::kBytes + 4 * Q * 4 + 2 * Q * 2; }
+
 // The output pass over segments of bf16 activations, from the states that enter
 // them and the convolved x.  Its own state only serves outputs that are rounded
-// to bf16: one fp16 part each, and X' and X'' formed in packed fp16.  One
-// workgroup per (sequence, segment, head), one wave per 32 rows of the state; the
-// waves share the left factor.
+// to bf16: one fp16 part each, and X' and X'' formed in packed fp16.  One wave
+// per 32 rows of the state; a workgroup is `heads` heads of one group, which share
+// C's and B's fragments, and a head's waves its M . G.  The decay of the state that
+// enters is put on the products' rows, so that C needs none of its own: 237 ->
+// 219 us at 32,768 tokens of 64 heads, P = 64, N = 128 (537 MB in and out, 2.5
+// TB/s), bound like the state pass by its chain of small phases per chunk.
 template <int N>
-__global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs a) {
+__global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs a, int heads) {
     using Act = uint16_t;
     using Sh = Shared<N, false>;
     using Tl = Tile<Act>;
     constexpr int NT = N / 32;
-    constexpr int kWaveBytes = Tl::kBytes + 4 * Q * 4 + 2 * Q * 2;
-    extern __shared__ __align__(16) char pool[];   // [waves][tile, factors], then the left factor
+    using Cs = Common<N>;
+    // [C and B][heads][M . G][waves][tile, factors]
+    extern __shared__ __align__(16) char pool[];
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave_wg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hi = lane >> 5, c = lane & 31;
-    const int waves = a.P / 32;
+    const int waves = a.P / 32, waves_wg = heads * waves;
+    const int wave = wave_wg % waves;
     Place w;
-    if (!place(a, true, w))
+    if (!place(a, true, w, heads, wave_wg / waves))
         return;
     const int col0 = w.h * a.P + wave * 32;
-    char* mine = pool + wave * kWaveBytes;
+    _Float16* common = reinterpret_cast<_Float16*>(pool);
+    _Float16* L = common + (Cs::kFrags + wave_wg / waves * Sh::GF) * 512;
+    char* mine = pool + (Cs::kFrags + heads * Sh::GF) * 1024 + wave_wg * out_wave_bytes();
     float* yt = reinterpret_cast<float*>(mine);
     float* fS = reinterpret_cast<float*>(mine + Tl::kBytes);   // 2^-s_C
     float* fK = fS + Q;                                        // D * s_F * 2^s_C
-    float* fH = fS + 2 * Q;                                    // c, high and low part
-    float* fL = fS + 3 * Q;
+    float* fH = fS + 2 * Q;                                    // c, high part
+    float* fE = fS + 3 * Q;                                    // 2^c
     _Float16* fF = reinterpret_cast<_Float16*>(fS + 4 * Q);    // d * 2^-s_B * s_F
     _Float16* fW = fF + Q;                                     // 2^(c_last - c)
-    _Float16* L = reinterpret_cast<_Float16*>(pool + waves * kWaveBytes);
     const float skip = a.p.D ? a.p.D[w.h] : 0.0f;
     const float* steps = a.steps + w.head * a.nc * (3 * Q);
     const _Float16* shared0 = a.shared + (static_cast<size_t>(w.seq) * a.G + w.g) * a.nc * Sh::kHalfs;
@@ -1111,8 +1232,14 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
             xq[ks] = ld_frag(reinterpret_cast<const _Float16*>(from), ks, lane);
         st_x = reinterpret_cast<const float*>(from + 4096)[c];
     };
-    BRing<N, false, false, 2> B;
-    Left<N, false, 12> left;
+    Cs cb;
+    constexpr int kG = 3;   // fragments of G in flight
+    h8 gf[kG];
+    auto load_g = [&](const _Float16* sh, int f0) {
+#pragma unroll
+        for (int k = 0; k < kG; ++k)
+            gf[k] = ld_frag(sh, Sh::kG + min(f0 + k * waves, Sh::GF - 1), lane);
+    };
     f16v S[NT];
     float unit = 1.0f;
     load_chunk(w.ch0);
@@ -1121,7 +1248,8 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
     for (int ch = w.ch0; ch < w.ch1; ++ch) {
         const _Float16* sh = shared0 + ch * Sh::kHalfs;
         const int next = min(ch + 1, w.ch1 - 1);
-        left.load(sh, wave, waves, lane);
+        load_g(sh, wave);
+        cb.load(sh, wave_wg, waves_wg, lane);
         const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
         const float F = st_d * st_b;
         const float sF = pow2_to<0, kMostF>(wave_max(F));
@@ -1131,7 +1259,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
         fS[lane] = st_c;
         fK[lane] = skip * sF * inverse_pow2(st_c);
         fH[lane] = st_h;
-        fL[lane] = st_l;
+        fE[lane] = __builtin_amdgcn_exp2f(st_h + st_l);
         const float decay = __builtin_amdgcn_exp2f(th + tl);
         wave_sync();
         // X', X'' in units of s_F / cs; x itself is taken up by Y below
@@ -1156,28 +1284,36 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
             pin(xh[ks]);
             pin(wh[ks]);
         }
-        left.build(sh, L, fH, fL, wave, waves, lane);
+        for (int f0 = wave; f0 < Sh::GF; f0 += kG * waves) {
+            if (f0 != wave)
+                load_g(sh, f0);
+#pragma unroll
+            for (int k = 0; k < kG; ++k)
+                if (f0 + k * waves < Sh::GF) {
+                    h8 mh, ml;
+                    decayed_g<Sh, false>(gf[k], gf[k], f0 + k * waves, fH, fH, lane, mh, ml);
+                    st_frag(L, f0 + k * waves, lane, mh);
+                }
+        }
+        cb.store(common, sh, wave_wg, waves_wg, lane);
         const float ss = pow2_to<8, kMostS>(state_max(S));   // on top of `unit`
-        phase();
-        B.load(sh, 0, lane);
-        B.load(sh, 1, lane);
-        phase();
         phase();
         __syncthreads();
         f16v Y[2] = {zero16(), zero16()};
-        state_product<N, false>(Y, S, ss, L, lane);
-        // to X's unit, and D x
+        state_product<N, false>(Y, S, ss, common, common, lane);
+        // to X's unit and the tokens' decays, and D x
         const float ratio = ux * (inverse_pow2(ss) * inverse_pow2(unit));
 #pragma unroll
         for (int it = 0; it < 2; ++it)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4 K = *reinterpret_cast<const float4*>(fK + 32 * it + 8 * q + 4 * hi);
-                const float kk[4] = {K.x, K.y, K.z, K.w};
+                const float4 E = *reinterpret_cast<const float4*>(fE + 32 * it + 8 * q + 4 * hi);
+                const float kk[4] = {K.x, K.y, K.z, K.w}, ee[4] = {E.x, E.y, E.z, E.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float y = __builtin_fmaf(static_cast<float>(xq[2 * it + q / 2][4 * (q % 2) + i]), kk[i],
-                                             Y[it][4 * q + i] * ratio);
+                                             Y[it][4 * q + i] * (ratio * ee[i]));
                     pin(y);
                     Y[it][4 * q + i] = y;
                 }
@@ -1190,17 +1326,17 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
         const size_t y0 = (static_cast<size_t>(w.seq) * a.T + ch * Q) * yrow + col0;
         phase();
         if (ch + 1 < w.ch1) {
-            B.update(S, decay * (ux * inverse_pow2(unit)), wh, wh, sh, lane);
+            Cs::update(S, decay * (ux * inverse_pow2(unit)), wh, common + Sh::CF * 512, lane);
             unit = ux;
         }
         phase();
         store_y<Act>(Y, fS, inverse_pow2(ux), yt, static_cast<Act*>(a.p.y) + y0,
                      a.p.z ? static_cast<const Act*>(a.p.z) + y0 : nullptr, static_cast<int>(yrow), w.len - ch * Q, lane);
-        __syncthreads();   // the left factor is rewritten by the next chunk
+        __syncthreads();   // what the waves share is rewritten by the next chunk
         wave_sync();       // and so are tile and factors
     }
     if (w.ch1 == w.last)
-        write_tails<Act>(a, w, col0, N, lane);
+        write_tails<Act>(a, w, wave, N, lane);
 }
 
 // The output pass that also carries the state (one segment), or takes the state
@@ -1356,7 +1492,8 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         phase();
         __syncthreads();
         const bool update = !SPLIT || ch + 1 < w.ch1;
-        state_product<N, FINE>(Y, S, u * inverse_pow2(unit), L, lane);
+        constexpr int GF = Sh::GF, AF = Sh::GF + Sh::CF;
+        state_product<N, FINE>(Y, S, u * inverse_pow2(unit), L + GF * 512, L + (AF + GF) * 512, lane);
         chunk_product<N, FINE>(Y, xh, xl, L, lane);
         if (update)
             B.load(sh, 0, lane);
@@ -1375,7 +1512,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     if constexpr (!SPLIT)
         store_state(S, inverse_pow2(unit), state_row);
     if (w.ch1 == w.last)
-        write_tails<Act>(a, w, col0, N, lane);
+        write_tails<Act>(a, w, wave, N, lane);
 }
 
 // ------------------------------------------------------------ host
@@ -1487,7 +1624,21 @@ static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const in
     const size_t lds_chunk = waves * (kTile + 6 * Q * 4) + kLeft;
     if (a.segs == 1)
         return launch_lds(ssm_chunk_kernel<N, Act, FINE, false>, grid, block, lds_chunk, s, a);
-    if ((e = launch_lds(ssm_state_kernel<N, Act, FINE>, grid, block, waves * (kTile + Q * 4), s, a)) != hipSuccess)
+    // Heads of a workgroup, which share what does not depend on the head.  It pays
+    // where the chip is more than half full, at two waves per SIMD or one (64 heads:
+    // 32,768 tokens 521 -> 478 us, 4 x 4,096 310 -> 271; N = 256, 1,024 waves: 124 ->
+    // 105); below that barriers and coarser workgroups cost more than the loads that
+    // they save (512 tokens 43.8 -> 46.5 us), except for heads of 128 rows, whose
+    // workgroups stay as they are.
+    const int rep = g.H / g.G;
+    const bool share = waves == 4 || wgs * waves > (N > 128 ? 512 : 1024);
+    const int heads = !share ? 1 : rep % (4 / waves) == 0 ? 4 / waves : waves == 1 && rep % 2 == 0 ? 2 : 1;
+    if (share && heads * waves == 4)
+        e = launch_lds(ssm_state_kernel<N, Act, FINE, true>, dim3(static_cast<unsigned>(wgs / heads)), dim3(256),
+                       4 * (kTile + Q * 4) + BShare<N, FINE>::kBytes, s, a);
+    else
+        e = launch_lds(ssm_state_kernel<N, Act, FINE, false>, grid, block, waves * (kTile + Q * 4), s, a);
+    if (e != hipSuccess)
         return e;
     const int quads = g.P * N / 4;
     const int64_t threads = static_cast<int64_t>(g.B) * g.H * quads;
@@ -1497,7 +1648,9 @@ static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const in
     if constexpr (FINE)
         return launch_lds(ssm_chunk_kernel<N, Act, true, true>, grid, block, lds_chunk, s, a);
     else
-        return launch_lds(ssm_out_kernel<N>, grid, block, waves * (kTile + 4 * Q * 4 + 2 * Q * 2) + kLeft, s, a);
+        return launch_lds(ssm_out_kernel<N>, dim3(static_cast<unsigned>(wgs / heads)), dim3(64 * heads * waves),
+                          heads * waves * out_wave_bytes() + (Common<N>::kFrags + heads * Shared<N, false>::GF) * 1024,
+                          s, a, heads);
 }
 
 hipError_t launch_ssm_chunked(const SsmGeo& g, const SsmArgs& p, int T, const int32_t* lengths, int32_t* status,

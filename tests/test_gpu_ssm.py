@@ -142,6 +142,16 @@ def test_prefill_many_chunks(bf16):
     m.check()
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("H,G,P,N", [(66, 33, 32, 32), (33, 1, 64, 64), (65, 1, 32, 32), (24, 2, 64, 256), (68, 1, 32, 64)])
+def test_prefill_of_segments_that_fill_the_chip(H, G, P, N, bf16):
+    """Long prompts with one, two and four heads to a workgroup."""
+    m = Layer(sr.make(33, 2, 2100, H, G, P, N, bf16))
+    lengths = np.array([2100, 1801], np.int32)
+    m.prefill(lengths=torch.from_numpy(lengths).cuda())
+    m.check(lengths)
+
+
 @pytest.mark.parametrize("name,H,G,P,N,bf16", LAYERS, ids=IDS)
 def test_prefill_then_tokens(name, H, G, P, N, bf16):
     """A prompt, then decode: both continue from the same state and tail as the reference's one run."""
