@@ -1519,10 +1519,10 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
 
 // Segments per sequence: as many as fill the chip once, which is two waves per
 // SIMD, or one where a wave needs more than 256 registers (N = 256, fp32).  One
-// 64-head prompt of 32,768 tokens: 540 us at 2,048 waves, 595 at 3,000, 605 at
-// 4,096; N = 256 (32 heads, 4,096 tokens) 106 us at 1,024 and 132 at 2,048.
+// 64-head prompt of 32,768 tokens: 476 us at 2,048 waves, 502 at 3,072, 489 at
+// 4,096; N = 256 (32 heads, 4,096 tokens) 100 us at 1,024 and 129 at 2,048.
 // Prompts of given lengths end at different times and take twice as many (eight
-// of up to 2,048 tokens: 362 against 390 us).  A segment has at least two chunks,
+// of up to 2,048 tokens: 326 against 347 us).  A segment has at least two chunks,
 // in fp32 one (64 heads, 512 tokens: 57 us with four, 45 with two, 49 with one;
 // fp32, 32 heads, 256 tokens: 57, 52 and 41 us).
 static void segments(const SsmGeo& g, int T, bool ragged, int& segs, int& per) {
