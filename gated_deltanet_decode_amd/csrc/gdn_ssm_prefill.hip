@@ -666,14 +666,15 @@ __device__ __forceinline__ void decayed_g(h8 gh, h8 gl, int f, const float* cH, 
     parts8<FINE>(m, mh, ml);
 }
 
-// The head's left factor of a chunk, [M . G | 2^c C], into LDS: each wave builds
+// The head's left factors of a chunk, [M . G | C] or with FOLD [M . G | 2^c C],
+// into LDS: each wave builds
 // the fragments wave, wave + waves, ..., BATCH of them loaded at a time.  The
 // first batch is asked for well before it is needed (with four at a time, each
 // waited for, the left factor took 94 of the output pass's 290 us).
-template <int N, bool FINE, int BATCH>
+template <int N, bool FINE, int BATCH, bool FOLD>
 struct Left {
     using Sh = Shared<N, FINE>;
-    static constexpr int AF = Sh::GF + Sh::CF, KS = N / 16;
+    static constexpr int AF = Sh::GF + Sh::CF;
     h8 fh[BATCH], fl[BATCH];
 
     __device__ void load(const _Float16* sh, int f0, int waves, int lane) {
@@ -685,10 +686,9 @@ struct Left {
                 fl[k] = ld_frag(sh, f < Sh::GF ? Sh::kGl + f : Sh::kCl + f - Sh::GF, lane);
         }
     }
-    // cH, cL: c per token.  The first batch is loaded.
-    __device__ void build(const _Float16* sh, _Float16* L, const float* cH, const float* cL, int wave, int waves,
-                          int lane) {
-        const int c = lane & 31;
+    // cH, cL: c per token, cE: 2^c.  The first batch is loaded.
+    __device__ void build(const _Float16* sh, _Float16* L, const float* cH, const float* cL, const float* cE, int wave,
+                          int waves, int lane) {
         for (int f0 = wave; f0 < AF; f0 += BATCH * waves) {
             if (f0 != wave)
                 load(sh, f0, waves, lane);
@@ -701,9 +701,9 @@ struct Left {
                 h8 mh, ml;
                 if (f < Sh::GF) {
                     decayed_g<Sh, FINE>(fh[k], fl[k], f, cH, cL, lane, mh, ml);
-                } else {
-                    const int row = f - Sh::GF < KS ? c : 32 + c;
-                    const float e2 = __builtin_amdgcn_exp2f(cH[row] + cL[row]);
+                } else if (FOLD) {
+                    const int row = f - Sh::GF < N / 16 ? lane & 31 : 32 + (lane & 31);
+                    const float e2 = cE[row];
                     if (FINE) {
                         float m[8];
 #pragma unroll
@@ -713,6 +713,9 @@ struct Left {
                     } else {
                         mh = fh[k] * static_cast<_Float16>(e2);
                     }
+                } else {
+                    mh = fh[k];
+                    ml = fl[k];
                 }
                 st_frag(L, f, lane, mh);
                 if (FINE)
@@ -1339,17 +1342,24 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
         write_tails<Act>(a, w, wave, N, lane);
 }
 
+// A wave's part of its LDS, less the left factor.
+template <typename Act>
+constexpr size_t chunk_wave_bytes() { return Tile<Act>::kBytes + 7 * Q * 4; }
+
 // The output pass that also carries the state (one segment), or takes the state
 // and the convolved x of segments in fp32.  One workgroup per (sequence, segment,
 // head), one wave per 32 rows of the state.  With every operand of a row in one
-// scale, a chunk's outputs are a single product over 64 + N terms,
-// Y = [M . G | 2^c C] [X'; S0^T]; the waves share its left factor.
+// scale, a chunk's outputs are formed in one unit; the waves share the left factors.
 template <int N, typename Act, bool FINE, bool SPLIT>
 __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel(ChunkArgs a) {
     using Sh = Shared<N, FINE>;
     using Tl = Tile<Act>;
     constexpr int NT = N / 32;
-    constexpr int kWaveBytes = Tl::kBytes + 6 * Q * 4;
+    // The decay of the state that enters goes to the products' rows (x waits for D x
+    // until then: 16 x 1,024 tokens of 64 heads, N = 128: 218 -> 205 us, fp32 208 ->
+    // 192); at N = 256 there are no registers for x, and it goes to C (16 x 500 tokens
+    // of 32 heads, P = 128: 216 against 227 us, fp32 303 against 342).
+    constexpr bool FOLD = N > 128;
     static_assert(FINE || !SPLIT, "bf16 segments are ssm_out_kernel's");
     extern __shared__ __align__(16) char pool[];   // [waves][tile, factors], then the left factor
     const int lane = threadIdx.x & 63;
@@ -1360,7 +1370,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     if (!place(a, true, w))
         return;
     const int col0 = w.h * a.P + wave * 32;
-    char* mine = pool + wave * kWaveBytes;
+    char* mine = pool + wave * chunk_wave_bytes<Act>();
     float* yt = reinterpret_cast<float*>(mine);
     float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B * s_F
     float* fW = fF + Q;                                        // the same times 2^(c_last - c)
@@ -1368,7 +1378,8 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     float* fK = fF + 3 * Q;                                    // D * s_F * 2^s_C
     float* fH = fF + 4 * Q;                                    // c, high and low part
     float* fL = fF + 5 * Q;
-    _Float16* L = reinterpret_cast<_Float16*>(pool + waves * kWaveBytes);
+    float* fE = fF + 6 * Q;                                    // 2^c
+    _Float16* L = reinterpret_cast<_Float16*>(pool + waves * chunk_wave_bytes<Act>());
     const float skip = a.p.D ? a.p.D[w.h] : 0.0f;
     const float* steps = a.steps + w.head * a.nc * (3 * Q);
     const _Float16* shared0 = a.shared + (static_cast<size_t>(w.seq) * a.G + w.g) * a.nc * Sh::kHalfs;
@@ -1391,7 +1402,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         st_c = sc[Q + lane];
     };
     BRing<N, FINE, true, 1> B;
-    Left<N, FINE, (FINE ? 4 : 8)> left;
+    Left<N, FINE, (FINE ? 4 : 8), FOLD> left;
     f16v S[NT];
     float unit = 1.0f;
     const size_t row_off = static_cast<size_t>(wave * 32 + c) * N + 4 * hi;
@@ -1418,6 +1429,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         fK[lane] = skip * sF * inverse_pow2(st_c);
         fH[lane] = st_h;
         fL[lane] = st_l;
+        fE[lane] = __builtin_amdgcn_exp2f(st_h + st_l);
         const float decay = __builtin_amdgcn_exp2f(th + tl);
         wave_sync();
         if constexpr (!SPLIT)
@@ -1456,9 +1468,9 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
                                unit * 0x1p40f);
         const float u = sx * sF;   // the unit of X', X'', Y and the next state
 
-        // X'' and X' as fragments; Y starts from D x
-        h8 wh[4], wl[4], xh[4], xl[4];
-        f16v Y[2];
+        // X'' and X' as fragments; x itself for D x (for bf16 outputs in fp16), or Y from D x on
+        h8 wh[4], wl[4], xh[4], xl[4], xq[4];
+        f16v Y[2] = {zero16(), zero16()};
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             float xw[8], xp[8];
@@ -1466,17 +1478,34 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
             for (int q = 0; q < 2; ++q) {
                 const float4 F = *reinterpret_cast<const float4*>(fF + 16 * ks + 8 * q + 4 * hi);
                 const float4 W = *reinterpret_cast<const float4*>(fW + 16 * ks + 8 * q + 4 * hi);
-                const float4 K = *reinterpret_cast<const float4*>(fK + 16 * ks + 8 * q + 4 * hi);
-                const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w}, kk[4] = {K.x, K.y, K.z, K.w};
+                const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = xc[8 * ks + 4 * q + i] * sx;
                     xw[4 * q + i] = x * ww[i];
                     xp[4 * q + i] = x * ff[i];
-                    float y = x * kk[i];
-                    pin(y);
-                    Y[ks / 2][8 * (ks % 2) + 4 * q + i] = y;
+                    xc[8 * ks + 4 * q + i] = x;
                 }
+            }
+            if constexpr (FOLD) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float4 K = *reinterpret_cast<const float4*>(fK + 16 * ks + 8 * q + 4 * hi);
+                    const float kk[4] = {K.x, K.y, K.z, K.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float y = xc[8 * ks + 4 * q + i] * kk[i];
+                        pin(y);
+                        Y[ks / 2][8 * (ks % 2) + 4 * q + i] = y;
+                    }
+                }
+            } else if constexpr (!FINE) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = xc[8 * ks + e];
+                xq[ks] = half8(v);
+                pin(xq[ks]);
             }
             split8(xw, wh[ks], wl[ks]);
             parts8<FINE>(xp, xh[ks], xl[ks]);
@@ -1488,12 +1517,29 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
             phase();
         }
         left.load(sh, wave, waves, lane);
-        left.build(sh, L, fH, fL, wave, waves, lane);
+        left.build(sh, L, fH, fL, fE, wave, waves, lane);
         phase();
         __syncthreads();
         const bool update = !SPLIT || ch + 1 < w.ch1;
         constexpr int GF = Sh::GF, AF = Sh::GF + Sh::CF;
         state_product<N, FINE>(Y, S, u * inverse_pow2(unit), L + GF * 512, L + (AF + GF) * 512, lane);
+        // the tokens' decays, and D x
+#pragma unroll
+        for (int it = 0; !FOLD && it < 2; ++it)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 K = *reinterpret_cast<const float4*>(fK + 32 * it + 8 * q + 4 * hi);
+                const float4 E = *reinterpret_cast<const float4*>(fE + 32 * it + 8 * q + 4 * hi);
+                const float kk[4] = {K.x, K.y, K.z, K.w}, ee[4] = {E.x, E.y, E.z, E.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = FINE ? xc[16 * it + 4 * q + i]
+                                         : static_cast<float>(xq[2 * it + q / 2][4 * (q % 2) + i]);
+                    float y = __builtin_fmaf(x, kk[i], Y[it][4 * q + i] * ee[i]);
+                    pin(y);
+                    Y[it][4 * q + i] = y;
+                }
+            }
         chunk_product<N, FINE>(Y, xh, xl, L, lane);
         if (update)
             B.load(sh, 0, lane);
@@ -1621,7 +1667,7 @@ static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const in
     const dim3 grid(static_cast<unsigned>(wgs)), block(64 * waves);
     constexpr int kTile = Tile<Act>::kBytes;
     constexpr int kLeft = (FINE ? 2 : 1) * (Shared<N, FINE>::GF + Shared<N, FINE>::CF) * 1024;
-    const size_t lds_chunk = waves * (kTile + 6 * Q * 4) + kLeft;
+    const size_t lds_chunk = waves * chunk_wave_bytes<Act>() + kLeft;
     if (a.segs == 1)
         return launch_lds(ssm_chunk_kernel<N, Act, FINE, false>, grid, block, lds_chunk, s, a);
     // Heads of a workgroup, which share what does not depend on the head.  It pays
