@@ -1610,22 +1610,22 @@ static size_t carve(const SsmGeo& g, int T, bool ragged, char* base, ChunkArgs* 
     auto take = [&](size_t bytes) {
         const size_t at = n;
         n += up256(bytes);
-        return base + at;
+        return at;
     };
-    char* shared = take(static_cast<size_t>(g.B) * g.G * nc * shared_halfs(g) * sizeof(_Float16));
-    char* steps = take(BH * nc * (3 * Q) * sizeof(float));
-    char *state = nullptr, *decay = nullptr, *conv = nullptr;
+    const size_t shared = take(static_cast<size_t>(g.B) * g.G * nc * shared_halfs(g) * sizeof(_Float16));
+    const size_t steps = take(BH * nc * (3 * Q) * sizeof(float));
+    size_t state = 0, decay = 0, conv = 0;
     if (segs > 1) {
         state = take(BH * segs * g.P * g.N * sizeof(float));
         decay = take(BH * segs * sizeof(float));
         conv = take(BH * nc * (g.P / 32) * (g.bf16 ? Conv<false>::kBytes : Conv<true>::kBytes));
     }
     if (a) {
-        a->shared = reinterpret_cast<_Float16*>(shared);
-        a->steps = reinterpret_cast<float*>(steps);
-        a->seg_state = reinterpret_cast<float*>(state);
-        a->seg_decay = reinterpret_cast<float*>(decay);
-        a->conv = conv;
+        a->shared = reinterpret_cast<_Float16*>(base + shared);
+        a->steps = reinterpret_cast<float*>(base + steps);
+        a->seg_state = reinterpret_cast<float*>(base + state);   // read with segments only, like the next two
+        a->seg_decay = reinterpret_cast<float*>(base + decay);
+        a->conv = base + conv;
         a->nc = static_cast<int>(nc);
         a->segs = segs;
         a->chunks_per_seg = per;
