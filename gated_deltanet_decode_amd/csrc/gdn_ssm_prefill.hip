@@ -1475,6 +1475,8 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
                                unit * 0x1p40f);
         const float u = sx * sF;   // the unit of X', X'', Y and the next state
 
+        // on their way while X' is formed (16 x 500 tokens of 32 heads, N = 256: 216 -> 208 us, fp32 303 -> 287)
+        left.load(sh, wave, waves, lane);
         // X'' and X' as fragments; x itself for D x (for bf16 outputs in fp16), or Y from D x on
         h8 wh[4], wl[4], xh[4], xl[4], xq[4];
         f16v Y[2] = {zero16(), zero16()};
@@ -1523,7 +1525,6 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
                 pin(xl[ks]);
             phase();
         }
-        left.load(sh, wave, waves, lane);
         left.build(sh, L, fH, fL, fE, wave, waves, lane);
         phase();
         __syncthreads();
