@@ -192,32 +192,51 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, a), __builtin_bit_cast(b2, b), c, false);
 }
 
-// SiLU(conv) of run r of this lane's channel: tokens 8 r + 4 hi .. + 3 of the tile.
+// SiLU(conv) of run r of this lane's channel: tokens 8 r + 4 hi .. + 3 of the tile,
+// as what is read for it and each of the four.
 // bf16: the transposing LDS read gives a lane four tokens of its channel; the
 // lane supplies the address of four channels of one token.
-__device__ __forceinline__ void conv_run(const uint16_t* tile, const Taps<uint16_t>& k, int r, int lane, float (&out)[4]) {
-    typedef __attribute__((address_space(3))) s4* lds4;
-    const int row = (lane >> 5) * 4 + ((lane & 15) >> 2);
-    const uint16_t* p = tile + row * Tile<uint16_t>::kPitch + (lane & 16) + (lane & 3) * 4 + 8 * r * Tile<uint16_t>::kPitch;
-    const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p));
-    const uint2 b = __builtin_bit_cast(
-        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * Tile<uint16_t>::kPitch)));
-    out[0] = silu(dot2(b.x, k.w3z, dot2(a.y, k.w12, dot2(a.x, k.z0, k.bias))));
-    out[1] = silu(dot2(b.x, k.w23, dot2(a.y, k.w01, k.bias)));
-    out[2] = silu(dot2(b.y, k.w3z, dot2(b.x, k.w12, dot2(a.y, k.z0, k.bias))));
-    out[3] = silu(dot2(b.y, k.w23, dot2(b.x, k.w01, k.bias)));
-}
-__device__ __forceinline__ void conv_run(const float* tile, const Taps<float>& k, int r, int lane, float (&out)[4]) {
-    const float* p = tile + ((lane >> 5) * 4 + 8 * r + 1) * Tile<float>::kPitch + (lane & 31);
-    float v[7];
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-        v[e] = p[e * Tile<float>::kPitch];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float win[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
-        out[i] = conv_bias_silu(k.w, win, k.bias);
+template <typename Act>
+struct Run;
+template <>
+struct Run<uint16_t> {
+    uint2 a, b;
+    __device__ void load(const uint16_t* tile, int r, int lane) {
+        typedef __attribute__((address_space(3))) s4* lds4;
+        constexpr int kPitch = Tile<uint16_t>::kPitch;
+        const int row = (lane >> 5) * 4 + ((lane & 15) >> 2);
+        const uint16_t* p = tile + row * kPitch + (lane & 16) + (lane & 3) * 4 + 8 * r * kPitch;
+        a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p));
+        b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * kPitch)));
     }
+    __device__ float out(const Taps<uint16_t>& k, int i) const {
+        return silu(i == 0   ? dot2(b.x, k.w3z, dot2(a.y, k.w12, dot2(a.x, k.z0, k.bias)))
+                    : i == 1 ? dot2(b.x, k.w23, dot2(a.y, k.w01, k.bias))
+                    : i == 2 ? dot2(b.y, k.w3z, dot2(b.x, k.w12, dot2(a.y, k.z0, k.bias)))
+                             : dot2(b.y, k.w23, dot2(b.x, k.w01, k.bias)));
+    }
+};
+template <>
+struct Run<float> {
+    float v[7];
+    __device__ void load(const float* tile, int r, int lane) {
+        const float* p = tile + ((lane >> 5) * 4 + 8 * r + 1) * Tile<float>::kPitch + (lane & 31);
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            v[e] = p[e * Tile<float>::kPitch];
+    }
+    __device__ float out(const Taps<float>& k, int i) const {
+        const float win[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+        return conv_bias_silu(k.w, win, k.bias);
+    }
+};
+template <typename Act>
+__device__ __forceinline__ void conv_run(const Act* tile, const Taps<Act>& k, int r, int lane, float (&out)[4]) {
+    Run<Act> run;
+    run.load(tile, r, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = run.out(k, i);
 }
 
 // A wave's path of x from memory through its tile, a chunk at a time.
@@ -920,8 +939,10 @@ struct BShare {
         for (int k = 0; k < PER; ++k)
             st_frag(B, wave * PER + k, lane, r[k]);
     }
+    // beside(ks, m): vector work that fills the time of k-step ks's m-th product (-1: before the first).
+    template <typename F>
     __device__ static void update(f16v (&S)[NT], float keep, const h8 (&wh)[4], const h8 (&wl)[4], const _Float16* B,
-                                  int lane) {
+                                  int lane, F&& beside) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -931,19 +952,25 @@ struct BShare {
         for (int ks = 0; ks < 4; ++ks) {
             h8 h[NT], l[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NT; ++nt)
                 h[nt] = ld_frag(B, nt * 4 + ks, lane);
+            beside(ks, -1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                S[nt] = mma(h[nt], wh[ks], S[nt]);
                 l[nt] = ld_frag(B, Sh::BF + nt * 4 + ks, lane);
+                beside(ks, nt);
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                S[nt] = mma(h[nt], wh[ks], S[nt]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
                 S[nt] = mma(h[nt], wl[ks], S[nt]);
+                beside(ks, NT + nt);
+            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
                 S[nt] = mma(l[nt], wh[ks], S[nt]);
+                beside(ks, 2 * NT + nt);
+            }
             phase();
         }
     }
@@ -952,11 +979,12 @@ struct BShare {
 // Each segment's own state from zero, the state's products in two fp16 parts, and
 // the convolved x for the output pass.  One wave per 32 rows of the state; a
 // workgroup is one head's waves, which share nothing, or (SHARE) four waves of
-// heads of one group, which load B's fragments once for all: 230 -> 199 us at
-// 32,768 tokens of 64 heads, P = 64, N = 128, 537 MB in and out at 2.7 TB/s.  What
-// is left: the matrix products (41 us at the peak rate), conv, SiLU and the fp16
-// parts on the vector unit, and a chain of these per chunk that two waves per
-// SIMD only partly overlap.
+// heads of one group, which load B's fragments once for all (230 -> 199 us at
+// 32,768 tokens of 64 heads, P = 64, N = 128) and convolve the next chunk between
+// the products of this one (184 us, 537 MB in and out at 2.9 TB/s).  What is left:
+// the matrix products (41 us at the peak rate), and on the vector unit conv, SiLU
+// and the fp16 parts, 590 instructions per chunk and wave (70 us).  The last chunk
+// has a copy of its own: with a branch for it the loop spills 104 registers.
 template <int N, typename Act, bool FINE, bool SHARE>
 __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkArgs a) {
     using Sh = Shared<N, FINE>;
@@ -999,36 +1027,10 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         S[nt] = zero16();
     float unit = 1.0f;   // S holds the state times this
     double seg_sum = 0.0;
-    in.load(w.ch0 * Q);
-    load_steps(w.ch0);
-    in.begin(static_cast<const Act*>(a.p.tail_in) + (static_cast<size_t>(w.seq) * a.C + col0) * 4, w.ch0 * Q);
-
-    for (int ch = w.ch0; ch < w.ch1; ++ch) {
-        const _Float16* sh = shared0 + ch * Sh::kHalfs;
-        const int next = min(ch + 1, w.ch1 - 1);
-        in.store();
-        const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
-        seg_sum += static_cast<double>(th) + static_cast<double>(tl);
-        // X'' = x F, F = d 2^-s_B 2^(c_last - c): x and F are scaled each for itself, so X'' is where x's scale puts it
-        const float F = st_d * st_b * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
-        const float sF = pow2_to<0, kMostF>(wave_max(F));
-        fF[lane] = F * sF;
-        const float decay = __builtin_amdgcn_exp2f(th + tl);
-        wave_sync();
-        // loads and stores are counted in the order of issue, so the far ones go first and stores last: no wait for
-        // a near one is a wait for them
-        if (SHARE)
-            B.load(sh, SHARE ? wave_wg : 0, lane);
-        in.load(next * Q);
-        load_steps(next);
-        if (!SHARE)
-            B.load(sh, 0, lane);
-        phase();
-
-        float xc[32];
-        float mx = 0.0f;
+    float xc[32], mx = 0.0f;   // the chunk's convolved x and its largest magnitude
+    auto conv_runs = [&](int r0, int r1) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
+        for (int r = r0; r < r1; ++r) {
             float v[4];
             conv_run(in.tile, taps, r, lane, v);
 #pragma unroll
@@ -1038,24 +1040,56 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
                 pin(xc[4 * r + i]);
             }
             pin(mx);
-            if (r % 2)
-                phase();
         }
-        in.save(Q);
+    };
+    in.load(w.ch0 * Q);
+    load_steps(w.ch0);
+    in.begin(static_cast<const Act*>(a.p.tail_in) + (static_cast<size_t>(w.seq) * a.C + col0) * 4, w.ch0 * Q);
+    in.store();
+    wave_sync();
+    in.load(min(w.ch0 + 1, w.ch1 - 1) * Q);
+    B.load(shared0 + w.ch0 * Sh::kHalfs, SHARE ? wave_wg : 0, lane);
+    phase();
+#pragma unroll
+    for (int r = 0; r < 8; r += 2) {
+        conv_runs(r, r + 2);
+        phase();
+    }
+
+    const auto step = [&](int ch, auto last) {
+        constexpr bool more = !decltype(last)::value;   // a chunk follows
+        const _Float16* sh = shared0 + ch * Sh::kHalfs;
+        const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
+        seg_sum += static_cast<double>(th) + static_cast<double>(tl);
+        // X'' = x F, F = d 2^-s_B 2^(c_last - c): x and F are scaled each for itself, so X'' is where x's scale puts it
+        const float F = st_d * st_b * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
+        const float sF = pow2_to<0, kMostF>(wave_max(F));
+        fF[lane] = F * sF;
+        const float decay = __builtin_amdgcn_exp2f(th + tl);
+        if (more)
+            in.save(Q);
+        wave_sync();
+        if (more)
+            load_steps(ch + 1);
         mx = fmaxf(mx, __shfl_xor(mx, 32));
 
-        h8 wh[4], wl[4], xq[4];
+        h8 wh[4], wl[4];
         const float sx = fminf(pow2_to<8, kMostX>(mx), unit * 0x1p40f);
         const float s2 = sx * sF;
+        char* to = conv + static_cast<size_t>(ch) * waves * Conv<FINE>::kBytes;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             float v[8], u[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 u[e] = xc[8 * ks + e] * sx;
-            if (!FINE) {
-                xq[ks] = half8(u);
-                pin(xq[ks]);
+            if constexpr (FINE) {
+#pragma unroll
+                for (int r = 2 * ks; r < 2 * ks + 2; ++r)
+                    reinterpret_cast<float4*>(to)[r * 64 + lane] =
+                        make_float4(xc[4 * r], xc[4 * r + 1], xc[4 * r + 2], xc[4 * r + 3]);
+            } else {
+                st_frag(reinterpret_cast<_Float16*>(to), ks, lane, half8(u));
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -1070,31 +1104,63 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
             pin(wl[ks]);
             phase();
         }
+        if (!FINE && lane < 32)
+            reinterpret_cast<float*>(to + 4096)[lane] = inverse_pow2(sx);
+        const float keep = decay * (s2 * inverse_pow2(unit));
+        unit = s2;
+        // the next chunk's rows into the tile; its conv runs beside the products of this one
+        if (more)
+            in.store();
+        mx = 0.0f;
+        Run<Act> run[2];
+        const auto beside = [&](int ks, int m) {   // two runs' eight values over 3 NT products
+            if (!more)
+                return;
+            if (m < 0) {
+                run[0].load(in.tile, 2 * ks, lane);
+                run[1].load(in.tile, 2 * ks + 1, lane);
+                return;
+            }
+#pragma unroll
+            for (int j = 8 * m / (3 * NT); j < 8 * (m + 1) / (3 * NT); ++j) {
+                const int e = 8 * ks + j;
+                xc[e] = run[j / 4].out(taps, j % 4);
+                mx = fmaxf(mx, fabsf(xc[e]));
+                pin(xc[e]);
+                pin(mx);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
         if constexpr (SHARE) {
             __syncthreads();   // the last chunk's fragments are used
             B.store(Bs, wave_wg, lane);
             __syncthreads();
-            B.update(S, decay * (s2 * inverse_pow2(unit)), wh, wl, Bs, lane);
-        } else {
-            B.update(S, decay * (s2 * inverse_pow2(unit)), wh, wl, sh, lane);
+            if (more)
+                B.load(sh + Sh::kHalfs, wave_wg, lane);
         }
-        unit = s2;
+        wave_sync();
+        if (more)
+            in.load(min(ch + 2, w.ch1 - 1) * Q);
         phase();
-        char* to = conv + static_cast<size_t>(ch) * waves * Conv<FINE>::kBytes;
-        if constexpr (FINE) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                reinterpret_cast<float4*>(to)[r * 64 + lane] =
-                    make_float4(xc[4 * r], xc[4 * r + 1], xc[4 * r + 2], xc[4 * r + 3]);
+        if constexpr (SHARE) {
+            B.update(S, keep, wh, wl, Bs, lane, beside);
         } else {
+            B.update(S, keep, wh, wl, sh, lane);
+            if (more) {
+                B.load(sh + Sh::kHalfs, 0, lane);
+                phase();
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                st_frag(reinterpret_cast<_Float16*>(to), ks, lane, xq[ks]);
-            if (lane < 32)
-                reinterpret_cast<float*>(to + 4096)[lane] = inverse_pow2(sx);
+                for (int r = 0; r < 8; r += 2) {
+                    conv_runs(r, r + 2);
+                    phase();
+                }
+            }
         }
-        wave_sync();   // tile and factors are rewritten by the next chunk
-    }
+        phase();
+    };
+    for (int ch = w.ch0; ch + 1 < w.ch1; ++ch)
+        step(ch, std::false_type{});
+    step(w.ch1 - 1, std::true_type{});
     store_state(S, inverse_pow2(unit),
                 a.seg_state + (w.head * a.segs + w.seg) * a.P * N + static_cast<size_t>(wave * 32 + c) * N + 4 * hi);
     if (wave == 0 && lane == 0)
