@@ -688,10 +688,8 @@ __device__ __forceinline__ void decayed_g(h8 gh, h8 gl, int f, const float* cH, 
 }
 
 // The head's left factors of a chunk, [M . G | C] or with FOLD [M . G | 2^c C],
-// into LDS: each wave builds
-// the fragments wave, wave + waves, ..., BATCH of them loaded at a time.  The
-// first batch is asked for well before it is needed (with four at a time, each
-// waited for, the left factor took 94 of the output pass's 290 us).
+// into LDS: each wave builds the fragments wave, wave + waves, ..., BATCH of them
+// loaded at a time, the first batch well before it is needed.
 template <int N, bool FINE, int BATCH, bool FOLD>
 struct Left {
     using Sh = Shared<N, FINE>;
@@ -792,12 +790,31 @@ __device__ __forceinline__ void chunk_product(f16v (&Y)[2], const h8 (&xh)[4], c
         }
 }
 
+// A chunk's gate z, 32 tokens at a time.  Where there are registers it is asked for
+// before the state's update and ahead of the far loads (N = 256, 2 x 4,000 tokens:
+// 234 -> 217 us).
+template <typename Act>
+struct Gate {
+    using Tl = Tile<Act>;
+    static constexpr int kHalf = Tl::kPerRow / 2;
+    u4 raw[2][kHalf];
+    __device__ void load(int it, const Act* z, int pitch, int rows, int lane) {
+        const int urow = lane / Tl::kPerRow, ucol = lane % Tl::kPerRow * Tl::kUnit;
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k) {
+            const int r = min(32 * it + urow + k * Tl::kRowStep, rows - 1);
+            raw[it][k] =
+                at<const u4>(z, static_cast<uint32_t>(r * pitch + ucol) * static_cast<uint32_t>(sizeof(Act)));
+        }
+    }
+};
+
 // Y * (rows' factors fS) * back, gated, to y: 32 tokens at a time through the
 // wave's tile, 16 bytes per store.  y and z point at the chunk's first token and
-// the wave's first channel.
-template <typename Act>
+// the wave's first channel.  AHEAD: the gate is loaded already.
+template <bool AHEAD, typename Act>
 __device__ __forceinline__ void store_y(const f16v (&Y)[2], const float* fS, float back, float* tile, Act* y,
-                                        const Act* z, int pitch, int rows, int lane) {
+                                        const Act* z, const Gate<Act>& gate, int pitch, int rows, int lane) {
     using Tl = Tile<Act>;
     constexpr int kHalf = Tl::kPerRow / 2;
     constexpr uint32_t kSize = sizeof(Act);
@@ -809,14 +826,9 @@ __device__ __forceinline__ void store_y(const f16v (&Y)[2], const float* fS, flo
     };
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
-        Unit zu[kHalf], yu;
-        if (z) {
-#pragma unroll
-            for (int k = 0; k < kHalf; ++k) {
-                const int r = min(32 * it + urow + k * Tl::kRowStep, rows - 1);
-                zu[k].raw = at<const u4>(z, static_cast<uint32_t>(r * pitch + ucol) * kSize);
-            }
-        }
+        Gate<Act> own;
+        if (!AHEAD && z)
+            own.load(it, z, pitch, rows, lane);
         phase();
         wave_sync();   // what was in the tile is read
 #pragma unroll
@@ -840,10 +852,12 @@ __device__ __forceinline__ void store_y(const f16v (&Y)[2], const float* fS, flo
                 o[4 * q + 2] = v.z;
                 o[4 * q + 3] = v.w;
             }
+            Unit yu, zu;
             if (z) {
+                zu.raw = (AHEAD ? gate : own).raw[it][k];
 #pragma unroll
                 for (int e = 0; e < Tl::kUnit; ++e)
-                    o[e] *= silu(widen(zu[k].v[e]));
+                    o[e] *= silu(widen(zu.v[e]));
             }
 #pragma unroll
             for (int e = 0; e < Tl::kUnit; ++e)
@@ -876,19 +890,18 @@ __device__ void write_tails(const ChunkArgs& a, const Place& w, int wave, int N,
             put(a.H * a.P + (i < N ? 0 : a.G * N) + w.g * N + i % N);
 }
 
-// B's fragments, in slots of one k-step that are loaded ahead of their products:
-// the caller loads the first SLOTS k-steps, update() the others as slots come free.
-template <int N, bool FINE, bool EXACT, int SLOTS>
-struct BRing {
+// B's fragments, a k-step at a time: the caller loads the first, update() each
+// other one as the products before it are issued.
+template <int N, bool FINE>
+struct BSteps {
     using Sh = Shared<N, FINE>;
     static constexpr int NT = N / 32;
-    h8 h[SLOTS][NT], l[SLOTS][NT];
+    h8 h[NT], l[NT];
     __device__ void load(const _Float16* sh, int ks, int lane) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            h[ks % SLOTS][nt] = ld_frag(sh, Sh::kB + nt * 4 + ks, lane);
-            if (EXACT)
-                l[ks % SLOTS][nt] = ld_frag(sh, Sh::kBl + nt * 4 + ks, lane);
+            h[nt] = ld_frag(sh, Sh::kB + nt * 4 + ks, lane);
+            l[nt] = ld_frag(sh, Sh::kBl + nt * 4 + ks, lane);
         }
     }
     // S = keep S + X''^T B
@@ -904,17 +917,15 @@ struct BRing {
             // parts outside, tiles inside: products of one accumulator do not follow one another
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                S[nt] = mma(h[ks % SLOTS][nt], wh[ks], S[nt]);
-            if (EXACT) {
+                S[nt] = mma(h[nt], wh[ks], S[nt]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    S[nt] = mma(h[ks % SLOTS][nt], wl[ks], S[nt]);
+            for (int nt = 0; nt < NT; ++nt)
+                S[nt] = mma(h[nt], wl[ks], S[nt]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    S[nt] = mma(l[ks % SLOTS][nt], wh[ks], S[nt]);
-            }
-            if (ks + SLOTS < 4) {
-                load(sh, ks + SLOTS, lane);
+            for (int nt = 0; nt < NT; ++nt)
+                S[nt] = mma(l[nt], wh[ks], S[nt]);
+            if (ks < 3) {
+                load(sh, ks + 1, lane);
                 phase();
             }
         }
@@ -1020,7 +1031,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         st_l = st[2 * Q + lane];
         st_b = reinterpret_cast<const float*>(shared0 + ch * Sh::kHalfs + Sh::kFrags * 512)[lane];
     };
-    std::conditional_t<SHARE, BShare<N, FINE>, BRing<N, FINE, true, 1>> B;
+    std::conditional_t<SHARE, BShare<N, FINE>, BSteps<N, FINE>> B;
     f16v S[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -1392,19 +1403,25 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
                 }
             }
         phase();
-        // loads are counted in the order of issue: the near ones first, so that no wait for them is one for the far
+        // loads are counted in the order of issue: those that are waited for first go first
+        const size_t y0 = (static_cast<size_t>(w.seq) * a.T + ch * Q) * yrow + col0;
+        const Act* z = a.p.z ? static_cast<const Act*>(a.p.z) + y0 : nullptr;
+        Gate<Act> gate;
+        if (z) {
+            gate.load(0, z, static_cast<int>(yrow), w.len - ch * Q, lane);
+            gate.load(1, z, static_cast<int>(yrow), w.len - ch * Q, lane);
+        }
         load_chunk(next);
         phase();
         chunk_product<N, false>(Y, xh, xh, L, lane);
-        const size_t y0 = (static_cast<size_t>(w.seq) * a.T + ch * Q) * yrow + col0;
         phase();
         if (ch + 1 < w.ch1) {
             Cs::update(S, decay * (ux * inverse_pow2(unit)), wh, common + Sh::CF * 512, lane);
             unit = ux;
         }
         phase();
-        store_y<Act>(Y, fS, inverse_pow2(ux), yt, static_cast<Act*>(a.p.y) + y0,
-                     a.p.z ? static_cast<const Act*>(a.p.z) + y0 : nullptr, static_cast<int>(yrow), w.len - ch * Q, lane);
+        store_y<true>(Y, fS, inverse_pow2(ux), yt, static_cast<Act*>(a.p.y) + y0, z, gate, static_cast<int>(yrow),
+                      w.len - ch * Q, lane);
         __syncthreads();   // what the waves share is rewritten by the next chunk
         wave_sync();       // and so are tile and factors
     }
@@ -1474,7 +1491,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         st_b = sc[lane];
         st_c = sc[Q + lane];
     };
-    BRing<N, FINE, true, 1> B;
+    BSteps<N, FINE> B;
     Left<N, FINE, (FINE ? 4 : 8), FOLD> left;
     f16v S[NT];
     float unit = 1.0f;
@@ -1482,7 +1499,16 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     float* state_row = SPLIT ? a.seg_state + (w.head * a.segs + w.seg) * a.P * N + row_off
                              : a.p.state + w.head * a.P * N + row_off;
     load_steps(w.ch0);
-    if constexpr (!SPLIT) {
+    float4 xn[8];   // the next chunk's convolved x (with the gate's early loads fp32, 2 x 5,000 tokens: 155 -> 134 us)
+    auto load_x = [&](int ch) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            xn[r] = reinterpret_cast<const float4*>(conv + static_cast<size_t>(ch) * waves *
+                                                               Conv<FINE>::kBytes)[r * 64 + lane];
+    };
+    if constexpr (SPLIT) {
+        load_x(w.ch0);
+    } else {
         in.load(w.ch0 * Q);
         in.begin(static_cast<const Act*>(a.p.tail_in) + (static_cast<size_t>(w.seq) * a.C + col0) * 4, w.ch0 * Q);
     }
@@ -1515,9 +1541,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         for (int r = 0; r < 8; ++r) {
             float v[4];
             if constexpr (SPLIT) {
-                const float4 q = reinterpret_cast<const float4*>(
-                    conv + static_cast<size_t>(ch) * waves * Conv<FINE>::kBytes)[r * 64 + lane];
-                v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+                v[0] = xn[r].x, v[1] = xn[r].y, v[2] = xn[r].z, v[3] = xn[r].w;
             } else {
                 conv_run(in.tile, taps, r, lane, v);
             }
@@ -1531,7 +1555,9 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
             if (!SPLIT && r % 2)
                 phase();
         }
-        if constexpr (!SPLIT)
+        if constexpr (SPLIT)
+            load_x(next);
+        else
             in.save(Q);
         mx = fmaxf(mx, __shfl_xor(mx, 32));
         // one scale for x, the state that enters and so all of the row: the state, up to a thousand times X', stays
@@ -1618,14 +1644,20 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         if (update)
             B.load(sh, 0, lane);
         const size_t y0 = (static_cast<size_t>(w.seq) * a.T + ch * Q) * yrow + col0;
+        const Act* z = a.p.z ? static_cast<const Act*>(a.p.z) + y0 : nullptr;
+        Gate<Act> gate;   // ahead where there are registers for it
+        if (FINE && z) {
+            gate.load(0, z, static_cast<int>(yrow), w.len - ch * Q, lane);
+            gate.load(1, z, static_cast<int>(yrow), w.len - ch * Q, lane);
+        }
         phase();
         if (update) {
             B.update(S, decay * (u * inverse_pow2(unit)), wh, wl, sh, lane);
             unit = u;
         }
         phase();
-        store_y<Act>(Y, fS, inverse_pow2(u), yt, static_cast<Act*>(a.p.y) + y0,
-                     a.p.z ? static_cast<const Act*>(a.p.z) + y0 : nullptr, static_cast<int>(yrow), w.len - ch * Q, lane);
+        store_y<FINE>(Y, fS, inverse_pow2(u), yt, static_cast<Act*>(a.p.y) + y0, z, gate, static_cast<int>(yrow),
+                      w.len - ch * Q, lane);
         __syncthreads();   // the left factor is rewritten by the next chunk
         wave_sync();       // and so are tile and factors
     }
