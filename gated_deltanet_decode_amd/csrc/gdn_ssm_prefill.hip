@@ -1264,7 +1264,7 @@ constexpr size_t out_wave_bytes() { return Tile<uint16_t>::kBytes + 4 * Q * 4 + 
 // per 32 rows of the state; a workgroup is `heads` heads of one group, which share
 // C's and B's fragments, and a head's waves its M . G.  The decay of the state that
 // enters is put on the products' rows, so that C needs none of its own: 237 ->
-// 219 us at 32,768 tokens of 64 heads, P = 64, N = 128 (537 MB in and out, 2.5
+// 212 us at 32,768 tokens of 64 heads, P = 64, N = 128 (537 MB in and out, 2.5
 // TB/s), bound like the state pass by its chain of small phases per chunk.
 template <int N>
 __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs a, int heads) {
@@ -1439,7 +1439,7 @@ constexpr size_t chunk_wave_bytes() { return Tile<Act>::kBytes + 7 * Q * 4; }
 // scale, a chunk's outputs are formed in one unit; the waves share the left factors.
 // 16 prompts of 1,024 tokens, 64 heads, P = 64, N = 128: 206 us with prep (272 MB,
 // 1.3 TB/s), bound by its chain per chunk at two waves per SIMD; fp32, 2 x 1,003
-// tokens in segments: 31 us, one wave per SIMD.
+// tokens in segments: 28 us, one wave per SIMD.
 template <int N, typename Act, bool FINE, bool SPLIT>
 __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel(ChunkArgs a) {
     using Sh = Shared<N, FINE>;
@@ -1672,7 +1672,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
 // Segments per sequence: as many as fill the chip once, which is two waves per
 // SIMD, or one where a wave needs more than 256 registers (N = 256, fp32).  One
 // 64-head prompt of 32,768 tokens: 476 us at 2,048 waves, 502 at 3,072, 489 at
-// 4,096; N = 256 (32 heads, 4,096 tokens) 100 us at 1,024 and 129 at 2,048.
+// 4,096 (before the state pass took its conv between the products); N = 256 (32 heads, 4,096 tokens) 100 us at 1,024 and 129 at 2,048.
 // Prompts of given lengths end at different times and take twice as many (eight
 // of up to 2,048 tokens: 326 against 347 us).  A segment has at least two chunks,
 // in fp32 one (64 heads, 512 tokens: 57 us with four, 45 with two, 49 with one;
@@ -1778,7 +1778,7 @@ static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const in
         return launch_lds(ssm_chunk_kernel<N, Act, FINE, false>, grid, block, lds_chunk, s, a);
     // Heads of a workgroup, which share what does not depend on the head.  It pays
     // where the chip is more than half full, at two waves per SIMD or one (64 heads:
-    // 32,768 tokens 521 -> 478 us, 4 x 4,096 310 -> 271; N = 256, 1,024 waves: 124 ->
+    // 32,768 tokens 521 -> 478 us, 4 x 4,096 310 -> 271, when it was built; N = 256, 1,024 waves: 124 ->
     // 105); below that barriers and coarser workgroups cost more than the loads that
     // they save (512 tokens 43.8 -> 46.5 us), except for heads of 128 rows, whose
     // workgroups stay as they are.
