@@ -100,11 +100,15 @@ struct Vec<float> {
     }
 };
 
+constexpr uint32_t kLeast = 0x00800000u;   // the key after -inf's
+
 // A T (a multiple of 2^low) that at least `want` of the lanes' values reach, and
 // the largest such if more do; 0 if fewer have a value.  A lane has R values,
 // value(0) .. value(R - 1).  With all 32 bits to go through, the search ends where
 // exactly `want` reach it (scan of fp32 logits 12.0 -> 11.3 us); with fewer the
-// largest T is worth its last steps (the join 7.0 -> 7.8 us without them).
+// largest T is worth its last steps (the join 7.0 -> 7.8 us without them).  It
+// does not end below kLeast: what lies under -inf's key is no logit's, and read as a
+// float it would be a NaN, which nothing reaches.
 template <int R, typename F>
 __device__ __forceinline__ uint32_t reached_by(int want, int low, F&& value) {
     uint32_t T = 0;
@@ -117,7 +121,7 @@ __device__ __forceinline__ uint32_t reached_by(int want, int low, F&& value) {
             n += __popcll(__ballot(value(r) >= c));
         if (n >= want)
             T = c;
-        if (low == 0 && n == want)
+        if (low == 0 && n == want && T >= kLeast)
             break;
     }
     return T;
@@ -487,8 +491,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void beam_join_kernel(
             places[at] = 0;
         }
     __syncthreads();
-    // each candidate's place, counted by as many threads as there are for it
-    const int c = count;
+    // each candidate's place, counted by as many threads as there are for it (at least S candidates: a bound is
+    // reached by S of a wave's, and every beam's spans hold the S best of its logits)
+    const int c = max(count, 1);
     const int parts = c < 64 * kJoinWaves ? 64 * kJoinWaves / c : 1;
     for (int e = tid / parts; e < c; e += 64 * kJoinWaves) {
         const uint64_t val = cv[e];
