@@ -101,6 +101,7 @@ struct Vec<float> {
 };
 
 constexpr uint32_t kLeast = 0x00800000u;   // the key after -inf's
+constexpr uint32_t kMost = 0xFF7FFFFFu;    // the largest finite value's
 
 // A T (a multiple of 2^low) that at least `want` of the lanes' values reach, and
 // the largest such if more do; 0 if fewer have a value.  A lane has R values,
@@ -216,8 +217,15 @@ __device__ __forceinline__ uint32_t cut_rounds(uint2* buf, int n, int S, int low
         hi[r] = k.x;
         lo[r] = k.y;
     }
-    const uint32_t T = reached_by<R>(S, low, [&](int r) { return hi[r]; });
-    const uint32_t top = T + ((1u << low) - 1);   // the values of this step: T .. top
+    uint32_t T = reached_by<R>(S, low, [&](int r) { return hi[r]; });
+    uint32_t top = T + ((1u << low) - 1);   // the values of this step: T .. top
+    if (top == kMost) {   // two values: bf16's largest, T, and what +inf counts as
+        int inf = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            inf += __popcll(__ballot(hi[r] == kMost));
+        (inf >= S ? T : top) = inf >= S ? kMost : T;
+    }
     int above = 0, reach = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
