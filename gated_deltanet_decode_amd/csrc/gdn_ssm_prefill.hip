@@ -114,12 +114,20 @@ __device__ __forceinline__ float pow2_to(float m) {
     const int f = 254 + TO - e;
     return __uint_as_float(static_cast<uint32_t>(f < 127 + MOST ? f : 127 + MOST) << 23);
 }
-// Caps of the scales.  A row of B, C, x, X' or X'' whose largest value is below
-// 2^-38 loses relative precision to fp16's absolute 2^-24 at that scale; in
-// return no product of scales and states leaves fp32's range.
-constexpr int kMostBC = 40, kMostX = 24, kMostF = 24, kMostS = 100;
+// Caps of the scales.  A row of B, C, x or X' whose largest value is below 2^-38,
+// or of X'' below 2^-56, loses relative precision to fp16's absolute 2^-24 at that
+// scale; in return no product of scales and states leaves fp32's range.
+constexpr int kMostBC = 40, kMostX = 24, kMostF = 24, kMostW = 64, kMostS = 100;
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
-
+// The unit of a row whose largest value is m, where values of at most `carried` in
+// the unit before are to be brought to it: they end below 2^100.
+__device__ __forceinline__ float unit_for(float m, float unit, float carried) {
+    const float most = unit * 0x1p60f * __builtin_amdgcn_rcpf(carried) * 0x1p40f;
+    const float cut = __uint_as_float(__float_as_uint(most) & 0x7F800000u);
+    return fminf(pow2_to<8, kMostW>(m), fmaxf(cut, 0x1p-120f));
+}
+// The largest that a chunk's X''^T B comes to: 64 products of less than 2^9 and 2^3.
+constexpr float kMostUpdate = 0x1p18f;
 
 // Nothing moves across, and values loaded before are loaded again after: the
 // compiler would otherwise hoist whole phases' loads, or keep their values, and
@@ -1013,7 +1021,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
     const int col0 = w.h * a.P + wave * 32;
     char* mine = pool + wave_wg * (Tl::kBytes + Q * 4);
     _Float16* Bs = reinterpret_cast<_Float16*>(pool + 4 * (Tl::kBytes + Q * 4));
-    float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B * 2^(c_last - c)
+    float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B * 2^(c_last - c), X'' over x
     const float* steps = a.steps + w.head * a.nc * (3 * Q);
     const _Float16* shared0 = a.shared + (static_cast<size_t>(w.seq) * a.G + w.g) * a.nc * Sh::kHalfs;
     char* conv = a.conv + (w.head * a.nc * waves + wave) * Conv<FINE>::kBytes;
@@ -1036,7 +1044,8 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         S[nt] = zero16();
-    float unit = 1.0f;   // S holds the state times this
+    float unit = 1.0f;   // S holds the state times this, at most `most`
+    float most = 0.0f;
     double seg_sum = 0.0;
     float xc[32], mx = 0.0f;   // the chunk's convolved x and its largest magnitude
     auto conv_runs = [&](int r0, int r1) {
@@ -1072,10 +1081,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
         const _Float16* sh = shared0 + ch * Sh::kHalfs;
         const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
         seg_sum += static_cast<double>(th) + static_cast<double>(tl);
-        // X'' = x F, F = d 2^-s_B 2^(c_last - c): x and F are scaled each for itself, so X'' is where x's scale puts it
-        const float F = st_d * st_b * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
-        const float sF = pow2_to<0, kMostF>(wave_max(F));
-        fF[lane] = F * sF;
+        fF[lane] = st_d * st_b * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
         const float decay = __builtin_amdgcn_exp2f(th + tl);
         if (more)
             in.save(Q);
@@ -1084,22 +1090,22 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
             load_steps(ch + 1);
         mx = fmaxf(mx, __shfl_xor(mx, 32));
 
-        h8 wh[4], wl[4];
-        const float sx = fminf(pow2_to<8, kMostX>(mx), unit * 0x1p40f);
-        const float s2 = sx * sF;
+        // x is left behind, and becomes X'' in its place
+        const float sx = pow2_to<8, kMostX>(mx);
         char* to = conv + static_cast<size_t>(ch) * waves * Conv<FINE>::kBytes;
+        float mw = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            float v[8], u[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                u[e] = xc[8 * ks + e] * sx;
             if constexpr (FINE) {
 #pragma unroll
                 for (int r = 2 * ks; r < 2 * ks + 2; ++r)
                     reinterpret_cast<float4*>(to)[r * 64 + lane] =
                         make_float4(xc[4 * r], xc[4 * r + 1], xc[4 * r + 2], xc[4 * r + 3]);
             } else {
+                float u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    u[e] = xc[8 * ks + e] * sx;
                 st_frag(reinterpret_cast<_Float16*>(to), ks, lane, half8(u));
             }
 #pragma unroll
@@ -1107,18 +1113,36 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
                 const float4 F = *reinterpret_cast<const float4*>(fF + 16 * ks + 8 * q + 4 * hi);
                 const float ff[4] = {F.x, F.y, F.z, F.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[4 * q + i] = u[4 * q + i] * ff[i];
+                for (int i = 0; i < 4; ++i) {
+                    const int e = 8 * ks + 4 * q + i;
+                    xc[e] *= ff[i];
+                    mw = fmaxf(mw, fabsf(xc[e]));
+                    pin(xc[e]);
+                }
             }
+            pin(mw);
+            phase();
+        }
+        // X'' in a scale of its own: a row's largest decides, wherever in the chunk decays and inputs leave it
+        mw = fmaxf(mw, __shfl_xor(mw, 32));
+        const float s2 = unit_for(mw, unit, decay * most);
+        h8 wh[4], wl[4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = xc[8 * ks + e] * s2;
             split8(v, wh[ks], wl[ks]);
             pin(wh[ks]);
             pin(wl[ks]);
-            phase();
         }
+        phase();
         if (!FINE && lane < 32)
             reinterpret_cast<float*>(to + 4096)[lane] = inverse_pow2(sx);
         const float keep = decay * (s2 * inverse_pow2(unit));
         unit = s2;
+        most = __builtin_fmaf(keep, most, kMostUpdate);
         // the next chunk's rows into the tile; its conv runs beside the products of this one
         if (more)
             in.store();
