@@ -1280,7 +1280,7 @@ struct Common {
 };
 
 // A wave's part of the output pass's LDS.
-constexpr size_t out_wave_bytes() { return Tile<uint16_t>::kBytes + 4 * Q * 4 + 2 * Q * 2; }
+constexpr size_t out_wave_bytes() { return Tile<uint16_t>::kBytes + 5 * Q * 4 + Q * 2; }
 
 // The output pass over segments of bf16 activations, from the states that enter
 // them and the convolved x.  Its own state only serves outputs that are rounded
@@ -1316,8 +1316,8 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
     float* fK = fS + Q;                                        // D * s_F * 2^s_C
     float* fH = fS + 2 * Q;                                    // c, high part
     float* fE = fS + 3 * Q;                                    // 2^c
-    _Float16* fF = reinterpret_cast<_Float16*>(fS + 4 * Q);    // d * 2^-s_B * s_F
-    _Float16* fW = fF + Q;                                     // 2^(c_last - c)
+    float* fW = fS + 4 * Q;                                    // d * 2^-s_B * 2^(c_last - c), X'' over x
+    _Float16* fF = reinterpret_cast<_Float16*>(fS + 5 * Q);    // d * 2^-s_B * s_F
     const float skip = a.p.D ? a.p.D[w.h] : 0.0f;
     const float* steps = a.steps + w.head * a.nc * (3 * Q);
     const _Float16* shared0 = a.shared + (static_cast<size_t>(w.seq) * a.G + w.g) * a.nc * Sh::kHalfs;
@@ -1363,33 +1363,50 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
         const float sF = pow2_to<0, kMostF>(wave_max(F));
         const float cs = st_x;
         fF[lane] = static_cast<_Float16>(F * sF);
-        fW[lane] = static_cast<_Float16>(__builtin_amdgcn_exp2f((th - st_h) + (tl - st_l)));
+        fW[lane] = F * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
         fS[lane] = st_c;
         fK[lane] = skip * sF * inverse_pow2(st_c);
         fH[lane] = st_h;
         fE[lane] = __builtin_amdgcn_exp2f(st_h + st_l);
         const float decay = __builtin_amdgcn_exp2f(th + tl);
         wave_sync();
-        // X', X'' in units of s_F / cs; x itself is taken up by Y below
+        // X' in units of s_F / cs; x itself is taken up by Y below.  X'' in fp32, then in a scale of its own: a row's
+        // largest decides, wherever in the chunk decays and inputs leave it
         const float ux = sF * inverse_pow2(cs);
         h8 xh[4], wh[4];
+        float xw[32], mw = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-            h8 f, g;
+            h8 f;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const h4 f4_ = *reinterpret_cast<const h4*>(fF + 16 * ks + 8 * q + 4 * hi);
-                const h4 g4_ = *reinterpret_cast<const h4*>(fW + 16 * ks + 8 * q + 4 * hi);
+                const float4 W = *reinterpret_cast<const float4*>(fW + 16 * ks + 8 * q + 4 * hi);
+                const float ww[4] = {W.x, W.y, W.z, W.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    const int e = 8 * ks + 4 * q + i;
                     f[4 * q + i] = f4_[i];
-                    g[4 * q + i] = g4_[i];
+                    xw[e] = __builtin_fmaf(static_cast<float>(xq[ks][4 * q + i]), ww[i], 0.0f);
+                    mw = fmaxf(mw, fabsf(xw[e]));
+                    pin(xw[e]);
                 }
             }
+            pin(mw);
             xh[ks] = xq[ks] * f;
-            wh[ks] = xh[ks] * g;
             pin(xh[ks]);
+        }
+        mw = fmaxf(mw, __shfl_xor(mw, 32));
+        const float largest = state_max(S);
+        const float uw = unit_for(mw * cs, unit, decay * largest);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = __builtin_fmaf(xw[8 * ks + e], uw * cs, 0.0f);
+            wh[ks] = half8(v);
             pin(wh[ks]);
         }
         for (int f0 = wave; f0 < Sh::GF; f0 += kG * waves) {
@@ -1404,7 +1421,7 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
                 }
         }
         cb.store(common, sh, wave_wg, waves_wg, lane);
-        const float ss = pow2_to<8, kMostS>(state_max(S));   // on top of `unit`
+        const float ss = pow2_to<8, kMostS>(largest);   // on top of `unit`
         phase();
         __syncthreads();
         f16v Y[2] = {zero16(), zero16()};
@@ -1440,8 +1457,8 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs
         chunk_product<N, false>(Y, xh, xh, L, lane);
         phase();
         if (ch + 1 < w.ch1) {
-            Cs::update(S, decay * (ux * inverse_pow2(unit)), wh, common + Sh::CF * 512, lane);
-            unit = ux;
+            Cs::update(S, decay * (uw * inverse_pow2(unit)), wh, common + Sh::CF * 512, lane);
+            unit = uw;
         }
         phase();
         store_y<true>(Y, fS, inverse_pow2(ux), yt, static_cast<Act*>(a.p.y) + y0, z, gate, static_cast<int>(yrow),

@@ -1,11 +1,11 @@
 """GPU: state space prompts whose small values follow large ones within a chunk
 of 64 tokens: a long step that wipes the state, with and without an input of its
-own, and an entering state that decays away.  Every state row is held to its own
-terms, so that nothing large elsewhere hides it.
+own, and an entering state that decays away.  Every state row and every output
+is held to its own terms, so that nothing large elsewhere hides it.
 
 Taps are (0, 0, 0, 1) without a bias, so that conv outputs are SiLU(x) and have
 no cancellation of their own.  With u = 2^-24 and magnitudes (the same
-recurrence over absolute values) S~ of a state entry:
+recurrence over absolute values) S~ of a state entry and y~ of an output:
 
 State.  An entry's terms err by 8 u each for x and B, 12 u for the fp16 parts and
 the product that they leave out, and for a decay of 2^-c by 4 u of the steps, u of
@@ -14,6 +14,12 @@ row here that is not zero.  A chunk's products are added to an accumulator 12
 times: 120 u over the ten chunks that a term may last.  Parts below fp16's range
 are off by 2^-25 beside a row's largest of 2^8.  So each
 entry is held to 400 u of its row's largest S~.
+bf16 outputs.  Half a step, 2^-8 of |y|, and fp16 operands: C, B and G cut
+(2^-10 each), M.G, x, X' and the state rounded (2^-11 each, X' twice), the
+decays' high part alone (2^-11): 6 * 2^-10 of y~.  And beside the chunk's largest product Z = N |C_t|
+max_j(d_j |B_j|) max_j |x_j| (largest entries over the chunk's tokens j) what is
+below fp16's range: 2^-16 of it, as the steps are fp16 numbers in one scale per
+chunk.
 """
 import numpy as np
 import pytest
@@ -73,9 +79,15 @@ def run(i, copies):
     m = Layer({**i, "B": 2 * copies, **{k: tile(i[k]) for k in ("state", "tail", "x", "dt")}})
     m.prefill()
     got_S = m.state.cpu().numpy().astype(np.float64).reshape(copies, *S.shape)
+    got_y = m.y.float().cpu().numpy().astype(np.float64).reshape(copies, *y.shape)
     lim = 400 * U * Sm.max(-1, keepdims=True)
     worst = (np.abs(got_S - S) / lim).max()
     assert worst <= 1, f"state: {worst:.3g} times the bound"
+    if not i["bf16"]:
+        return
+    lim = 2.0 ** -8 * np.abs(y) + 6 * 2.0 ** -10 * ym + 2.0 ** -16 * Z
+    worst = (np.abs(got_y - y) / (lim + 1e-37)).max()
+    assert worst <= 1, f"outputs: {worst:.3g} times the bound"
 
 
 # name, T, H, G, P, N, copies of the two sequences
