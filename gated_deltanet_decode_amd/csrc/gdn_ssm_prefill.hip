@@ -695,10 +695,9 @@ __device__ __forceinline__ void decayed_g(h8 gh, h8 gl, int f, const float* cH, 
     parts8<FINE>(m, mh, ml);
 }
 
-// The head's left factors of a chunk, [M . G | C] or with FOLD [M . G | 2^c C],
-// into LDS: each wave builds the fragments wave, wave + waves, ..., BATCH of them
+// The head's left factors of a chunk, [M . G | C], into LDS: each wave builds the fragments wave, wave + waves, ..., BATCH of them
 // loaded at a time, the first batch well before it is needed.
-template <int N, bool FINE, int BATCH, bool FOLD>
+template <int N, bool FINE, int BATCH>
 struct Left {
     using Sh = Shared<N, FINE>;
     static constexpr int AF = Sh::GF + Sh::CF;
@@ -713,9 +712,9 @@ struct Left {
                 fl[k] = ld_frag(sh, f < Sh::GF ? Sh::kGl + f : Sh::kCl + f - Sh::GF, lane);
         }
     }
-    // cH, cL: c per token, cE: 2^c.  The first batch is loaded.
-    __device__ void build(const _Float16* sh, _Float16* L, const float* cH, const float* cL, const float* cE, int wave,
-                          int waves, int lane) {
+    // cH, cL: c per token.  The first batch is loaded.
+    __device__ void build(const _Float16* sh, _Float16* L, const float* cH, const float* cL, int wave, int waves,
+                          int lane) {
         for (int f0 = wave; f0 < AF; f0 += BATCH * waves) {
             if (f0 != wave)
                 load(sh, f0, waves, lane);
@@ -728,18 +727,6 @@ struct Left {
                 h8 mh, ml;
                 if (f < Sh::GF) {
                     decayed_g<Sh, FINE>(fh[k], fl[k], f, cH, cL, lane, mh, ml);
-                } else if (FOLD) {
-                    const int row = f - Sh::GF < N / 16 ? lane & 31 : 32 + (lane & 31);
-                    const float e2 = cE[row];
-                    if (FINE) {
-                        float m[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            m[e] = (static_cast<float>(fh[k][e]) + static_cast<float>(fl[k][e])) * e2;
-                        split8(m, mh, ml);
-                    } else {
-                        mh = fh[k] * static_cast<_Float16>(e2);
-                    }
                 } else {
                     mh = fh[k];
                     ml = fl[k];
@@ -1478,6 +1465,7 @@ constexpr size_t chunk_wave_bytes() { return Tile<Act>::kBytes + 7 * Q * 4; }
 // and the convolved x of segments in fp32.  One workgroup per (sequence, segment,
 // head), one wave per 32 rows of the state.  With every operand of a row in one
 // scale, a chunk's outputs are formed in one unit; the waves share the left factors.
+// The decay of the state that enters goes to the products' rows in fp32, not to C.
 // 16 prompts of 1,024 tokens, 64 heads, P = 64, N = 128: 206 us with prep (272 MB,
 // 1.3 TB/s), bound by its chain per chunk at two waves per SIMD; fp32, 2 x 1,003
 // tokens in segments: 28 us, one wave per SIMD.
@@ -1486,11 +1474,6 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     using Sh = Shared<N, FINE>;
     using Tl = Tile<Act>;
     constexpr int NT = N / 32;
-    // The decay of the state that enters goes to the products' rows (x waits for D x
-    // until then: 16 x 1,024 tokens of 64 heads, N = 128: 218 -> 205 us, fp32 208 ->
-    // 192); at N = 256 there are no registers for x, and it goes to C (16 x 500 tokens
-    // of 32 heads, P = 128: 216 against 227 us, fp32 303 against 342).
-    constexpr bool FOLD = N > 128;
     static_assert(FINE || !SPLIT, "bf16 segments are ssm_out_kernel's");
     extern __shared__ __align__(16) char pool[];   // [waves][tile, factors], then the left factor
     const int lane = threadIdx.x & 63;
@@ -1533,7 +1516,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         st_c = sc[Q + lane];
     };
     BSteps<N, FINE> B;
-    Left<N, FINE, (FINE ? 4 : 8), FOLD> left;
+    Left<N, FINE, (FINE ? 4 : 8)> left;
     f16v S[NT];
     float unit = 1.0f;
     const size_t row_off = static_cast<size_t>(wave * 32 + c) * N + 4 * hi;
@@ -1610,7 +1593,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
 
         // on their way while X' is formed (16 x 500 tokens of 32 heads, N = 256: 216 -> 208 us, fp32 303 -> 287)
         left.load(sh, wave, waves, lane);
-        // X'' and X' as fragments; x itself for D x (for bf16 outputs in fp16), or Y from D x on
+        // X'' and X' as fragments; x itself for D x (for bf16 outputs in fp16)
         h8 wh[4], wl[4], xh[4], xl[4], xq[4];
         f16v Y[2] = {zero16(), zero16()};
 #pragma unroll
@@ -1629,19 +1612,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
                     xc[8 * ks + 4 * q + i] = x;
                 }
             }
-            if constexpr (FOLD) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float4 K = *reinterpret_cast<const float4*>(fK + 16 * ks + 8 * q + 4 * hi);
-                    const float kk[4] = {K.x, K.y, K.z, K.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float y = xc[8 * ks + 4 * q + i] * kk[i];
-                        pin(y);
-                        Y[ks / 2][8 * (ks % 2) + 4 * q + i] = y;
-                    }
-                }
-            } else if constexpr (!FINE) {
+            if constexpr (!FINE) {
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -1658,7 +1629,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
                 pin(xl[ks]);
             phase();
         }
-        left.build(sh, L, fH, fL, fE, wave, waves, lane);
+        left.build(sh, L, fH, fL, wave, waves, lane);
         phase();
         __syncthreads();
         const bool update = !SPLIT || ch + 1 < w.ch1;
@@ -1666,7 +1637,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         state_product<N, FINE>(Y, S, u * inverse_pow2(unit), L + GF * 512, L + (AF + GF) * 512, lane);
         // the tokens' decays, and D x
 #pragma unroll
-        for (int it = 0; !FOLD && it < 2; ++it)
+        for (int it = 0; it < 2; ++it)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4 K = *reinterpret_cast<const float4*>(fK + 32 * it + 8 * q + 4 * hi);

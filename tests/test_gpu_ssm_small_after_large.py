@@ -12,14 +12,15 @@ the product that they leave out, and for a decay of 2^-c by 4 u of the steps, u 
 the rate and u of the rounded sum, 6 u c ln 2: 250 u for c = 60, the most of any
 row here that is not zero.  A chunk's products are added to an accumulator 12
 times: 120 u over the ten chunks that a term may last.  Parts below fp16's range
-are off by 2^-25 beside a row's largest of 2^8.  So each
-entry is held to 400 u of its row's largest S~.
-bf16 outputs.  Half a step, 2^-8 of |y|, and fp16 operands: C, B and G cut
-(2^-10 each), M.G, x, X' and the state rounded (2^-11 each, X' twice), the
-decays' high part alone (2^-11): 6 * 2^-10 of y~.  And beside the chunk's largest product Z = N |C_t|
+are off by 2^-25 beside a row's largest of 2^8.  So each entry is held to
+400 u of its row's largest S~.
+Outputs.  fp32: the same, C's 8 u and the sums' 64 u: 500 u of y~.  bf16: half a
+step, 2^-8 of |y|, and fp16 operands: C, B and G cut (2^-10 each), M.G, x, X'
+and the state rounded (2^-11 each, X' twice), the decays' high part alone
+(2^-11): 6 * 2^-10 of y~.  And beside the chunk's largest product Z = N |C_t|
 max_j(d_j |B_j|) max_j |x_j| (largest entries over the chunk's tokens j) what is
-below fp16's range: 2^-16 of it, as the steps are fp16 numbers in one scale per
-chunk.
+below fp16's range: 2^-24 of it in fp32, 2^-16 in bf16, whose steps are fp16
+numbers in one scale per chunk.
 """
 import numpy as np
 import pytest
@@ -72,7 +73,7 @@ def raw_step(d):
     return np.log(np.expm1(d)).astype(np.float32)
 
 
-def run(i, copies):
+def run(i, copies, outputs=False):
     """The prompts, each `copies` times over (enough to fill the chip takes the form of one segment)."""
     y, S, ym, Sm, Z = reference(i)
     tile = lambda v: np.tile(v, (copies,) + (1,) * (v.ndim - 1))
@@ -83,9 +84,9 @@ def run(i, copies):
     lim = 400 * U * Sm.max(-1, keepdims=True)
     worst = (np.abs(got_S - S) / lim).max()
     assert worst <= 1, f"state: {worst:.3g} times the bound"
-    if not i["bf16"]:
+    if not (i["bf16"] or outputs):
         return
-    lim = 2.0 ** -8 * np.abs(y) + 6 * 2.0 ** -10 * ym + 2.0 ** -16 * Z
+    lim = 2.0 ** -8 * np.abs(y) + 6 * 2.0 ** -10 * ym + 2.0 ** -16 * Z if i["bf16"] else 500 * U * ym + U * Z
     worst = (np.abs(got_y - y) / (lim + 1e-37)).max()
     assert worst <= 1, f"outputs: {worst:.3g} times the bound"
 
@@ -94,6 +95,8 @@ def run(i, copies):
 FORMS = [("segments", 270, 6, 2, 64, 64, 1), ("segments_n128_p128", 400, 4, 2, 128, 128, 1),
          ("segments_n256", 270, 3, 1, 32, 256, 1)]
 forms = pytest.mark.parametrize("T,H,G,P,N,copies", [f[1:] for f in FORMS], ids=[f[0] for f in FORMS])
+MORE = [("one_segment_n256", 140, 64, 1, 64, 256, 4)]
+every_form = pytest.mark.parametrize("T,H,G,P,N,copies", [f[1:] for f in FORMS + MORE], ids=[f[0] for f in FORMS + MORE])
 types = pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
 
 
@@ -107,6 +110,17 @@ def test_a_wipe_without_an_input(T, H, G, P, N, copies, bf16):
     i["dt"][:, 63] = raw_step(bits * np.log(2) / -i["A"])
     i["x"][:, 63:, :H * P] = 0
     run(i, copies)
+
+
+@pytest.mark.parametrize("bf16", [True], ids=["bf16"])
+@every_form
+def test_an_entering_state_behind_a_wipe(T, H, G, P, N, copies, bf16):
+    """No inputs at all, and a step that decays the entering state by 2^-6 to 2^-40 within the first chunk."""
+    i = quiet(5, T, H, G, P, N, bf16, 0.003)
+    bits = np.resize(np.array([6, 18.5, 20.5, 22.5, 25.5, 40]), H)
+    i["dt"][:, 5] = raw_step(bits * np.log(2) / -i["A"])
+    i["x"][..., :H * P] = 0
+    run(i, copies, True)
 
 
 @types
