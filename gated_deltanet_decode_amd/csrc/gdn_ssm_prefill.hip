@@ -120,11 +120,12 @@ __device__ __forceinline__ float pow2_to(float m) {
 constexpr int kMostBC = 40, kMostX = 24, kMostF = 24, kMostW = 64, kMostS = 100;
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 // The unit of a row whose largest value is m, where values of at most `carried` in
-// the unit before are to be brought to it: they end below 2^100.
+// the unit before are to be brought to it: they end below 2^100, and the ratio of the
+// units is finite.
 __device__ __forceinline__ float unit_for(float m, float unit, float carried) {
     const float most = unit * 0x1p60f * __builtin_amdgcn_rcpf(carried) * 0x1p40f;
     const float cut = __uint_as_float(__float_as_uint(most) & 0x7F800000u);
-    return fminf(pow2_to<8, kMostW>(m), fmaxf(cut, 0x1p-120f));
+    return fminf(fminf(pow2_to<8, kMostW>(m), unit * 0x1p120f), fmaxf(cut, 0x1p-120f));
 }
 // The largest that a chunk's X''^T B comes to: 64 products of less than 2^9 and 2^3.
 constexpr float kMostUpdate = 0x1p18f;
@@ -1463,12 +1464,12 @@ constexpr size_t chunk_wave_bytes() { return Tile<Act>::kBytes + 7 * Q * 4; }
 
 // The output pass that also carries the state (one segment), or takes the state
 // and the convolved x of segments in fp32.  One workgroup per (sequence, segment,
-// head), one wave per 32 rows of the state.  With every operand of a row in one
-// scale, a chunk's outputs are formed in one unit; the waves share the left factors.
-// The decay of the state that enters goes to the products' rows in fp32, not to C.
-// 16 prompts of 1,024 tokens, 64 heads, P = 64, N = 128: 206 us with prep (272 MB,
+// head), one wave per 32 rows of the state; the waves share the left factors.  The
+// decay of the state that enters goes to the products' rows in fp32, not to C.
+// 16 prompts of 1,024 tokens, 64 heads, P = 64, N = 128: 216 us with prep (272 MB,
 // 1.3 TB/s), bound by its chain per chunk at two waves per SIMD; fp32, 2 x 1,003
-// tokens in segments: 28 us, one wave per SIMD.
+// tokens in segments: 28 us, one wave per SIMD.  One scale per row for X', X'' and
+// the state takes 202 us, but then what is large in one takes bits from another.
 template <int N, typename Act, bool FINE, bool SPLIT>
 __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel(ChunkArgs a) {
     using Sh = Shared<N, FINE>;
@@ -1486,10 +1487,10 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
     const int col0 = w.h * a.P + wave * 32;
     char* mine = pool + wave * chunk_wave_bytes<Act>();
     float* yt = reinterpret_cast<float*>(mine);
-    float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B * s_F
-    float* fW = fF + Q;                                        // the same times 2^(c_last - c)
+    float* fF = reinterpret_cast<float*>(mine + Tl::kBytes);   // d * 2^-s_B, X' over x
+    float* fW = fF + Q;                                        // the same times 2^(c_last - c), X'' over x
     float* fS = fF + 2 * Q;                                    // 2^-s_C
-    float* fK = fF + 3 * Q;                                    // D * s_F * 2^s_C
+    float* fK = fF + 3 * Q;                                    // D * 2^s_C
     float* fH = fF + 4 * Q;                                    // c, high and low part
     float* fL = fF + 5 * Q;
     float* fE = fF + 6 * Q;                                    // 2^c
@@ -1544,12 +1545,11 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         if constexpr (!SPLIT)
             in.store();
         const float th = __shfl(st_h, 63), tl = __shfl(st_l, 63);
-        const float sF = pow2_to<0, kMostF>(wave_max(st_d * st_b));
-        const float F = st_d * st_b * sF;
+        const float F = st_d * st_b;
         fF[lane] = F;
         fW[lane] = F * __builtin_amdgcn_exp2f((th - st_h) + (tl - st_l));
         fS[lane] = st_c;
-        fK[lane] = skip * sF * inverse_pow2(st_c);
+        fK[lane] = skip * inverse_pow2(st_c);
         fH[lane] = st_h;
         fL[lane] = st_l;
         fE[lane] = __builtin_amdgcn_exp2f(st_h + st_l);
@@ -1560,7 +1560,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         load_steps(next);
 
         float xc[32];
-        float mx = 0.0f;
+        float mx = 0.0f, mF = 0.0f, mW = 0.0f;   // largest of x, X' and X''
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             float v[4];
@@ -1569,13 +1569,20 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
             } else {
                 conv_run(in.tile, taps, r, lane, v);
             }
+            const float4 F4 = *reinterpret_cast<const float4*>(fF + 8 * r + 4 * hi);
+            const float4 W4 = *reinterpret_cast<const float4*>(fW + 8 * r + 4 * hi);
+            const float ff[4] = {F4.x, F4.y, F4.z, F4.w}, ww[4] = {W4.x, W4.y, W4.z, W4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 xc[4 * r + i] = v[i];
                 mx = fmaxf(mx, fabsf(v[i]));
+                mF = fmaxf(mF, fabsf(v[i] * ff[i]));
+                mW = fmaxf(mW, fabsf(v[i] * ww[i]));
                 pin(xc[4 * r + i]);
             }
             pin(mx);
+            pin(mF);
+            pin(mW);
             if (!SPLIT && r % 2)
                 phase();
         }
@@ -1584,39 +1591,39 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         else
             in.save(Q);
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        // one scale for x, the state that enters and so all of the row: the state, up to a thousand times X', stays
-        // below 2^15 in it, and X' is the less exact the smaller it is beside the state
-        const float ms = state_max(S) * inverse_pow2(unit);
-        const float sx = fminf(fminf(pow2_to<8, kMostX>(mx), pow2_to<14, kMostS>(ms) * inverse_pow2(sF)),
-                               unit * 0x1p40f);
-        const float u = sx * sF;   // the unit of X', X'', Y and the next state
-
+        mF = fmaxf(mF, __shfl_xor(mF, 32));
+        mW = fmaxf(mW, __shfl_xor(mW, 32));
         // on their way while X' is formed (16 x 500 tokens of 32 heads, N = 256: 216 -> 208 us, fp32 303 -> 287)
         left.load(sh, wave, waves, lane);
+        // X' and with it Y, X'' and with it the next state, and the state that enters, each in a scale of its own: what
+        // is large in one does not take bits from another.  D x stays within fp32's range in Y's.
+        const float largest = state_max(S);
+        const float u = fminf(unit_for(mF, unit, largest), pow2_to<60, 100>(mx));
+        const float uw = unit_for(mW, unit, decay * largest);
+        const float ss = pow2_to<8, kMostS>(largest);   // on top of `unit`
         // X'' and X' as fragments; x itself for D x (for bf16 outputs in fp16)
+        const float sx = FINE ? 1.0f : pow2_to<8, kMostX>(mx);
         h8 wh[4], wl[4], xh[4], xl[4], xq[4];
-        f16v Y[2] = {zero16(), zero16()};
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             float xw[8], xp[8];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const float4 F = *reinterpret_cast<const float4*>(fF + 16 * ks + 8 * q + 4 * hi);
-                const float4 W = *reinterpret_cast<const float4*>(fW + 16 * ks + 8 * q + 4 * hi);
-                const float ff[4] = {F.x, F.y, F.z, F.w}, ww[4] = {W.x, W.y, W.z, W.w};
+                const float4 F4 = *reinterpret_cast<const float4*>(fF + 16 * ks + 8 * q + 4 * hi);
+                const float4 W4 = *reinterpret_cast<const float4*>(fW + 16 * ks + 8 * q + 4 * hi);
+                const float ff[4] = {F4.x, F4.y, F4.z, F4.w}, ww[4] = {W4.x, W4.y, W4.z, W4.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float x = xc[8 * ks + 4 * q + i] * sx;
-                    xw[4 * q + i] = x * ww[i];
-                    xp[4 * q + i] = x * ff[i];
-                    xc[8 * ks + 4 * q + i] = x;
+                    const float x = xc[8 * ks + 4 * q + i];
+                    xw[4 * q + i] = x * ww[i] * uw;
+                    xp[4 * q + i] = x * ff[i] * u;
                 }
             }
             if constexpr (!FINE) {
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] = xc[8 * ks + e];
+                    v[e] = xc[8 * ks + e] * sx;
                 xq[ks] = half8(v);
                 pin(xq[ks]);
             }
@@ -1634,8 +1641,10 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         __syncthreads();
         const bool update = !SPLIT || ch + 1 < w.ch1;
         constexpr int GF = Sh::GF, AF = Sh::GF + Sh::CF;
-        state_product<N, FINE>(Y, S, u * inverse_pow2(unit), L + GF * 512, L + (AF + GF) * 512, lane);
-        // the tokens' decays, and D x
+        f16v Y[2] = {zero16(), zero16()};
+        state_product<N, FINE>(Y, S, ss, L + GF * 512, L + (AF + GF) * 512, lane);
+        // to Y's unit and the tokens' decays, and D x
+        const float ratio = u * (inverse_pow2(ss) * inverse_pow2(unit)), ux = u * inverse_pow2(sx);
 #pragma unroll
         for (int it = 0; it < 2; ++it)
 #pragma unroll
@@ -1647,7 +1656,7 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
                 for (int i = 0; i < 4; ++i) {
                     const float x = FINE ? xc[16 * it + 4 * q + i]
                                          : static_cast<float>(xq[2 * it + q / 2][4 * (q % 2) + i]);
-                    float y = __builtin_fmaf(x, kk[i], Y[it][4 * q + i] * ee[i]);
+                    float y = __builtin_fmaf(x * ux, kk[i], Y[it][4 * q + i] * (ratio * ee[i]));
                     pin(y);
                     Y[it][4 * q + i] = y;
                 }
@@ -1664,8 +1673,8 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
         }
         phase();
         if (update) {
-            B.update(S, decay * (u * inverse_pow2(unit)), wh, wl, sh, lane);
-            unit = u;
+            B.update(S, decay * (uw * inverse_pow2(unit)), wh, wl, sh, lane);
+            unit = uw;
         }
         phase();
         store_y<FINE>(Y, fS, inverse_pow2(u), yt, static_cast<Act*>(a.p.y) + y0, z, gate, static_cast<int>(yrow),
