@@ -575,9 +575,13 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(float* __restrict__ S
 
 }  // namespace beam
 
+// Room for at least B * K * spans_of() spans, in numbers that do not fall as any
+// argument grows: a workspace sized for the largest call serves the smaller ones.
 size_t beam_select_ws_bytes(int B, int K, int V, int S) {
-    const size_t slots = static_cast<size_t>(B) * K * beam::spans_of(B, K, V, S);
-    return slots * (sizeof(beam::Part) + sizeof(uint2) * static_cast<size_t>(S));
+    const int64_t rows = static_cast<int64_t>(B) * K;
+    const int64_t per_row = std::min<int64_t>(std::max<int64_t>((static_cast<int64_t>(V) + 1023) / 1024, 4), beam::kMaxSpans);
+    const int64_t slots = std::min(rows * per_row, std::max(4 * rows, 4096 + rows));
+    return static_cast<size_t>(slots) * (sizeof(beam::Part) + sizeof(uint2) * static_cast<size_t>(S));
 }
 
 hipError_t launch_beam_select(const BeamGeo& g, const void* logits, const float* scores, const uint8_t* finished,

@@ -1698,15 +1698,17 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
 // of up to 2,048 tokens: 326 against 347 us).  A segment has at least two chunks,
 // in fp32 one (64 heads, 512 tokens: 57 us with four, 45 with two, 49 with one;
 // fp32, 32 heads, 256 tokens: 57, 52 and 41 us).
-static void segments(const SsmGeo& g, int T, bool ragged, int& segs, int& per) {
+// Returns the number before it is evened out, which does not fall as T grows.
+static int segments(const SsmGeo& g, int T, bool ragged, int& segs, int& per) {
     const int nc = (T + Q - 1) / Q;
     const int64_t waves = static_cast<int64_t>(g.B) * g.H * (g.P / 32);
     const int64_t fill = (g.N > 128 || !g.bf16 ? 1024 : 2048) * (ragged ? 2 : 1);
     const int64_t want = (fill + waves - 1) / waves;
     const int most = std::max(1, nc / (g.bf16 ? 2 : 1));
-    segs = static_cast<int>(std::min<int64_t>(want, most));
-    per = (nc + segs - 1) / segs;
+    const int limit = static_cast<int>(std::min<int64_t>(want, most));
+    per = (nc + limit - 1) / limit;
     segs = (nc + per - 1) / per;
+    return limit;
 }
 
 static size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -1721,10 +1723,11 @@ static size_t shared_halfs(const SsmGeo& g) {
     }
 }
 
-// The workspace: fragments, steps, and with segments their states, decays and the convolved x.
+// The workspace: fragments, steps, and with segments their states, decays and the convolved x.  It has room for the
+// segments' limit, so that one sized for a prompt serves every shorter one.
 static size_t carve(const SsmGeo& g, int T, bool ragged, char* base, ChunkArgs* a) {
     int segs, per;
-    segments(g, T, ragged, segs, per);
+    const int limit = segments(g, T, ragged, segs, per);
     const size_t nc = (T + Q - 1) / Q, BH = static_cast<size_t>(g.B) * g.H;
     size_t n = 0;
     auto take = [&](size_t bytes) {
@@ -1735,9 +1738,9 @@ static size_t carve(const SsmGeo& g, int T, bool ragged, char* base, ChunkArgs* 
     const size_t shared = take(static_cast<size_t>(g.B) * g.G * nc * shared_halfs(g) * sizeof(_Float16));
     const size_t steps = take(BH * nc * (3 * Q) * sizeof(float));
     size_t state = 0, decay = 0, conv = 0;
-    if (segs > 1) {
-        state = take(BH * segs * g.P * g.N * sizeof(float));
-        decay = take(BH * segs * sizeof(float));
+    if (limit > 1) {
+        state = take(BH * limit * g.P * g.N * sizeof(float));
+        decay = take(BH * limit * sizeof(float));
         conv = take(BH * nc * (g.P / 32) * (g.bf16 ? Conv<false>::kBytes : Conv<true>::kBytes));
     }
     if (a) {

@@ -527,7 +527,8 @@ gdn_status gdn_ssm_decode_token(const gdn_ssm_dims* d, float* state, const void*
  *   status i32 [B] or NULL: per sequence GDN_OK, or GDN_ERR_INDEX when its
  *           length is out of range (that sequence is untouched)
  *   workspace device bytes >= gdn_ssm_prefill_workspace_bytes(d, T), 256-byte
- *           aligned.  1 <= T <= GDN_SSM_MAX_TOKENS.
+ *           aligned; a size serves every smaller T of the same dims, not other
+ *           batches.  1 <= T <= GDN_SSM_MAX_TOKENS.
  * State and fp32 outputs agree with the token-by-token call to fp32 rounding,
  * bf16 outputs to the rounding of bf16 (where step sizes within 64 tokens differ
  * by more than 2^14, relative to a head's largest outputs there).  A NaN or infinity in a token's inputs
@@ -562,7 +563,8 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_dims* d, float* state, void* conv_tail,
  * out_scores may be scores itself where S == K, and must not overlap it
  * otherwise (GDN_ERR_ALIAS).
  * logits may be aligned to its element size only; the other arrays and the
- * workspace (gdn_beam_select_workspace_bytes) are 16-byte aligned.
+ * workspace are 16-byte aligned.  A size of gdn_beam_select_workspace_bytes
+ * serves every call of no more sequences, beams, entries and places.
  */
 #define GDN_MAX_BEAMS 32
 #define GDN_MAX_BEAM_SELECT 64
