@@ -547,7 +547,9 @@ def ssm_prefill(d: SsmDims, state, tail, w, x, dt, A, y, workspace, conv_bias=No
     B, H, P, act = d.batch, d.num_heads, d.head_dim, torch.bfloat16 if d.act_dtype == BF16 else torch.float32
     HP, f32 = H * P, torch.float32
     Cc = HP + 2 * d.num_groups * d.state_dim
-    if not x.numel() or x.numel() % (B * Cc):
+    if B < 1 or Cc < 1:
+        raise GdnError(2, "gdn_ssm_prefill")
+    if not isinstance(x, torch.Tensor) or not x.numel() or x.numel() % (B * Cc):
         raise ValueError("x must be [B][T][C]")
     T = x.numel() // (B * Cc)
     dev, s = _here(stream)
@@ -602,7 +604,8 @@ def beam_select(logits, scores, out_scores, parent, token, workspace, finished=N
     ptr, nbytes = _ws(workspace, _lib.gdn_beam_select_workspace_bytes(B, K, V, S), dev)
     fin = None
     if finished is not None:
-        fin = _p(finished, "finished", torch.uint8 if finished.dtype is torch.uint8 else torch.bool, B * K, dev)
+        byte = getattr(finished, "dtype", None) is torch.uint8
+        fin = _p(finished, "finished", torch.uint8 if byte else torch.bool, B * K, dev)
     _check(_lib.gdn_beam_select(B, K, V, pitch, act, logits.data_ptr(), _p(scores, "scores", torch.float32, B * K, dev),
                                 fin, eos, S, _p(out_scores, "out_scores", torch.float32, B * S, dev),
                                 _p(parent, "parent", torch.int32, B * S, dev),
