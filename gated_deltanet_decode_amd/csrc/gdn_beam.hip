@@ -12,12 +12,14 @@
 //         row's logits reach (the S-th largest of the workgroup's 256, by
 //         bisection with ballots); what reaches it goes to the wave's buffer in
 //         LDS.  A buffer that fills is cut to its S best, and its bound raised, by
-//         the same bisection.  64 x 8 rows of 128,000 bf16 logits: 32 us, 3.3 TB/s
+//         the same bisection.  64 x 8 rows of 128,000 bf16 logits: 33.5 us, 3.1 TB/s
 //         of what it reads (rows of ended beams are not); what is beside the
 //         stream is the running sum's exponentials and the upkeep of the bound.
 //   join  one workgroup per sequence: each beam's sum over the spans in fp64,
 //         then the S best of the spans' entries by their fp64 value; 5 to 7 us, a
-//         chain of loads, sums and three barriers.
+//         chain of loads, sums and three barriers.  Candidates are counted against
+//         each other: where nearly all are equal (rows of one value, K * S = 2,048)
+//         that is 8,192 against 8,192.
 // Keys (ordered logit bits, complement of the index) are unique, so the result
 // does not depend on the order in which spans or waves finish.
 #include <algorithm>
@@ -409,7 +411,9 @@ constexpr int kMaxEntries = 8192;   // of one sequence, over beams and spans
 // One workgroup per sequence.  Every entry is taken once, by one thread.  Each
 // wave finds a bound that S of its threads' best reach; what reaches the largest
 // of these bounds is gathered in LDS and each candidate counts those before it:
-// that is its place.  R: entries per thread.
+// that is its place.  R: entries per thread; 8, for K * S > 512, needs more than the
+// 128 registers that 1,024 threads leave and spills 120 (one request of 32 beams,
+// best 64 of 150,000 entries each: 145 us a call).
 template <int R>
 __global__ __launch_bounds__(64 * kJoinWaves) void beam_join_kernel(
     const Part* __restrict__ sums, const uint2* __restrict__ keys, const float* scores,
@@ -526,9 +530,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void beam_join_kernel(
     }
 }
 
-// Spans per row: four waves per SIMD over all rows, spans of at least 1,024
-// logits, at most one span per lane of a joining wave and kMaxEntries entries per
-// sequence; a multiple of the four waves of a workgroup.
+// Spans per row: 4,096 waves over all rows, spans of at least 1,024 logits, at most
+// one span per lane of a joining wave and kMaxEntries entries per sequence; a
+// multiple of the four waves of a workgroup.  4,096 waves are what the bf16 scan has
+// room for, four per SIMD (64 x 8 rows of 128,000: 41 us a call, 45 with 2,048, 42 to
+// 44 with 8,192); the fp32 scan has room for three and loses little by it (the same
+// rows, best 8: 61 us, 57.5 with 3,072, 63 with 8,192).
 static int spans_of(int B, int K, int V, int S) {
     const int64_t rows = static_cast<int64_t>(B) * K;
     int64_t n = std::min<int64_t>((4096 + rows - 1) / rows, (static_cast<int64_t>(V) + 1023) / 1024);
@@ -542,7 +549,7 @@ static int spans_of(int B, int K, int V, int S) {
 // other thread touches those units, so the move is in place without a second
 // copy of the states, and slots that keep their own state cost nothing.  Bound
 // by HBM: the sources that move are read, the slots that move are written (8 x 4
-// beams of 3.2 MB with parents drawn at random: 137 MB in 19.9 us).
+// beams of 3.2 MB with parents drawn at random: 137 MB in 21.8 us).
 template <int KM>
 __global__ __launch_bounds__(256) void beam_reorder_kernel(float* __restrict__ S, float* __restrict__ T, int64_t su,
                                                            int64_t tu, int K, const int32_t* __restrict__ parent,
@@ -605,7 +612,7 @@ hipError_t launch_beam_select(const BeamGeo& g, const void* logits, const float*
     const auto join = entries <= 1024   ? beam::beam_join_kernel<1>
                       : entries <= 2048 ? beam::beam_join_kernel<2>
                                         : beam::beam_join_kernel<beam::kMaxEntries / (64 * beam::kJoinWaves)>;
-    if (lds > 32768) {   // with the static part more than the 64 KB that need no asking
+    if (lds > 32768) {   // asked for well before static and dynamic part pass the 64 KB that need no asking
         e = hipFuncSetAttribute(reinterpret_cast<const void*>(join), hipFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(lds));
         if (e != hipSuccess)

@@ -3,8 +3,8 @@
 //
 // Decode moves the state once in and once out, 8*H*P*N bytes per sequence
 // against 6 flops per state entry: HBM sets the time once there are enough
-// sequences (64 of 48 heads of 128 x 128: 416 MB in 66.0 us, 6.3 TB/s), the launch
-// itself before that (one: 4.4 us).  The layout is the delta-rule token
+// sequences (64 of 48 heads of 128 x 128: 416 MB in 67.6 us, 6.2 TB/s), the launch
+// itself before that (one: 4.8 us).  The layout is the delta-rule token
 // kernel's: a row of N entries over 16 (N = 32: 8) lanes, so that the read-out
 // S C is a short DPP sum, with the few conv loads issued ahead of the state
 // loads because the memory counter retires in order.  Every workgroup convolves
@@ -136,10 +136,9 @@ static hipError_t token_cfg(const SsmGeo& g, const SsmArgs& a, hipStream_t s) {
 template <typename Act>
 static hipError_t token_act(const SsmGeo& g, const SsmArgs& a, hipStream_t s) {
     // Once there are enough (sequence, head) pairs to fill the chip, more rows per
-    // workgroup share its conv.  At batch 64: N = 64 (64 heads of 64 rows) 35.1 us
-    // with 16 rows, 27.3 with 32, 25.3 with 64; N = 128 (48 heads of 128 rows) 70.8,
-    // 67.8 and 69.7 us; N = 256 47 us with any.  Few pairs want many workgroups
-    // instead (one sequence of 48 heads: 4.8 us with 16 rows).
+    // workgroup share its conv.  Calls back to back at batch 64: N = 64 (64 heads of 64
+    // rows) 37.4 us with 16 rows, 28.7 with 32, 26.3 with 64; N = 128 (48 heads of 128
+    // rows) 79, 69.7 and 71.1 us.  Few pairs want many workgroups instead.
     const bool many = static_cast<int64_t>(g.B) * g.H >= 512;
     switch (g.N) {
         case 32: return token_cfg<32, 1, Act>(g, a, s);

@@ -28,7 +28,12 @@
 // exact and undone on the accumulators.  Products that reach the state or fp32
 // outputs take each operand as the sum of two fp16 numbers (22 bits) and three
 // matrix products, so that the state is as exact as one kept in fp32.  Outputs
-// that are rounded to bf16 take one fp16 number (11 bits against bf16's 8).
+// that are rounded to bf16 take one fp16 number (11 bits against bf16's 8).  Each
+// of X', X'' and the state has its own scale, from its own largest value: a step
+// that wipes the state leaves X'' far below X', and the state far below both.
+// Within a chunk M . G has none: an output whose terms M takes below 2^-14 keeps
+// fewer bits, 2^-24 (bf16, with the steps of the segments' pass in fp16, 2^-16) of
+// the chunk's largest products being what is left out at most.
 #include <algorithm>
 #include <type_traits>
 
@@ -412,8 +417,8 @@ __device__ void steps_part(const ChunkArgs& a, int id, float* lds) {
 // One workgroup of N / 16 waves per (sequence, group, chunk): a wave convolves 32
 // of the group's 2 N channels.  B goes out straight from registers (a lane's
 // runs of four tokens are the fragments' k order); C and the rows that G is
-// formed from pass through LDS.  31 us at 32,768 tokens and one group (44 MB of
-// fragments and inputs, 25 MB of steps), 63 us for eight prompts of up to 2,048
+// formed from pass through LDS.  35 us at 32,768 tokens and one group (44 MB of
+// fragments and inputs, 25 MB of steps), 68 us for eight prompts of up to 2,048
 // tokens and 16 groups: bound by its chain of conv, scales, G and stores.
 template <int N, typename Act, bool FINE>
 __global__ __launch_bounds__(4 * N) void ssm_prep_kernel(ChunkArgs a, int prep_wgs) {
@@ -986,11 +991,12 @@ struct BShare {
 // Each segment's own state from zero, the state's products in two fp16 parts, and
 // the convolved x for the output pass.  One wave per 32 rows of the state; a
 // workgroup is one head's waves, which share nothing, or (SHARE) four waves of
-// heads of one group, which load B's fragments once for all (230 -> 199 us at
-// 32,768 tokens of 64 heads, P = 64, N = 128) and convolve the next chunk between
-// the products of this one (184 us, 537 MB in and out at 2.9 TB/s).  What is left:
-// the matrix products (41 us at the peak rate), and on the vector unit conv, SiLU
-// and the fp16 parts, 590 instructions per chunk and wave (70 us).  The last chunk
+// heads of one group, which load B's fragments once for all and convolve the next
+// chunk between the products of this one.  32,768 tokens of 64 heads, P = 64,
+// N = 128: 193 us at the fastest of 20 calls back to back (221 in the median, as
+// the clock falls), 537 MB in and out at 2.8 TB/s.  What is left: the matrix
+// products (41 us at the peak rate), and on the vector unit conv, SiLU, X''s scale
+// and the fp16 parts, 670 instructions per chunk and wave (75 us).  The last chunk
 // has a copy of its own: with a branch for it the loop spills 104 registers.
 template <int N, typename Act, bool FINE, bool SHARE>
 __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkArgs a) {
@@ -1191,8 +1197,8 @@ __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_state_kernel(ChunkAr
 }
 
 // Each segment's own state becomes the state that enters it; the state itself
-// goes to the end of the prompt.  One thread per four entries; 15 us for 32
-// segments' states of 64 heads of 64 x 128 (67 MB each way), 24 us for eight
+// goes to the end of the prompt.  One thread per four entries; 16 us for 32
+// segments' states of 64 heads of 64 x 128 (67 MB each way), 26 us for eight
 // prompts of 48 heads of 128 x 128.
 __global__ __launch_bounds__(256) void ssm_join_kernel(ChunkArgs a, int quads) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -1272,12 +1278,14 @@ constexpr size_t out_wave_bytes() { return Tile<uint16_t>::kBytes + 5 * Q * 4 + 
 
 // The output pass over segments of bf16 activations, from the states that enter
 // them and the convolved x.  Its own state only serves outputs that are rounded
-// to bf16: one fp16 part each, and X' and X'' formed in packed fp16.  One wave
-// per 32 rows of the state; a workgroup is `heads` heads of one group, which share
-// C's and B's fragments, and a head's waves its M . G.  The decay of the state that
-// enters is put on the products' rows, so that C needs none of its own: 237 ->
-// 212 us at 32,768 tokens of 64 heads, P = 64, N = 128 (537 MB in and out, 2.5
-// TB/s), bound like the state pass by its chain of small phases per chunk.
+// to bf16: one fp16 part each, X' formed in packed fp16 and X'', which needs a
+// scale of its own, in fp32 (in fp16 too, 219 instead of 224 us, it would be gone
+// behind a decay of 2^-25).  One wave per 32 rows of the state; a workgroup is
+// `heads` heads of one group, which share C's and B's fragments, and a head's waves
+// its M . G.  The decay of the state that enters is put on the products' rows, so
+// that C needs none of its own.  32,768 tokens of 64 heads, P = 64, N = 128: 224 us
+// at the fastest of 20 calls back to back (255 in the median), 537 MB in and out at
+// 2.4 TB/s, bound like the state pass by its chain of small phases per chunk.
 template <int N>
 __global__ __launch_bounds__(256, N > 128 ? 1 : 2) void ssm_out_kernel(ChunkArgs a, int heads) {
     using Act = uint16_t;
@@ -1466,10 +1474,11 @@ constexpr size_t chunk_wave_bytes() { return Tile<Act>::kBytes + 7 * Q * 4; }
 // and the convolved x of segments in fp32.  One workgroup per (sequence, segment,
 // head), one wave per 32 rows of the state; the waves share the left factors.  The
 // decay of the state that enters goes to the products' rows in fp32, not to C.
-// 16 prompts of 1,024 tokens, 64 heads, P = 64, N = 128: 216 us with prep (272 MB,
-// 1.3 TB/s), bound by its chain per chunk at two waves per SIMD; fp32, 2 x 1,003
-// tokens in segments: 28 us, one wave per SIMD.  One scale per row for X', X'' and
-// the state takes 202 us, but then what is large in one takes bits from another.
+// 16 prompts of 1,024 tokens, 64 heads, P = 64, N = 128: 212 to 218 us a call with
+// prep (272 MB, 1.3 TB/s), bound by its chain per chunk at two waves per SIMD; fp32,
+// 2 x 1,003 tokens in segments: 28 us, one wave per SIMD.  One scale per row for X',
+// X'' and the state took 202 us, but what is large in one takes bits from another.
+// Spills: 3 registers at N = 128, 12 to 24 at N = 256.
 template <int N, typename Act, bool FINE, bool SPLIT>
 __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel(ChunkArgs a) {
     using Sh = Shared<N, FINE>;
@@ -1692,12 +1701,12 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
 
 // Segments per sequence: as many as fill the chip once, which is two waves per
 // SIMD, or one where a wave needs more than 256 registers (N = 256, fp32).  One
-// 64-head prompt of 32,768 tokens: 476 us at 2,048 waves, 502 at 3,072, 489 at
-// 4,096 (before the state pass took its conv between the products); N = 256 (32 heads, 4,096 tokens) 100 us at 1,024 and 129 at 2,048.
-// Prompts of given lengths end at different times and take twice as many (eight
-// of up to 2,048 tokens: 326 against 347 us).  A segment has at least two chunks,
-// in fp32 one (64 heads, 512 tokens: 57 us with four, 45 with two, 49 with one;
-// fp32, 32 heads, 256 tokens: 57, 52 and 41 us).
+// 64-head prompt of 32,768 tokens: 463 us at 2,048 waves, 478 at 3,072, 477 at
+// 4,096; N = 256 (32 heads, 4,096 tokens) 100 us at 1,024, 127 at 1,536 and 129 at
+// 2,048.  Prompts of given lengths end at different times and take twice as many
+// (eight of up to 2,048 tokens: 313 against 335 us).  A segment has at least two
+// chunks, in fp32 one (64 heads, 512 tokens: 54 us with four, 43 with two, 47 with
+// one; fp32, 32 heads, 256 tokens: 53, 45 and 36 us).
 // Returns the number before it is evened out, which does not fall as T grows.
 static int segments(const SsmGeo& g, int T, bool ragged, int& segs, int& per) {
     const int nc = (T + Q - 1) / Q;
@@ -1802,10 +1811,10 @@ static hipError_t chunked_cfg(const SsmGeo& g, const SsmArgs& p, int T, const in
         return launch_lds(ssm_chunk_kernel<N, Act, FINE, false>, grid, block, lds_chunk, s, a);
     // Heads of a workgroup, which share what does not depend on the head.  It pays
     // where the chip is more than half full, at two waves per SIMD or one (64 heads:
-    // 32,768 tokens 521 -> 478 us, 4 x 4,096 310 -> 271, when it was built; N = 256, 1,024 waves: 124 ->
-    // 105); below that barriers and coarser workgroups cost more than the loads that
-    // they save (512 tokens 43.8 -> 46.5 us), except for heads of 128 rows, whose
-    // workgroups stay as they are.
+    // 32,768 tokens 592 -> 463 us, 4 x 4,096 318 -> 248; N = 256, 32 heads, 4,096
+    // tokens 121 -> 100); below that barriers and coarser workgroups cost more than the
+    // loads that they save (512 tokens 43.0 -> 45.6 us), except for heads of 128 rows,
+    // whose workgroups stay as they are (eight prompts of up to 2,048: 327 -> 313 us).
     const int rep = g.H / g.G;
     const bool share = waves == 4 || wgs * waves > (N > 128 ? 512 : 1024);
     const int heads = !share ? 1 : rep % (4 / waves) == 0 ? 4 / waves : waves == 1 && rep % 2 == 0 ? 2 : 1;

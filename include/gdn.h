@@ -529,10 +529,14 @@ gdn_status gdn_ssm_decode_token(const gdn_ssm_dims* d, float* state, const void*
  *   workspace device bytes >= gdn_ssm_prefill_workspace_bytes(d, T), 256-byte
  *           aligned; a size serves every smaller T of the same dims, not other
  *           batches.  1 <= T <= GDN_SSM_MAX_TOKENS.
- * State and fp32 outputs agree with the token-by-token call to fp32 rounding,
- * bf16 outputs to the rounding of bf16 (where step sizes within 64 tokens differ
- * by more than 2^14, relative to a head's largest outputs there).  A NaN or infinity in a token's inputs
- * may reach the outputs of every token of its chunk of 64, not only later ones.
+ * The state agrees with the token-by-token call to fp32 rounding, each row (of N
+ * entries) beside the magnitudes of its own terms.  Outputs do so beside the
+ * magnitudes of theirs, in fp32 to fp32 rounding and in bf16 to bf16's and that of
+ * operands of 11 bits (2^-8 and at most 6 * 2^-10), but for 2^-24 (fp32) or 2^-16
+ * (bf16) of N |C| max|d B| max|x|, largest entries over the tokens of their chunk of
+ * 64: what is that small there, behind a decay within the chunk or beside larger
+ * steps, keeps fewer bits.  A NaN or infinity in a token's inputs may reach the
+ * outputs of every token of its chunk, not only later ones.
  */
 #define GDN_SSM_MAX_TOKENS (1 << 22)
 size_t gdn_ssm_prefill_workspace_bytes(const gdn_ssm_dims* d, int32_t T);
@@ -558,6 +562,9 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_dims* d, float* state, void* conv_tail,
  * largest finite value.  A row of masked logits, and a score of -inf or NaN,
  * make all of the beam's candidates -inf.  -inf candidates are ordered like
  * any equal values, by the lowest index, where fewer than S others are left.
+ * Values are compared in fp64.  Which of a beam's logits that differ but give the
+ * same value there (beside a +inf, say) enter a result that has no room for all
+ * of them is not specified.
  * 1 <= K <= GDN_MAX_BEAMS, 1 <= S <= min(GDN_MAX_BEAM_SELECT, K*V),
  * K*V < 2^31, B*K <= 2^20 (GDN_ERR_SHAPE otherwise; GDN_ERR_INDEX for eos).
  * out_scores may be scores itself where S == K, and must not overlap it
