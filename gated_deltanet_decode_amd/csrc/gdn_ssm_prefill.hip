@@ -1475,7 +1475,7 @@ constexpr size_t chunk_wave_bytes() { return Tile<Act>::kBytes + 7 * Q * 4; }
 // head), one wave per 32 rows of the state; the waves share the left factors.  The
 // decay of the state that enters goes to the products' rows in fp32, not to C.
 // 16 prompts of 1,024 tokens, 64 heads, P = 64, N = 128: 212 to 218 us a call with
-// prep (272 MB, 1.3 TB/s), bound by its chain per chunk at two waves per SIMD; fp32,
+// prep (348 MB with the states, 1.6 TB/s), bound by its chain per chunk at two waves per SIMD; fp32,
 // 2 x 1,003 tokens in segments: 28 us, one wave per SIMD.  One scale per row for X',
 // X'' and the state took 202 us, but what is large in one takes bits from another.
 // Spills: 3 registers at N = 128, 12 to 24 at N = 256.
