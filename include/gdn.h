@@ -535,7 +535,8 @@ gdn_status gdn_ssm_decode_token(const gdn_ssm_dims* d, float* state, const void*
  * operands of 11 bits (2^-8 and at most 6 * 2^-10), but for 2^-24 (fp32) or 2^-16
  * (bf16) of N |C| max|d B| max|x|, largest entries over the tokens of their chunk of
  * 64: what is that small there, behind a decay within the chunk or beside larger
- * steps, keeps fewer bits.  A NaN or infinity in a token's inputs may reach the
+ * steps, keeps fewer bits, and so do channels of x, and tokens' rows of B and C, that
+ * are below 2^-38 throughout a chunk.  A NaN or infinity in a token's inputs may reach the
  * outputs of every token of its chunk, not only later ones.
  */
 #define GDN_SSM_MAX_TOKENS (1 << 22)
@@ -562,9 +563,11 @@ gdn_status gdn_ssm_prefill(const gdn_ssm_dims* d, float* state, void* conv_tail,
  * largest finite value.  A row of masked logits, and a score of -inf or NaN,
  * make all of the beam's candidates -inf.  -inf candidates are ordered like
  * any equal values, by the lowest index, where fewer than S others are left.
- * Values are compared in fp64.  Which of a beam's logits that differ but give the
- * same value there (beside a +inf, say) enter a result that has no room for all
- * of them is not specified.
+ * Values are compared in fp64; the exponentials that a beam's logarithm sums are
+ * fp32, which leaves it within 2^-18: candidates of different beams that are nearer
+ * than that may change places.  Which of a beam's logits that differ but give the
+ * same value (beside a +inf, say) enter a result that has no room for all of them
+ * is not specified.
  * 1 <= K <= GDN_MAX_BEAMS, 1 <= S <= min(GDN_MAX_BEAM_SELECT, K*V),
  * K*V < 2^31, B*K <= 2^20 (GDN_ERR_SHAPE otherwise; GDN_ERR_INDEX for eos).
  * out_scores may be scores itself where S == K, and must not overlap it
