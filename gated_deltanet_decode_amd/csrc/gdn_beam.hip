@@ -535,7 +535,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void beam_join_kernel(
 // multiple of the four waves of a workgroup.  4,096 waves are what the bf16 scan has
 // room for, four per SIMD (64 x 8 rows of 128,000: 41 us a call, 45 with 2,048, 42 to
 // 44 with 8,192); the fp32 scan has room for three and loses little by it (the same
-// rows, best 8: 61 us, 57.5 with 3,072, 63 with 8,192).
+// rows, best 8: 61 us, 57.5 with a quarter fewer, 63 with 8,192).
 static int spans_of(int B, int K, int V, int S) {
     const int64_t rows = static_cast<int64_t>(B) * K;
     int64_t n = std::min<int64_t>((4096 + rows - 1) / rows, (static_cast<int64_t>(V) + 1023) / 1024);

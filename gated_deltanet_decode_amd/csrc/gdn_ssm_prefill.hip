@@ -1701,12 +1701,12 @@ __global__ __launch_bounds__(256, N > 128 || FINE ? 1 : 2) void ssm_chunk_kernel
 
 // Segments per sequence: as many as fill the chip once, which is two waves per
 // SIMD, or one where a wave needs more than 256 registers (N = 256, fp32).  One
-// 64-head prompt of 32,768 tokens: 463 us at 2,048 waves, 478 at 3,072, 477 at
-// 4,096; N = 256 (32 heads, 4,096 tokens) 100 us at 1,024, 127 at 1,536 and 129 at
-// 2,048.  Prompts of given lengths end at different times and take twice as many
-// (eight of up to 2,048 tokens: 313 against 335 us).  A segment has at least two
-// chunks, in fp32 one (64 heads, 512 tokens: 54 us with four, 43 with two, 47 with
-// one; fp32, 32 heads, 256 tokens: 53, 45 and 36 us).
+// 64-head prompt of 32,768 tokens: 463 us at 2,048 waves, 478 at half as many
+// again, 477 at 4,096; N = 256 (32 heads, 4,096 tokens) 100 us at 1,024, 127 at
+// 1,536 and 129 at 2,048.  Prompts of given lengths end at different times and take
+// twice as many (eight of up to 2,048 tokens: 313 against 335 us).  A segment has at
+// least two chunks, in fp32 one (64 heads, 512 tokens: 54 us with four, 43 with two,
+// 47 with one; fp32, 32 heads, 256 tokens: 53, 45 and 36 us).
 // Returns the number before it is evened out, which does not fall as T grows.
 static int segments(const SsmGeo& g, int T, bool ragged, int& segs, int& per) {
     const int nc = (T + Q - 1) / Q;
