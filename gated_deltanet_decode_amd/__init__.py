@@ -26,6 +26,10 @@ __all__ = [
     "SsmDims", "ssm_dims", "ssm_conv_channels", "ssm_state_bytes", "ssm_conv_tail_bytes", "ssm_decode_token",
     "ssm_prefill_workspace_bytes", "ssm_prefill", "SSM_MAX_TOKENS",
     "beam_select_workspace_bytes", "beam_select", "beam_reorder", "MAX_BEAMS", "MAX_BEAM_SELECT",
+    "LruDims", "lru_dims", "lru_state_bytes", "lru_decode_token", "lru_prefill_workspace_bytes", "lru_saved_bytes",
+    "lru_prefill", "lru_backward_workspace_bytes", "lru_backward", "LRU_MAX_WIDTH", "LRU_MAX_TOKENS",
+    "residual_norm", "residual_norm_backward_workspace_bytes", "residual_norm_backward", "gated_norm",
+    "gated_norm_backward_workspace_bytes", "gated_norm_backward", "NORM_MAX_WIDTH",
     "LIB_PATH", "MAX_TREE_NODES", "MAX_TREE_DEPTH", "PREFILL_CHUNK", "PREFILL_SEGMENT", "F32", "BF16",
 ]
 
@@ -41,6 +45,10 @@ NOALLOC_SCRATCH_BYTES = 16 << 20
 SSM_MAX_TOKENS = 1 << 22
 MAX_BEAMS = 32
 MAX_BEAM_SELECT = 64
+LRU_MAX_WIDTH = 1 << 18
+LRU_MAX_TOKENS = 1 << 22
+NORM_MAX_WIDTH = 16384
+_GATE_FIRST, _WEIGHT_PER_HEAD = 1, 2
 _STATUS_TREE = 5
 
 if not os.path.exists(LIB_PATH):
@@ -86,7 +94,26 @@ def ssm_dims(batch, num_heads, num_groups, head_dim, state_dim, conv_width=4, ac
                    BF16 if act in ("bf16", BF16, torch.bfloat16) else F32)
 
 
+class LruDims(C.Structure):
+    """A gated linear recurrent layer (gdn_lru_dims)."""
+    _fields_ = [(n, C.c_int32) for n in ("batch", "width", "act_dtype")]
+
+    @property
+    def act_torch(self):
+        return torch.bfloat16 if self.act_dtype == BF16 else torch.float32
+
+
+def lru_dims(batch, width, act="bf16") -> LruDims:
+    return LruDims(batch, width, BF16 if act in ("bf16", BF16, torch.bfloat16) else F32)
+
+
+class _LruPitches(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("x", "r", "i", "z", "y")]
+
+
 _P = C.c_void_p
+_L = C.POINTER(LruDims)
+_LP = C.POINTER(_LruPitches)
 _M = C.POINTER(SsmDims)
 _D = C.POINTER(Dims)
 _I = C.c_int32
@@ -131,6 +158,20 @@ _sig = {
     "gdn_beam_select": ([_I, _I, _I, C.c_int64, _I, _P, _P, _P, _I, _I, _P, _P, _P, _P, C.c_size_t, _P], C.c_int),
     "gdn_beam_reorder": ([_D, _I, _P, _P, _P, _P, _P], C.c_int),
     "gdn_ssm_beam_reorder": ([_M, _I, _P, _P, _P, _P, _P], C.c_int),
+    "gdn_lru_state_bytes": ([_L], C.c_size_t),
+    "gdn_lru_decode_token": ([_L, _LP] + [_P] * 8, C.c_int),
+    "gdn_lru_prefill_workspace_bytes": ([_L, _I], C.c_size_t),
+    "gdn_lru_saved_bytes": ([_L, _I], C.c_size_t),
+    "gdn_lru_prefill": ([_L, _LP, _P, _I] + [_P] * 10 + [C.c_size_t, _P], C.c_int),
+    "gdn_lru_backward_workspace_bytes": ([_L, _I], C.c_size_t),
+    "gdn_lru_backward": ([_L, _LP, _LP, _I] + [_P] * 17 + [C.c_size_t, _P], C.c_int),
+    "gdn_residual_norm": ([C.c_int64, _I, _I, _I, C.c_float] + [_P] * 8, C.c_int),
+    "gdn_residual_norm_backward_workspace_bytes": ([C.c_int64, _I], C.c_size_t),
+    "gdn_residual_norm_backward": ([C.c_int64, _I, _I, _I, C.c_float] + [_P] * 13 + [C.c_size_t, _P], C.c_int),
+    "gdn_gated_norm": ([C.c_int64] + [_I] * 5 + [C.c_float, _P, _P, C.c_int64, _P, _P, _P], C.c_int),
+    "gdn_gated_norm_backward_workspace_bytes": ([C.c_int64, _I, _I], C.c_size_t),
+    "gdn_gated_norm_backward": ([C.c_int64] + [_I] * 5 + [C.c_float, _P, _P, C.c_int64, _P, _P, _P, _P, C.c_int64, _P,
+                                                         _P, C.c_size_t, _P], C.c_int),
 }
 for _name, (_args, _res) in _sig.items():
     _f = getattr(_lib, _name)
@@ -626,3 +667,240 @@ def beam_reorder(d, state, tail, parent, status=None, stream=None) -> None:
     _check(f(C.byref(d), beams, _p(state, "state", torch.float32, d.batch * n, dev),
              _p(tail, "conv_tail", d.act_torch, d.batch * d.C * 4, dev), _p(parent, "parent", torch.int32, d.batch, dev),
              None if status is None else _p(status, "status", torch.int32, groups, dev), s), name)
+
+
+# ------------------------------------------------ gated linear recurrent layers
+
+def _rows(t, name, dtype, lead, W, dev):
+    """(address, pitch) of rows of W contiguous values that follow each other at one pitch, lead of
+    them in all; pitch 0 for a contiguous tensor.  A slice of a wider projection's output is one."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.numel() == lead * W:
+            if t.is_contiguous():
+                return t.data_ptr(), 0
+            shape, strides = t.shape, t.stride()
+            if shape[-1] == W and (W == 1 or strides[-1] == 1):
+                pitch, span = 0, 1          # span: rows of the dimensions behind this one
+                for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+                    if n == 1:
+                        continue
+                    if pitch == 0:
+                        pitch = s
+                    if s != pitch * span:
+                        break
+                    span *= n
+                else:
+                    return t.data_ptr(), max(pitch, 0)
+            raise ValueError(f"{name} must have contiguous rows of {W} at one pitch")
+    except AttributeError:
+        pass
+    return _p(t, name, dtype, lead * W, dev), 0
+
+
+def _pitches(x, r, i, z, y):
+    return C.byref(_LruPitches(x, r, i, z, y)) if x or r or i or z or y else None
+
+
+def lru_state_bytes(d: LruDims) -> int:
+    return _lib.gdn_lru_state_bytes(C.byref(d))
+
+
+def lru_decode_token(d: LruDims, state, x, r, i, A, y, z=None, stream=None) -> None:
+    """One token of a gated linear recurrent layer: x, r, i, y and z [B][W], state [B][W] in place."""
+    B, W, act, f32 = d.batch, d.width, torch.bfloat16 if d.act_dtype == BF16 else torch.float32, torch.float32
+    dev, s = _here(stream)
+    (xp, px), (rp, pr), (ip, pi) = _rows(x, "x", act, B, W, dev), _rows(r, "r", act, B, W, dev), _rows(i, "i", act, B, W, dev)
+    zp, pz = (None, 0) if z is None else _rows(z, "z", act, B, W, dev)
+    yp, py = _rows(y, "y", act, B, W, dev)
+    _check(_lib.gdn_lru_decode_token(C.byref(d), _pitches(px, pr, pi, pz, py), _p(state, "state", f32, B * W, dev), xp, rp,
+                                     ip, _p(A, "A", f32, W, dev), zp, yp, s), "gdn_lru_decode_token")
+
+
+def lru_prefill_workspace_bytes(d: LruDims, T: int) -> int:
+    return _lib.gdn_lru_prefill_workspace_bytes(C.byref(d), T)
+
+
+def lru_saved_bytes(d: LruDims, T: int) -> int:
+    return _lib.gdn_lru_saved_bytes(C.byref(d), T)
+
+
+def _lru_tokens(d, x, call):
+    if d.batch < 1 or d.width < 1:
+        raise GdnError(2, call)
+    if not isinstance(x, torch.Tensor) or not x.numel() or x.numel() % (d.batch * d.width):
+        raise ValueError("x must be [B][T][W]")
+    T = x.numel() // (d.batch * d.width)
+    if T >= 1 << 31:   # C's integers would wrap
+        raise GdnError(2, call)
+    return T
+
+
+def _room(buf, name, need, dev):
+    """Address and bytes of a device buffer of at least need bytes; None serves where none are needed."""
+    if buf is None and need == 0:
+        return None, 0
+    ptr, nbytes = _blob(buf, need, name)
+    if buf.get_device() != dev:
+        raise ValueError(f"{name} is on {buf.device}, but the current device is cuda:{dev}")
+    return ptr, nbytes
+
+
+def lru_prefill(d: LruDims, state, x, r, i, A, y, workspace, z=None, lengths=None, saved=None, status=None,
+                stream=None) -> None:
+    """Prompts of a gated linear recurrent layer, or a training step's forward pass: x, r, i, y and z
+    [B][T][W] (slices of wider rows are taken as they are), state [B][W] in place.  lengths [B]
+    (int32, device): tokens of each sequence, None for T.  saved: a device byte tensor of at least
+    lru_saved_bytes(d, T) bytes for lru_backward.  workspace: one of at least
+    lru_prefill_workspace_bytes(d, T) bytes (None where that is 0)."""
+    T = _lru_tokens(d, x, "gdn_lru_prefill")
+    B, W, act, f32 = d.batch, d.width, d.act_torch, torch.float32
+    dev, s = _here(stream)
+    n = B * T
+    (xp, px), (rp, pr), (ip, pi) = _rows(x, "x", act, n, W, dev), _rows(r, "r", act, n, W, dev), _rows(i, "i", act, n, W, dev)
+    zp, pz = (None, 0) if z is None else _rows(z, "z", act, n, W, dev)
+    yp, py = _rows(y, "y", act, n, W, dev)
+    ws, nbytes = _room(workspace, "workspace", _lib.gdn_lru_prefill_workspace_bytes(C.byref(d), T), dev)
+    keep = None if saved is None else _room(saved, "saved", _lib.gdn_lru_saved_bytes(C.byref(d), T), dev)[0]
+    _check(_lib.gdn_lru_prefill(C.byref(d), _pitches(px, pr, pi, pz, py), _p(state, "state", f32, B * W, dev), T, xp, rp, ip,
+                                _p(A, "A", f32, W, dev), zp,
+                                None if lengths is None else _p(lengths, "lengths", torch.int32, B, dev), yp, keep,
+                                None if status is None else _p(status, "status", torch.int32, B, dev), ws, nbytes, s),
+           "gdn_lru_prefill")
+
+
+def lru_backward_workspace_bytes(d: LruDims, T: int) -> int:
+    return _lib.gdn_lru_backward_workspace_bytes(C.byref(d), T)
+
+
+def lru_backward(d: LruDims, x, r, i, A, dy, saved, dx, dr, di, dA, workspace, z=None, dz=None, dstate=None,
+                 dstate0=None, lengths=None, status=None, stream=None) -> None:
+    """Gradients of lru_prefill: from dy [B][T][W] and dstate [B][W] (None: 0) to dx, dr, di, dz, dA [W]
+    and dstate0 [B][W].  x, r, i, A, z and lengths as the forward pass had them, saved as it left it;
+    rows behind a sequence's end have gradients of 0."""
+    T = _lru_tokens(d, x, "gdn_lru_backward")
+    B, W, act, f32 = d.batch, d.width, d.act_torch, torch.float32
+    dev, s = _here(stream)
+    n = B * T
+    row = lambda t, name: (None, 0) if t is None and name in ("z", "dz") else _rows(t, name, act, n, W, dev)
+    (xp, px), (rp, pr), (ip, pi), (zp, pz), (yp, py) = (row(x, "x"), row(r, "r"), row(i, "i"), row(z, "z"), row(dy, "dy"))
+    (xg, gx), (rg, gr), (ig, gi), (zg, gz) = row(dx, "dx"), row(dr, "dr"), row(di, "di"), row(dz, "dz")
+    ws, nbytes = _room(workspace, "workspace", _lib.gdn_lru_backward_workspace_bytes(C.byref(d), T), dev)
+    _check(_lib.gdn_lru_backward(C.byref(d), _pitches(px, pr, pi, pz, py), _pitches(gx, gr, gi, gz, 0), T, xp, rp, ip,
+                                 _p(A, "A", f32, W, dev), zp,
+                                 None if lengths is None else _p(lengths, "lengths", torch.int32, B, dev),
+                                 _room(saved, "saved", _lib.gdn_lru_saved_bytes(C.byref(d), T), dev)[0], yp,
+                                 None if dstate is None else _p(dstate, "dstate", f32, B * W, dev), xg, rg, ig, zg,
+                                 _p(dA, "dA", f32, W, dev),
+                                 None if dstate0 is None else _p(dstate0, "dstate0", f32, B * W, dev),
+                                 None if status is None else _p(status, "status", torch.int32, B, dev), ws, nbytes, s),
+           "gdn_lru_backward")
+
+
+# ------------------------------------------------ the norms around a block
+
+def _kind(t, name):
+    dtype = getattr(t, "dtype", None)
+    if dtype is torch.bfloat16:
+        return BF16
+    if dtype is torch.float32:
+        return F32
+    raise ValueError(f"{name} must be a bfloat16 or float32 device tensor")
+
+
+def _width(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() < 1 or not t.numel():
+        raise ValueError(f"{name} must be [rows][W]")
+    W = t.shape[-1]
+    if W >= 1 << 31:   # C's integers would wrap
+        raise ValueError(f"{name} has rows of {W}")
+    return W, t.numel() // W
+
+
+def residual_norm(residual, delta, w, out, y, scale=None, w_post=None, eps=1e-6, stream=None) -> None:
+    """The residual sum behind a block and the norm before the next: out = residual + scale * n with n =
+    delta, or its RMS norm times w_post; y = RMS norm of out times w.  residual, out [rows][W] (fp32, or
+    delta's and y's type; out may be residual); w, scale, w_post [W] fp32.  delta and out None: the norm
+    of residual alone."""
+    W, rows = _width(residual, "residual")
+    res, act = _kind(residual, "residual"), _kind(y, "y")
+    dev, s = _here(stream)
+    n, f32, rt, at = rows * W, torch.float32, residual.dtype, y.dtype
+    _check(_lib.gdn_residual_norm(rows, W, act, res, eps, _p(residual, "residual", rt, n, dev),
+                                  None if delta is None else _p(delta, "delta", at, n, dev),
+                                  None if scale is None else _p(scale, "scale", f32, W, dev),
+                                  None if w_post is None else _p(w_post, "w_post", f32, W, dev), _p(w, "w", f32, W, dev),
+                                  None if out is None else _p(out, "out", rt, n, dev), _p(y, "y", at, n, dev), s),
+           "gdn_residual_norm")
+
+
+def residual_norm_backward_workspace_bytes(rows: int, W: int) -> int:
+    return _lib.gdn_residual_norm_backward_workspace_bytes(rows, W)
+
+
+def residual_norm_backward(out, delta, w, dy, dresidual, ddelta, dw, workspace, ds=None, scale=None, w_post=None,
+                           dscale=None, dw_post=None, eps=1e-6, stream=None) -> None:
+    """Gradients of residual_norm: out as it left it (where delta is None, the residual), dy [rows][W], ds
+    the gradient that reaches out from elsewhere (None: 0).  dresidual may be ds."""
+    W, rows = _width(out, "out")
+    res, act = _kind(out, "out"), _kind(dy, "dy")
+    dev, s = _here(stream)
+    n, f32, rt, at = rows * W, torch.float32, out.dtype, dy.dtype
+    ws, nbytes = _room(workspace, "workspace", _lib.gdn_residual_norm_backward_workspace_bytes(rows, W), dev)
+    opt = lambda t, name, dtype, k: None if t is None else _p(t, name, dtype, k, dev)
+    _check(_lib.gdn_residual_norm_backward(rows, W, act, res, eps, _p(out, "out", rt, n, dev), opt(delta, "delta", at, n),
+                                           opt(scale, "scale", f32, W), opt(w_post, "w_post", f32, W),
+                                           _p(w, "w", f32, W, dev), _p(dy, "dy", at, n, dev), opt(ds, "ds", rt, n),
+                                           _p(dresidual, "dresidual", rt, n, dev), opt(ddelta, "ddelta", at, n),
+                                           _p(dw, "dw", f32, W, dev), opt(dscale, "dscale", f32, W),
+                                           opt(dw_post, "dw_post", f32, W), ws, nbytes, s), "gdn_residual_norm_backward")
+
+
+def _heads(o, w, gate_first):
+    if not isinstance(o, torch.Tensor) or o.dim() < 2 or not o.numel():
+        raise ValueError("o must be [rows][H][D]")
+    H, D = o.shape[-2:]
+    if H * D >= 1 << 31:   # C's integers would wrap
+        raise ValueError(f"o has rows of {H} x {D}")
+    each = isinstance(w, torch.Tensor) and w.numel() != D
+    return o.numel() // (H * D), H, D, (_GATE_FIRST if gate_first else 0) | (_WEIGHT_PER_HEAD if each else 0), D * (H if each else 1)
+
+
+def _head_rows(t, name, dtype, rows, H, D, dev):
+    """_rows over the heads' H * D values; the heads of a row lie next to each other."""
+    if isinstance(t, torch.Tensor) and not t.is_contiguous():
+        if t.dim() < 2 or tuple(t.shape[-2:]) != (H, D) or (H > 1 and t.stride(-2) != D) or (D > 1 and t.stride(-1) != 1):
+            raise ValueError(f"{name} must be [rows][H][D] with contiguous rows at one pitch")
+        t = t.flatten(-2) if H * D else t
+    return _rows(t, name, dtype, rows, H * D, dev)
+
+
+def gated_norm(o, z, w, y, eps=1e-6, gate_first=False, stream=None) -> None:
+    """The norm of a mixer's output with its gate: y = RMS norm of o over each head's D values, times w
+    and SiLU(z); with gate_first the norm is of o * SiLU(z).  o [rows][H][D] (fp32, or z's and y's
+    type); z [rows][H][D], its rows may be a slice of wider ones; w [D] or [H][D] fp32."""
+    rows, H, D, flags, nw = _heads(o, w, gate_first)
+    ok, act = _kind(o, "o"), _kind(y, "y")
+    dev, s = _here(stream)
+    n, at = rows * H * D, y.dtype
+    zp, pz = _head_rows(z, "z", at, rows, H, D, dev)
+    _check(_lib.gdn_gated_norm(rows, H, D, ok, act, flags, eps, _p(o, "o", o.dtype, n, dev), zp, pz,
+                               _p(w, "w", torch.float32, nw, dev), _p(y, "y", at, n, dev), s), "gdn_gated_norm")
+
+
+def gated_norm_backward_workspace_bytes(rows: int, H: int, D: int) -> int:
+    return _lib.gdn_gated_norm_backward_workspace_bytes(rows, H, D)
+
+
+def gated_norm_backward(o, z, w, dy, do, dz, dw, workspace, eps=1e-6, gate_first=False, stream=None) -> None:
+    """Gradients of gated_norm: do has o's type, dz z's (its rows may be a slice), dw w's shape."""
+    rows, H, D, flags, nw = _heads(o, w, gate_first)
+    ok, act = _kind(o, "o"), _kind(dy, "dy")
+    dev, s = _here(stream)
+    n, at, f32 = rows * H * D, dy.dtype, torch.float32
+    zp, pz = _head_rows(z, "z", at, rows, H, D, dev)
+    zg, gz = _head_rows(dz, "dz", at, rows, H, D, dev)
+    ws, nbytes = _room(workspace, "workspace", _lib.gdn_gated_norm_backward_workspace_bytes(rows, H, D), dev)
+    _check(_lib.gdn_gated_norm_backward(rows, H, D, ok, act, flags, eps, _p(o, "o", o.dtype, n, dev), zp, pz,
+                                        _p(w, "w", f32, nw, dev), _p(dy, "dy", at, n, dev),
+                                        _p(do, "do", o.dtype, n, dev), zg, gz, _p(dw, "dw", f32, nw, dev), ws, nbytes, s),
+           "gdn_gated_norm_backward")

@@ -32,7 +32,7 @@ FLAGS = [
 ]
 SOURCES = ["gdn_api.hip", "gdn_decode.hip", "gdn_token.hip", "gdn_tree.hip", "gdn_prefill.hip", "gdn_state.hip",
            "gdn_selfcheck.hip", "gdn_noalloc.hip", "gdn_ssm.hip",
-           "gdn_ssm_prefill.hip", "gdn_beam.hip"]
+           "gdn_ssm_prefill.hip", "gdn_beam.hip", "gdn_lru.hip", "gdn_norm.hip"]
 # The prefill kernels keep their MFMA accumulators in ordinary VGPRs: the scan
 # scales and converts its state accumulators every chunk, which would otherwise
 # cost a copy out of and back into the accumulation registers each time.

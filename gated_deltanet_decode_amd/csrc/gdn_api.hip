@@ -108,6 +108,101 @@ bool beam_sizes_ok(int32_t batch, int32_t beams, int32_t vocab, int32_t select) 
            select <= static_cast<int64_t>(beams) * vocab && static_cast<int64_t>(batch) * beams <= (1ll << 20);
 }
 
+// An operand as the alias check sees it: `rows` rows of `bytes` bytes, `pitch` bytes apart.
+struct Span {
+    const void* p;
+    int64_t rows, bytes, pitch;
+};
+
+bool overlap(const Span& a, const Span& b) {
+    if (!a.p || !b.p)
+        return false;
+    const int64_t pa = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p)),
+                  pb = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p));
+    const int64_t ea = pa + (a.rows - 1) * a.pitch + a.bytes, eb = pb + (b.rows - 1) * b.pitch + b.bytes;
+    if (pa >= eb || pb >= ea)
+        return false;
+    if (a.pitch != b.pitch)
+        return true;
+    // rows of one pitch may lie between each other's
+    int64_t d = (pb - pa) % a.pitch;
+    d = d < 0 ? d + a.pitch : d;
+    return d < a.bytes || a.pitch - d < b.bytes;
+}
+
+// Whether an output overlaps an input or another output.
+bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& i : ins)
+            if (overlap(*o, i))
+                return true;
+        for (const Span* u = o + 1; u != outs.end(); ++u)
+            if (overlap(*o, *u))
+                return true;
+    }
+    return false;
+}
+
+gdn_status lru_pitch(const gdn_lru_pitches* q, int W, gdn::Pitches& p) {
+    const int64_t w = W;
+    p = {w, w, w, w, w};
+    if (!q)
+        return GDN_OK;
+    const int64_t in[5] = {q->x, q->r, q->i, q->z, q->y};
+    int64_t* const out[5] = {&p.x, &p.r, &p.i, &p.z, &p.y};
+    for (int k = 0; k < 5; ++k) {
+        if (in[k] == 0)
+            continue;
+        // a tile of rows is addressed by 32-bit byte offsets
+        if (in[k] < w || in[k] % 8 != 0 || in[k] > (1 << 20))
+            return GDN_ERR_SHAPE;
+        *out[k] = in[k];
+    }
+    return GDN_OK;
+}
+
+gdn_status check_lru(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, int64_t T, gdn::LruGeo& g) {
+    if (!d)
+        return GDN_ERR_NULL;
+    if (d->act_dtype != GDN_F32 && d->act_dtype != GDN_BF16)
+        return GDN_ERR_DTYPE;
+    if (d->batch < 1 || d->width < 8 || d->width % 8 != 0 || d->width > GDN_LRU_MAX_WIDTH || T < 1 ||
+        T > GDN_LRU_MAX_TOKENS)
+        return GDN_ERR_SHAPE;
+    // a launch counts 2^32 threads, and workgroups of 512 take 64 channels and at least 64 tokens
+    if (static_cast<int64_t>(d->batch) * ((d->width + 63) / 64) * ((T + 63) / 64) >= (1ll << 23))
+        return GDN_ERR_SHAPE;
+    g.B = d->batch;
+    g.W = d->width;
+    g.bf16 = d->act_dtype == GDN_BF16;
+    return lru_pitch(pitch, g.W, g.p);
+}
+
+Span lru_rows(const gdn::LruGeo& g, const void* p, int64_t T, int64_t pitch) {
+    const int64_t e = g.bf16 ? 2 : 4;
+    return {p, g.B * T, g.W * e, pitch * e};
+}
+Span dense(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+
+bool act_ok(int32_t t) { return t == GDN_F32 || t == GDN_BF16; }
+
+gdn_status norm_sizes(int64_t rows, int32_t H, int32_t D, int32_t act, int32_t other, float eps) {
+    if (!act_ok(act) || !act_ok(other) || (other != GDN_F32 && other != act))
+        return GDN_ERR_DTYPE;
+    if (rows < 1 || rows >= (1ll << 31) || H < 1 || H > 65536 || rows * H >= (1ll << 31) || D < 8 || D % 8 != 0 ||
+        D > GDN_NORM_MAX_WIDTH || !(eps > 0.0f) || !(eps <= 3.402823466e38f))
+        return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+
+gdn_status workspace_ok(const void* workspace, size_t have, size_t need) {
+    if (need == 0)
+        return GDN_OK;
+    if (!workspace || have < need)
+        return GDN_ERR_WORKSPACE;
+    return reinterpret_cast<uintptr_t>(workspace) & 255u ? GDN_ERR_ALIGN : GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -668,6 +763,229 @@ gdn_status gdn_ssm_beam_reorder(const gdn_ssm_dims* d, int32_t beams, float* sta
         return st;
     return beam_reorder(g.B, beams, static_cast<int64_t>(g.H) * g.P * g.N * 4,
                         static_cast<int64_t>(g.C) * 4 * (g.bf16 ? 2 : 4), state, conv_tail, parent, status, stream);
+}
+
+size_t gdn_lru_state_bytes(const gdn_lru_dims* d) {
+    gdn::LruGeo g;
+    return check_lru(d, nullptr, 1, g) == GDN_OK ? static_cast<size_t>(g.B) * g.W * sizeof(float) : 0;
+}
+
+gdn_status gdn_lru_decode_token(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, float* state, const void* x,
+                                const void* r, const void* i, const float* A, const void* z, void* y, void* stream) {
+    gdn::LruGeo g;
+    gdn_status st = check_lru(d, pitch, 1, g);
+    if (st == GDN_OK)
+        st = ptrs_ok({state, x, r, i, A, y});
+    if (st == GDN_OK)
+        st = aligned_or_null({z});
+    if (st != GDN_OK)
+        return st;
+    if (any_overlap({lru_rows(g, y, 1, g.p.y), dense(state, 4ll * g.B * g.W)},
+                    {lru_rows(g, x, 1, g.p.x), lru_rows(g, r, 1, g.p.r), lru_rows(g, i, 1, g.p.i),
+                     lru_rows(g, z, 1, g.p.z), dense(A, 4ll * g.W)}))
+        return GDN_ERR_ALIAS;
+    return launched(gdn::launch_lru_token(g, {state, x, r, i, A, z, y}, as_stream(stream)));
+}
+
+size_t gdn_lru_prefill_workspace_bytes(const gdn_lru_dims* d, int32_t T) {
+    gdn::LruGeo g;
+    return check_lru(d, nullptr, T, g) == GDN_OK ? gdn::lru_prefill_ws_bytes(g, T) : 0;
+}
+
+size_t gdn_lru_saved_bytes(const gdn_lru_dims* d, int32_t T) {
+    gdn::LruGeo g;
+    return check_lru(d, nullptr, T, g) == GDN_OK ? gdn::lru_saved_bytes(g, T) : 0;
+}
+
+gdn_status gdn_lru_prefill(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, float* state, int32_t T, const void* x,
+                           const void* r, const void* i, const float* A, const void* z, const int32_t* lengths,
+                           void* y, float* saved, int32_t* status, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    gdn::LruGeo g;
+    gdn_status st = check_lru(d, pitch, T, g);
+    if (st == GDN_OK)
+        st = ptrs_ok({state, x, r, i, A, y});
+    if (st == GDN_OK)
+        st = aligned_or_null({z, lengths, saved, status});
+    if (st != GDN_OK)
+        return st;
+    const size_t need = gdn::lru_prefill_ws_bytes(g, T);
+    st = workspace_ok(workspace, workspace_bytes, need);
+    if (st != GDN_OK)
+        return st;
+    const Span ws = dense(need ? workspace : nullptr, static_cast<int64_t>(need));
+    if (any_overlap({lru_rows(g, y, T, g.p.y), dense(state, 4ll * g.B * g.W),
+                     dense(saved, static_cast<int64_t>(gdn::lru_saved_bytes(g, T))), dense(status, 4ll * g.B), ws},
+                    {lru_rows(g, x, T, g.p.x), lru_rows(g, r, T, g.p.r), lru_rows(g, i, T, g.p.i),
+                     lru_rows(g, z, T, g.p.z), dense(A, 4ll * g.W), dense(lengths, 4ll * g.B)}))
+        return GDN_ERR_ALIAS;
+    return launched(gdn::launch_lru_prefill(g, {state, x, r, i, A, z, y}, T, lengths, saved, status, workspace,
+                                            as_stream(stream)));
+}
+
+size_t gdn_lru_backward_workspace_bytes(const gdn_lru_dims* d, int32_t T) {
+    gdn::LruGeo g;
+    return check_lru(d, nullptr, T, g) == GDN_OK ? gdn::lru_backward_ws_bytes(g, T) : 0;
+}
+
+gdn_status gdn_lru_backward(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, const gdn_lru_pitches* grad_pitch,
+                            int32_t T, const void* x, const void* r, const void* i, const float* A, const void* z,
+                            const int32_t* lengths, const float* saved, const void* dy, const float* dstate, void* dx,
+                            void* dr, void* di, void* dz, float* dA, float* dstate0, int32_t* status, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    gdn::LruGeo g;
+    gdn_status st = check_lru(d, pitch, T, g);
+    if (st == GDN_OK)
+        st = lru_pitch(grad_pitch, g.W, g.gp);
+    if (st == GDN_OK)
+        st = ptrs_ok({x, r, i, A, saved, dy, dx, dr, di, dA});
+    if (st == GDN_OK && (z == nullptr) != (dz == nullptr))
+        st = GDN_ERR_NULL;
+    if (st == GDN_OK)
+        st = aligned_or_null({z, dz, lengths, dstate, dstate0, status});
+    if (st != GDN_OK)
+        return st;
+    const size_t need = gdn::lru_backward_ws_bytes(g, T);
+    st = workspace_ok(workspace, workspace_bytes, need);
+    if (st != GDN_OK)
+        return st;
+    const int64_t rows4 = 4ll * g.B * g.W;
+    const Span in_x = lru_rows(g, x, T, g.p.x), in_r = lru_rows(g, r, T, g.p.r), in_i = lru_rows(g, i, T, g.p.i),
+               in_z = lru_rows(g, z, T, g.p.z), in_dy = lru_rows(g, dy, T, g.p.y), in_A = dense(A, 4ll * g.W),
+               in_len = dense(lengths, 4ll * g.B),
+               in_saved = dense(saved, static_cast<int64_t>(gdn::lru_saved_bytes(g, T)));
+    // dstate0 may be dstate itself: a channel's first is read before its last is written
+    if (any_overlap({lru_rows(g, dx, T, g.gp.x), lru_rows(g, dr, T, g.gp.r), lru_rows(g, di, T, g.gp.i),
+                     lru_rows(g, dz, T, g.gp.z), dense(dA, 4ll * g.W), dense(dstate0, rows4), dense(status, 4ll * g.B),
+                     dense(workspace, static_cast<int64_t>(need))},
+                    {in_x, in_r, in_i, in_z, in_dy, in_A, in_len, in_saved, dense(dstate == dstate0 ? nullptr : dstate, rows4)}))
+        return GDN_ERR_ALIAS;
+    return launched(gdn::launch_lru_backward(g, {x, r, i, A, z, saved, dy, dstate, dx, dr, di, dz, dA, dstate0}, T,
+                                             lengths, status, workspace, as_stream(stream)));
+}
+
+gdn_status gdn_residual_norm(int64_t rows, int32_t W, int32_t act_dtype, int32_t res_dtype, float eps,
+                             const void* residual, const void* delta, const float* scale, const float* w_post,
+                             const float* w, void* out, void* y, void* stream) {
+    gdn_status st = norm_sizes(rows, 1, W, act_dtype, res_dtype, eps);
+    if (st == GDN_OK)
+        st = ptrs_ok({residual, w, y});
+    if (st == GDN_OK && ((delta == nullptr) != (out == nullptr) || (!delta && (scale || w_post))))
+        st = GDN_ERR_NULL;
+    if (st == GDN_OK)
+        st = aligned_or_null({delta, scale, w_post, out});
+    if (st != GDN_OK)
+        return st;
+    const bool act16 = act_dtype == GDN_BF16, res16 = res_dtype == GDN_BF16;
+    const int64_t n = rows * W, na = n * (act16 ? 2 : 4), nr = n * (res16 ? 2 : 4);
+    if (any_overlap({dense(out, nr), dense(y, na)},
+                    {dense(out == residual ? nullptr : residual, nr), dense(delta, na), dense(scale, 4ll * W),
+                     dense(w_post, 4ll * W), dense(w, 4ll * W)}) ||
+        overlap(dense(y, na), dense(residual, nr)))
+        return GDN_ERR_ALIAS;
+    return launched(gdn::launch_residual_norm({rows, W, act16, res16, eps, residual, delta, scale, w_post, w, out, y},
+                                              as_stream(stream)));
+}
+
+size_t gdn_residual_norm_backward_workspace_bytes(int64_t rows, int32_t W) {
+    return norm_sizes(rows, 1, W, GDN_F32, GDN_F32, 1.0f) == GDN_OK ? gdn::residual_norm_back_ws_bytes(rows, W) : 0;
+}
+
+gdn_status gdn_residual_norm_backward(int64_t rows, int32_t W, int32_t act_dtype, int32_t res_dtype, float eps,
+                                      const void* out, const void* delta, const float* scale, const float* w_post,
+                                      const float* w, const void* dy, const void* ds, void* dresidual, void* ddelta,
+                                      float* dw, float* dscale, float* dw_post, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+    gdn_status st = norm_sizes(rows, 1, W, act_dtype, res_dtype, eps);
+    if (st == GDN_OK)
+        st = ptrs_ok({out, w, dy, dresidual, dw});
+    if (st == GDN_OK && ((delta == nullptr) != (ddelta == nullptr) || (scale == nullptr) != (dscale == nullptr) ||
+                         (w_post == nullptr) != (dw_post == nullptr) || (!delta && (scale || w_post))))
+        st = GDN_ERR_NULL;
+    if (st == GDN_OK)
+        st = aligned_or_null({delta, scale, w_post, ds, ddelta, dscale, dw_post});
+    if (st != GDN_OK)
+        return st;
+    const size_t need = gdn::residual_norm_back_ws_bytes(rows, W);
+    st = workspace_ok(workspace, workspace_bytes, need);
+    if (st != GDN_OK)
+        return st;
+    const bool act16 = act_dtype == GDN_BF16, res16 = res_dtype == GDN_BF16;
+    const int64_t n = rows * W, na = n * (act16 ? 2 : 4), nr = n * (res16 ? 2 : 4), nw = 4ll * W;
+    if (any_overlap({dense(dresidual, nr), dense(ddelta, na), dense(dw, nw), dense(dscale, nw), dense(dw_post, nw),
+                     dense(workspace, static_cast<int64_t>(need))},
+                    {dense(out, nr), dense(delta, na), dense(scale, nw), dense(w_post, nw), dense(w, nw),
+                     dense(dy, na), dense(ds == dresidual ? nullptr : ds, nr)}))
+        return GDN_ERR_ALIAS;
+    return launched(gdn::launch_residual_norm_backward({rows, W, act16, res16, eps, out, delta, scale, w_post, w, dy,
+                                                        ds, dresidual, ddelta, dw, dscale, dw_post},
+                                                       workspace, as_stream(stream)));
+}
+
+static gdn_status gated_sizes(int64_t rows, int32_t H, int32_t D, int32_t o_dtype, int32_t act_dtype, int32_t flags,
+                              float eps, int64_t& z_pitch) {
+    const gdn_status st = norm_sizes(rows, H, D, act_dtype, o_dtype, eps);
+    if (st != GDN_OK)
+        return st;
+    const int64_t row = static_cast<int64_t>(H) * D;
+    if (z_pitch == 0)
+        z_pitch = row;
+    // weights are counted in 32 bits; a pitch of 2^32 elements keeps offsets within 64
+    if (flags & ~(GDN_GATE_FIRST | GDN_WEIGHT_PER_HEAD) || row >= (1ll << 30) || z_pitch < row || z_pitch % 8 != 0 ||
+        z_pitch > (1ll << 32))
+        return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+
+gdn_status gdn_gated_norm(int64_t rows, int32_t H, int32_t D, int32_t o_dtype, int32_t act_dtype, int32_t flags,
+                          float eps, const void* o, const void* z, int64_t z_pitch, const float* w, void* y,
+                          void* stream) {
+    gdn_status st = gated_sizes(rows, H, D, o_dtype, act_dtype, flags, eps, z_pitch);
+    if (st == GDN_OK)
+        st = ptrs_ok({o, z, w, y});
+    if (st != GDN_OK)
+        return st;
+    const bool o16 = o_dtype == GDN_BF16, act16 = act_dtype == GDN_BF16, each = flags & GDN_WEIGHT_PER_HEAD;
+    const int64_t row = static_cast<int64_t>(H) * D, ea = act16 ? 2 : 4;
+    const int64_t nw = 4ll * D * (each ? H : 1);
+    if (any_overlap({dense(y, rows * row * ea)}, {dense(o, rows * row * (o16 ? 2 : 4)), dense(w, nw)}) ||
+        overlap({y, rows, row * ea, row * ea}, {z, rows, row * ea, z_pitch * ea}))
+        return GDN_ERR_ALIAS;
+    return launched(gdn::launch_gated_norm(
+        {rows, H, D, o16, act16, each, (flags & GDN_GATE_FIRST) != 0, eps, z_pitch, o, z, w, y}, as_stream(stream)));
+}
+
+size_t gdn_gated_norm_backward_workspace_bytes(int64_t rows, int32_t H, int32_t D) {
+    int64_t pitch = 0;
+    return gated_sizes(rows, H, D, GDN_F32, GDN_F32, 0, 1.0f, pitch) == GDN_OK
+               ? gdn::gated_norm_back_ws_bytes(rows, H, D) : 0;
+}
+
+gdn_status gdn_gated_norm_backward(int64_t rows, int32_t H, int32_t D, int32_t o_dtype, int32_t act_dtype,
+                                   int32_t flags, float eps, const void* o, const void* z, int64_t z_pitch,
+                                   const float* w, const void* dy, void* do_, void* dz, int64_t dz_pitch, float* dw,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    gdn_status st = gated_sizes(rows, H, D, o_dtype, act_dtype, flags, eps, z_pitch);
+    if (st == GDN_OK)
+        st = gated_sizes(rows, H, D, o_dtype, act_dtype, flags, eps, dz_pitch);
+    if (st == GDN_OK)
+        st = ptrs_ok({o, z, w, dy, do_, dz, dw});
+    if (st != GDN_OK)
+        return st;
+    const size_t need = gdn::gated_norm_back_ws_bytes(rows, H, D);
+    st = workspace_ok(workspace, workspace_bytes, need);
+    if (st != GDN_OK)
+        return st;
+    const bool o16 = o_dtype == GDN_BF16, act16 = act_dtype == GDN_BF16, each = flags & GDN_WEIGHT_PER_HEAD;
+    const int64_t row = static_cast<int64_t>(H) * D, ea = act16 ? 2 : 4, no = rows * row * (o16 ? 2 : 4);
+    const int64_t nw = 4ll * D * (each ? H : 1);
+    if (any_overlap({dense(do_, no), {dz, rows, row * ea, dz_pitch * ea}, dense(dw, nw),
+                     dense(workspace, static_cast<int64_t>(need))},
+                    {dense(o, no), {z, rows, row * ea, z_pitch * ea}, dense(w, nw), dense(dy, rows * row * ea)}))
+        return GDN_ERR_ALIAS;
+    return launched(gdn::launch_gated_norm_backward(
+        {rows, H, D, o16, act16, each, (flags & GDN_GATE_FIRST) != 0, eps, z_pitch, o, z, w, nullptr},
+        {dy, do_, dz, dz_pitch, dw}, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -79,6 +79,86 @@ hipError_t launch_beam_select(const BeamGeo& g, const void* logits, const float*
 hipError_t launch_beam_reorder(int groups, int K, int64_t state_bytes, int64_t tail_bytes, void* state, void* tail,
                                const int32_t* parent, int32_t* status, hipStream_t s);
 
+// The gated linear recurrent layer: rows of W channels at a pitch of their own.
+struct Pitches {
+    int64_t x, r, i, z, y;
+};
+struct LruGeo {
+    int B, W;
+    bool bf16;
+    Pitches p, gp;   // gp: the gradients' (y unused)
+};
+struct LruArgs {
+    float* state;
+    const void *x, *r, *i;
+    const float* A;
+    const void* z;   // optional
+    void* y;
+};
+struct LruGrads {
+    const void *x, *r, *i;
+    const float* A;
+    const void* z;   // optional, with dz
+    const float* saved;
+    const void* dy;
+    const float* dstate;   // optional
+    void *dx, *dr, *di, *dz;
+    float *dA, *dstate0;   // dstate0 optional
+};
+hipError_t launch_lru_token(const LruGeo& g, const LruArgs& a, hipStream_t s);
+size_t lru_saved_bytes(const LruGeo& g, int T);
+size_t lru_prefill_ws_bytes(const LruGeo& g, int T);
+// lengths, saved, status optional.
+hipError_t launch_lru_prefill(const LruGeo& g, const LruArgs& a, int T, const int32_t* lengths, float* saved,
+                              int32_t* status, void* ws, hipStream_t s);
+size_t lru_backward_ws_bytes(const LruGeo& g, int T);
+hipError_t launch_lru_backward(const LruGeo& g, const LruGrads& a, int T, const int32_t* lengths, int32_t* status,
+                               void* ws, hipStream_t s);
+
+// The norms around a block.  Optional: delta (with out, ddelta), scale (with dscale), post (with dpost), ds.
+struct ResidualNorm {
+    int64_t rows;
+    int W;
+    bool act_bf16, res_bf16;
+    float eps;
+    const void *residual, *delta;
+    const float *scale, *post, *w;
+    void *out, *y;
+};
+struct ResidualNormGrad {
+    int64_t rows;
+    int W;
+    bool act_bf16, res_bf16;
+    float eps;
+    const void *stream, *delta;
+    const float *scale, *post, *w;
+    const void *dy, *ds;
+    void *dres, *ddelta;
+    float *dw, *dscale, *dpost;
+};
+struct GatedNorm {
+    int64_t rows;
+    int H, D;
+    bool o_bf16, act_bf16, per_head, first;
+    float eps;
+    int64_t z_pitch;
+    const void *o, *z;
+    const float* w;
+    void* y;
+};
+struct GatedNormGrad {
+    const void* dy;
+    void *dov, *dz;
+    int64_t dz_pitch;
+    float* dw;
+};
+hipError_t launch_residual_norm(const ResidualNorm& a, hipStream_t s);
+size_t residual_norm_back_ws_bytes(int64_t rows, int W);
+hipError_t launch_residual_norm_backward(const ResidualNormGrad& a, void* ws, hipStream_t s);
+hipError_t launch_gated_norm(const GatedNorm& a, hipStream_t s);
+size_t gated_norm_back_ws_bytes(int64_t rows, int H, int D);
+hipError_t launch_gated_norm_backward(const GatedNorm& a, const GatedNormGrad& g, void* ws, hipStream_t s);
+
 size_t self_check_ws_bytes(const Geo& g);
 hipError_t launch_self_check(const Geo& g, void* ws, uint32_t seed, int perturb, int32_t* result, hipStream_t s);
 // Device address of the library-held scratch array on the current device.

@@ -1,0 +1,658 @@
+// gdn_norm.hip -- the norms on either side of a block: the residual sum with
+// the norm before the next block, and the norm of a mixer's output with its
+// gate; both with their gradients.
+//
+// A row (of the residual stream, or of one head) is held in the registers of a
+// team of lanes: part of a wave, or a workgroup, so that every value is read
+// once and written once.  All of it is fp32 but for what is stored.
+#include "gdn.h"
+#include "gdn_lru.hpp"
+
+namespace gdn {
+namespace norm {
+
+using lru::silu;
+using lru::silu_slope;
+
+constexpr int kMaxSums = 3;     // weight gradients of one call
+
+// U consecutive values.
+template <typename T, int U>
+struct Unit;
+template <>
+struct Unit<uint16_t, 4> {
+    __device__ static void load(const uint16_t* p, float (&f)[4]) { Quad<uint16_t>::to_float(Quad<uint16_t>::load(p), f); }
+    __device__ static void store(uint16_t* p, const float (&f)[4]) { Quad<uint16_t>::store(p, lru::pack(f, uint16_t())); }
+};
+template <>
+struct Unit<float, 4> {
+    __device__ static void load(const float* p, float (&f)[4]) { Quad<float>::to_float(Quad<float>::load(p), f); }
+    __device__ static void store(float* p, const float (&f)[4]) { Quad<float>::store(p, lru::pack(f, float())); }
+};
+template <>
+struct Unit<uint16_t, 8> {
+    __device__ static void load(const uint16_t* p, float (&f)[8]) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[2 * k] = __uint_as_float(u[k] << 16);
+            f[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+        }
+    }
+    __device__ static void store(uint16_t* p, const float (&f)[8]) {
+        const float lo[4] = {f[0], f[1], f[2], f[3]}, hi[4] = {f[4], f[5], f[6], f[7]};
+        const uint2 a = lru::pack(lo, uint16_t()), b = lru::pack(hi, uint16_t());
+        *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
+    }
+};
+template <>
+struct Unit<float, 8> {
+    __device__ static void load(const float* p, float (&f)[8]) {
+        const float4 a = Quad<float>::load(p), b = Quad<float>::load(p + 4);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+};
+
+template <typename A, typename B>
+constexpr int unit_of() { return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4; }
+
+// A team: LPR lanes of a wave (LPR <= 64), or a whole workgroup (LPR == 0).
+template <int LPR>
+struct Team {
+    int index, slot, size, teams, flip = 0;
+    float* mem;   // 2 x 16 floats, workgroup teams only
+    __device__ explicit Team(float* m)
+        : index(LPR ? threadIdx.x % (LPR ? LPR : 1) : threadIdx.x), slot(LPR ? threadIdx.x / (LPR ? LPR : 1) : 0),
+          size(LPR ? LPR : blockDim.x), teams(LPR ? blockDim.x / (LPR ? LPR : 1) : 1), mem(m) {}
+    __device__ float sum(float v) {
+        if constexpr (LPR == 32) {
+            v = group_sum<16>(v);
+            return v + __shfl_xor(v, 16);
+        } else if constexpr (LPR != 0) {
+            return group_sum<LPR>(v);
+        } else {
+            v = group_sum<64>(v);
+            float* m = mem + flip;
+            flip ^= 16;
+            if ((threadIdx.x & 63) == 0)
+                m[threadIdx.x >> 6] = v;
+            __syncthreads();
+            const int waves = blockDim.x >> 6;
+            float s = 0.0f;
+            for (int w = 0; w < waves; ++w)
+                s += m[w];
+            return s;
+        }
+    }
+};
+
+__device__ __forceinline__ float inv_rms(float sum, float inv_n, float eps) {
+    return __builtin_amdgcn_rsqf(__builtin_fmaf(sum, inv_n, eps));
+}
+
+// ------------------------------------------------------------ residual and norm
+
+template <typename Act, typename Res, int U, int LPR, int NV, bool POST>
+__global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
+    const Res* residual, const Act* __restrict__ delta, const float* __restrict__ scale,
+    const float* __restrict__ post, const float* __restrict__ w, Res* out, Act* __restrict__ y, int64_t rows, int W,
+    float inv_n, float eps) {
+    __shared__ float mem[32];
+    Team<LPR> team(mem);
+    using RU = Unit<Res, U>;
+    using AU = Unit<Act, U>;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot; row < rows;
+         row += static_cast<int64_t>(gridDim.x) * team.teams) {
+        const int64_t base = row * W;
+        float s[NV][U], d[NV][U];
+        bool on[NV];
+        int c[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int u = (team.index + j * team.size) * U;
+            on[j] = u < W;
+            c[j] = on[j] ? u : 0;
+            RU::load(residual + base + c[j], s[j]);
+            if (delta)
+                AU::load(delta + base + c[j], d[j]);
+        }
+        if (delta) {
+            float p = 1.0f;
+            if constexpr (POST) {
+                float sq = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int k = 0; k < U; ++k)
+                        sq = on[j] ? __builtin_fmaf(d[j][k], d[j][k], sq) : sq;
+                p = inv_rms(team.sum(sq), inv_n, eps);
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float ws[U], wp[U];
+                if (scale)
+                    Unit<float, U>::load(scale + c[j], ws);
+                if constexpr (POST)
+                    Unit<float, U>::load(post + c[j], wp);
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const float n = POST ? d[j][k] * p * wp[k] : d[j][k];
+                    s[j][k] = scale ? __builtin_fmaf(ws[k], n, s[j][k]) : s[j][k] + n;
+                    if constexpr (sizeof(Res) == 2)   // y is the norm of the stream as it is stored
+                        s[j][k] = static_cast<float>(static_cast<__bf16>(s[j][k]));
+                }
+                if (on[j])
+                    RU::store(out + base + c[j], s[j]);
+            }
+        }
+        float sq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                sq = on[j] ? __builtin_fmaf(s[j][k], s[j][k], sq) : sq;
+        const float q = inv_rms(team.sum(sq), inv_n, eps);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float ww[U];
+            Unit<float, U>::load(w + c[j], ww);
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                ww[k] *= s[j][k] * q;
+            if (on[j])
+                AU::store(y + base + c[j], ww);
+        }
+    }
+}
+
+// Adds the teams' sums of one workgroup in a fixed order and writes them as row
+// blockIdx.x of parts; sums is what each thread gathered for its columns.
+template <int LPR, int U, int NV>
+__device__ __forceinline__ void write_part(const Team<LPR>& team, float (&sums)[NV][U], int W, float* lds,
+                                           float* __restrict__ part) {
+    if constexpr (LPR == 0) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (team.index + j * team.size) * U;
+            if (c < W)
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    part[c + k] = sums[j][k];
+        }
+    } else {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                lds[(team.slot * NV + j) * LPR * U + team.index * U + k] = sums[j][k];
+        __syncthreads();
+        for (int c = threadIdx.x; c < W; c += blockDim.x) {
+            const int j = c / (LPR * U), in = c % (LPR * U);
+            float s = 0.0f;
+            for (int t = 0; t < team.teams; ++t)
+                s += lds[(t * NV + j) * LPR * U + in];
+            part[c] = s;
+        }
+    }
+}
+
+template <typename Act, typename Res, int U, int LPR, int NV, bool POST>
+__global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kernel(
+    const Res* __restrict__ stream, const Act* __restrict__ delta, const float* __restrict__ scale,
+    const float* __restrict__ post, const float* __restrict__ w, const Act* __restrict__ dy, const Res* ds,
+    Res* dres, Act* __restrict__ ddelta, float* __restrict__ parts, int64_t rows, int W, float inv_n, float eps) {
+    __shared__ float mem[32];
+    __shared__ float lds[LPR ? 256 * NV * U : 1];
+    Team<LPR> team(mem);
+    using RU = Unit<Res, U>;
+    using AU = Unit<Act, U>;
+    float sw[NV][U] = {}, ss[NV][U] = {}, sp[NV][U] = {};
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot; row < rows;
+         row += static_cast<int64_t>(gridDim.x) * team.teams) {
+        const int64_t base = row * W;
+        float s[NV][U], g[NV][U], d[NV][U], t[NV][U];
+        bool on[NV];
+        int c[NV];
+        float sq = 0.0f, dot = 0.0f, dq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int u = (team.index + j * team.size) * U;
+            on[j] = u < W;
+            c[j] = on[j] ? u : 0;
+            RU::load(stream + base + c[j], s[j]);
+            AU::load(dy + base + c[j], g[j]);
+            if (delta)
+                AU::load(delta + base + c[j], d[j]);
+            if (ds)
+                RU::load(ds + base + c[j], t[j]);
+            else
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    t[j][k] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float ww[U];
+            Unit<float, U>::load(w + c[j], ww);
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (on[j]) {
+                    sq = __builtin_fmaf(s[j][k], s[j][k], sq);
+                    dot = __builtin_fmaf(g[j][k] * ww[k], s[j][k], dot);
+                    if constexpr (POST)
+                        dq = __builtin_fmaf(d[j][k], d[j][k], dq);
+                }
+        }
+        sq = team.sum(sq);
+        dot = team.sum(dot);
+        const float q = inv_rms(sq, inv_n, eps);
+        const float back = q * q * (dot * inv_n);
+        float p = 1.0f;
+        if constexpr (POST)
+            p = inv_rms(team.sum(dq), inv_n, eps);
+        float dot2 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float ww[U], ws[U], wp[U], o[U];
+            Unit<float, U>::load(w + c[j], ww);
+            if (scale)
+                Unit<float, U>::load(scale + c[j], ws);
+            if constexpr (POST)
+                Unit<float, U>::load(post + c[j], wp);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                sw[j][k] = __builtin_fmaf(g[j][k], s[j][k] * q, sw[j][k]);
+                o[k] = t[j][k] = __builtin_fmaf(q, g[j][k] * ww[k] - s[j][k] * back, t[j][k]);
+                if (delta) {
+                    const float dn = POST ? d[j][k] * p : d[j][k];
+                    if (scale) {
+                        ss[j][k] = __builtin_fmaf(t[j][k], POST ? dn * wp[k] : dn, ss[j][k]);
+                        t[j][k] *= ws[k];
+                    }
+                    if constexpr (POST) {
+                        sp[j][k] = __builtin_fmaf(t[j][k], dn, sp[j][k]);
+                        t[j][k] *= wp[k];
+                        if (on[j])
+                            dot2 = __builtin_fmaf(t[j][k], d[j][k], dot2);
+                    }
+                }
+            }
+            if (on[j])
+                RU::store(dres + base + c[j], o);
+        }
+        if (!delta)
+            continue;
+        if constexpr (POST) {
+            const float back2 = p * p * (team.sum(dot2) * inv_n);
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    t[j][k] = p * (t[j][k] - d[j][k] * back2);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (on[j])
+                AU::store(ddelta + base + c[j], t[j]);
+    }
+    const int64_t plane = static_cast<int64_t>(gridDim.x) * W;
+    float* part = parts + static_cast<int64_t>(blockIdx.x) * W;
+    write_part<LPR, U, NV>(team, sw, W, lds, part);
+    if (delta && scale)
+        write_part<LPR, U, NV>(team, ss, W, lds, part + plane);
+    if constexpr (POST)
+        write_part<LPR, U, NV>(team, sp, W, lds, part + 2 * plane);
+}
+
+struct Sums {
+    float* out[kMaxSums];
+};
+
+// Column sums of the workgroups' parts, in a fixed order.  blockIdx.y: which.
+__global__ __launch_bounds__(1024) void part_sum_kernel(const float* __restrict__ parts, Sums sums, int rows, int W) {
+    __shared__ float mem[16][64];
+    float* out = sums.out[blockIdx.y];
+    if (!out)
+        return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
+    const float* p = parts + static_cast<int64_t>(blockIdx.y) * rows * W + c;
+    float s = 0.0f;
+    if (c < W)
+        for (int row = wave; row < rows; row += 16)
+            s += p[static_cast<int64_t>(row) * W];
+    mem[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < W) {
+        float t = 0.0f;
+        for (int w = 0; w < 16; ++w)
+            t += mem[w][lane];
+        out[c] = t;
+    }
+}
+
+// ------------------------------------------------------------ norm and gate
+
+template <typename O, typename Act, int U, int LPR, int NV, bool FIRST>
+__global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
+    const O* __restrict__ o, const Act* __restrict__ z, const float* __restrict__ w, Act* __restrict__ y,
+    int64_t items, int H, int D, int64_t z_pitch, int w_step, float inv_n, float eps) {
+    __shared__ float mem[32];
+    Team<LPR> team(mem);
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot; item < items;
+         item += static_cast<int64_t>(gridDim.x) * team.teams) {
+        const int64_t row = item / H;
+        const int h = static_cast<int>(item - row * H);
+        float v[NV][U], gate[NV][U];
+        bool on[NV];
+        int c[NV];
+        float sq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int u = (team.index + j * team.size) * U;
+            on[j] = u < D;
+            c[j] = on[j] ? u : 0;
+            Unit<O, U>::load(o + item * D + c[j], v[j]);
+            Unit<Act, U>::load(z + row * z_pitch + static_cast<int64_t>(h) * D + c[j], gate[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                gate[j][k] = silu(gate[j][k]);
+                if constexpr (FIRST)
+                    v[j][k] *= gate[j][k];
+                sq = on[j] ? __builtin_fmaf(v[j][k], v[j][k], sq) : sq;
+            }
+        const float q = inv_rms(team.sum(sq), inv_n, eps);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float ww[U];
+            Unit<float, U>::load(w + static_cast<int64_t>(h) * w_step + c[j], ww);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                ww[k] *= v[j][k] * q;
+                if constexpr (!FIRST)
+                    ww[k] *= gate[j][k];
+            }
+            if (on[j])
+                Unit<Act, U>::store(y + item * D + c[j], ww);
+        }
+    }
+}
+
+// Team g keeps head g % H and walks every `step`-th row, so that its weight
+// gradient stays in registers.  One weight for all heads: parts [blocks][D], else
+// [step][H][D].
+template <typename O, typename Act, int U, int LPR, int NV, bool FIRST>
+__global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
+    const O* __restrict__ o, const Act* __restrict__ z, const float* __restrict__ w, const Act* __restrict__ dy,
+    O* __restrict__ dov, Act* __restrict__ dz, float* __restrict__ parts, int64_t rows, int H, int D, int64_t step,
+    int64_t z_pitch, int64_t dz_pitch, int w_step, float inv_n, float eps) {
+    __shared__ float mem[32];
+    __shared__ float lds[LPR ? 256 * NV * U : 1];
+    Team<LPR> team(mem);
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot;
+    const int h = static_cast<int>(id % H);
+    const int64_t first = id / H;
+    float sw[NV][U] = {}, ww[NV][U];
+    bool on[NV];
+    int c[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int u = (team.index + j * team.size) * U;
+        on[j] = u < D;
+        c[j] = on[j] ? u : 0;
+        Unit<float, U>::load(w + static_cast<int64_t>(h) * w_step + c[j], ww[j]);
+    }
+    if (first < step)
+        for (int64_t row = first; row < rows; row += step) {
+            const int64_t base = (row * H + h) * D;
+            float v[NV][U], gate[NV][U], slope[NV][U], g[NV][U];
+            float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                Unit<O, U>::load(o + base + c[j], v[j]);
+                Unit<Act, U>::load(z + row * z_pitch + static_cast<int64_t>(h) * D + c[j], gate[j]);
+                Unit<Act, U>::load(dy + base + c[j], g[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    silu_slope(gate[j][k], gate[j][k], slope[j][k]);
+                    const float u = FIRST ? v[j][k] * gate[j][k] : v[j][k];
+                    const float dn = (FIRST ? g[j][k] : g[j][k] * gate[j][k]) * ww[j][k];
+                    if (on[j]) {
+                        sq = __builtin_fmaf(u, u, sq);
+                        dot = __builtin_fmaf(dn, u, dot);
+                    }
+                }
+            sq = team.sum(sq);
+            dot = team.sum(dot);
+            const float q = inv_rms(sq, inv_n, eps);
+            const float back = q * q * (dot * inv_n);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float a[U], b[U];
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const float u = FIRST ? v[j][k] * gate[j][k] : v[j][k];
+                    const float dn = FIRST ? g[j][k] : g[j][k] * gate[j][k];
+                    const float n = u * q;
+                    sw[j][k] = __builtin_fmaf(dn, n, sw[j][k]);
+                    const float du = q * (dn * ww[j][k] - u * back);
+                    a[k] = FIRST ? du * gate[j][k] : du;
+                    b[k] = (FIRST ? du * v[j][k] : g[j][k] * n * ww[j][k]) * slope[j][k];
+                }
+                if (on[j]) {
+                    Unit<O, U>::store(dov + base + c[j], a);
+                    Unit<Act, U>::store(dz + row * dz_pitch + static_cast<int64_t>(h) * D + c[j], b);
+                }
+            }
+        }
+    if (w_step == 0) {
+        write_part<LPR, U, NV>(team, sw, D, lds, parts + static_cast<int64_t>(blockIdx.x) * D);
+    } else if (first < step) {
+        float* part = parts + (first * H + h) * D;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (on[j])
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    part[c[j] + k] = sw[j][k];
+    }
+}
+
+// ------------------------------------------------------------ launches
+
+// Lanes of a team and units per lane for rows of n units: the smallest part of a
+// wave that holds a row, or a workgroup.
+struct Shape {
+    int lpr, nv, threads;
+};
+inline Shape shape_of(int n) {
+    for (int lpr = 4; lpr <= 64; lpr *= 2)
+        if (n <= lpr)
+            return {lpr, 1, 256};
+    int nv = 1;
+    while (n > 1024 * nv)
+        nv *= 2;
+    const int per = (n + nv - 1) / nv;
+    return {0, nv, (per + 63) / 64 * 64};
+}
+
+template <typename F>
+static hipError_t with_shape(const Shape& s, F f) {
+    switch (s.lpr) {
+        case 4: return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+        case 8: return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+        case 16: return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+        case 32: return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
+        case 64: return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
+        default: break;
+    }
+    switch (s.nv) {
+        case 1: return f(std::integral_constant<int, 0>(), std::integral_constant<int, 1>());
+        case 2: return f(std::integral_constant<int, 0>(), std::integral_constant<int, 2>());
+        default: return f(std::integral_constant<int, 0>(), std::integral_constant<int, 4>());
+    }
+}
+
+constexpr int64_t kBlocks = 1 << 16;         // forward workgroups; longer calls loop
+constexpr int64_t kBackBlocks = 512;         // backward workgroups, each with its own weight sums
+
+inline int64_t back_blocks(int64_t teams_needed, int teams) {
+    const int64_t need = (teams_needed + teams - 1) / teams;
+    return need < kBackBlocks ? need : kBackBlocks;
+}
+
+template <typename Act, typename Res>
+static hipError_t residual_cfg(const ResidualNorm& a, hipStream_t s) {
+    constexpr int U = unit_of<Act, Res>();
+    const Shape sh = shape_of(a.W / U);
+    const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
+    const int64_t need = (a.rows + teams - 1) / teams;
+    const dim3 grid(static_cast<unsigned>(need < kBlocks ? need : kBlocks)), block(sh.threads);
+    return with_shape(sh, [&](auto lpr, auto nv) {
+        auto go = [&](auto post) {
+            hipLaunchKernelGGL((residual_norm_kernel<Act, Res, U, lpr(), nv(), post()>), grid, block, 0, s,
+                               static_cast<const Res*>(a.residual), static_cast<const Act*>(a.delta), a.scale, a.post,
+                               a.w, static_cast<Res*>(a.out), static_cast<Act*>(a.y), a.rows, a.W, 1.0f / a.W, a.eps);
+            return hipGetLastError();
+        };
+        return a.post ? go(std::true_type()) : go(std::false_type());
+    });
+}
+
+template <typename Act, typename Res>
+static hipError_t residual_back_cfg(const ResidualNormGrad& a, void* ws, hipStream_t s) {
+    constexpr int U = unit_of<Act, Res>();
+    const Shape sh = shape_of(a.W / U);
+    const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
+    const int64_t blocks = back_blocks(a.rows, teams);
+    float* parts = static_cast<float*>(ws);
+    hipError_t e = with_shape(sh, [&](auto lpr, auto nv) {
+        auto go = [&](auto post) {
+            hipLaunchKernelGGL((residual_norm_backward_kernel<Act, Res, U, lpr(), nv(), post()>),
+                               dim3(static_cast<unsigned>(blocks)), dim3(sh.threads), 0, s,
+                               static_cast<const Res*>(a.stream), static_cast<const Act*>(a.delta), a.scale, a.post,
+                               a.w, static_cast<const Act*>(a.dy), static_cast<const Res*>(a.ds),
+                               static_cast<Res*>(a.dres), static_cast<Act*>(a.ddelta), parts, a.rows, a.W,
+                               1.0f / a.W, a.eps);
+            return hipGetLastError();
+        };
+        return a.post ? go(std::true_type()) : go(std::false_type());
+    });
+    if (e != hipSuccess)
+        return e;
+    const Sums sums{{a.dw, a.dscale, a.dpost}};
+    hipLaunchKernelGGL(part_sum_kernel, dim3((a.W + 63) / 64, a.dpost ? 3 : a.dscale ? 2 : 1), dim3(1024), 0, s, parts,
+                       sums, static_cast<int>(blocks), a.W);
+    return hipGetLastError();
+}
+
+template <typename O, typename Act>
+static hipError_t gated_cfg(const GatedNorm& a, hipStream_t s) {
+    constexpr int U = unit_of<O, Act>();
+    const Shape sh = shape_of(a.D / U);
+    const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
+    const int64_t items = a.rows * a.H, need = (items + teams - 1) / teams;
+    const dim3 grid(static_cast<unsigned>(need < kBlocks ? need : kBlocks)), block(sh.threads);
+    return with_shape(sh, [&](auto lpr, auto nv) {
+        auto go = [&](auto first) {
+            hipLaunchKernelGGL((gated_norm_kernel<O, Act, U, lpr(), nv(), first()>), grid, block, 0, s,
+                               static_cast<const O*>(a.o), static_cast<const Act*>(a.z), a.w, static_cast<Act*>(a.y),
+                               items, a.H, a.D, a.z_pitch, a.per_head ? a.D : 0, 1.0f / a.D, a.eps);
+            return hipGetLastError();
+        };
+        return a.first ? go(std::true_type()) : go(std::false_type());
+    });
+}
+
+// Workgroups of a gated norm's gradient and the rows that are walked side by side.
+struct GatedPlan {
+    int64_t blocks, step;
+};
+inline GatedPlan gated_plan(int64_t rows, int H, int teams) {
+    int64_t step = kBackBlocks * teams / H;
+    step = step < 1 ? 1 : step > rows ? rows : step;
+    return {(step * H + teams - 1) / teams, step};
+}
+
+template <typename O, typename Act>
+static hipError_t gated_back_cfg(const GatedNorm& a, const GatedNormGrad& g, void* ws, hipStream_t s) {
+    constexpr int U = unit_of<O, Act>();
+    const Shape sh = shape_of(a.D / U);
+    const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
+    const GatedPlan plan = gated_plan(a.rows, a.H, teams);
+    float* parts = static_cast<float*>(ws);
+    hipError_t e = with_shape(sh, [&](auto lpr, auto nv) {
+        auto go = [&](auto first) {
+            hipLaunchKernelGGL((gated_norm_backward_kernel<O, Act, U, lpr(), nv(), first()>),
+                               dim3(static_cast<unsigned>(plan.blocks)), dim3(sh.threads), 0, s,
+                               static_cast<const O*>(a.o), static_cast<const Act*>(a.z), a.w,
+                               static_cast<const Act*>(g.dy), static_cast<O*>(g.dov), static_cast<Act*>(g.dz), parts,
+                               a.rows, a.H, a.D, plan.step, a.z_pitch, g.dz_pitch, a.per_head ? a.D : 0, 1.0f / a.D,
+                               a.eps);
+            return hipGetLastError();
+        };
+        return a.first ? go(std::true_type()) : go(std::false_type());
+    });
+    if (e != hipSuccess)
+        return e;
+    const int cols = a.per_head ? a.H * a.D : a.D;
+    hipLaunchKernelGGL(part_sum_kernel, dim3((cols + 63) / 64, 1), dim3(1024), 0, s, parts, Sums{{g.dw, nullptr, nullptr}},
+                       static_cast<int>(a.per_head ? plan.step : plan.blocks), cols);
+    return hipGetLastError();
+}
+
+}  // namespace norm
+
+size_t residual_norm_back_ws_bytes(int64_t rows, int W) {
+    return static_cast<size_t>(norm::kMaxSums) * (rows < norm::kBackBlocks ? rows : norm::kBackBlocks) * W *
+           sizeof(float);
+}
+
+// The larger of the two layouts, for the unit that makes the most teams.
+size_t gated_norm_back_ws_bytes(int64_t rows, int H, int D) {
+    size_t most = 0;
+    for (int U = 4; U <= 8; U += 4) {
+        const norm::Shape sh = norm::shape_of(D / U);
+        const norm::GatedPlan plan = norm::gated_plan(rows, H, sh.lpr ? sh.threads / sh.lpr : 1);
+        const size_t shared = static_cast<size_t>(plan.blocks) * D, each = static_cast<size_t>(plan.step) * H * D;
+        most = most > shared ? most : shared;
+        most = most > each ? most : each;
+    }
+    return most * sizeof(float);
+}
+
+hipError_t launch_residual_norm(const ResidualNorm& a, hipStream_t s) {
+    if (!a.act_bf16)
+        return norm::residual_cfg<float, float>(a, s);
+    return a.res_bf16 ? norm::residual_cfg<uint16_t, uint16_t>(a, s) : norm::residual_cfg<uint16_t, float>(a, s);
+}
+
+hipError_t launch_residual_norm_backward(const ResidualNormGrad& a, void* ws, hipStream_t s) {
+    if (!a.act_bf16)
+        return norm::residual_back_cfg<float, float>(a, ws, s);
+    return a.res_bf16 ? norm::residual_back_cfg<uint16_t, uint16_t>(a, ws, s)
+                      : norm::residual_back_cfg<uint16_t, float>(a, ws, s);
+}
+
+hipError_t launch_gated_norm(const GatedNorm& a, hipStream_t s) {
+    if (!a.act_bf16)
+        return norm::gated_cfg<float, float>(a, s);
+    return a.o_bf16 ? norm::gated_cfg<uint16_t, uint16_t>(a, s) : norm::gated_cfg<float, uint16_t>(a, s);
+}
+
+hipError_t launch_gated_norm_backward(const GatedNorm& a, const GatedNormGrad& g, void* ws, hipStream_t s) {
+    if (!a.act_bf16)
+        return norm::gated_back_cfg<float, float>(a, g, ws, s);
+    return a.o_bf16 ? norm::gated_back_cfg<uint16_t, uint16_t>(a, g, ws, s)
+                    : norm::gated_back_cfg<float, uint16_t>(a, g, ws, s);
+}
+
+}  // namespace gdn

@@ -602,6 +602,180 @@ gdn_status gdn_beam_reorder(const gdn_dims* d, int32_t beams, float* state, void
 gdn_status gdn_ssm_beam_reorder(const gdn_ssm_dims* d, int32_t beams, float* state, void* conv_tail,
                                 const int32_t* parent, int32_t* status, void* stream);
 
+/*
+ * The gated linear recurrent layer -- a recurrent mixer with a diagonal state:
+ * every channel keeps one value and has gates of its own.  The conventions
+ * above (memory, errors, streams, concurrency) hold, but for rows that lie at
+ * a pitch.  Per channel, token and sequence:
+ *   decay  la = min(A, 0) * sigmoid(r), a = exp(la)
+ *   state  h <- a*h + sqrt(1 - a^2) * sigmoid(i) * x
+ *   output y = h, times SiLU(z) where z is given
+ * A gate or 1 - a^2 below 2^-126 (fp32's smallest normal number) may count as 0.
+ * Types: state, A and their gradients are fp32; x, r, i, z, y and their
+ * gradients have the activation type and are rounded once, on output.
+ * Supported shapes: width a multiple of 8, at most GDN_LRU_MAX_WIDTH;
+ * 1 <= T <= GDN_LRU_MAX_TOKENS; batch * ceil(width/64) * ceil(T/64) < 2^23
+ * (GDN_ERR_SHAPE otherwise).
+ */
+#define GDN_LRU_MAX_WIDTH (1 << 18)
+#define GDN_LRU_MAX_TOKENS (1 << 22)
+typedef struct {
+    int32_t batch;     /* B: independent sequences */
+    int32_t width;     /* W: channels */
+    int32_t act_dtype; /* gdn_dtype of x, r, i, z, y and their gradients */
+} gdn_lru_dims;
+
+/*
+ * Elements from one token's row of an array to the next: at least W, a multiple
+ * of 8, at most 2^20; 0 for W.  A NULL gdn_lru_pitches means W throughout.  The
+ * rows of a call's sequences follow each other at the one pitch, so that x, r,
+ * i and z may be parts of one projection's output.  Outputs overlap neither
+ * each other nor an input (GDN_ERR_ALIAS); the rows of two arrays of one pitch
+ * may lie between each other's.
+ */
+typedef struct {
+    int64_t x, r, i, z, y;
+} gdn_lru_pitches;
+
+size_t gdn_lru_state_bytes(const gdn_lru_dims* d); /* B*W*4 */
+
+/*
+ * gdn_lru_decode_token -- one token for every sequence, in one launch.
+ *   state f32 [B][W]  (in/out);  A f32 [W]
+ *   x, r, i act [B][W];  z act [B][W] or NULL (no gate);  y act [B][W] (written)
+ */
+gdn_status gdn_lru_decode_token(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, float* state, const void* x,
+                                const void* r, const void* i, const float* A, const void* z, void* y, void* stream);
+
+/*
+ * gdn_lru_prefill -- up to T tokens per sequence; decode continues from the
+ * state.  It is also the forward pass of a training step.
+ *   state f32 [B][W] (in/out);  A f32 [W];  x, r, i, y act [B][T][W];  z the same or NULL
+ *   lengths i32 [B] (device) or NULL: tokens of each sequence, 0..T (NULL: T).
+ *           Rows behind a sequence's end are not read into any result, and their
+ *           y is not written; length 0 leaves the state as it is.
+ *   saved   f32, gdn_lru_saved_bytes(d, T) bytes, or NULL: receives what
+ *           gdn_lru_backward needs of this call's states
+ *   status  i32 [B] or NULL: per sequence GDN_OK, or GDN_ERR_INDEX when its
+ *           length is out of range (that sequence is untouched)
+ *   workspace  device bytes >= gdn_lru_prefill_workspace_bytes(d, T), which is 0
+ *           for short calls (then it may be NULL), 256-byte aligned; a size
+ *           serves every call of no more sequences, tokens and channels
+ * State and fp32 outputs agree with the token-by-token call to fp32 rounding of
+ * the terms they are sums of; bf16 outputs add their own rounding.  A NaN or
+ * infinity in a token's inputs reaches its own channel from that token on.
+ */
+size_t gdn_lru_prefill_workspace_bytes(const gdn_lru_dims* d, int32_t T);
+size_t gdn_lru_saved_bytes(const gdn_lru_dims* d, int32_t T);
+gdn_status gdn_lru_prefill(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, float* state, int32_t T, const void* x,
+                           const void* r, const void* i, const float* A, const void* z, const int32_t* lengths,
+                           void* y, float* saved, int32_t* status, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * gdn_lru_backward -- the gradients of a prefill from those of its outputs and
+ * of the state it left.
+ *   x, r, i, A, z, lengths  as the prefill had them;  saved  as it left it
+ *   dy     act [B][T][W] (at pitch->y);  rows behind a sequence's end are not read
+ *   dstate f32 [B][W] or NULL (0): gradient of the final state
+ *   dx, dr, di act [B][T][W] at grad_pitch (written; 0 behind a sequence's end)
+ *   dz     the same; given where z is, else NULL
+ *   dA     f32 [W] (written): the sum over sequences and tokens, 0 where A >= 0
+ *   dstate0  f32 [B][W] or NULL (written): gradient of the state before; it may
+ *          be dstate itself
+ *   status as in gdn_lru_prefill: a sequence whose length is out of range adds
+ *          nothing to dA and its gradients are not written
+ *   workspace  device bytes >= gdn_lru_backward_workspace_bytes(d, T), 256-byte
+ *          aligned; a size serves every call of no more sequences, tokens and channels
+ * Where sqrt(1 - a^2) is 0 (a gate shut to the last bit, a rate of 0) its
+ * derivative is taken as 0.  Sums have a fixed order: equal inputs give equal bits.
+ */
+size_t gdn_lru_backward_workspace_bytes(const gdn_lru_dims* d, int32_t T);
+gdn_status gdn_lru_backward(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, const gdn_lru_pitches* grad_pitch,
+                            int32_t T, const void* x, const void* r, const void* i, const float* A, const void* z,
+                            const int32_t* lengths, const float* saved, const void* dy, const float* dstate, void* dx,
+                            void* dr, void* di, void* dz, float* dA, float* dstate0, int32_t* status, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_residual_norm -- the residual sum behind a block and the norm before the
+ * next one, over rows of W values:
+ *   n   = delta, or with w_post  delta / sqrt(mean(delta^2) + eps) * w_post
+ *   out = residual + scale * n      (rounded once, to the stream's type)
+ *   y   = out / sqrt(mean(out^2) + eps) * w
+ *   residual, out  res_dtype [rows][W];  out may be residual itself
+ *   delta  act [rows][W], or NULL: the norm of residual alone (out, scale and
+ *          w_post are then NULL too)
+ *   scale, w_post  f32 [W] or NULL (1, and no norm of delta);  w f32 [W]
+ *   y      act [rows][W] (written)
+ * res_dtype is GDN_F32 or act_dtype.  Supported shapes: W a multiple of 8, at
+ * most GDN_NORM_MAX_WIDTH; 1 <= rows < 2^31; eps positive and finite
+ * (GDN_ERR_SHAPE otherwise).  Sums are fp32: rows whose mean square is beyond
+ * fp32 have a norm of 0.
+ */
+#define GDN_NORM_MAX_WIDTH 16384
+gdn_status gdn_residual_norm(int64_t rows, int32_t W, int32_t act_dtype, int32_t res_dtype, float eps,
+                             const void* residual, const void* delta, const float* scale, const float* w_post,
+                             const float* w, void* out, void* y, void* stream);
+
+/*
+ * gdn_residual_norm_backward -- its gradients.
+ *   out    res_dtype [rows][W]: the stream that the forward call left (where
+ *          delta is NULL: the residual);  delta, scale, w_post, w as it had them
+ *   dy     act [rows][W];  ds res_dtype [rows][W] or NULL (0): the gradient that
+ *          reaches the stream from elsewhere
+ *   dresidual  res_dtype [rows][W] (written); may be ds itself
+ *   ddelta act [rows][W] (written; NULL where delta is)
+ *   dw, dscale, dw_post  f32 [W] (written; the latter two given where scale and
+ *          w_post are, else NULL)
+ *   workspace  device bytes >= gdn_residual_norm_backward_workspace_bytes(rows, W),
+ *          256-byte aligned; a size serves every call of no more rows and channels
+ * Sums have a fixed order: equal inputs give equal bits.
+ */
+size_t gdn_residual_norm_backward_workspace_bytes(int64_t rows, int32_t W);
+gdn_status gdn_residual_norm_backward(int64_t rows, int32_t W, int32_t act_dtype, int32_t res_dtype, float eps,
+                                      const void* out, const void* delta, const float* scale, const float* w_post,
+                                      const float* w, const void* dy, const void* ds, void* dresidual, void* ddelta,
+                                      float* dw, float* dscale, float* dw_post, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_gated_norm -- the norm of a mixer's output with its gate, per head of D
+ * values (or per group of channels of a state space layer, or whole row: H = 1):
+ *   y = o / sqrt(mean(o^2) + eps) * w * SiLU(z)
+ * or, with GDN_GATE_FIRST,
+ *   u = o * SiLU(z),  y = u / sqrt(mean(u^2) + eps) * w
+ *   o      o_dtype [rows][H][D]: the output of a decode, verify or prefill call
+ *   z      act [rows][H][D], rows at a pitch of z_pitch >= H*D elements, a
+ *          multiple of 8 (0: H*D)
+ *   w      f32 [D], or with GDN_WEIGHT_PER_HEAD [H][D]
+ *   y      act [rows][H][D] (written)
+ * o_dtype is GDN_F32 or act_dtype.  Supported shapes: D a multiple of 8, at most
+ * GDN_NORM_MAX_WIDTH; 1 <= H <= 65536; rows >= 1, rows*H < 2^31; eps positive
+ * and finite (GDN_ERR_SHAPE otherwise, and for other flags).  Sums are fp32, as
+ * in gdn_residual_norm.
+ */
+#define GDN_GATE_FIRST 1
+#define GDN_WEIGHT_PER_HEAD 2
+gdn_status gdn_gated_norm(int64_t rows, int32_t H, int32_t D, int32_t o_dtype, int32_t act_dtype, int32_t flags,
+                          float eps, const void* o, const void* z, int64_t z_pitch, const float* w, void* y,
+                          void* stream);
+
+/*
+ * gdn_gated_norm_backward -- its gradients.
+ *   o, z, w  as the forward call had them;  dy act [rows][H][D]
+ *   do_    o_dtype [rows][H][D] (written);  dz act, at a pitch of dz_pitch (written)
+ *   dw     f32, as w (written): the sum over rows, and over heads where w is shared
+ *   workspace  device bytes >= gdn_gated_norm_backward_workspace_bytes(rows, H, D),
+ *          256-byte aligned; a size serves every call of no more rows of these H and D
+ * Sums have a fixed order: equal inputs give equal bits.
+ */
+size_t gdn_gated_norm_backward_workspace_bytes(int64_t rows, int32_t H, int32_t D);
+gdn_status gdn_gated_norm_backward(int64_t rows, int32_t H, int32_t D, int32_t o_dtype, int32_t act_dtype,
+                                   int32_t flags, float eps, const void* o, const void* z, int64_t z_pitch,
+                                   const float* w, const void* dy, void* do_, void* dz, int64_t dz_pitch, float* dw,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
