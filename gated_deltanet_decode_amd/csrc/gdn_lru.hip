@@ -54,56 +54,72 @@ __global__ __launch_bounds__(256) void lru_token_kernel(float* __restrict__ stat
 }
 
 // ------------------------------------------------------------ prompts
+//
+// A tile is 64 channels (16 lanes of 4) by 32 groups of N consecutive tokens, 4
+// groups to a wave, and one workgroup's work.  The tiles of 64 channels of a
+// sequence form a chain along the tokens.  Every tile reads its inputs once and
+// keeps a and v in registers; it announces its own map as soon as that is known,
+// then gathers the maps of the tiles before it, back to one whose leaving state
+// is known already, eight of them at a time (one to a wave), and announces its
+// own leaving state.  So the chain costs one exchange of 8 bytes per channel and
+// tile, and inputs are not read a second time.
+//
+// A workgroup takes its tile from a counter, in the order of the chains' tokens:
+// whoever holds a tile, all tiles before it are held by workgroups that already
+// run and that announce their maps without waiting for anyone.  So every wait
+// ends.  An announcement is one relaxed atomic word that is its own flag: the
+// words are filled with ones, which no map and no state is (NaNs are made
+// canonical), before the kernel starts.
 
-// A tile: 64 channels (16 lanes of 4) by 32 groups of N consecutive tokens, 4
-// groups to a wave.
-template <typename Act, int N, bool GATE>
-__global__ __launch_bounds__(kThreads) void lru_scan_kernel(float* __restrict__ state, const Act* __restrict__ x,
-                                                            const Act* __restrict__ r, const Act* __restrict__ i,
-                                                            const float* __restrict__ A, const Act* __restrict__ z,
-                                                            const int32_t* __restrict__ lengths, Act* __restrict__ y,
-                                                            float* __restrict__ saved, int32_t* __restrict__ status,
-                                                            int T, int W, int blocks, Pitches p) {
+template <typename Act, int N, bool GATE, bool CHAIN>
+__global__ __launch_bounds__(kThreads, 4) void lru_scan_kernel(
+    float* __restrict__ state, const Act* __restrict__ x, const Act* __restrict__ r, const Act* __restrict__ i,
+    const float* __restrict__ A, const Act* __restrict__ z, const int32_t* __restrict__ lengths, Act* __restrict__ y,
+    float* __restrict__ saved, int32_t* __restrict__ status, int T, int W, int blocks, int chains, int segs, Chain ch,
+    Pitches p) {
     using Q = Quad<Act>;
     constexpr int L = N * kGroups;
-    __shared__ float4 maps[2][kWaves][2][16];
+    __shared__ Exchange ex;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int q = lane & 15, group = wave * 4 + (lane >> 4);
-    const int b = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * kChannels + q * 4;
-    const bool on = c0 < W;
-    const int c = on ? c0 : W - 4;
+    const int tile = CHAIN ? take_tile(ch, ex) : blockIdx.x;
+    if (tile >= chains * segs)
+        return;
+    const int chain = tile % chains, seg = tile / chains;
+    const int b = chain / blocks, c_block = (chain % blocks) * kChannels;
+    const bool on = c_block + q * 4 < W;
+    const int c = on ? c_block + q * 4 : W - 4;
     const int n = lengths ? lengths[b] : T;
     const bool bad = n < 0 || n > T;
-    if (status && threadIdx.x == 0 && blockIdx.x % blocks == 0)
+    if (status && threadIdx.x == 0 && seg == 0 && c_block == 0)
         status[b] = bad ? GDN_ERR_INDEX : GDN_OK;
-    if (bad || n == 0)
+    const int live = bad ? 0 : n - seg * L;   // tokens of the tile and behind it
+    if (live <= 0)
         return;
-    const int64_t row0 = static_cast<int64_t>(b) * T;
-    x += row0 * p.x + c;
-    r += row0 * p.r + c;
-    i += row0 * p.i + c;
-    y += row0 * p.y + c;
-    if constexpr (GATE)
-        z += row0 * p.z + c;
+    const int64_t row0 = static_cast<int64_t>(b) * T + seg * L;
     const float4 rate4 = *reinterpret_cast<const float4*>(A + c);
     const float rt[4] = {rate2(rate4.x), rate2(rate4.y), rate2(rate4.z), rate2(rate4.w)};
-    float4* hp = reinterpret_cast<float4*>(state + static_cast<int64_t>(b) * W + c);
-    const float4 h4 = *hp;
-    float carry[4] = {h4.x, h4.y, h4.z, h4.w};
-    const int marks = (T + kSaveStep - 1) / kSaveStep;
 
-    for (int seg = 0; seg * L < n; ++seg) {
-        const int t0 = seg * L + group * N;
-        float a[N][4], v[N][4];
+    const int t0 = group * N;
+    float a[N][4], v[N][4];
+    float am[4] = {1, 1, 1, 1}, hm[4] = {0, 0, 0, 0};   // the lane's map
+    typename Q::raw rz[N];
+    {
         typename Q::raw rx[N], rr[N], ri[N];
+        const Rows<Act> xs(x, row0, p.x, c), rs(r, row0, p.r, c), is(i, row0, p.i, c);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int64_t t = min(t0 + j, n - 1);
-            rx[j] = Q::load(x + t * p.x);
-            rr[j] = Q::load(r + t * p.r);
-            ri[j] = Q::load(i + t * p.i);
+            const int t = min(t0 + j, live - 1);
+            rr[j] = rs.load(t);
+            ri[j] = is.load(t);
+            rx[j] = xs.load(t);
         }
-        float am[4] = {1, 1, 1, 1}, hm[4] = {0, 0, 0, 0};   // the lane's map
+        if constexpr (GATE) {
+            const Rows<Act> zs(z, row0, p.z, c);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                rz[j] = zs.load(min(t0 + j, live - 1));
+        }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             float fx[4], fr[4], fi[4];
@@ -113,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void lru_scan_kernel(float* __restrict__ 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 step(fx[k], fr[k], fi[k], rt[k], a[j][k], v[j][k]);
-                if (t0 + j >= n) {
+                if (t0 + j >= live) {
                     a[j][k] = 1.0f;
                     v[j][k] = 0.0f;
                 }
@@ -121,44 +137,76 @@ __global__ __launch_bounds__(kThreads) void lru_scan_kernel(float* __restrict__ 
                 am[k] *= a[j][k];
             }
         }
-        scan_forward(lane, am, hm);
-        if (lane >= 48) {
-            maps[seg & 1][wave][0][q] = make_float4(am[0], am[1], am[2], am[3]);
-            maps[seg & 1][wave][1][q] = make_float4(hm[0], hm[1], hm[2], hm[3]);
-        }
-        shift_forward(lane, am, hm);
-        __syncthreads();
-        float h[4] = {carry[0], carry[1], carry[2], carry[3]};
+    }
+    scan_forward(lane, am, hm);
+    if (lane >= 48) {
+        ex.maps[wave][0][q] = make_float4(am[0], am[1], am[2], am[3]);
+        ex.maps[wave][1][q] = make_float4(hm[0], hm[1], hm[2], hm[3]);
+    }
+    shift_forward(lane, am, hm);
+    __syncthreads();
+
+    // the state that enters the tile, and the one that leaves it (one channel to a lane of the first wave)
+    const bool last = live <= L;
+    float h[4];
+    {
+        float at = 1.0f, ht = 0.0f;
+        const int mine = c_block + lane < W ? c_block + lane : W - 1;
+        if (wave == 0) {
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const float4 ma = maps[seg & 1][w][0][q], mh = maps[seg & 1][w][1][q];
-            compose(carry, ma, mh);
-            if (w < wave)
-                compose(h, ma, mh);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            h[k] = __builtin_fmaf(am[k], h[k], hm[k]);
-        if (saved && on && t0 % kSaveStep == 0 && t0 < n)
-            *reinterpret_cast<float4*>(saved + (static_cast<int64_t>(b) * marks + t0 / kSaveStep) * W + c) =
-                make_float4(h[0], h[1], h[2], h[3]);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            float out[4], fz[4];
-            const int64_t t = min(t0 + j, n - 1);
-            if constexpr (GATE)
-                Q::to_float(Q::load(z + t * p.z), fz);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                h[k] = __builtin_fmaf(a[j][k], h[k], v[j][k]);
-                out[k] = GATE ? h[k] * silu(fz[k]) : h[k];
+            for (int w = 0; w < kWaves; ++w) {
+                const float wa = ex.map(w, 0)[lane], wh = ex.map(w, 1)[lane];
+                ht = __builtin_fmaf(wa, ht, wh);
+                at *= wa;
             }
-            if (on && t0 + j < n)
-                Q::store(y + t * p.y, pack(out, Act()));
+            if (CHAIN && !last && seg > 0)
+                ch.announce_map(tile, lane, at, ht);
+        }
+        float* first = state + static_cast<int64_t>(b) * W;
+        float enter = gather<CHAIN>(ch, ex, tile, chains, seg, first + mine, h);
+        if (wave == 0) {
+            const float leave = __builtin_fmaf(at, enter, ht);
+            if (!last)
+                ch.announce_state(tile, lane, leave);
+            else if (c_block + lane < W)
+                first[mine] = leave;
         }
     }
-    if (on && group == 0)
-        *hp = make_float4(carry[0], carry[1], carry[2], carry[3]);
+#pragma unroll
+    for (int w = 0; w < kWaves - 1; ++w)
+        if (w < wave)
+            compose(h, ex.maps[w][0][q], ex.maps[w][1][q]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        h[k] = __builtin_fmaf(am[k], h[k], hm[k]);
+    if (saved && on && (seg * L + t0) % kSaveStep == 0 && t0 < live) {
+        const int marks = (T + kSaveStep - 1) / kSaveStep;
+        *reinterpret_cast<float4*>(saved + (static_cast<int64_t>(b) * marks + (seg * L + t0) / kSaveStep) * W + c) =
+            make_float4(h[0], h[1], h[2], h[3]);
+    }
+    const Rows<Act> ys(y, row0, p.y, c);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        float out[4], fz[4];
+        if constexpr (GATE)
+            Q::to_float(rz[j], fz);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = __builtin_fmaf(a[j][k], h[k], v[j][k]);
+            out[k] = GATE ? h[k] * silu(fz[k]) : h[k];
+        }
+        if (on && t0 + j < live)
+            ys.store(t0 + j, pack(out, Act()));
+    }
+}
+
+// Ones in every announcement and 0 in the counter, ahead of a chained kernel.
+__global__ __launch_bounds__(256) void lru_clear_kernel(uint4* __restrict__ words, int64_t n, unsigned* __restrict__ next) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; k < n; k += step)
+        words[k] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *next = 0;
 }
 
 // ------------------------------------------------------------ the gradient
@@ -376,15 +424,53 @@ static hipError_t token_cfg(const LruGeo& g, const LruArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The workspace of a chained call: 256 bytes with the counter, then a word of 8
+// bytes (map) and one of 4 (state) per channel and tile.
+// Tokens of a lane's group in a chained prompt: what its registers hold.
+constexpr int tokens_of(bool bf16) { return bf16 ? 8 : 4; }
+inline int64_t scan_tiles(const LruGeo& g, int T) {
+    const int L = tokens_of(g.bf16) * kGroups;
+    return static_cast<int64_t>(g.B) * ((g.W + kChannels - 1) / kChannels) * ((T + L - 1) / L);
+}
+inline size_t chain_bytes(int64_t tiles) { return 256 + static_cast<size_t>(tiles) * kChannels * 12; }
+
+static hipError_t clear_chain(void* ws, int64_t tiles, Chain& ch, hipStream_t s) {
+    char* p = static_cast<char*>(ws);
+    ch.next = reinterpret_cast<unsigned*>(p);
+    ch.maps = reinterpret_cast<uint64_t*>(p + 256);
+    ch.states = reinterpret_cast<uint32_t*>(p + 256 + tiles * kChannels * 8);
+    const int64_t words = tiles * kChannels * 12 / 16;
+    const int64_t grid = (words + 1023) / 1024;
+    hipLaunchKernelGGL(lru_clear_kernel, dim3(static_cast<unsigned>(grid < 2048 ? grid : 2048)), dim3(256), 0, s,
+                       reinterpret_cast<uint4*>(p + 256), words, ch.next);
+    return hipGetLastError();
+}
+
+template <typename Act, int N, bool GATE, bool CHAIN>
+static hipError_t scan_launch(const LruGeo& g, const LruArgs& a, int T, const int32_t* lengths, float* saved,
+                              int32_t* status, const Chain& ch, hipStream_t s) {
+    const int blocks = (g.W + kChannels - 1) / kChannels, segs = CHAIN ? (T + N * kGroups - 1) / (N * kGroups) : 1;
+    hipLaunchKernelGGL((lru_scan_kernel<Act, N, GATE, CHAIN>), dim3(static_cast<unsigned>(g.B) * blocks * segs),
+                       dim3(kThreads), 0, s, a.state, static_cast<const Act*>(a.x), static_cast<const Act*>(a.r),
+                       static_cast<const Act*>(a.i), a.A, static_cast<const Act*>(a.z), lengths,
+                       static_cast<Act*>(a.y), saved, status, T, g.W, blocks, g.B * blocks, segs, ch, g.p);
+    return hipGetLastError();
+}
+
+
 template <typename Act, bool GATE>
 static hipError_t scan_cfg(const LruGeo& g, const LruArgs& a, int T, const int32_t* lengths, float* saved,
-                           int32_t* status, hipStream_t s) {
-    const int blocks = (g.W + kChannels - 1) / kChannels;
-    hipLaunchKernelGGL((lru_scan_kernel<Act, 4, GATE>), dim3(g.B * blocks), dim3(kThreads), 0, s, a.state,
-                       static_cast<const Act*>(a.x), static_cast<const Act*>(a.r), static_cast<const Act*>(a.i), a.A,
-                       static_cast<const Act*>(a.z), lengths, static_cast<Act*>(a.y), saved, status, T, g.W, blocks,
-                       g.p);
-    return hipGetLastError();
+                           int32_t* status, void* ws, hipStream_t s) {
+    constexpr int N = tokens_of(sizeof(Act) == 2);
+    Chain ch = {};
+    if (T <= 2 * kGroups)
+        return scan_launch<Act, 2, GATE, false>(g, a, T, lengths, saved, status, ch, s);
+    if (T <= 4 * kGroups)
+        return scan_launch<Act, 4, GATE, false>(g, a, T, lengths, saved, status, ch, s);
+    if (T <= N * kGroups)
+        return scan_launch<Act, N, GATE, false>(g, a, T, lengths, saved, status, ch, s);
+    const hipError_t e = clear_chain(ws, scan_tiles(g, T), ch, s);
+    return e != hipSuccess ? e : scan_launch<Act, N, GATE, true>(g, a, T, lengths, saved, status, ch, s);
 }
 
 template <typename Act, bool GATE>
@@ -417,15 +503,17 @@ size_t lru_saved_bytes(const LruGeo& g, int T) {
     return static_cast<size_t>(g.B) * ((T + lru::kSaveStep - 1) / lru::kSaveStep) * g.W * sizeof(float);
 }
 
-size_t lru_prefill_ws_bytes(const LruGeo&, int) { return 0; }
+size_t lru_prefill_ws_bytes(const LruGeo& g, int T) {
+    return T <= lru::tokens_of(g.bf16) * lru::kGroups ? 0 : lru::chain_bytes(lru::scan_tiles(g, T));
+}
 
 hipError_t launch_lru_prefill(const LruGeo& g, const LruArgs& a, int T, const int32_t* lengths, float* saved,
-                              int32_t* status, void*, hipStream_t s) {
+                              int32_t* status, void* ws, hipStream_t s) {
     if (g.bf16)
-        return a.z ? lru::scan_cfg<uint16_t, true>(g, a, T, lengths, saved, status, s)
-                   : lru::scan_cfg<uint16_t, false>(g, a, T, lengths, saved, status, s);
-    return a.z ? lru::scan_cfg<float, true>(g, a, T, lengths, saved, status, s)
-               : lru::scan_cfg<float, false>(g, a, T, lengths, saved, status, s);
+        return a.z ? lru::scan_cfg<uint16_t, true>(g, a, T, lengths, saved, status, ws, s)
+                   : lru::scan_cfg<uint16_t, false>(g, a, T, lengths, saved, status, ws, s);
+    return a.z ? lru::scan_cfg<float, true>(g, a, T, lengths, saved, status, ws, s)
+               : lru::scan_cfg<float, false>(g, a, T, lengths, saved, status, ws, s);
 }
 
 size_t lru_backward_ws_bytes(const LruGeo& g, int T) { return lru_saved_bytes(g, T); }

@@ -136,5 +136,140 @@ __device__ __forceinline__ void shift_reverse(int lane, float (&a)[4], float (&v
     }
 }
 
+// Rows of an array from one of them on, for one lane's four channels: a uniform
+// base and 32-bit byte offsets (a tile's rows lie within 2^31 bytes).
+template <typename Act>
+struct Rows {
+    const char* base;
+    uint32_t pitch, lane;
+    __device__ Rows(const Act* p, int64_t row, int64_t elements, int c)
+        : base(reinterpret_cast<const char*>(p + row * elements)),
+          pitch(static_cast<uint32_t>(elements * sizeof(Act))), lane(static_cast<uint32_t>(c * sizeof(Act))) {}
+    __device__ typename Quad<Act>::raw load(int t) const {
+        return Quad<Act>::load(reinterpret_cast<const Act*>(base + (static_cast<uint32_t>(t) * pitch + lane)));
+    }
+    __device__ void store(int t, typename Quad<Act>::raw v) const {
+        Quad<Act>::store(reinterpret_cast<Act*>(const_cast<char*>(base) + (static_cast<uint32_t>(t) * pitch + lane)), v);
+    }
+};
+
+// ------------------------------------------------------------ chains of tiles
+
+constexpr uint32_t kNan = 0x7FC00000u;
+
+// Announcements of a chained kernel's tiles, tile * 64 + channel, and the counter
+// that hands the tiles out.
+struct Chain {
+    unsigned* next;
+    uint64_t* maps;
+    uint32_t* states;
+    __device__ void announce_map(int tile, int lane, float a, float v) const {
+        const uint32_t ua = a != a ? kNan : __float_as_uint(a);
+        __hip_atomic_store(maps + static_cast<int64_t>(tile) * kChannels + lane,
+                           static_cast<uint64_t>(ua) << 32 | __float_as_uint(v), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __device__ void announce_state(int tile, int lane, float h) const {
+        __hip_atomic_store(states + static_cast<int64_t>(tile) * kChannels + lane, h != h ? kNan : __float_as_uint(h),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+};
+
+// What the waves of a workgroup tell each other: the maps of their groups, the
+// tiles that each of them has looked up, and the tile that was taken.
+struct Exchange {
+    float4 maps[kWaves][2][16];
+    float4 look[kWaves][2][16];
+    int known[kWaves];   // 2: a state, 1: a map, 0: neither (ahead of the chain's start)
+    int tile;
+    __device__ const float* map(int w, int k) const { return reinterpret_cast<const float*>(maps[w][k]); }
+};
+
+__device__ __forceinline__ int take_tile(const Chain& ch, Exchange& ex) {
+    if (threadIdx.x == 0)
+        ex.tile = static_cast<int>(__hip_atomic_fetch_add(ch.next, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    __syncthreads();
+    return ex.tile;
+}
+
+// The state that enters a tile: h for this lane's four channels, and as the
+// result, in the first wave, the one of channel `lane`.  `first` is where the
+// state lies that enters the chain.  Only the first wave of the chain's first tile
+// reads it, before it announces what it leaves, so that the last tile may replace
+// it.  A chain's tiles are `chains` apart.
+//
+// The wait is bounded all the same: where a word does not come (a second call on
+// the same workspace has cleared it, against the rules), the tile goes on with NaN.
+constexpr int kPolls = 1 << 22;   // some seconds
+template <bool CHAIN>
+__device__ __forceinline__ float gather(const Chain& ch, Exchange& ex, int tile, int chains, int seg, const float* first,
+                                        float (&h)[4]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane & 15;
+    float ga[4] = {1, 1, 1, 1}, gv[4] = {0, 0, 0, 0};   // the maps between the window and the tile
+    float la = 1.0f, lv = 0.0f;                           // the same of channel `lane`
+    for (int near = seg - 1;; near -= kWaves) {
+        const int s = near - wave;
+        int known = 0;
+        float a = 0.0f, v = 0.0f;
+        if (!CHAIN || seg == 0) {
+            known = 2;
+            if (wave == 0)
+                v = *first;
+        } else if (s >= 0) {
+            const int64_t at = (static_cast<int64_t>(tile) - static_cast<int64_t>(seg - s) * chains) * kChannels + lane;
+            for (int poll = 0;; ++poll) {
+                const uint32_t st = __hip_atomic_load(ch.states + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                const uint64_t mp = __hip_atomic_load(ch.maps + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                if (__all(st != ~0u)) {
+                    known = 2;
+                    v = __uint_as_float(st);
+                    break;
+                }
+                if (__all(static_cast<uint32_t>(mp >> 32) != ~0u)) {
+                    known = 1;
+                    a = __uint_as_float(static_cast<uint32_t>(mp >> 32));
+                    v = __uint_as_float(static_cast<uint32_t>(mp));
+                    break;
+                }
+                if (poll == kPolls) {
+                    known = 2;
+                    v = __uint_as_float(kNan);
+                    break;
+                }
+                __builtin_amdgcn_s_sleep(1);
+            }
+        }
+        reinterpret_cast<float*>(ex.look[wave][0])[lane] = a;
+        reinterpret_cast<float*>(ex.look[wave][1])[lane] = v;
+        if (lane == 0)
+            ex.known[wave] = known;
+        __syncthreads();
+        int w = 0;
+        for (; w < kWaves; ++w) {
+            const float4 va = ex.look[w][0][q], vv = ex.look[w][1][q];
+            const float ma = reinterpret_cast<const float*>(ex.look[w][0])[lane],
+                        mv = reinterpret_cast<const float*>(ex.look[w][1])[lane];
+            const bool end = __builtin_amdgcn_readfirstlane(ex.known[w]) == 2;
+            const float fa[4] = {va.x, va.y, va.z, va.w}, fv[4] = {vv.x, vv.y, vv.z, vv.w};
+            lv = __builtin_fmaf(la, mv, lv);
+            la *= ma;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                gv[k] = __builtin_fmaf(ga[k], fv[k], gv[k]);
+                ga[k] *= fa[k];
+            }
+            if (end)
+                break;
+        }
+        if (w < kWaves)
+            break;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        h[k] = gv[k];
+    return lv;
+}
+
 }  // namespace lru
 }  // namespace gdn
