@@ -13,6 +13,9 @@
 #include "gdn.h"
 #include "gdn_lru.hpp"
 
+#ifndef LRU_BOCC
+#define LRU_BOCC 2
+#endif
 namespace gdn {
 namespace lru {
 
@@ -55,38 +58,38 @@ __global__ __launch_bounds__(256) void lru_token_kernel(float* __restrict__ stat
 
 // ------------------------------------------------------------ prompts
 //
-// A tile is 64 channels (16 lanes of 4) by 32 groups of N consecutive tokens, 4
-// groups to a wave, and one workgroup's work.  The tiles of 64 channels of a
-// sequence form a chain along the tokens.  Every tile reads its inputs once and
-// keeps a and v in registers; it announces its own map as soon as that is known,
-// then gathers the maps of the tiles before it, back to one whose leaving state
-// is known already, eight of them at a time (one to a wave), and announces its
-// own leaving state.  So the chain costs one exchange of 8 bytes per channel and
+// A tile is a block of channels by some tokens, and one workgroup's work.  The tiles
+// of a sequence's channels form a chain along the tokens.  Every tile reads its
+// inputs once and keeps a and v in registers; it announces its own map as soon as
+// that is known, then gathers the maps of the tiles before it, back to one whose
+// leaving state is known already, as many at a time as it has waves, and announces
+// its own leaving state.  So the chain costs one word of 8 bytes per channel and
 // tile, and inputs are not read a second time.
 //
 // A workgroup takes its tile from a counter, in the order of the chains' tokens:
 // whoever holds a tile, all tiles before it are held by workgroups that already
 // run and that announce their maps without waiting for anyone.  So every wait
-// ends.  An announcement is one relaxed atomic word that is its own flag: the
-// words are filled with ones, which no map and no state is (NaNs are made
-// canonical), before the kernel starts.
+// ends.  An announcement is one relaxed atomic word that is its own flag, so that
+// it orders no other memory; the words are filled with ones, which no announcement
+// is, before the kernel starts.
 
-template <typename Act, int N, bool GATE, bool CHAIN>
-__global__ __launch_bounds__(kThreads, 4) void lru_scan_kernel(
+template <typename Act, int LPC, int WAVES, int N, bool GATE, bool CHAIN>
+__global__ __launch_bounds__(WAVES * kWave, 4) void lru_scan_kernel(
     float* __restrict__ state, const Act* __restrict__ x, const Act* __restrict__ r, const Act* __restrict__ i,
     const float* __restrict__ A, const Act* __restrict__ z, const int32_t* __restrict__ lengths, Act* __restrict__ y,
     float* __restrict__ saved, int32_t* __restrict__ status, int T, int W, int blocks, int chains, int segs, Chain ch,
     Pitches p) {
     using Q = Quad<Act>;
-    constexpr int L = N * kGroups;
-    __shared__ Exchange ex;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int q = lane & 15, group = wave * 4 + (lane >> 4);
+    using TL = Tile<LPC, WAVES, N>;
+    constexpr int L = TL::kTokens, E = TL::kWords;
+    __shared__ Exchange<TL, WAVES, 2> ex;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane % LPC, group = wave * TL::kPerWave + lane / LPC;
     const int tile = CHAIN ? take_tile(ch, ex) : blockIdx.x;
     if (tile >= chains * segs)
         return;
     const int chain = tile % chains, seg = tile / chains;
-    const int b = chain / blocks, c_block = (chain % blocks) * kChannels;
+    const int b = chain / blocks, c_block = (chain % blocks) * TL::kChannels;
     const bool on = c_block + q * 4 < W;
     const int c = on ? c_block + q * 4 : W - 4;
     const int n = lengths ? lengths[b] : T;
@@ -97,96 +100,111 @@ __global__ __launch_bounds__(kThreads, 4) void lru_scan_kernel(
     if (live <= 0)
         return;
     const int64_t row0 = static_cast<int64_t>(b) * T + seg * L;
-    const float4 rate4 = *reinterpret_cast<const float4*>(A + c);
-    const float rt[4] = {rate2(rate4.x), rate2(rate4.y), rate2(rate4.z), rate2(rate4.w)};
-
     const int t0 = group * N;
-    float a[N][4], v[N][4];
-    float am[4] = {1, 1, 1, 1}, hm[4] = {0, 0, 0, 0};   // the lane's map
-    typename Q::raw rz[N];
-    {
-        typename Q::raw rx[N], rr[N], ri[N];
-        const Rows<Act> xs(x, row0, p.x, c), rs(r, row0, p.r, c), is(i, row0, p.i, c);
+    const Rows<Act> xs(x, row0, p.x, c), rs(r, row0, p.r, c), is(i, row0, p.i, c), zs(GATE ? z : x, row0, p.z, c);
+    typename Q::raw rx[N], rr[N], ri[N], rz[N];
+    if (live >= L) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            rr[j] = rs.load(t0, j);
+            ri[j] = is.load(t0, j);
+            rx[j] = xs.load(t0, j);
+        }
+        if constexpr (GATE)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                rz[j] = zs.load(t0, j);
+    } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int t = min(t0 + j, live - 1);
             rr[j] = rs.load(t);
             ri[j] = is.load(t);
             rx[j] = xs.load(t);
+            if constexpr (GATE)
+                rz[j] = zs.load(t);
         }
-        if constexpr (GATE) {
-            const Rows<Act> zs(z, row0, p.z, c);
+    }
+    float* enter = state + static_cast<int64_t>(b) * W;
+    const int mine = c_block + wave * kWave + lane;   // of the first E waves: the channel they hold for the chain
+    const float first = seg == 0 && wave < E ? enter[min(mine, W - 1)] : 0.0f;
+    const float4 rate4 = *reinterpret_cast<const float4*>(A + c);
+    const float rt[4] = {rate2(rate4.x), rate2(rate4.y), rate2(rate4.z), rate2(rate4.w)};
+
+    float a[N][4], v[N][4];
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                rz[j] = zs.load(min(t0 + j, live - 1));
+    for (int j = 0; j < N; ++j) {
+        float fx[4], fr[4], fi[4];
+        Q::to_float(rx[j], fx);
+        Q::to_float(rr[j], fr);
+        Q::to_float(ri[j], fi);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+        {
+            step(fx[k], fr[k], fi[k], rt[k], a[j][k], v[j][k]);
+            settle(v[j][k]);
         }
+    }
+    if (live < L)
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            float fx[4], fr[4], fi[4];
-            Q::to_float(rx[j], fx);
-            Q::to_float(rr[j], fr);
-            Q::to_float(ri[j], fi);
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                step(fx[k], fr[k], fi[k], rt[k], a[j][k], v[j][k]);
+            for (int k = 0; k < 4; ++k)
                 if (t0 + j >= live) {
                     a[j][k] = 1.0f;
                     v[j][k] = 0.0f;
                 }
-                hm[k] = __builtin_fmaf(a[j][k], hm[k], v[j][k]);
-                am[k] *= a[j][k];
-            }
+    float am[4] = {1, 1, 1, 1}, hm[4] = {0, 0, 0, 0}, wa[4], wv[4];   // the lane's map, then the wave's
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            hm[k] = __builtin_fmaf(a[j][k], hm[k], v[j][k]);
+            am[k] *= a[j][k];
         }
+    scan_forward<LPC>(lane, am, hm, wa, wv);
+    if (lane >= kWave - LPC) {
+        ex.maps[wave][0][q] = make_float4(wa[0], wa[1], wa[2], wa[3]);
+        ex.maps[wave][1][q] = make_float4(wv[0], wv[1], wv[2], wv[3]);
     }
-    scan_forward(lane, am, hm);
-    if (lane >= 48) {
-        ex.maps[wave][0][q] = make_float4(am[0], am[1], am[2], am[3]);
-        ex.maps[wave][1][q] = make_float4(hm[0], hm[1], hm[2], hm[3]);
-    }
-    shift_forward(lane, am, hm);
     __syncthreads();
 
-    // the state that enters the tile, and the one that leaves it (one channel to a lane of the first wave)
     const bool last = live <= L;
-    float h[4];
-    {
-        float at = 1.0f, ht = 0.0f;
-        const int mine = c_block + lane < W ? c_block + lane : W - 1;
-        if (wave == 0) {
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float wa = ex.map(w, 0)[lane], wh = ex.map(w, 1)[lane];
-                ht = __builtin_fmaf(wa, ht, wh);
-                at *= wa;
-            }
-            if (CHAIN && !last && seg > 0)
-                ch.announce_map(tile, lane, at, ht);
+    const int64_t word = static_cast<int64_t>(tile) * TL::kChannels + wave * kWave + lane;
+    float at = 1.0f, ht = 0.0f, h[4];   // the tile's map of that channel
+    if (wave < E) {
+#pragma unroll 2
+        for (int w = 0; w < WAVES; ++w) {
+            const float ma = ex.map(w, 0, wave * kWave + lane);
+            ht = __builtin_fmaf(ma, ht, ex.map(w, 1, wave * kWave + lane));
+            at *= ma;
         }
-        float* first = state + static_cast<int64_t>(b) * W;
-        float enter = gather<CHAIN>(ch, ex, tile, chains, seg, first + mine, h);
-        if (wave == 0) {
-            const float leave = __builtin_fmaf(at, enter, ht);
-            if (!last)
-                ch.announce_state(tile, lane, leave);
-            else if (c_block + lane < W)
-                first[mine] = leave;
-        }
+        if (CHAIN && !last && seg > 0)
+            ch.announce_map(word, at, ht);
     }
-#pragma unroll
-    for (int w = 0; w < kWaves - 1; ++w)
-        if (w < wave)
-            compose(h, ex.maps[w][0][q], ex.maps[w][1][q]);
+    const float into = gather<TL, WAVES, CHAIN>(ch, ex, wave, tile, chains, seg, first, h);
+    if (wave < E) {
+        const float leave = __builtin_fmaf(at, into, ht);
+        if (!last)
+            ch.announce_state(word, leave);
+        else if (mine < W)
+            enter[mine] = leave;
+    }
+#pragma unroll 2
+    for (int w = 0; w < wave; ++w)
+        compose(h, ex.maps[w][0][q], ex.maps[w][1][q]);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         h[k] = __builtin_fmaf(am[k], h[k], hm[k]);
-    if (saved && on && (seg * L + t0) % kSaveStep == 0 && t0 < live) {
-        const int marks = (T + kSaveStep - 1) / kSaveStep;
-        *reinterpret_cast<float4*>(saved + (static_cast<int64_t>(b) * marks + (seg * L + t0) / kSaveStep) * W + c) =
-            make_float4(h[0], h[1], h[2], h[3]);
-    }
     const Rows<Act> ys(y, row0, p.y, c);
+    const bool whole = live >= L && c_block + TL::kChannels <= W;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
+        if (saved && (seg * L + t0 + j) % kSaveStep == 0 && on && t0 + j < live) {
+            const int marks = (T + kSaveStep - 1) / kSaveStep;
+            *reinterpret_cast<float4*>(saved + (static_cast<int64_t>(b) * marks + (seg * L + t0 + j) / kSaveStep) * W + c) =
+                make_float4(h[0], h[1], h[2], h[3]);
+        }
         float out[4], fz[4];
         if constexpr (GATE)
             Q::to_float(rz[j], fz);
@@ -195,8 +213,8 @@ __global__ __launch_bounds__(kThreads, 4) void lru_scan_kernel(
             h[k] = __builtin_fmaf(a[j][k], h[k], v[j][k]);
             out[k] = GATE ? h[k] * silu(fz[k]) : h[k];
         }
-        if (on && t0 + j < live)
-            ys.store(t0 + j, pack(out, Act()));
+        if (whole || (on && t0 + j < live))
+            ys.store(t0, j, pack(out, Act()));
     }
 }
 
@@ -210,209 +228,290 @@ __global__ __launch_bounds__(256) void lru_clear_kernel(uint4* __restrict__ word
 }
 
 // ------------------------------------------------------------ the gradient
+//
+// The chains run from the last token to the first.  A tile starts from a state that
+// the forward pass saved, so its own h need no chain; what it passes on is K, the
+// gradient of the state before its first token, whose map has the same a.  With
+// P = a sigmoid(i) x / m, the gradient of la is G (a h' - a^2 sigmoid(i) x / m) =
+// K (h' - P) for h' the state before the token, so the two parts of a token's
+// decay share one product.  What the outputs need of a token (ten values) stays in
+// registers while the chain is waited for: its exponentials are taken once.
+// Of a tile's tokens each channel's part of dA goes to `parts`.
 
-template <typename Act, int N, bool GATE>
-__global__ __launch_bounds__(kThreads) void lru_backward_kernel(
+template <typename Act, int LPC, int WAVES, int N, bool GATE, bool CHAIN>
+__global__ __launch_bounds__(WAVES * kWave, LRU_BOCC) void lru_backward_kernel(
     const Act* __restrict__ x, const Act* __restrict__ r, const Act* __restrict__ i, const float* __restrict__ A,
     const Act* __restrict__ z, const int32_t* __restrict__ lengths, const float* __restrict__ saved,
-    const Act* __restrict__ dy, const float* __restrict__ dstate, Act* __restrict__ dx, Act* __restrict__ dr,
-    Act* __restrict__ di, Act* __restrict__ dz, float* __restrict__ dstate0, float* __restrict__ parts,
-    int32_t* __restrict__ status, int T, int W, int blocks, Pitches p, Pitches gp) {
+    const Act* __restrict__ dy, const float* dstate, Act* __restrict__ dx, Act* __restrict__ dr, Act* __restrict__ di,
+    Act* __restrict__ dz, float* dstate0, float* __restrict__ parts, int32_t* __restrict__ status, int T, int W,
+    int blocks, int chains, int segs, Chain ch, Pitches p, Pitches gp) {
     using Q = Quad<Act>;
-    constexpr int L = N * kGroups;
-    static_assert(L == kSaveStep, "a tile starts where a state was saved");
-    __shared__ float4 maps[2][kWaves][3][16];
-    __shared__ float4 sums[2][kWaves][16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int q = lane & 15, group = wave * 4 + (lane >> 4);
-    const int b = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * kChannels + q * 4;
-    const bool on = c0 < W;
-    const int c = on ? c0 : W - 4;
-    const int len = lengths ? lengths[b] : T;
-    const bool bad = len < 0 || len > T;
-    const int n = bad ? 0 : len;
-    if (status && threadIdx.x == 0 && blockIdx.x % blocks == 0)
+    using TL = Tile<LPC, WAVES, N>;
+    constexpr int L = TL::kTokens, E = TL::kWords;
+    static_assert(L % kSaveStep == 0, "a tile starts where a state was saved");
+    __shared__ Exchange<TL, WAVES, 3> ex;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane % LPC, group = wave * TL::kPerWave + lane / LPC;
+    const int tile = CHAIN ? take_tile(ch, ex) : blockIdx.x;
+    if (tile >= chains * segs)
+        return;
+    const int chain = tile % chains, seg = segs - 1 - tile / chains;
+    const int b = chain / blocks, c_block = (chain % blocks) * TL::kChannels;
+    const bool on = c_block + q * 4 < W;
+    const int c = on ? c_block + q * 4 : W - 4;
+    const int n = lengths ? lengths[b] : T;
+    const bool bad = n < 0 || n > T;
+    if (status && threadIdx.x == 0 && seg == 0 && c_block == 0)
         status[b] = bad ? GDN_ERR_INDEX : GDN_OK;
-    const int64_t row0 = static_cast<int64_t>(b) * T;
-    x += row0 * p.x + c;
-    r += row0 * p.r + c;
-    i += row0 * p.i + c;
-    dy += row0 * p.y + c;
-    dx += row0 * gp.x + c;
-    dr += row0 * gp.r + c;
-    di += row0 * gp.i + c;
-    if constexpr (GATE) {
-        z += row0 * p.z + c;
-        dz += row0 * gp.z + c;
-    }
-    const float4 A4 = *reinterpret_cast<const float4*>(A + c);
-    const float rate[4] = {rate_of(A4.x), rate_of(A4.y), rate_of(A4.z), rate_of(A4.w)};
-    float carry[4] = {0, 0, 0, 0};
-    if (dstate) {
-        const float4 g = *reinterpret_cast<const float4*>(dstate + static_cast<int64_t>(b) * W + c);
-        carry[0] = g.x, carry[1] = g.y, carry[2] = g.z, carry[3] = g.w;
-    }
-    const int marks = (T + kSaveStep - 1) / kSaveStep;
-    for (int seg = marks - 1; seg >= 0; --seg) {
-        const int t0 = seg * L + group * N;
-        float* part = parts + (static_cast<int64_t>(b) * marks + seg) * W + c;
-        if (seg * L >= n) {   // behind the sequence's end: gradients of what was not read
-            if (on) {
-                const float zero[4] = {0, 0, 0, 0};
-                for (int j = 0; j < N; ++j) {
-                    const int64_t t = t0 + j;
-                    if (t < T && !bad) {
-                        Q::store(dx + t * gp.x, pack(zero, Act()));
-                        Q::store(dr + t * gp.r, pack(zero, Act()));
-                        Q::store(di + t * gp.i, pack(zero, Act()));
-                        if constexpr (GATE)
-                            Q::store(dz + t * gp.z, pack(zero, Act()));
-                    }
-                }
-                if (group == 0)
-                    *reinterpret_cast<float4*>(part) = make_float4(0, 0, 0, 0);
+    const int64_t row0 = static_cast<int64_t>(b) * T + seg * L;
+    const int t0 = group * N, rows = min(T - seg * L, L), live = bad ? 0 : n - seg * L;
+    const Rows<Act> xg(dx, row0, gp.x, c), rg(dr, row0, gp.r, c), ig(di, row0, gp.i, c), zg(GATE ? dz : dx, row0, gp.z, c);
+    float* part = parts + (static_cast<int64_t>(b) * segs + seg) * W;
+    const int mine = c_block + wave * kWave + lane;   // of the first E waves: the channel they hold for the chain
+    if (live <= 0) {   // behind the sequence's end: the gradient of what was not read
+        const float zero[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (on && !bad && t0 + j < rows) {
+                xg.store(t0, j, pack(zero, Act()));
+                rg.store(t0, j, pack(zero, Act()));
+                ig.store(t0, j, pack(zero, Act()));
+                if constexpr (GATE)
+                    zg.store(t0, j, pack(zero, Act()));
             }
-            continue;
-        }
-        float fx[N][4], a[N][4], m[N][4], im[N][4], rho[N][4], drho[N][4], gi[N][4], dgi[N][4], v[N][4], e[N][4], fdy[N][4],
-            sz[N][4], dsz[N][4];
-        float am[4] = {1, 1, 1, 1}, hm[4] = {0, 0, 0, 0};
+        if (on && group == 0)
+            *reinterpret_cast<float4*>(part + c) = make_float4(0, 0, 0, 0);
+        if (seg == 0 && wave < E && !bad && dstate0 && mine < W)   // no token at all: the state passes through
+            dstate0[static_cast<int64_t>(b) * W + mine] = dstate ? dstate[static_cast<int64_t>(b) * W + mine] : 0.0f;
+        return;
+    }
+    const Rows<Act> xs(x, row0, p.x, c), rs(r, row0, p.r, c), is(i, row0, p.i, c), ds(dy, row0, p.y, c),
+        zs(GATE ? z : x, row0, p.z, c);
+    typename Q::raw rx[N], rr[N], ri[N], rd[N], rz[N];
+    if (live >= L) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int64_t t = min(t0 + j, n - 1);
-            float fr[4], fi[4], fz[4];
-            Q::to_float(Q::load(x + t * p.x), fx[j]);
-            Q::to_float(Q::load(r + t * p.r), fr);
-            Q::to_float(Q::load(i + t * p.i), fi);
-            Q::to_float(Q::load(dy + t * p.y), fdy[j]);
+            rr[j] = rs.load(t0, j);
+            ri[j] = is.load(t0, j);
+            rx[j] = xs.load(t0, j);
+            rd[j] = ds.load(t0, j);
             if constexpr (GATE)
-                Q::to_float(Q::load(z + t * p.z), fz);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                sigmoid_slope(fr[k], rho[j][k], drho[j][k]);
-                sigmoid_slope(fi[k], gi[j][k], dgi[j][k]);
-                decay(rate[k] * kLog2e * rho[j][k], a[j][k], m[j][k], im[j][k]);
-                v[j][k] = m[j][k] * gi[j][k] * fx[j][k];
-                if constexpr (GATE) {
-                    silu_slope(fz[k], sz[j][k], dsz[j][k]);
-                    e[j][k] = fdy[j][k] * sz[j][k];
-                } else {
-                    e[j][k] = fdy[j][k];
-                }
-                if (t0 + j >= n) {
-                    a[j][k] = 1.0f;
-                    v[j][k] = e[j][k] = 0.0f;
-                }
-                hm[k] = __builtin_fmaf(a[j][k], hm[k], v[j][k]);
-                am[k] *= a[j][k];
-            }
+                rz[j] = zs.load(t0, j);
         }
-        float ar[4] = {am[0], am[1], am[2], am[3]}, km[4] = {0, 0, 0, 0};
+    } else {
 #pragma unroll
-        for (int j = N - 1; j >= 0; --j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                km[k] = a[j][k] * (e[j][k] + km[k]);
-        scan_forward(lane, am, hm);
-        scan_reverse(lane, ar, km);
-        if (lane >= 48) {
-            maps[seg & 1][wave][0][q] = make_float4(am[0], am[1], am[2], am[3]);
-            maps[seg & 1][wave][1][q] = make_float4(hm[0], hm[1], hm[2], hm[3]);
+        for (int j = 0; j < N; ++j) {
+            const int t = min(t0 + j, live - 1);
+            rr[j] = rs.load(t);
+            ri[j] = is.load(t);
+            rx[j] = xs.load(t);
+            rd[j] = ds.load(t);
+            if constexpr (GATE)
+                rz[j] = zs.load(t);
         }
-        if (lane < 16)
-            maps[seg & 1][wave][2][q] = make_float4(km[0], km[1], km[2], km[3]);
-        shift_forward(lane, am, hm);
-        shift_reverse(lane, ar, km);
-        __syncthreads();
-        const float4 h4 = *reinterpret_cast<const float4*>(saved + (static_cast<int64_t>(b) * marks + seg) * W + c);
-        float h[4] = {h4.x, h4.y, h4.z, h4.w}, K[4] = {carry[0], carry[1], carry[2], carry[3]};
+    }
+    const int marks = (T + kSaveStep - 1) / kSaveStep;
+    const float4 h4 = *reinterpret_cast<const float4*>(saved + (static_cast<int64_t>(b) * marks + seg * (L / kSaveStep)) * W + c);
+    const int dist = (n + L - 1) / L - 1 - seg;   // place in the chain: the sequence's last tile is its first
+    const float first = dist == 0 && wave < E && dstate ? dstate[static_cast<int64_t>(b) * W + min(mine, W - 1)] : 0.0f;
+    const float4 A4 = *reinterpret_cast<const float4*>(A + c);
+    const float rate[4] = {rate_of(A4.x), rate_of(A4.y), rate_of(A4.z), rate_of(A4.w)};
+
+    // of a token: its map, the output's gradient, and the factors of the outputs
+    float a[N][4], v[N][4], eg[N][4], fx[N][4], fi[N][4], fp[N][4], fr[N][4], rho[N][4], fd[N][4];
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            if (w < wave)
-                compose(h, maps[seg & 1][w][0][q], maps[seg & 1][w][1][q]);
-#pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w) {
-            const float4 ma = maps[seg & 1][w][0][q], mk = maps[seg & 1][w][2][q];
-            compose(carry, ma, mk);
-            if (w > wave)
-                compose(K, ma, mk);
-        }
-        float before[N][4], after[N][4], dA[4] = {0, 0, 0, 0};
+    for (int j = 0; j < N; ++j) {
+        float x4[4], r4[4], i4[4], d4[4], z4[4];
+        Q::to_float(rx[j], x4);
+        Q::to_float(rr[j], r4);
+        Q::to_float(ri[j], i4);
+        Q::to_float(rd[j], d4);
+        if constexpr (GATE)
+            Q::to_float(rz[j], z4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            h[k] = __builtin_fmaf(am[k], h[k], hm[k]);
-            K[k] = __builtin_fmaf(ar[k], K[k], km[k]);
+            float slope, g, shut, m, inv;
+            sigmoid_slope(r4[k], rho[j][k], slope);
+            fr[j][k] = rate[k] * slope;
+            decay(rate[k] * kLog2e * rho[j][k], a[j][k], m, inv);
+            sigmoid_both(i4[k], g, shut);
+            const float gx = g * x4[k];
+            v[j][k] = m * gx;
+            fx[j][k] = m * g;
+            fi[j][k] = v[j][k] * shut;
+            fp[j][k] = a[j][k] * inv * gx;
+            if constexpr (GATE) {
+                float s, ds;
+                silu_slope(z4[k], s, ds);
+                eg[j][k] = d4[k] * s;
+                fd[j][k] = d4[k] * ds;
+                settle(fd[j][k]);
+            } else {
+                eg[j][k] = d4[k];
+            }
+            settle(v[j][k]);
+            settle(eg[j][k]);
+            settle(fx[j][k]);
+            settle(fi[j][k]);
+            settle(fp[j][k]);
+            settle(fr[j][k]);
         }
+    }
+    if (live < L)
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                before[j][k] = h[k];
-                h[k] = __builtin_fmaf(a[j][k], h[k], v[j][k]);
-                after[j][k] = h[k];
-            }
+            for (int k = 0; k < 4; ++k)
+                if (t0 + j >= live) {
+                    a[j][k] = 1.0f;
+                    v[j][k] = eg[j][k] = rho[j][k] = 0.0f;
+                }
+    float am[4] = {1, 1, 1, 1}, hm[4] = {0, 0, 0, 0}, km[4] = {0, 0, 0, 0}, ar[4], wa[4], wv[4], wk[4];
 #pragma unroll
-        for (int j = N - 1; j >= 0; --j) {
-            float ox[4], orr[4], oi[4], oz[4];
-            const bool live = t0 + j < n;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float G = e[j][k] + K[k];
-                K[k] = a[j][k] * G;
-                const float gx = gi[j][k] * fx[j][k];
-                const float dla = G * (a[j][k] * before[j][k] - a[j][k] * a[j][k] * im[j][k] * gx);
-                ox[k] = live ? G * m[j][k] * gi[j][k] : 0.0f;
-                oi[k] = live ? G * m[j][k] * fx[j][k] * dgi[j][k] : 0.0f;
-                orr[k] = live ? dla * rate[k] * drho[j][k] : 0.0f;
-                if constexpr (GATE)
-                    oz[k] = live ? fdy[j][k] * after[j][k] * dsz[j][k] : 0.0f;
-                dA[k] += live ? dla * rho[j][k] : 0.0f;
-            }
-            const int64_t t = t0 + j;
-            if (on && t < T) {
-                Q::store(dx + t * gp.x, pack(ox, Act()));
-                Q::store(dr + t * gp.r, pack(orr, Act()));
-                Q::store(di + t * gp.i, pack(oi, Act()));
-                if constexpr (GATE)
-                    Q::store(dz + t * gp.z, pack(oz, Act()));
-            }
-        }
+    for (int j = 0; j < N; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            dA[k] += __shfl_xor(dA[k], 16);
-            dA[k] += __shfl_xor(dA[k], 32);
+            hm[k] = __builtin_fmaf(a[j][k], hm[k], v[j][k]);
+            am[k] *= a[j][k];
         }
-        if (lane < 16)
-            sums[seg & 1][wave][q] = make_float4(dA[0], dA[1], dA[2], dA[3]);
-        __syncthreads();
-        if (on && group == 0) {
-            float s[4] = {0, 0, 0, 0};
-            for (int w = 0; w < kWaves; ++w) {
-                const float4 u = sums[seg & 1][w][q];
-                s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
-            }
-            *reinterpret_cast<float4*>(part) = make_float4(s[0], s[1], s[2], s[3]);
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            km[k] = a[j][k] * (eg[j][k] + km[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        ar[k] = am[k];
+    scan_forward<LPC>(lane, am, hm, wa, wv);
+    scan_reverse<LPC>(lane, ar, km, wk);
+    if (lane >= kWave - LPC) {
+        ex.maps[wave][0][q] = make_float4(wa[0], wa[1], wa[2], wa[3]);
+        ex.maps[wave][1][q] = make_float4(wv[0], wv[1], wv[2], wv[3]);
+    }
+    if (lane < LPC)
+        ex.maps[wave][2][q] = make_float4(wk[0], wk[1], wk[2], wk[3]);
+    __syncthreads();
+
+    const bool last = seg == 0;
+    const int64_t word = static_cast<int64_t>(tile) * TL::kChannels + wave * kWave + lane;
+    float at = 1.0f, kt = 0.0f, K[4];
+    if (wave < E) {
+#pragma unroll 2
+        for (int w = WAVES - 1; w >= 0; --w) {
+            const float ma = ex.map(w, 0, wave * kWave + lane);
+            kt = __builtin_fmaf(ma, kt, ex.map(w, 2, wave * kWave + lane));
+            at *= ma;
+        }
+        if (CHAIN && !last && dist > 0)
+            ch.announce_map(word, at, kt);
+    }
+    // h before each token, less P, while the chain's words are under way
+    float h[4] = {h4.x, h4.y, h4.z, h4.w};
+#pragma unroll 2
+    for (int w = 0; w < wave; ++w)
+        compose(h, ex.maps[w][0][q], ex.maps[w][1][q]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        h[k] = __builtin_fmaf(am[k], h[k], hm[k]);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            fp[j][k] = h[k] - fp[j][k];
+            h[k] = __builtin_fmaf(a[j][k], h[k], v[j][k]);
+            if constexpr (GATE)
+                fd[j][k] *= h[k];
+        }
+    const float into = gather<TL, WAVES, CHAIN>(ch, ex, wave, tile, chains, dist, first, K);
+    if (wave < E) {
+        const float leave = __builtin_fmaf(at, into, kt);
+        if (!last)
+            ch.announce_state(word, leave);
+        else if (dstate0 && mine < W)
+            dstate0[static_cast<int64_t>(b) * W + mine] = leave;
+    }
+#pragma unroll 2
+    for (int w = WAVES - 1; w > wave; --w)
+        compose(K, ex.maps[w][0][q], ex.maps[w][2][q]);
+    float dA[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        K[k] = __builtin_fmaf(ar[k], K[k], km[k]);
+    const bool whole = live >= L && c_block + TL::kChannels <= W;
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j) {
+        float ox[4], orr[4], oi[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float G = eg[j][k] + K[k];
+            K[k] = a[j][k] * G;
+            const float dla = K[k] * fp[j][k];
+            ox[k] = G * fx[j][k];
+            oi[k] = G * fi[j][k];
+            orr[k] = dla * fr[j][k];
+            dA[k] = __builtin_fmaf(dla, rho[j][k], dA[k]);
+        }
+        if (whole) {
+            xg.store(t0, j, pack(ox, Act()));
+            rg.store(t0, j, pack(orr, Act()));
+            ig.store(t0, j, pack(oi, Act()));
+            if constexpr (GATE)
+                zg.store(t0, j, pack(fd[j], Act()));
+        } else if (on && t0 + j < rows) {
+            const bool dead = t0 + j >= live;
+            if (dead)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    ox[k] = oi[k] = orr[k] = fd[j][k] = 0.0f;
+            xg.store(t0, j, pack(ox, Act()));
+            rg.store(t0, j, pack(orr, Act()));
+            ig.store(t0, j, pack(oi, Act()));
+            if constexpr (GATE)
+                zg.store(t0, j, pack(fd[j], Act()));
         }
     }
-    if (on && group == 0 && !bad && dstate0)
-        *reinterpret_cast<float4*>(dstate0 + static_cast<int64_t>(b) * W + c) =
-            make_float4(carry[0], carry[1], carry[2], carry[3]);
+    // the tile's part of dA: over a wave's groups, then over the waves
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int d = LPC; d < kWave; d *= 2)
+            dA[k] += __shfl_xor(dA[k], d);
+    __syncthreads();
+    if (lane < LPC)
+        ex.look[wave][0][q] = make_float4(dA[0], dA[1], dA[2], dA[3]);
+    __syncthreads();
+    if (wave == 0 && lane < LPC && on) {
+        float s[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float4 u = ex.look[w][0][q];
+            s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
+        }
+        *reinterpret_cast<float4*>(part + c) = make_float4(s[0], s[1], s[2], s[3]);
+    }
 }
 
-// dA from the tiles' sums, in a fixed order: 4 waves take every fourth row each.
-__global__ __launch_bounds__(256) void lru_rate_kernel(const float* __restrict__ parts, const float* __restrict__ A,
-                                                       float* __restrict__ dA, int rows, int W) {
-    __shared__ float sums[4][64];
+// dA from the tiles' parts, in a fixed order: 16 waves take every 16th row each.
+__global__ __launch_bounds__(1024) void lru_rate_kernel(const float* __restrict__ parts, const float* __restrict__ A,
+                                                        float* __restrict__ dA, int rows, int W) {
+    __shared__ float sums[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane;
     float s = 0.0f;
-    if (c < W)
-        for (int row = wave; row < rows; row += 4)
-            s += parts[static_cast<int64_t>(row) * W + c];
+    if (c < W) {
+        const float* p = parts + c;
+#pragma unroll 8
+        for (int row = wave; row < rows; row += 16)
+            s += p[static_cast<int64_t>(row) * W];
+    }
     sums[wave][lane] = s;
     __syncthreads();
-    if (wave == 0 && c < W)
-        dA[c] = A[c] < 0.0f ? (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]) : 0.0f;
+    if (wave == 0 && c < W) {
+        float t = 0.0f;
+        for (int w = 0; w < 16; ++w)
+            t += sums[w][lane];
+        dA[c] = A[c] < 0.0f ? t : 0.0f;
+    }
 }
 
 template <typename Act, bool GATE>
@@ -424,70 +523,133 @@ static hipError_t token_cfg(const LruGeo& g, const LruArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// The workspace of a chained call: 256 bytes with the counter, then a word of 8
-// bytes (map) and one of 4 (state) per channel and tile.
-// Tokens of a lane's group in a chained prompt: what its registers hold.
-constexpr int tokens_of(bool bf16) { return bf16 ? 8 : 4; }
-inline int64_t scan_tiles(const LruGeo& g, int T) {
-    const int L = tokens_of(g.bf16) * kGroups;
-    return static_cast<int64_t>(g.B) * ((g.W + kChannels - 1) / kChannels) * ((T + L - 1) / L);
+// Tiles of the kernels over prompts.  Wide calls take 256 channels to a tile (512 or
+// 1,024 bytes of a row); where that leaves too few workgroups, 64.
+struct Shape {
+    int channels, tokens, blocks, segs;
+    int64_t tiles;
+};
+inline Shape shape_of(const LruGeo& g, int T, int channels, int tokens) {
+    Shape s;
+    s.channels = channels;
+    s.tokens = tokens;
+    s.blocks = (g.W + channels - 1) / channels;
+    s.segs = (T + tokens - 1) / tokens;
+    s.tiles = static_cast<int64_t>(g.B) * s.blocks * s.segs;
+    return s;
 }
-inline size_t chain_bytes(int64_t tiles) { return 256 + static_cast<size_t>(tiles) * kChannels * 12; }
+#ifndef FW
+#define FW 8
+#endif
+#ifndef FN
+#define FN 8
+#endif
+#ifndef BW
+#define BW 8
+#endif
+#ifndef BN
+#define BN 4
+#endif
+constexpr int kWideTiles = 512;
+inline bool wide(const LruGeo& g, int T, int tokens) { return shape_of(g, T, 256, tokens).tiles >= kWideTiles; }
+inline Shape scan_shape(const LruGeo& g, int T) {
+    if (T > 64 && wide(g, T, FW * FN))
+        return shape_of(g, T, 256, FW * FN);
+    return shape_of(g, T, 64, T <= 32 ? 32 : T <= 64 ? 64 : 128);
+}
+inline Shape back_shape(const LruGeo& g, int T) {
+    if (wide(g, T, BW * BN))
+        return shape_of(g, T, 256, BW * BN);
+    return shape_of(g, T, 64, T <= 32 ? 32 : 64);
+}
 
-static hipError_t clear_chain(void* ws, int64_t tiles, Chain& ch, hipStream_t s) {
+// The workspace of a chained call: 256 bytes with the counter, then a word of 8
+// bytes per channel and tile.
+inline size_t chain_bytes(const Shape& s) {
+    return s.segs == 1 ? 0 : 256 + static_cast<size_t>(s.tiles) * s.channels * sizeof(uint64_t);
+}
+
+static hipError_t clear_chain(void* ws, const Shape& sh, Chain& ch, hipStream_t s) {
     char* p = static_cast<char*>(ws);
     ch.next = reinterpret_cast<unsigned*>(p);
-    ch.maps = reinterpret_cast<uint64_t*>(p + 256);
-    ch.states = reinterpret_cast<uint32_t*>(p + 256 + tiles * kChannels * 8);
-    const int64_t words = tiles * kChannels * 12 / 16;
+    ch.words = reinterpret_cast<uint64_t*>(p + 256);
+    const int64_t words = sh.tiles * sh.channels / 2;   // of 16 bytes
     const int64_t grid = (words + 1023) / 1024;
     hipLaunchKernelGGL(lru_clear_kernel, dim3(static_cast<unsigned>(grid < 2048 ? grid : 2048)), dim3(256), 0, s,
                        reinterpret_cast<uint4*>(p + 256), words, ch.next);
     return hipGetLastError();
 }
 
-template <typename Act, int N, bool GATE, bool CHAIN>
+template <typename Act, int LPC, int WAVES, int N, bool GATE, bool CHAIN>
 static hipError_t scan_launch(const LruGeo& g, const LruArgs& a, int T, const int32_t* lengths, float* saved,
-                              int32_t* status, const Chain& ch, hipStream_t s) {
-    const int blocks = (g.W + kChannels - 1) / kChannels, segs = CHAIN ? (T + N * kGroups - 1) / (N * kGroups) : 1;
-    hipLaunchKernelGGL((lru_scan_kernel<Act, N, GATE, CHAIN>), dim3(static_cast<unsigned>(g.B) * blocks * segs),
-                       dim3(kThreads), 0, s, a.state, static_cast<const Act*>(a.x), static_cast<const Act*>(a.r),
+                              int32_t* status, const Shape& sh, const Chain& ch, hipStream_t s) {
+    hipLaunchKernelGGL((lru_scan_kernel<Act, LPC, WAVES, N, GATE, CHAIN>), dim3(static_cast<unsigned>(sh.tiles)),
+                       dim3(WAVES * kWave), 0, s, a.state, static_cast<const Act*>(a.x), static_cast<const Act*>(a.r),
                        static_cast<const Act*>(a.i), a.A, static_cast<const Act*>(a.z), lengths,
-                       static_cast<Act*>(a.y), saved, status, T, g.W, blocks, g.B * blocks, segs, ch, g.p);
+                       static_cast<Act*>(a.y), saved, status, T, g.W, sh.blocks, g.B * sh.blocks, sh.segs, ch, g.p);
     return hipGetLastError();
 }
-
 
 template <typename Act, bool GATE>
 static hipError_t scan_cfg(const LruGeo& g, const LruArgs& a, int T, const int32_t* lengths, float* saved,
                            int32_t* status, void* ws, hipStream_t s) {
-    constexpr int N = tokens_of(sizeof(Act) == 2);
+    const Shape sh = scan_shape(g, T);
     Chain ch = {};
-    if (T <= 2 * kGroups)
-        return scan_launch<Act, 2, GATE, false>(g, a, T, lengths, saved, status, ch, s);
-    if (T <= 4 * kGroups)
-        return scan_launch<Act, 4, GATE, false>(g, a, T, lengths, saved, status, ch, s);
-    if (T <= N * kGroups)
-        return scan_launch<Act, N, GATE, false>(g, a, T, lengths, saved, status, ch, s);
-    const hipError_t e = clear_chain(ws, scan_tiles(g, T), ch, s);
-    return e != hipSuccess ? e : scan_launch<Act, N, GATE, true>(g, a, T, lengths, saved, status, ch, s);
+    if (sh.segs > 1) {
+        const hipError_t e = clear_chain(ws, sh, ch, s);
+        if (e != hipSuccess)
+            return e;
+        if (sh.channels == 256)
+            return scan_launch<Act, 64, FW, FN, GATE, true>(g, a, T, lengths, saved, status, sh, ch, s);
+        return scan_launch<Act, 16, 8, 4, GATE, true>(g, a, T, lengths, saved, status, sh, ch, s);
+    }
+    if (sh.tokens == 32)
+        return scan_launch<Act, 16, 4, 2, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
+    if (sh.tokens == 64)
+        return scan_launch<Act, 16, 8, 2, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
+    return scan_launch<Act, 16, 8, 4, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
+}
+
+template <typename Act, int LPC, int WAVES, int N, bool GATE, bool CHAIN>
+static hipError_t backward_launch(const LruGeo& g, const LruGrads& a, int T, const int32_t* lengths, int32_t* status,
+                                  float* parts, const Shape& sh, const Chain& ch, hipStream_t s) {
+    hipLaunchKernelGGL((lru_backward_kernel<Act, LPC, WAVES, N, GATE, CHAIN>), dim3(static_cast<unsigned>(sh.tiles)),
+                       dim3(WAVES * kWave), 0, s, static_cast<const Act*>(a.x), static_cast<const Act*>(a.r),
+                       static_cast<const Act*>(a.i), a.A, static_cast<const Act*>(a.z), lengths, a.saved,
+                       static_cast<const Act*>(a.dy), a.dstate, static_cast<Act*>(a.dx), static_cast<Act*>(a.dr),
+                       static_cast<Act*>(a.di), static_cast<Act*>(a.dz), a.dstate0, parts, status, T, g.W, sh.blocks,
+                       g.B * sh.blocks, sh.segs, ch, g.p, g.gp);
+    return hipGetLastError();
+}
+
+inline size_t parts_bytes(const LruGeo& g, const Shape& sh) {
+    return (static_cast<size_t>(g.B) * sh.segs * g.W * sizeof(float) + 255) / 256 * 256;
 }
 
 template <typename Act, bool GATE>
 static hipError_t backward_cfg(const LruGeo& g, const LruGrads& a, int T, const int32_t* lengths, int32_t* status,
                                void* ws, hipStream_t s) {
-    const int blocks = (g.W + kChannels - 1) / kChannels;
+    const Shape sh = back_shape(g, T);
     float* parts = static_cast<float*>(ws);
-    hipLaunchKernelGGL((lru_backward_kernel<Act, 4, GATE>), dim3(g.B * blocks), dim3(kThreads), 0, s,
-                       static_cast<const Act*>(a.x), static_cast<const Act*>(a.r), static_cast<const Act*>(a.i), a.A,
-                       static_cast<const Act*>(a.z), lengths, a.saved, static_cast<const Act*>(a.dy), a.dstate,
-                       static_cast<Act*>(a.dx), static_cast<Act*>(a.dr), static_cast<Act*>(a.di),
-                       static_cast<Act*>(a.dz), a.dstate0, parts, status, T, g.W, blocks, g.p, g.gp);
-    hipError_t e = hipGetLastError();
+    Chain ch = {};
+    hipError_t e = hipSuccess;
+    if (sh.segs > 1)
+        e = clear_chain(static_cast<char*>(ws) + parts_bytes(g, sh), sh, ch, s);
     if (e != hipSuccess)
         return e;
-    const int rows = g.B * ((T + kSaveStep - 1) / kSaveStep);
-    hipLaunchKernelGGL(lru_rate_kernel, dim3((g.W + 63) / 64), dim3(256), 0, s, parts, a.A, a.dA, rows, g.W);
+    if (sh.segs > 1 && sh.channels == 256)
+        e = backward_launch<Act, 64, BW, BN, GATE, true>(g, a, T, lengths, status, parts, sh, ch, s);
+    else if (sh.segs > 1)
+        e = backward_launch<Act, 16, 8, 2, GATE, true>(g, a, T, lengths, status, parts, sh, ch, s);
+    else if (sh.channels == 256)
+        e = backward_launch<Act, 64, BW, BN, GATE, false>(g, a, T, lengths, status, parts, sh, ch, s);
+    else if (sh.tokens == 32)
+        e = backward_launch<Act, 16, 4, 2, GATE, false>(g, a, T, lengths, status, parts, sh, ch, s);
+    else
+        e = backward_launch<Act, 16, 8, 2, GATE, false>(g, a, T, lengths, status, parts, sh, ch, s);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(lru_rate_kernel, dim3((g.W + 63) / 64), dim3(1024), 0, s, parts, a.A, a.dA, g.B * sh.segs, g.W);
     return hipGetLastError();
 }
 
@@ -503,9 +665,7 @@ size_t lru_saved_bytes(const LruGeo& g, int T) {
     return static_cast<size_t>(g.B) * ((T + lru::kSaveStep - 1) / lru::kSaveStep) * g.W * sizeof(float);
 }
 
-size_t lru_prefill_ws_bytes(const LruGeo& g, int T) {
-    return T <= lru::tokens_of(g.bf16) * lru::kGroups ? 0 : lru::chain_bytes(lru::scan_tiles(g, T));
-}
+size_t lru_prefill_ws_bytes(const LruGeo& g, int T) { return lru::chain_bytes(lru::scan_shape(g, T)); }
 
 hipError_t launch_lru_prefill(const LruGeo& g, const LruArgs& a, int T, const int32_t* lengths, float* saved,
                               int32_t* status, void* ws, hipStream_t s) {
@@ -516,7 +676,10 @@ hipError_t launch_lru_prefill(const LruGeo& g, const LruArgs& a, int T, const in
                : lru::scan_cfg<float, false>(g, a, T, lengths, saved, status, ws, s);
 }
 
-size_t lru_backward_ws_bytes(const LruGeo& g, int T) { return lru_saved_bytes(g, T); }
+size_t lru_backward_ws_bytes(const LruGeo& g, int T) {
+    const lru::Shape sh = lru::back_shape(g, T);
+    return lru::parts_bytes(g, sh) + lru::chain_bytes(sh);
+}
 
 hipError_t launch_lru_backward(const LruGeo& g, const LruGrads& a, int T, const int32_t* lengths, int32_t* status,
                                void* ws, hipStream_t s) {
