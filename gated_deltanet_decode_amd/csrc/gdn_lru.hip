@@ -13,9 +13,6 @@
 #include "gdn.h"
 #include "gdn_lru.hpp"
 
-#ifndef LRU_BOCC
-#define LRU_BOCC 2
-#endif
 namespace gdn {
 namespace lru {
 
@@ -103,6 +100,8 @@ __global__ __launch_bounds__(WAVES * kWave, 4) void lru_scan_kernel(
     const int t0 = group * N;
     const Rows<Act> xs(x, row0, p.x, c), rs(r, row0, p.r, c), is(i, row0, p.i, c), zs(GATE ? z : x, row0, p.z, c);
     typename Q::raw rx[N], rr[N], ri[N], rz[N];
+    // z is asked for with the rest in bf16; fp32 has no registers for it until x, r and i are used
+    constexpr bool LATE = GATE && sizeof(Act) == 4;
     if (live >= L) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -110,7 +109,7 @@ __global__ __launch_bounds__(WAVES * kWave, 4) void lru_scan_kernel(
             ri[j] = is.load(t0, j);
             rx[j] = xs.load(t0, j);
         }
-        if constexpr (GATE)
+        if constexpr (GATE && !LATE)
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 rz[j] = zs.load(t0, j);
@@ -121,13 +120,12 @@ __global__ __launch_bounds__(WAVES * kWave, 4) void lru_scan_kernel(
             rr[j] = rs.load(t);
             ri[j] = is.load(t);
             rx[j] = xs.load(t);
-            if constexpr (GATE)
+            if constexpr (GATE && !LATE)
                 rz[j] = zs.load(t);
         }
     }
     float* enter = state + static_cast<int64_t>(b) * W;
-    const int mine = c_block + wave * kWave + lane;   // of the first E waves: the channel they hold for the chain
-    const float first = seg == 0 && wave < E ? enter[min(mine, W - 1)] : 0.0f;
+    const float first = seg == 0 && wave < E ? enter[min(c_block + wave * kWave + lane, W - 1)] : 0.0f;
     const float4 rate4 = *reinterpret_cast<const float4*>(A + c);
     const float rt[4] = {rate2(rate4.x), rate2(rate4.y), rate2(rate4.z), rate2(rate4.w)};
 
@@ -154,6 +152,10 @@ __global__ __launch_bounds__(WAVES * kWave, 4) void lru_scan_kernel(
                     a[j][k] = 1.0f;
                     v[j][k] = 0.0f;
                 }
+    if constexpr (LATE)
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            rz[j] = zs.load(min(t0 + j, live - 1));
     float am[4] = {1, 1, 1, 1}, hm[4] = {0, 0, 0, 0}, wa[4], wv[4];   // the lane's map, then the wave's
 #pragma unroll
     for (int j = 0; j < N; ++j)
@@ -162,37 +164,44 @@ __global__ __launch_bounds__(WAVES * kWave, 4) void lru_scan_kernel(
             hm[k] = __builtin_fmaf(a[j][k], hm[k], v[j][k]);
             am[k] *= a[j][k];
         }
-    scan_forward<LPC>(lane, am, hm, wa, wv);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        scan_forward<LPC>(lane, am[k], hm[k], wa[k], wv[k]);
     if (lane >= kWave - LPC) {
-        ex.maps[wave][0][q] = make_float4(wa[0], wa[1], wa[2], wa[3]);
-        ex.maps[wave][1][q] = make_float4(wv[0], wv[1], wv[2], wv[3]);
+        put4(ex.maps[wave][0], q, wa);
+        put4(ex.maps[wave][1], q, wv);
     }
     __syncthreads();
 
-    const bool last = live <= L;
-    const int64_t word = static_cast<int64_t>(tile) * TL::kChannels + wave * kWave + lane;
-    float at = 1.0f, ht = 0.0f, h[4];   // the tile's map of that channel
-    if (wave < E) {
-#pragma unroll 2
+    const bool last = live <= L, holds = wave < E;
+    const int hc = wave * kWave + lane;   // the channel that the first E waves' lanes hold, of the tile's
+    const int64_t word = static_cast<int64_t>(tile) * TL::kChannels + hc;
+    float at = 1.0f, ht = 0.0f;           // the tile's map
+    if (holds) {
+#pragma unroll
         for (int w = 0; w < WAVES; ++w) {
-            const float ma = ex.map(w, 0, wave * kWave + lane);
-            ht = __builtin_fmaf(ma, ht, ex.map(w, 1, wave * kWave + lane));
-            at *= ma;
+            ht = __builtin_fmaf(ex.maps[w][0][hc], ht, ex.maps[w][1][hc]);
+            at *= ex.maps[w][0][hc];
         }
         if (CHAIN && !last && seg > 0)
             ch.announce_map(word, at, ht);
     }
-    const float into = gather<TL, WAVES, CHAIN>(ch, ex, wave, tile, chains, seg, first, h);
-    if (wave < E) {
-        const float leave = __builtin_fmaf(at, into, ht);
+    float in = gather<TL, WAVES, CHAIN>(ch, ex, wave, tile, chains, seg, first);
+    if (holds) {
+        const float leave = __builtin_fmaf(at, in, ht);
         if (!last)
             ch.announce_state(word, leave);
-        else if (mine < W)
-            enter[mine] = leave;
+        else if (c_block + hc < W)
+            enter[c_block + hc] = leave;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            ex.into[0][w][hc] = in;
+            in = __builtin_fmaf(ex.maps[w][0][hc], in, ex.maps[w][1][hc]);
+        }
     }
-#pragma unroll 2
-    for (int w = 0; w < wave; ++w)
-        compose(h, ex.maps[w][0][q], ex.maps[w][1][q]);
+    __syncthreads();
+    float h[4];
+    get4(ex.into[0][wave], q, h);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         h[k] = __builtin_fmaf(am[k], h[k], hm[k]);
@@ -239,7 +248,7 @@ __global__ __launch_bounds__(256) void lru_clear_kernel(uint4* __restrict__ word
 // Of a tile's tokens each channel's part of dA goes to `parts`.
 
 template <typename Act, int LPC, int WAVES, int N, bool GATE, bool CHAIN>
-__global__ __launch_bounds__(WAVES * kWave, LRU_BOCC) void lru_backward_kernel(
+__global__ __launch_bounds__(WAVES * kWave, 4) void lru_backward_kernel(
     const Act* __restrict__ x, const Act* __restrict__ r, const Act* __restrict__ i, const float* __restrict__ A,
     const Act* __restrict__ z, const int32_t* __restrict__ lengths, const float* __restrict__ saved,
     const Act* __restrict__ dy, const float* dstate, Act* __restrict__ dx, Act* __restrict__ dr, Act* __restrict__ di,
@@ -267,7 +276,8 @@ __global__ __launch_bounds__(WAVES * kWave, LRU_BOCC) void lru_backward_kernel(
     const int t0 = group * N, rows = min(T - seg * L, L), live = bad ? 0 : n - seg * L;
     const Rows<Act> xg(dx, row0, gp.x, c), rg(dr, row0, gp.r, c), ig(di, row0, gp.i, c), zg(GATE ? dz : dx, row0, gp.z, c);
     float* part = parts + (static_cast<int64_t>(b) * segs + seg) * W;
-    const int mine = c_block + wave * kWave + lane;   // of the first E waves: the channel they hold for the chain
+    const bool holds = wave < E;
+    const int hc = wave * kWave + lane, mine = min(c_block + hc, W - 1);   // the channel that the first E waves' lanes hold
     if (live <= 0) {   // behind the sequence's end: the gradient of what was not read
         const float zero[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -281,7 +291,7 @@ __global__ __launch_bounds__(WAVES * kWave, LRU_BOCC) void lru_backward_kernel(
             }
         if (on && group == 0)
             *reinterpret_cast<float4*>(part + c) = make_float4(0, 0, 0, 0);
-        if (seg == 0 && wave < E && !bad && dstate0 && mine < W)   // no token at all: the state passes through
+        if (seg == 0 && holds && !bad && dstate0 && c_block + hc < W)   // no token at all: the state passes through
             dstate0[static_cast<int64_t>(b) * W + mine] = dstate ? dstate[static_cast<int64_t>(b) * W + mine] : 0.0f;
         return;
     }
@@ -311,9 +321,9 @@ __global__ __launch_bounds__(WAVES * kWave, LRU_BOCC) void lru_backward_kernel(
         }
     }
     const int marks = (T + kSaveStep - 1) / kSaveStep;
-    const float4 h4 = *reinterpret_cast<const float4*>(saved + (static_cast<int64_t>(b) * marks + seg * (L / kSaveStep)) * W + c);
+    float h0 = holds ? saved[(static_cast<int64_t>(b) * marks + seg * (L / kSaveStep)) * W + mine] : 0.0f;
     const int dist = (n + L - 1) / L - 1 - seg;   // place in the chain: the sequence's last tile is its first
-    const float first = dist == 0 && wave < E && dstate ? dstate[static_cast<int64_t>(b) * W + min(mine, W - 1)] : 0.0f;
+    const float first = dist == 0 && holds && dstate ? dstate[static_cast<int64_t>(b) * W + mine] : 0.0f;
     const float4 A4 = *reinterpret_cast<const float4*>(A + c);
     const float rate[4] = {rate_of(A4.x), rate_of(A4.y), rate_of(A4.z), rate_of(A4.w)};
 
@@ -382,34 +392,52 @@ __global__ __launch_bounds__(WAVES * kWave, LRU_BOCC) void lru_backward_kernel(
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         ar[k] = am[k];
-    scan_forward<LPC>(lane, am, hm, wa, wv);
-    scan_reverse<LPC>(lane, ar, km, wk);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        scan_forward<LPC>(lane, am[k], hm[k], wa[k], wv[k]);
+        scan_reverse<LPC>(lane, ar[k], km[k], wk[k]);
+    }
     if (lane >= kWave - LPC) {
-        ex.maps[wave][0][q] = make_float4(wa[0], wa[1], wa[2], wa[3]);
-        ex.maps[wave][1][q] = make_float4(wv[0], wv[1], wv[2], wv[3]);
+        put4(ex.maps[wave][0], q, wa);
+        put4(ex.maps[wave][1], q, wv);
     }
     if (lane < LPC)
-        ex.maps[wave][2][q] = make_float4(wk[0], wk[1], wk[2], wk[3]);
+        put4(ex.maps[wave][2], q, wk);
     __syncthreads();
 
     const bool last = seg == 0;
-    const int64_t word = static_cast<int64_t>(tile) * TL::kChannels + wave * kWave + lane;
-    float at = 1.0f, kt = 0.0f, K[4];
-    if (wave < E) {
-#pragma unroll 2
+    const int64_t word = static_cast<int64_t>(tile) * TL::kChannels + hc;
+    float at = 1.0f, kt = 0.0f;   // the tile's map
+    if (holds) {
+#pragma unroll
         for (int w = WAVES - 1; w >= 0; --w) {
-            const float ma = ex.map(w, 0, wave * kWave + lane);
-            kt = __builtin_fmaf(ma, kt, ex.map(w, 2, wave * kWave + lane));
-            at *= ma;
+            kt = __builtin_fmaf(ex.maps[w][0][hc], kt, ex.maps[w][2][hc]);
+            at *= ex.maps[w][0][hc];
         }
         if (CHAIN && !last && dist > 0)
             ch.announce_map(word, at, kt);
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            ex.into[0][w][hc] = h0;
+            h0 = __builtin_fmaf(ex.maps[w][0][hc], h0, ex.maps[w][1][hc]);
+        }
     }
-    // h before each token, less P, while the chain's words are under way
-    float h[4] = {h4.x, h4.y, h4.z, h4.w};
-#pragma unroll 2
-    for (int w = 0; w < wave; ++w)
-        compose(h, ex.maps[w][0][q], ex.maps[w][1][q]);
+    float in = gather<TL, WAVES, CHAIN>(ch, ex, wave, tile, chains, dist, first);
+    if (holds) {
+        const float leave = __builtin_fmaf(at, in, kt);
+        if (!last)
+            ch.announce_state(word, leave);
+        else if (dstate0 && c_block + hc < W)
+            dstate0[static_cast<int64_t>(b) * W + mine] = leave;
+#pragma unroll
+        for (int w = WAVES - 1; w >= 0; --w) {
+            ex.into[1][w][hc] = in;
+            in = __builtin_fmaf(ex.maps[w][0][hc], in, ex.maps[w][2][hc]);
+        }
+    }
+    // h before each token, less P
+    float h[4], K[4], dA[4] = {0, 0, 0, 0};
+    get4(ex.into[0][wave], q, h);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         h[k] = __builtin_fmaf(am[k], h[k], hm[k]);
@@ -422,18 +450,8 @@ __global__ __launch_bounds__(WAVES * kWave, LRU_BOCC) void lru_backward_kernel(
             if constexpr (GATE)
                 fd[j][k] *= h[k];
         }
-    const float into = gather<TL, WAVES, CHAIN>(ch, ex, wave, tile, chains, dist, first, K);
-    if (wave < E) {
-        const float leave = __builtin_fmaf(at, into, kt);
-        if (!last)
-            ch.announce_state(word, leave);
-        else if (dstate0 && mine < W)
-            dstate0[static_cast<int64_t>(b) * W + mine] = leave;
-    }
-#pragma unroll 2
-    for (int w = WAVES - 1; w > wave; --w)
-        compose(K, ex.maps[w][0][q], ex.maps[w][2][q]);
-    float dA[4] = {0, 0, 0, 0};
+    __syncthreads();
+    get4(ex.into[1][wave], q, K);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         K[k] = __builtin_fmaf(ar[k], K[k], km[k]);
@@ -476,18 +494,15 @@ __global__ __launch_bounds__(WAVES * kWave, LRU_BOCC) void lru_backward_kernel(
 #pragma unroll
         for (int d = LPC; d < kWave; d *= 2)
             dA[k] += __shfl_xor(dA[k], d);
-    __syncthreads();
     if (lane < LPC)
-        ex.look[wave][0][q] = make_float4(dA[0], dA[1], dA[2], dA[3]);
+        put4(ex.look[wave][0], q, dA);   // the chain's words have been read
     __syncthreads();
-    if (wave == 0 && lane < LPC && on) {
-        float s[4] = {0, 0, 0, 0};
+    if (holds && c_block + hc < W) {
+        float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            const float4 u = ex.look[w][0][q];
-            s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
-        }
-        *reinterpret_cast<float4*>(part + c) = make_float4(s[0], s[1], s[2], s[3]);
+        for (int w = 0; w < WAVES; ++w)
+            s += ex.look[w][0][hc];
+        part[c_block + hc] = s;
     }
 }
 
@@ -523,8 +538,7 @@ static hipError_t token_cfg(const LruGeo& g, const LruArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Tiles of the kernels over prompts.  Wide calls take 256 channels to a tile (512 or
-// 1,024 bytes of a row); where that leaves too few workgroups, 64.
+// Tiles of the kernels over prompts.
 struct Shape {
     int channels, tokens, blocks, segs;
     int64_t tiles;
@@ -538,28 +552,19 @@ inline Shape shape_of(const LruGeo& g, int T, int channels, int tokens) {
     s.tiles = static_cast<int64_t>(g.B) * s.blocks * s.segs;
     return s;
 }
-#ifndef FW
-#define FW 8
-#endif
-#ifndef FN
-#define FN 8
-#endif
-#ifndef BW
-#define BW 8
-#endif
-#ifndef BN
-#define BN 4
-#endif
-constexpr int kWideTiles = 512;
-inline bool wide(const LruGeo& g, int T, int tokens) { return shape_of(g, T, 256, tokens).tiles >= kWideTiles; }
+
+constexpr int kWide = 128;   // channels of a wide tile
+constexpr int kScanTokens = 128, kBackTokens = 32;
 inline Shape scan_shape(const LruGeo& g, int T) {
-    if (T > 64 && wide(g, T, FW * FN))
-        return shape_of(g, T, 256, FW * FN);
-    return shape_of(g, T, 64, T <= 32 ? 32 : T <= 64 ? 64 : 128);
+    const Shape s = shape_of(g, T, kWide, kScanTokens);
+    if (s.segs > 1 && s.tiles >= (g.bf16 ? 256 : 1024))
+        return s;
+    return shape_of(g, T, 64, T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : T <= 256 ? 256 : 128);
 }
 inline Shape back_shape(const LruGeo& g, int T) {
-    if (wide(g, T, BW * BN))
-        return shape_of(g, T, 256, BW * BN);
+    const Shape s = shape_of(g, T, kWide, kBackTokens);
+    if (s.segs > 1 && s.tiles >= 2048)
+        return s;
     return shape_of(g, T, 64, T <= 32 ? 32 : 64);
 }
 
@@ -599,15 +604,16 @@ static hipError_t scan_cfg(const LruGeo& g, const LruArgs& a, int T, const int32
         const hipError_t e = clear_chain(ws, sh, ch, s);
         if (e != hipSuccess)
             return e;
-        if (sh.channels == 256)
-            return scan_launch<Act, 64, FW, FN, GATE, true>(g, a, T, lengths, saved, status, sh, ch, s);
+        if (sh.channels == kWide)
+            return scan_launch<Act, 32, 8, 8, GATE, true>(g, a, T, lengths, saved, status, sh, ch, s);
         return scan_launch<Act, 16, 8, 4, GATE, true>(g, a, T, lengths, saved, status, sh, ch, s);
     }
-    if (sh.tokens == 32)
-        return scan_launch<Act, 16, 4, 2, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
-    if (sh.tokens == 64)
-        return scan_launch<Act, 16, 8, 2, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
-    return scan_launch<Act, 16, 8, 4, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
+    switch (sh.tokens) {
+        case 32: return scan_launch<Act, 16, 4, 2, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
+        case 64: return scan_launch<Act, 16, 8, 2, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
+        case 128: return scan_launch<Act, 16, 8, 4, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
+        default: return scan_launch<Act, 16, 8, 8, GATE, false>(g, a, T, lengths, saved, status, sh, ch, s);
+    }
 }
 
 template <typename Act, int LPC, int WAVES, int N, bool GATE, bool CHAIN>
@@ -637,16 +643,14 @@ static hipError_t backward_cfg(const LruGeo& g, const LruGrads& a, int T, const 
         e = clear_chain(static_cast<char*>(ws) + parts_bytes(g, sh), sh, ch, s);
     if (e != hipSuccess)
         return e;
-    if (sh.segs > 1 && sh.channels == 256)
-        e = backward_launch<Act, 64, BW, BN, GATE, true>(g, a, T, lengths, status, parts, sh, ch, s);
+    if (sh.channels == kWide)
+        e = backward_launch<Act, 32, 8, 2, GATE, true>(g, a, T, lengths, status, parts, sh, ch, s);
     else if (sh.segs > 1)
         e = backward_launch<Act, 16, 8, 2, GATE, true>(g, a, T, lengths, status, parts, sh, ch, s);
-    else if (sh.channels == 256)
-        e = backward_launch<Act, 64, BW, BN, GATE, false>(g, a, T, lengths, status, parts, sh, ch, s);
-    else if (sh.tokens == 32)
-        e = backward_launch<Act, 16, 4, 2, GATE, false>(g, a, T, lengths, status, parts, sh, ch, s);
-    else
+    else if (sh.tokens == 64)
         e = backward_launch<Act, 16, 8, 2, GATE, false>(g, a, T, lengths, status, parts, sh, ch, s);
+    else
+        e = backward_launch<Act, 16, 4, 2, GATE, false>(g, a, T, lengths, status, parts, sh, ch, s);
     if (e != hipSuccess)
         return e;
     hipLaunchKernelGGL(lru_rate_kernel, dim3((g.W + 63) / 64), dim3(1024), 0, s, parts, a.A, a.dA, g.B * sh.segs, g.W);

@@ -107,58 +107,61 @@ __device__ __forceinline__ void decay(float l2, float& a, float& m, float& inv) 
     m = m2 * inv;
 }
 
-__device__ __forceinline__ void compose(float (&h)[4], float4 a, float4 v) {
-    h[0] = __builtin_fmaf(a.x, h[0], v.x);
-    h[1] = __builtin_fmaf(a.y, h[1], v.y);
-    h[2] = __builtin_fmaf(a.z, h[2], v.z);
-    h[3] = __builtin_fmaf(a.w, h[3], v.w);
+// A value of the wave's lower and of its upper 32 lanes, in all lanes.
+__device__ __forceinline__ void both_halves(float x, float& lower, float& upper) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    lower = __uint_as_float(r[0]);
+    upper = __uint_as_float(r[1]);
 }
 
-// Scan of maps over a wave's groups of LPC lanes.  On return `a, v` is the map of the
-// groups before this one (first group first), and lanes of the last group hold the
-// wave's in `wa, wv`.
+// Maps of a wave's groups of LPC lanes, of one channel: `a, v` becomes the map of the
+// groups before this one (first group first); `wa, wv` is the wave's, in the last
+// group's lanes.
 template <int LPC>
-__device__ __forceinline__ void scan_forward(int lane, float (&a)[4], float (&v)[4], float (&wa)[4], float (&wv)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
+__device__ __forceinline__ void scan_forward(int lane, float& a, float& v, float& wa, float& wv) {
+    if constexpr (LPC == 32) {
+        float a0, a1, v0, v1;
+        both_halves(a, a0, a1);
+        both_halves(v, v0, v1);
+        wa = a0 * a1;
+        wv = __builtin_fmaf(a1, v0, v1);
+        a = lane >= 32 ? a0 : 1.0f;
+        v = lane >= 32 ? v0 : 0.0f;
+    } else {
 #pragma unroll
         for (int d = LPC; d < kWave; d *= 2) {
-            const float pa = __shfl_up(a[k], d), pv = __shfl_up(v[k], d);
-            v[k] = lane >= d ? __builtin_fmaf(a[k], pv, v[k]) : v[k];
-            a[k] = lane >= d ? a[k] * pa : a[k];
+            const float pa = __shfl_up(a, d), pv = __shfl_up(v, d);
+            v = lane >= d ? __builtin_fmaf(a, pv, v) : v;
+            a = lane >= d ? a * pa : a;
         }
-        wa[k] = a[k];
-        wv[k] = v[k];
-        if constexpr (LPC < kWave) {
-            const float pa = __shfl_up(a[k], LPC), pv = __shfl_up(v[k], LPC);
-            a[k] = lane >= LPC ? pa : 1.0f;
-            v[k] = lane >= LPC ? pv : 0.0f;
-        } else {
-            a[k] = 1.0f;
-            v[k] = 0.0f;
-        }
+        wa = a;
+        wv = v;
+        const float pa = __shfl_up(a, LPC), pv = __shfl_up(v, LPC);
+        a = lane >= LPC ? pa : 1.0f;
+        v = lane >= LPC ? pv : 0.0f;
     }
 }
-// The same from the last group back; the first group's lanes hold the wave's.
+// The same from the last group back; the wave's is in the first group's lanes.
 template <int LPC>
-__device__ __forceinline__ void scan_reverse(int lane, float (&a)[4], float (&v)[4], float (&wv)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
+__device__ __forceinline__ void scan_reverse(int lane, float& a, float& v, float& wv) {
+    if constexpr (LPC == 32) {
+        float a0, a1, v0, v1;
+        both_halves(a, a0, a1);
+        both_halves(v, v0, v1);
+        wv = __builtin_fmaf(a0, v1, v0);
+        a = lane >= 32 ? 1.0f : a1;
+        v = lane >= 32 ? 0.0f : v1;
+    } else {
 #pragma unroll
         for (int d = LPC; d < kWave; d *= 2) {
-            const float pa = __shfl_down(a[k], d), pv = __shfl_down(v[k], d);
-            v[k] = lane < kWave - d ? __builtin_fmaf(a[k], pv, v[k]) : v[k];
-            a[k] = lane < kWave - d ? a[k] * pa : a[k];
+            const float pa = __shfl_down(a, d), pv = __shfl_down(v, d);
+            v = lane < kWave - d ? __builtin_fmaf(a, pv, v) : v;
+            a = lane < kWave - d ? a * pa : a;
         }
-        wv[k] = v[k];
-        if constexpr (LPC < kWave) {
-            const float pa = __shfl_down(a[k], LPC), pv = __shfl_down(v[k], LPC);
-            a[k] = lane < kWave - LPC ? pa : 1.0f;
-            v[k] = lane < kWave - LPC ? pv : 0.0f;
-        } else {
-            a[k] = 1.0f;
-            v[k] = 0.0f;
-        }
+        wv = v;
+        const float pa = __shfl_down(a, LPC), pv = __shfl_down(v, LPC);
+        a = lane < kWave - LPC ? pa : 1.0f;
+        v = lane < kWave - LPC ? pv : 0.0f;
     }
 }
 
@@ -212,16 +215,27 @@ struct Chain {
     __device__ void announce_state(int64_t at, float h) const { put(at, kState, h); }
 };
 
-// What the waves of a workgroup tell each other: the MAPS parts of their own maps,
-// the tiles that each of them has looked up, and the tile that was taken.
+// What the waves of a workgroup tell each other, per channel: the MAPS parts of their
+// maps, the tiles that each of them has looked up, and what enters each wave's tokens
+// (the state and, in a gradient, what is passed back).  The first kWords waves hold a
+// channel to a lane where one value is carried over all waves.
 template <typename TL, int WAVES, int MAPS>
 struct Exchange {
-    float4 maps[WAVES][MAPS][TL::kChannels / 4];
-    float4 look[WAVES][2][TL::kChannels / 4];
+    using Row = float[TL::kChannels];
+    alignas(16) Row maps[WAVES][MAPS];
+    alignas(16) Row look[WAVES][2];
+    alignas(16) Row into[MAPS - 1][WAVES];
     int known[WAVES];   // 2: a state, 1: a map, 0: neither (ahead of the chain's start)
     int tile;
-    __device__ float map(int w, int part, int c) const { return reinterpret_cast<const float*>(maps[w][part])[c]; }
 };
+
+__device__ __forceinline__ void put4(float* row, int q, const float (&v)[4]) {
+    reinterpret_cast<float4*>(row)[q] = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void get4(const float* row, int q, float (&v)[4]) {
+    const float4 f = reinterpret_cast<const float4*>(row)[q];
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+}
 
 template <typename EX>
 __device__ __forceinline__ int take_tile(const Chain& ch, EX& ex) {
@@ -235,28 +249,23 @@ __device__ __forceinline__ int take_tile(const Chain& ch, EX& ex) {
 // a second call on the same workspace has cleared the word, against the rules.
 constexpr int kPolls = 1 << 22;   // some seconds
 
-// The value that enters a tile: `h` for this lane's four channels, and as the result,
-// in the first kWords waves, the one of channel 64 * wave + lane.  The tile is the
-// dist-th of its chain, whose tiles are `chains` apart.  `first` is what enters the
-// first of them, for the same channels: only that tile has read it, before it
-// announces what it leaves, so that the last tile may replace it in memory.
+// The value that enters a tile, in the first kWords waves, for the channel
+// 64 * wave + lane.  The tile is the dist-th of its chain, whose tiles are `chains`
+// apart.  `first` is what enters the first of them, for the same channels: only that
+// tile has read it, before it announces what it leaves, so that the last tile may
+// replace it in memory.  All waves pass a barrier here.
 //
 // Each wave looks at one of the tiles before, the nearest to the first wave, until
 // one of them shows a state; from there the maps are applied one after the other, as
 // those tiles apply theirs themselves.  So the bits do not depend on which tile had
 // come how far.
 template <typename TL, int WAVES, bool CHAIN, typename EX>
-__device__ __forceinline__ float gather(const Chain& ch, EX& ex, int wave, int tile, int chains, int dist, float first,
-                                        float (&h)[4]) {
+__device__ __forceinline__ float gather(const Chain& ch, EX& ex, int wave, int tile, int chains, int dist, float first) {
     constexpr int E = TL::kWords;
     static_assert(E <= WAVES, "a wave to each 64 channels");
-    const int lane = threadIdx.x & 63, q = lane % (TL::kChannels / 4);
+    const int lane = threadIdx.x & 63;
     if (!CHAIN || dist == 0) {
-        if (wave < E)
-            reinterpret_cast<float*>(ex.look[0][1])[wave * kWave + lane] = first;
         __syncthreads();
-        const float4 v = ex.look[0][1][q];
-        h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
         return first;
     }
     const int s = dist - 1 - wave;
@@ -296,8 +305,8 @@ __device__ __forceinline__ float gather(const Chain& ch, EX& ex, int wave, int t
             if (known != before)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    reinterpret_cast<float*>(ex.look[wave][0])[e * kWave + lane] = a[e];
-                    reinterpret_cast<float*>(ex.look[wave][1])[e * kWave + lane] = v[e];
+                    ex.look[wave][0][e * kWave + lane] = a[e];
+                    ex.look[wave][1][e * kWave + lane] = v[e];
                 }
         }
         if (lane == 0)
@@ -309,16 +318,14 @@ __device__ __forceinline__ float gather(const Chain& ch, EX& ex, int wave, int t
             break;
         __syncthreads();
     }
-    float mine = wave < E ? reinterpret_cast<const float*>(ex.look[w][1])[wave * kWave + lane] : 0.0f;
-    const float4 from = ex.look[w][1][q];
-    h[0] = from.x, h[1] = from.y, h[2] = from.z, h[3] = from.w;
-    while (--w >= 0) {
-        compose(h, ex.look[w][0][q], ex.look[w][1][q]);
-        if (wave < E)
-            mine = __builtin_fmaf(reinterpret_cast<const float*>(ex.look[w][0])[wave * kWave + lane], mine,
-                                  reinterpret_cast<const float*>(ex.look[w][1])[wave * kWave + lane]);
+    float in = 0.0f;
+    if (wave < E) {
+        const int c = wave * kWave + lane;
+        in = ex.look[w][1][c];
+        while (--w >= 0)
+            in = __builtin_fmaf(ex.look[w][0][c], in, ex.look[w][1][c]);
     }
-    return mine;
+    return in;
 }
 
 }  // namespace lru

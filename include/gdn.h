@@ -660,7 +660,7 @@ gdn_status gdn_lru_decode_token(const gdn_lru_dims* d, const gdn_lru_pitches* pi
  *           length is out of range (that sequence is untouched)
  *   workspace  device bytes >= gdn_lru_prefill_workspace_bytes(d, T), which is 0
  *           for short calls (then it may be NULL), 256-byte aligned; a size
- *           serves every call of no more sequences, tokens and channels
+ *           serves every call of no more sequences, tokens and channels of its type
  * State and fp32 outputs agree with the token-by-token call to fp32 rounding of
  * the terms they are sums of; bf16 outputs add their own rounding.  A NaN or
  * infinity in a token's inputs reaches its own channel from that token on.
@@ -687,6 +687,7 @@ gdn_status gdn_lru_prefill(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, 
  *          nothing to dA and its gradients are not written
  *   workspace  device bytes >= gdn_lru_backward_workspace_bytes(d, T), 256-byte
  *          aligned; a size serves every call of no more sequences, tokens and channels
+ *          of its type
  * Where sqrt(1 - a^2) is 0 (a gate shut to the last bit, a rate of 0) its
  * derivative is taken as 0.  Sums have a fixed order: equal inputs give equal bits.
  */

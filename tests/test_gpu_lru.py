@@ -131,6 +131,18 @@ def test_many_segments(bf16, gate):
     m.check_grads(f)
 
 
+@pytest.mark.parametrize("B,T,W", [(16, 128, 2056), (16, 100, 2056), (40, 33, 1032), (70, 32, 2056), (6, 300, 2056), (3, 1100, 1032),
+                                   (24, 129, 1544)])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_batches_that_fill_the_chip(B, T, W, bf16):
+    """Enough channels and sequences for the wide tiles, on both sides of their lengths."""
+    m = Layer(lr.make(9, B, T, W, bf16, gate=T != 100))
+    m.prefill(saved=True)
+    f = m.check()
+    m.backward()
+    m.check_grads(f)
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 def test_no_saved_states_and_no_gradient_of_the_state(bf16):
     i = lr.make(8, 2, 300, 64, bf16)
