@@ -16,43 +16,52 @@ using lru::silu_slope;
 
 constexpr int kMaxSums = 3;     // weight gradients of one call
 
-// U consecutive values.
+// U consecutive values of a row: read once and written once, past what the caches
+// hold for reuse.
 template <typename T, int U>
 struct Unit;
-template <>
-struct Unit<uint16_t, 4> {
-    __device__ static void load(const uint16_t* p, float (&f)[4]) { Quad<uint16_t>::to_float(Quad<uint16_t>::load(p), f); }
-    __device__ static void store(uint16_t* p, const float (&f)[4]) { Quad<uint16_t>::store(p, lru::pack(f, uint16_t())); }
+template <int U>
+struct Unit<uint16_t, U> {
+    static constexpr int WORDS = U / 2;
+    typedef uint32_t raw __attribute__((ext_vector_type(WORDS)));
+    __device__ static raw load(const uint16_t* p) { return __builtin_nontemporal_load(reinterpret_cast<const raw*>(p)); }
+    __device__ static void to_float(raw v, float (&f)[U]) {
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) {
+            f[2 * k] = __uint_as_float(v[k] << 16);
+            f[2 * k + 1] = __uint_as_float(v[k] & 0xFFFF0000u);
+        }
+    }
+    __device__ static void store(uint16_t* p, const float (&f)[U]) {
+        raw v;
+#pragma unroll
+        for (int k = 0; k < WORDS; k += 2) {
+            const float four[4] = {f[2 * k], f[2 * k + 1], f[2 * k + 2], f[2 * k + 3]};
+            const uint2 w = lru::pack(four, uint16_t());
+            v[k] = w.x;
+            v[k + 1] = w.y;
+        }
+        __builtin_nontemporal_store(v, reinterpret_cast<raw*>(p));
+    }
 };
 template <>
 struct Unit<float, 4> {
-    __device__ static void load(const float* p, float (&f)[4]) { Quad<float>::to_float(Quad<float>::load(p), f); }
-    __device__ static void store(float* p, const float (&f)[4]) { Quad<float>::store(p, lru::pack(f, float())); }
+    typedef float raw __attribute__((ext_vector_type(4)));
+    __device__ static raw load(const float* p) { return __builtin_nontemporal_load(reinterpret_cast<const raw*>(p)); }
+    __device__ static void to_float(raw v, float (&f)[4]) { f[0] = v[0], f[1] = v[1], f[2] = v[2], f[3] = v[3]; }
+    __device__ static void store(float* p, const float (&f)[4]) {
+        __builtin_nontemporal_store(raw{f[0], f[1], f[2], f[3]}, reinterpret_cast<raw*>(p));
+    }
 };
-template <>
-struct Unit<uint16_t, 8> {
-    __device__ static void load(const uint16_t* p, float (&f)[8]) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+// Weights are read by every row.
+template <int U>
+__device__ __forceinline__ void load_weight(const float* p, float (&f)[U]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            f[2 * k] = __uint_as_float(u[k] << 16);
-            f[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-        }
+    for (int k = 0; k < U; k += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + k);
+        f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
     }
-    __device__ static void store(uint16_t* p, const float (&f)[8]) {
-        const float lo[4] = {f[0], f[1], f[2], f[3]}, hi[4] = {f[4], f[5], f[6], f[7]};
-        const uint2 a = lru::pack(lo, uint16_t()), b = lru::pack(hi, uint16_t());
-        *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
-    }
-};
-template <>
-struct Unit<float, 8> {
-    __device__ static void load(const float* p, float (&f)[8]) {
-        const float4 a = Quad<float>::load(p), b = Quad<float>::load(p + 4);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    }
-};
+}
 
 template <typename A, typename B>
 constexpr int unit_of() { return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4; }
@@ -61,28 +70,38 @@ constexpr int unit_of() { return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4; }
 template <int LPR>
 struct Team {
     int index, slot, size, teams, flip = 0;
-    float* mem;   // 2 x 16 floats, workgroup teams only
+    float* mem;   // 2 x 48 floats, workgroup teams only
     __device__ explicit Team(float* m)
         : index(LPR ? threadIdx.x % (LPR ? LPR : 1) : threadIdx.x), slot(LPR ? threadIdx.x / (LPR ? LPR : 1) : 0),
           size(LPR ? LPR : blockDim.x), teams(LPR ? blockDim.x / (LPR ? LPR : 1) : 1), mem(m) {}
-    __device__ float sum(float v) {
-        if constexpr (LPR == 32) {
-            v = group_sum<16>(v);
-            return v + __shfl_xor(v, 16);
-        } else if constexpr (LPR != 0) {
-            return group_sum<LPR>(v);
-        } else {
-            v = group_sum<64>(v);
+    // Sums of K values over the team, in a fixed order, in all of its lanes.
+    template <int K>
+    __device__ void sum(float (&v)[K]) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if constexpr (LPR == 32) {
+                v[k] = group_sum<16>(v[k]);
+                v[k] += __shfl_xor(v[k], 16);
+            } else {
+                v[k] = group_sum<LPR ? LPR : 64>(v[k]);
+            }
+        }
+        if constexpr (LPR == 0) {
             float* m = mem + flip;
-            flip ^= 16;
+            flip ^= 48;
             if ((threadIdx.x & 63) == 0)
-                m[threadIdx.x >> 6] = v;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    m[k * 16 + (threadIdx.x >> 6)] = v[k];
             __syncthreads();
             const int waves = blockDim.x >> 6;
-            float s = 0.0f;
-            for (int w = 0; w < waves; ++w)
-                s += m[w];
-            return s;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float s = 0.0f;
+                for (int w = 0; w < waves; ++w)
+                    s += m[k * 16 + w];
+                v[k] = s;
+            }
         }
     }
 };
@@ -98,14 +117,14 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
     const Res* residual, const Act* __restrict__ delta, const float* __restrict__ scale,
     const float* __restrict__ post, const float* __restrict__ w, Res* out, Act* __restrict__ y, int64_t rows, int W,
     float inv_n, float eps) {
-    __shared__ float mem[32];
+    __shared__ float mem[96];
     Team<LPR> team(mem);
     using RU = Unit<Res, U>;
     using AU = Unit<Act, U>;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot; row < rows;
          row += static_cast<int64_t>(gridDim.x) * team.teams) {
         const int64_t base = row * W;
-        float s[NV][U], d[NV][U];
+        float s[NV][U], d[NV][U], sq[1];
         bool on[NV];
         int c[NV];
 #pragma unroll
@@ -113,28 +132,29 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
             const int u = (team.index + j * team.size) * U;
             on[j] = u < W;
             c[j] = on[j] ? u : 0;
-            RU::load(residual + base + c[j], s[j]);
             if (delta)
-                AU::load(delta + base + c[j], d[j]);
+                AU::to_float(AU::load(delta + base + c[j]), d[j]);
+            RU::to_float(RU::load(residual + base + c[j]), s[j]);
         }
         if (delta) {
             float p = 1.0f;
             if constexpr (POST) {
-                float sq = 0.0f;
+                sq[0] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
 #pragma unroll
                     for (int k = 0; k < U; ++k)
-                        sq = on[j] ? __builtin_fmaf(d[j][k], d[j][k], sq) : sq;
-                p = inv_rms(team.sum(sq), inv_n, eps);
+                        sq[0] = on[j] ? __builtin_fmaf(d[j][k], d[j][k], sq[0]) : sq[0];
+                team.sum(sq);
+                p = inv_rms(sq[0], inv_n, eps);
             }
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 float ws[U], wp[U];
                 if (scale)
-                    Unit<float, U>::load(scale + c[j], ws);
+                    load_weight<U>(scale + c[j], ws);
                 if constexpr (POST)
-                    Unit<float, U>::load(post + c[j], wp);
+                    load_weight<U>(post + c[j], wp);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     const float n = POST ? d[j][k] * p * wp[k] : d[j][k];
@@ -146,17 +166,18 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
                     RU::store(out + base + c[j], s[j]);
             }
         }
-        float sq = 0.0f;
+        sq[0] = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                sq = on[j] ? __builtin_fmaf(s[j][k], s[j][k], sq) : sq;
-        const float q = inv_rms(team.sum(sq), inv_n, eps);
+                sq[0] = on[j] ? __builtin_fmaf(s[j][k], s[j][k], sq[0]) : sq[0];
+        team.sum(sq);
+        const float q = inv_rms(sq[0], inv_n, eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float ww[U];
-            Unit<float, U>::load(w + c[j], ww);
+            load_weight<U>(w + c[j], ww);
 #pragma unroll
             for (int k = 0; k < U; ++k)
                 ww[k] *= s[j][k] * q;
@@ -198,94 +219,107 @@ __device__ __forceinline__ void write_part(const Team<LPR>& team, float (&sums)[
     }
 }
 
+// Two sums to wait for per row (three values, then with `post` one), the next row
+// asked for before them.
 template <typename Act, typename Res, int U, int LPR, int NV, bool POST>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kernel(
     const Res* __restrict__ stream, const Act* __restrict__ delta, const float* __restrict__ scale,
     const float* __restrict__ post, const float* __restrict__ w, const Act* __restrict__ dy, const Res* ds,
     Res* dres, Act* __restrict__ ddelta, float* __restrict__ parts, int64_t rows, int W, float inv_n, float eps) {
-    __shared__ float mem[32];
+    __shared__ float mem[96];
     __shared__ float lds[LPR ? 256 * NV * U : 1];
     Team<LPR> team(mem);
     using RU = Unit<Res, U>;
     using AU = Unit<Act, U>;
-    float sw[NV][U] = {}, ss[NV][U] = {}, sp[NV][U] = {};
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot; row < rows;
-         row += static_cast<int64_t>(gridDim.x) * team.teams) {
-        const int64_t base = row * W;
-        float s[NV][U], g[NV][U], d[NV][U], t[NV][U];
-        bool on[NV];
-        int c[NV];
-        float sq = 0.0f, dot = 0.0f, dq = 0.0f;
+    float sw[NV][U] = {}, ss[NV][U] = {}, sp[NV][U] = {}, ww[NV][U], ws[NV][U], wp[NV][U];
+    bool on[NV];
+    int c[NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int u = (team.index + j * team.size) * U;
-            on[j] = u < W;
-            c[j] = on[j] ? u : 0;
-            RU::load(stream + base + c[j], s[j]);
-            AU::load(dy + base + c[j], g[j]);
-            if (delta)
-                AU::load(delta + base + c[j], d[j]);
-            if (ds)
-                RU::load(ds + base + c[j], t[j]);
-            else
-#pragma unroll
-                for (int k = 0; k < U; ++k)
-                    t[j][k] = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float ww[U];
-            Unit<float, U>::load(w + c[j], ww);
+    for (int j = 0; j < NV; ++j) {
+        const int u = (team.index + j * team.size) * U;
+        on[j] = u < W;
+        c[j] = on[j] ? u : 0;
+        load_weight<U>(w + c[j], ww[j]);
+        if (scale)
+            load_weight<U>(scale + c[j], ws[j]);
+        else
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                if (on[j]) {
-                    sq = __builtin_fmaf(s[j][k], s[j][k], sq);
-                    dot = __builtin_fmaf(g[j][k] * ww[k], s[j][k], dot);
-                    if constexpr (POST)
-                        dq = __builtin_fmaf(d[j][k], d[j][k], dq);
-                }
-        }
-        sq = team.sum(sq);
-        dot = team.sum(dot);
-        const float q = inv_rms(sq, inv_n, eps);
-        const float back = q * q * (dot * inv_n);
-        float p = 1.0f;
+                ws[j][k] = 1.0f;
         if constexpr (POST)
-            p = inv_rms(team.sum(dq), inv_n, eps);
-        float dot2 = 0.0f;
+            load_weight<U>(post + c[j], wp[j]);
+    }
+    typename RU::raw rs[NV], rt[NV] = {};
+    typename AU::raw rg[NV], rd[NV] = {};
+    auto ask = [&](int64_t row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float ww[U], ws[U], wp[U], o[U];
-            Unit<float, U>::load(w + c[j], ww);
-            if (scale)
-                Unit<float, U>::load(scale + c[j], ws);
-            if constexpr (POST)
-                Unit<float, U>::load(post + c[j], wp);
+            rs[j] = RU::load(stream + row * W + c[j]);
+            rg[j] = AU::load(dy + row * W + c[j]);
+            if (delta)
+                rd[j] = AU::load(delta + row * W + c[j]);
+            if (ds)
+                rt[j] = RU::load(ds + row * W + c[j]);
+        }
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * team.teams;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot;
+    if (row < rows)
+        ask(row);
+    for (; row < rows; row += step) {
+        const int64_t base = row * W;
+        float s[NV][U], g[NV][U], d[NV][U], t[NV][U], sums[POST ? 3 : 2] = {};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            RU::to_float(rs[j], s[j]);
+            AU::to_float(rg[j], g[j]);
+            AU::to_float(rd[j], d[j]);
+            RU::to_float(rt[j], t[j]);
+        }
+        if (row + step < rows)
+            ask(row + step);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (on[j])
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    sums[0] = __builtin_fmaf(s[j][k], s[j][k], sums[0]);
+                    sums[1] = __builtin_fmaf(g[j][k] * ww[j][k], s[j][k], sums[1]);
+                    if constexpr (POST)
+                        sums[2] = __builtin_fmaf(d[j][k], d[j][k], sums[2]);
+                }
+        team.sum(sums);
+        const float q = inv_rms(sums[0], inv_n, eps);
+        const float back = q * q * (sums[1] * inv_n);
+        const float p = POST ? inv_rms(sums[POST ? 2 : 0], inv_n, eps) : 1.0f;
+        float dot[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 sw[j][k] = __builtin_fmaf(g[j][k], s[j][k] * q, sw[j][k]);
-                o[k] = t[j][k] = __builtin_fmaf(q, g[j][k] * ww[k] - s[j][k] * back, t[j][k]);
-                if (delta) {
-                    const float dn = POST ? d[j][k] * p : d[j][k];
-                    if (scale) {
-                        ss[j][k] = __builtin_fmaf(t[j][k], POST ? dn * wp[k] : dn, ss[j][k]);
-                        t[j][k] *= ws[k];
-                    }
-                    if constexpr (POST) {
-                        sp[j][k] = __builtin_fmaf(t[j][k], dn, sp[j][k]);
-                        t[j][k] *= wp[k];
-                        if (on[j])
-                            dot2 = __builtin_fmaf(t[j][k], d[j][k], dot2);
-                    }
-                }
+                t[j][k] = __builtin_fmaf(q, g[j][k] * ww[j][k] - s[j][k] * back, t[j][k]);
             }
             if (on[j])
-                RU::store(dres + base + c[j], o);
+                RU::store(dres + base + c[j], t[j]);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const float dn = d[j][k] * p;
+                ss[j][k] = __builtin_fmaf(t[j][k], POST ? dn * wp[j][k] : dn, ss[j][k]);
+                t[j][k] *= ws[j][k];
+                if constexpr (POST) {
+                    sp[j][k] = __builtin_fmaf(t[j][k], dn, sp[j][k]);
+                    t[j][k] *= wp[j][k];
+                    if (on[j])
+                        dot[0] = __builtin_fmaf(t[j][k], d[j][k], dot[0]);
+                }
+            }
         }
         if (!delta)
             continue;
         if constexpr (POST) {
-            const float back2 = p * p * (team.sum(dot2) * inv_n);
+            team.sum(dot);
+            const float back2 = p * p * (dot[0] * inv_n);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -321,6 +355,7 @@ __global__ __launch_bounds__(1024) void part_sum_kernel(const float* __restrict_
     const float* p = parts + static_cast<int64_t>(blockIdx.y) * rows * W + c;
     float s = 0.0f;
     if (c < W)
+#pragma unroll 8
         for (int row = wave; row < rows; row += 16)
             s += p[static_cast<int64_t>(row) * W];
     mem[wave][lane] = s;
@@ -339,7 +374,7 @@ template <typename O, typename Act, int U, int LPR, int NV, bool FIRST>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
     const O* __restrict__ o, const Act* __restrict__ z, const float* __restrict__ w, Act* __restrict__ y,
     int64_t items, int H, int D, int64_t z_pitch, int w_step, float inv_n, float eps) {
-    __shared__ float mem[32];
+    __shared__ float mem[96];
     Team<LPR> team(mem);
     for (int64_t item = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot; item < items;
          item += static_cast<int64_t>(gridDim.x) * team.teams) {
@@ -348,14 +383,14 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
         float v[NV][U], gate[NV][U];
         bool on[NV];
         int c[NV];
-        float sq = 0.0f;
+        float sq[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int u = (team.index + j * team.size) * U;
             on[j] = u < D;
             c[j] = on[j] ? u : 0;
-            Unit<O, U>::load(o + item * D + c[j], v[j]);
-            Unit<Act, U>::load(z + row * z_pitch + static_cast<int64_t>(h) * D + c[j], gate[j]);
+            Unit<O, U>::to_float(Unit<O, U>::load(o + item * D + c[j]), v[j]);
+            Unit<Act, U>::to_float(Unit<Act, U>::load(z + row * z_pitch + static_cast<int64_t>(h) * D + c[j]), gate[j]);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -364,13 +399,14 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
                 gate[j][k] = silu(gate[j][k]);
                 if constexpr (FIRST)
                     v[j][k] *= gate[j][k];
-                sq = on[j] ? __builtin_fmaf(v[j][k], v[j][k], sq) : sq;
+                sq[0] = on[j] ? __builtin_fmaf(v[j][k], v[j][k], sq[0]) : sq[0];
             }
-        const float q = inv_rms(team.sum(sq), inv_n, eps);
+        team.sum(sq);
+        const float q = inv_rms(sq[0], inv_n, eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float ww[U];
-            Unit<float, U>::load(w + static_cast<int64_t>(h) * w_step + c[j], ww);
+            load_weight<U>(w + static_cast<int64_t>(h) * w_step + c[j], ww);
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 ww[k] *= v[j][k] * q;
@@ -391,7 +427,7 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
     const O* __restrict__ o, const Act* __restrict__ z, const float* __restrict__ w, const Act* __restrict__ dy,
     O* __restrict__ dov, Act* __restrict__ dz, float* __restrict__ parts, int64_t rows, int H, int D, int64_t step,
     int64_t z_pitch, int64_t dz_pitch, int w_step, float inv_n, float eps) {
-    __shared__ float mem[32];
+    __shared__ float mem[96];
     __shared__ float lds[LPR ? 256 * NV * U : 1];
     Team<LPR> team(mem);
     const int64_t id = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot;
@@ -405,18 +441,18 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
         const int u = (team.index + j * team.size) * U;
         on[j] = u < D;
         c[j] = on[j] ? u : 0;
-        Unit<float, U>::load(w + static_cast<int64_t>(h) * w_step + c[j], ww[j]);
+        load_weight<U>(w + static_cast<int64_t>(h) * w_step + c[j], ww[j]);
     }
     if (first < step)
         for (int64_t row = first; row < rows; row += step) {
             const int64_t base = (row * H + h) * D;
             float v[NV][U], gate[NV][U], slope[NV][U], g[NV][U];
-            float sq = 0.0f, dot = 0.0f;
+            float sums[2] = {};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                Unit<O, U>::load(o + base + c[j], v[j]);
-                Unit<Act, U>::load(z + row * z_pitch + static_cast<int64_t>(h) * D + c[j], gate[j]);
-                Unit<Act, U>::load(dy + base + c[j], g[j]);
+                Unit<O, U>::to_float(Unit<O, U>::load(o + base + c[j]), v[j]);
+                Unit<Act, U>::to_float(Unit<Act, U>::load(z + row * z_pitch + static_cast<int64_t>(h) * D + c[j]), gate[j]);
+                Unit<Act, U>::to_float(Unit<Act, U>::load(dy + base + c[j]), g[j]);
             }
 #pragma unroll
             for (int j = 0; j < NV; ++j)
@@ -426,14 +462,13 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
                     const float u = FIRST ? v[j][k] * gate[j][k] : v[j][k];
                     const float dn = (FIRST ? g[j][k] : g[j][k] * gate[j][k]) * ww[j][k];
                     if (on[j]) {
-                        sq = __builtin_fmaf(u, u, sq);
-                        dot = __builtin_fmaf(dn, u, dot);
+                        sums[0] = __builtin_fmaf(u, u, sums[0]);
+                        sums[1] = __builtin_fmaf(dn, u, sums[1]);
                     }
                 }
-            sq = team.sum(sq);
-            dot = team.sum(dot);
-            const float q = inv_rms(sq, inv_n, eps);
-            const float back = q * q * (dot * inv_n);
+            team.sum(sums);
+            const float q = inv_rms(sums[0], inv_n, eps);
+            const float back = q * q * (sums[1] * inv_n);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 float a[U], b[U];
@@ -502,11 +537,16 @@ static hipError_t with_shape(const Shape& s, F f) {
 }
 
 constexpr int64_t kBlocks = 1 << 16;         // forward workgroups; longer calls loop
-constexpr int64_t kBackBlocks = 512;         // backward workgroups, each with its own weight sums
 
-inline int64_t back_blocks(int64_t teams_needed, int teams) {
-    const int64_t need = (teams_needed + teams - 1) / teams;
-    return need < kBackBlocks ? need : kBackBlocks;
+constexpr int kBackUnit = 4;                 // half the registers of 8, and twice the lanes to a row
+constexpr int64_t kGatedBlocks = 768;        // workgroups of a gated norm's gradient, each with its own weight sums
+
+// Workgroups of a residual norm's gradient: what the chip holds at about 80 registers
+// to a lane, since each leaves its own weight sums behind.
+inline int64_t back_blocks(int64_t rows, const Shape& sh) {
+    const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
+    const int64_t need = (rows + teams - 1) / teams, most = 256 * (sh.nv == 1 && sh.threads < 1280 ? 1280 / sh.threads : 1);
+    return need < most ? need : most;
 }
 
 template <typename Act, typename Res>
@@ -529,10 +569,9 @@ static hipError_t residual_cfg(const ResidualNorm& a, hipStream_t s) {
 
 template <typename Act, typename Res>
 static hipError_t residual_back_cfg(const ResidualNormGrad& a, void* ws, hipStream_t s) {
-    constexpr int U = unit_of<Act, Res>();
+    constexpr int U = kBackUnit;
     const Shape sh = shape_of(a.W / U);
-    const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
-    const int64_t blocks = back_blocks(a.rows, teams);
+    const int64_t blocks = back_blocks(a.rows, sh);
     float* parts = static_cast<float*>(ws);
     hipError_t e = with_shape(sh, [&](auto lpr, auto nv) {
         auto go = [&](auto post) {
@@ -577,7 +616,7 @@ struct GatedPlan {
     int64_t blocks, step;
 };
 inline GatedPlan gated_plan(int64_t rows, int H, int teams) {
-    int64_t step = kBackBlocks * teams / H;
+    int64_t step = kGatedBlocks * teams / H;
     step = step < 1 ? 1 : step > rows ? rows : step;
     return {(step * H + teams - 1) / teams, step};
 }
@@ -612,7 +651,7 @@ static hipError_t gated_back_cfg(const GatedNorm& a, const GatedNormGrad& g, voi
 }  // namespace norm
 
 size_t residual_norm_back_ws_bytes(int64_t rows, int W) {
-    return static_cast<size_t>(norm::kMaxSums) * (rows < norm::kBackBlocks ? rows : norm::kBackBlocks) * W *
+    return static_cast<size_t>(norm::kMaxSums) * norm::back_blocks(rows, norm::shape_of(W / norm::kBackUnit)) * W *
            sizeof(float);
 }
 

@@ -730,7 +730,7 @@ gdn_status gdn_residual_norm(int64_t rows, int32_t W, int32_t act_dtype, int32_t
  *   dw, dscale, dw_post  f32 [W] (written; the latter two given where scale and
  *          w_post are, else NULL)
  *   workspace  device bytes >= gdn_residual_norm_backward_workspace_bytes(rows, W),
- *          256-byte aligned; a size serves every call of no more rows and channels
+ *          256-byte aligned; a size serves every call of no more rows of this W
  * Sums have a fixed order: equal inputs give equal bits.
  */
 size_t gdn_residual_norm_backward_workspace_bytes(int64_t rows, int32_t W);
