@@ -679,18 +679,22 @@ def _rows(t, name, dtype, lead, W, dev):
             if t.is_contiguous():
                 return t.data_ptr(), 0
             shape, strides = t.shape, t.stride()
-            if shape[-1] == W and (W == 1 or strides[-1] == 1):
+            n = len(shape)
+            if shape[-1] == W and strides[-1] == 1:
+                if n == 2 or (n == 3 and shape[0] == 1):
+                    return t.data_ptr(), strides[-2]
+                if n == 3 and shape[1] > 1 and strides[0] == shape[1] * strides[1]:
+                    return t.data_ptr(), strides[1]
                 pitch, span = 0, 1          # span: rows of the dimensions behind this one
-                for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
-                    if n == 1:
+                for m, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+                    if m == 1:
                         continue
-                    if pitch == 0:
-                        pitch = s
+                    pitch = pitch or s
                     if s != pitch * span:
                         break
-                    span *= n
+                    span *= m
                 else:
-                    return t.data_ptr(), max(pitch, 0)
+                    return t.data_ptr(), pitch
             raise ValueError(f"{name} must have contiguous rows of {W} at one pitch")
     except AttributeError:
         pass
@@ -707,9 +711,12 @@ def lru_state_bytes(d: LruDims) -> int:
 
 def lru_decode_token(d: LruDims, state, x, r, i, A, y, z=None, stream=None) -> None:
     """One token of a gated linear recurrent layer: x, r, i, y and z [B][W], state [B][W] in place."""
-    B, W, act, f32 = d.batch, d.width, torch.bfloat16 if d.act_dtype == BF16 else torch.float32, torch.float32
+    B, W, f32 = d.batch, d.width, torch.float32
+    act = torch.bfloat16 if d.act_dtype == BF16 else f32
     dev, s = _here(stream)
-    (xp, px), (rp, pr), (ip, pi) = _rows(x, "x", act, B, W, dev), _rows(r, "r", act, B, W, dev), _rows(i, "i", act, B, W, dev)
+    xp, px = _rows(x, "x", act, B, W, dev)
+    rp, pr = _rows(r, "r", act, B, W, dev)
+    ip, pi = _rows(i, "i", act, B, W, dev)
     zp, pz = (None, 0) if z is None else _rows(z, "z", act, B, W, dev)
     yp, py = _rows(y, "y", act, B, W, dev)
     _check(_lib.gdn_lru_decode_token(C.byref(d), _pitches(px, pr, pi, pz, py), _p(state, "state", f32, B * W, dev), xp, rp,
@@ -739,10 +746,13 @@ def _room(buf, name, need, dev):
     """Address and bytes of a device buffer of at least need bytes; None serves where none are needed."""
     if buf is None and need == 0:
         return None, 0
-    ptr, nbytes = _blob(buf, need, name)
-    if buf.get_device() != dev:
-        raise ValueError(f"{name} is on {buf.device}, but the current device is cuda:{dev}")
-    return ptr, nbytes
+    try:
+        if buf.get_device() == dev and buf.is_contiguous() and buf.nbytes >= need:
+            return buf.data_ptr(), buf.nbytes
+    except AttributeError:
+        pass
+    _blob(buf, need, name)   # says what is wrong
+    raise ValueError(f"{name} is on {buf.device}, but the current device is cuda:{dev}")
 
 
 def lru_prefill(d: LruDims, state, x, r, i, A, y, workspace, z=None, lengths=None, saved=None, status=None,
@@ -753,13 +763,16 @@ def lru_prefill(d: LruDims, state, x, r, i, A, y, workspace, z=None, lengths=Non
     lru_saved_bytes(d, T) bytes for lru_backward.  workspace: one of at least
     lru_prefill_workspace_bytes(d, T) bytes (None where that is 0)."""
     T = _lru_tokens(d, x, "gdn_lru_prefill")
-    B, W, act, f32 = d.batch, d.width, d.act_torch, torch.float32
+    B, W, f32 = d.batch, d.width, torch.float32
+    act = torch.bfloat16 if d.act_dtype == BF16 else f32
     dev, s = _here(stream)
     n = B * T
-    (xp, px), (rp, pr), (ip, pi) = _rows(x, "x", act, n, W, dev), _rows(r, "r", act, n, W, dev), _rows(i, "i", act, n, W, dev)
+    xp, px = _rows(x, "x", act, n, W, dev)
+    rp, pr = _rows(r, "r", act, n, W, dev)
+    ip, pi = _rows(i, "i", act, n, W, dev)
     zp, pz = (None, 0) if z is None else _rows(z, "z", act, n, W, dev)
     yp, py = _rows(y, "y", act, n, W, dev)
-    ws, nbytes = _room(workspace, "workspace", _lib.gdn_lru_prefill_workspace_bytes(C.byref(d), T), dev)
+    ws, nbytes = _room(workspace, "workspace", 0, dev)   # the library knows what it needs
     keep = None if saved is None else _room(saved, "saved", _lib.gdn_lru_saved_bytes(C.byref(d), T), dev)[0]
     _check(_lib.gdn_lru_prefill(C.byref(d), _pitches(px, pr, pi, pz, py), _p(state, "state", f32, B * W, dev), T, xp, rp, ip,
                                 _p(A, "A", f32, W, dev), zp,
@@ -867,11 +880,14 @@ def _heads(o, w, gate_first):
 
 def _head_rows(t, name, dtype, rows, H, D, dev):
     """_rows over the heads' H * D values; the heads of a row lie next to each other."""
-    if isinstance(t, torch.Tensor) and not t.is_contiguous():
-        if t.dim() < 2 or tuple(t.shape[-2:]) != (H, D) or (H > 1 and t.stride(-2) != D) or (D > 1 and t.stride(-1) != 1):
-            raise ValueError(f"{name} must be [rows][H][D] with contiguous rows at one pitch")
-        t = t.flatten(-2) if H * D else t
-    return _rows(t, name, dtype, rows, H * D, dev)
+    if not isinstance(t, torch.Tensor) or t.is_contiguous():
+        return _p(t, name, dtype, rows * H * D, dev), 0
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 2 or shape[-2:] != (H, D) or strides[-1] != 1 or (H > 1 and strides[-2] != D):
+        raise ValueError(f"{name} must be [rows][H][D] with contiguous rows at one pitch")
+    if len(shape) == 3 and t.get_device() == dev and t.dtype is dtype and shape[0] == rows:
+        return t.data_ptr(), strides[0]
+    return _rows(t.flatten(-2), name, dtype, rows, H * D, dev)
 
 
 def gated_norm(o, z, w, y, eps=1e-6, gate_first=False, stream=None) -> None:

@@ -930,9 +930,9 @@ static gdn_status gated_sizes(int64_t rows, int32_t H, int32_t D, int32_t o_dtyp
     const int64_t row = static_cast<int64_t>(H) * D;
     if (z_pitch == 0)
         z_pitch = row;
-    // weights are counted in 32 bits; a pitch of 2^32 elements keeps offsets within 64
-    if (flags & ~(GDN_GATE_FIRST | GDN_WEIGHT_PER_HEAD) || row >= (1ll << 30) || z_pitch < row || z_pitch % 8 != 0 ||
-        z_pitch > (1ll << 32))
+    // weights are counted in 32 bits, and offsets of z stay within 64
+    if ((flags & ~(GDN_GATE_FIRST | GDN_WEIGHT_PER_HEAD)) || row >= (1ll << 30) || z_pitch < row || z_pitch % 8 != 0 ||
+        z_pitch > (1ll << 56) / rows)
         return GDN_ERR_SHAPE;
     return GDN_OK;
 }
