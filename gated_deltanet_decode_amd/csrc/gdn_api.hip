@@ -190,7 +190,7 @@ gdn_status norm_sizes(int64_t rows, int32_t H, int32_t D, int32_t act, int32_t o
     if (!act_ok(act) || !act_ok(other) || (other != GDN_F32 && other != act))
         return GDN_ERR_DTYPE;
     if (rows < 1 || rows >= (1ll << 31) || H < 1 || H > 65536 || rows * H >= (1ll << 31) || D < 8 || D % 8 != 0 ||
-        D > GDN_NORM_MAX_WIDTH || !(eps > 0.0f) || !(eps <= 3.402823466e38f))
+        D > GDN_NORM_MAX_WIDTH || !(eps >= 1.17549435e-38f) || !(eps <= 3.402823466e38f))
         return GDN_ERR_SHAPE;
     return GDN_OK;
 }

@@ -17,17 +17,23 @@ namespace gdn {
 namespace lru {
 
 // ------------------------------------------------------------ one token
+//
+// Four channels to a lane, everything read once and written once.  Below some 10 MB
+// the launch sets the time (one sequence of 5,120 channels 2.3 us, 200 of 4,096, 14.7
+// MB, 4.5 us in a trace).
 
 template <typename Act, bool GATE>
 __global__ __launch_bounds__(256) void lru_token_kernel(float* __restrict__ state, const Act* __restrict__ x,
                                                         const Act* __restrict__ r, const Act* __restrict__ i,
                                                         const float* __restrict__ A, const Act* __restrict__ z,
-                                                        Act* __restrict__ y, int W, Pitches p) {
+                                                        Act* __restrict__ y, unsigned lanes, unsigned per_row, int W,
+                                                        Pitches p) {
     using Q = Quad<Act>;
-    const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
-    if (c >= W)
+    const unsigned at = blockIdx.x * 256 + threadIdx.x;   // four channels of one sequence
+    if (at >= lanes)
         return;
-    const int64_t b = blockIdx.y;
+    const int64_t b = at / per_row;
+    const int c = static_cast<int>(at % per_row) * 4;
     const typename Q::raw rr = Q::load(r + b * p.r + c), ri = Q::load(i + b * p.i + c), rx = Q::load(x + b * p.x + c);
     const float4 rate4 = *reinterpret_cast<const float4*>(A + c);
     float4* hp = reinterpret_cast<float4*>(state + b * W + c);
@@ -68,7 +74,17 @@ __global__ __launch_bounds__(256) void lru_token_kernel(float* __restrict__ stat
 // run and that announce their maps without waiting for anyone.  So every wait
 // ends.  An announcement is one relaxed atomic word that is its own flag, so that
 // it orders no other memory; the words are filled with ones, which no announcement
-// is, before the kernel starts.
+// is, before the kernel starts.  (Workgroups that stay and take one tile after the
+// other hold a tile back while they finish another, and its chain with it: 388
+// against 260 us at 32,768 tokens of 4,096 channels.)
+//
+// What bounds it is how HBM takes a tile's rows: a kernel that only moves the same
+// pieces of rows takes 268 us where they are 128 bytes, 229 at 256 bytes and 225 at
+// 512, against 218 in linear order; without its exponentials this one takes no less,
+// without the chain 238 us.  Half a wave to a row (256 bytes in bf16) and 8 tokens to
+// a lane keep the registers at 121, two workgroups to a CU.
+// Measured: 32,768 tokens of 4,096 channels, z, bf16: 260 us, 5.2 TB/s (a copy of
+// 1 GiB runs at 5.2); 4 x 4,096 tokens in fp32: 247 us, 5.4 TB/s.
 
 template <typename Act, int LPC, int WAVES, int N, bool GATE, bool CHAIN>
 __global__ __launch_bounds__(WAVES * kWave, 4) void lru_scan_kernel(
@@ -243,9 +259,16 @@ __global__ __launch_bounds__(256) void lru_clear_kernel(uint4* __restrict__ word
 // gradient of the state before its first token, whose map has the same a.  With
 // P = a sigmoid(i) x / m, the gradient of la is G (a h' - a^2 sigmoid(i) x / m) =
 // K (h' - P) for h' the state before the token, so the two parts of a token's
-// decay share one product.  What the outputs need of a token (ten values) stays in
-// registers while the chain is waited for: its exponentials are taken once.
-// Of a tile's tokens each channel's part of dA goes to `parts`.
+// decay share one product.  What the outputs need of a token (nine values) stays in
+// registers while the chain is waited for, so that its exponentials are taken once;
+// that is 72 registers at 2 tokens to a lane.  Each tile's part of dA goes to `parts`.
+//
+// Nine streams (five in, four out).  Measured, 4 x 4,096 tokens of 4,096 channels
+// with z: bf16 280-295 us, 4.2 TB/s; fp32 403 us, 6.0 TB/s.  The arithmetic does not set
+// it (270 us without the exponentials in bf16, 399 in fp32), nor the chain (270): a
+// bf16 tile has half the bytes under way of an fp32 one, for the same latencies.
+// Four tokens to a lane, which doubles them, halve the waves: 297 against 283 us at
+// 16 x 1,024 tokens.
 
 template <typename Act, int LPC, int WAVES, int N, bool GATE, bool CHAIN>
 __global__ __launch_bounds__(WAVES * kWave, 4) void lru_backward_kernel(
@@ -525,16 +548,16 @@ __global__ __launch_bounds__(1024) void lru_rate_kernel(const float* __restrict_
         float t = 0.0f;
         for (int w = 0; w < 16; ++w)
             t += sums[w][lane];
-        dA[c] = A[c] < 0.0f ? t : 0.0f;
+        dA[c] = A[c] >= 0.0f ? 0.0f : t;
     }
 }
 
 template <typename Act, bool GATE>
 static hipError_t token_cfg(const LruGeo& g, const LruArgs& a, hipStream_t s) {
-    const dim3 grid((g.W / 4 + 255) / 256, g.B);
-    hipLaunchKernelGGL((lru_token_kernel<Act, GATE>), grid, dim3(256), 0, s, a.state, static_cast<const Act*>(a.x),
-                       static_cast<const Act*>(a.r), static_cast<const Act*>(a.i), a.A, static_cast<const Act*>(a.z),
-                       static_cast<Act*>(a.y), g.W, g.p);
+    const unsigned per_row = g.W / 4, lanes = g.B * per_row;   // fewer than 2^27: B * ceil(W / 64) < 2^23
+    hipLaunchKernelGGL((lru_token_kernel<Act, GATE>), dim3((lanes + 255) / 256), dim3(256), 0, s, a.state,
+                       static_cast<const Act*>(a.x), static_cast<const Act*>(a.r), static_cast<const Act*>(a.i), a.A,
+                       static_cast<const Act*>(a.z), static_cast<Act*>(a.y), lanes, per_row, g.W, g.p);
     return hipGetLastError();
 }
 
@@ -555,12 +578,24 @@ inline Shape shape_of(const LruGeo& g, int T, int channels, int tokens) {
 
 constexpr int kWide = 128;   // channels of a wide tile
 constexpr int kScanTokens = 128, kBackTokens = 32;
+
+// Wide tiles (32 lanes to a row) where they are enough for the chip, 64 channels else.
+// bf16, wide against narrow: 16 x 256 tokens of 1,024 channels (256 tiles) 16.8 and
+// 19.4 us, 1 x 1,024 of 2,560 (160) 15.1 and 15.7.  fp32, whose narrow rows are 256
+// bytes already: 1 x 4,096 of 2,560 (640) 56 and 49 us, 8 x 2,500 (3,200) 196 both.
+// Up to 256 tokens one narrow tile holds the whole prompt and nothing is chained: 1 x
+// 256 of 2,560 9.5 us against 10.9 in two tiles.
 inline Shape scan_shape(const LruGeo& g, int T) {
     const Shape s = shape_of(g, T, kWide, kScanTokens);
-    if (s.segs > 1 && s.tiles >= (g.bf16 ? 256 : 1024))
+    if (s.segs > 1 && s.tiles >= (g.bf16 ? 128 : 1024))
         return s;
     return shape_of(g, T, 64, T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : T <= 256 ? 256 : 128);
 }
+// A wide tile of the gradient has 32 tokens, a narrow one 64, so that narrow chains are
+// half as long: 16 x 64 tokens of 4,096 channels (1,024 wide tiles) 30 us wide, 22
+// narrow; 1 x 8,192 of 512 (1,024) 67 and 43; 3 x 1,003 of 1,544 (1,248) 44 and 49;
+// 1 x 4,096 of 2,560 (2,560) 66 both; 16 x 1,024 of 4,096 (16,384) 283 and 288, 4 x
+// 4,096 of 4,096 in fp32 403 and 476.
 inline Shape back_shape(const LruGeo& g, int T) {
     const Shape s = shape_of(g, T, kWide, kBackTokens);
     if (s.segs > 1 && s.tiles >= 2048)

@@ -710,8 +710,8 @@ gdn_status gdn_lru_backward(const gdn_lru_dims* d, const gdn_lru_pitches* pitch,
  *   scale, w_post  f32 [W] or NULL (1, and no norm of delta);  w f32 [W]
  *   y      act [rows][W] (written)
  * res_dtype is GDN_F32 or act_dtype.  Supported shapes: W a multiple of 8, at
- * most GDN_NORM_MAX_WIDTH; 1 <= rows < 2^31; eps positive and finite
- * (GDN_ERR_SHAPE otherwise).  Sums are fp32: rows whose mean square is beyond
+ * most GDN_NORM_MAX_WIDTH; 1 <= rows < 2^31; eps a normal positive
+ * number (GDN_ERR_SHAPE otherwise).  Sums are fp32: rows whose mean square is beyond
  * fp32 have a norm of 0.
  */
 #define GDN_NORM_MAX_WIDTH 16384
@@ -752,8 +752,8 @@ gdn_status gdn_residual_norm_backward(int64_t rows, int32_t W, int32_t act_dtype
  *   w      f32 [D], or with GDN_WEIGHT_PER_HEAD [H][D]
  *   y      act [rows][H][D] (written)
  * o_dtype is GDN_F32 or act_dtype.  Supported shapes: D a multiple of 8, at most
- * GDN_NORM_MAX_WIDTH; 1 <= H <= 65536; rows >= 1, rows*H < 2^31; eps positive
- * and finite (GDN_ERR_SHAPE otherwise, and for other flags).  Sums are fp32, as
+ * GDN_NORM_MAX_WIDTH; 1 <= H <= 65536; rows >= 1, rows*H < 2^31; eps a normal
+ * positive number (GDN_ERR_SHAPE otherwise, and for other flags).  Sums are fp32, as
  * in gdn_residual_norm.
  */
 #define GDN_GATE_FIRST 1

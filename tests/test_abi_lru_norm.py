@@ -161,7 +161,7 @@ def test_residual_norm_refusals(lib):  # noqa: F811
                         *[a[n] for n in gn], a.get("n", 1 << 30), None])
     for call in (f, g):
         for kw in (dict(rows=0), dict(rows=-1), dict(rows=1 << 31), dict(W=0), dict(W=4), dict(W=60), dict(W=16392),
-                   dict(eps=0.0), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf"))):
+                   dict(eps=0.0), dict(eps=-1.0), dict(eps=1e-39), dict(eps=float("nan")), dict(eps=float("inf"))):
             assert call(**kw) == 2, kw
         assert call(act=2) == 3 and call(res=2) == 3 and call(act=0, res=1) == 3
         for n in call.names:

@@ -342,3 +342,48 @@ def test_rows_whose_offsets_pass_32_bits():
     f = m.check()
     m.backward()
     m.check_grads(f)
+
+
+def test_two_prompts_at_once():
+    """Chained calls on two streams, each with a workspace of its own, several times over: both end as they do alone."""
+    i, j = lr.make(81, 4, 2000, 264, True), lr.make(82, 2, 3100, 520, False)
+    want = [Layer(i), Layer(j)]
+    for m in want:
+        m.prefill(saved=True)
+        m.backward()
+    torch.cuda.synchronize()
+    got, streams = [Layer(i), Layer(j)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    ws = [m.ws(max(m.gdn.lru_prefill_workspace_bytes(m.d, m.i["T"]), m.gdn.lru_backward_workspace_bytes(m.d, m.i["T"]))) for m in got]
+    first, dy = [m.state.clone() for m in got], [dev(m.i["dy"], m.i["bf16"]) for m in got]
+    g = [dev(m.i["dstate"]) for m in got]
+    saved = [m.ws(m.gdn.lru_saved_bytes(m.d, m.i["T"])) for m in got]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for k, m in enumerate(got):
+            with torch.cuda.stream(streams[k]):
+                m.state.copy_(first[k])
+                m.gdn.lru_prefill(m.d, m.state, m.x, m.r, m.i_, m.A, m.y, ws[k], z=m.z, saved=saved[k])
+                m.gdn.lru_backward(m.d, m.x, m.r, m.i_, m.A, dy[k], saved[k], m.dx, m.dr, m.di, m.dA, ws[k], z=m.z, dz=m.dz,
+                                   dstate=g[k], dstate0=m.dstate0)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for k in ("y", "state", "dx", "dr", "di", "dz", "dA", "dstate0"):
+            assert torch.equal(getattr(a, k), getattr(b, k)), k
+
+
+def test_more_sequences_than_a_grid_is_high():
+    """70,000 sequences of 8 channels: tokens, and prompts of two tokens."""
+    i = lr.make(83, 70000, 2, 8, True)
+    m, n = Layer(i), Layer(i)
+    m.prefill(saved=True)
+    for t in range(2):
+        at = lambda v: v[:, t].contiguous().clone()
+        y = torch.empty(70000, 8, device="cuda", dtype=torch.bfloat16)
+        n.gdn.lru_decode_token(n.d, n.state, at(n.x), at(n.r), at(n.i_), n.A, y, z=at(n.z))
+        n.y[:, t] = y
+    torch.cuda.synchronize()
+    # both are within 100 u of values below 8, and round a bf16 half a step of a value below 12 each at most
+    assert (m.state - n.state).abs().max() < 5e-5 and (m.y.float() - n.y.float()).abs().max() < 0.1
+    f = lr.run({**i, "B": 3, **{k: i[k][-3:] for k in ("x", "r", "i", "z", "dy", "state", "dstate")}})
+    near(n.state[-3:], f["state"], f["es"], "state")
+    near(m.y[-3:], f["y"], f["ey"], "y")
