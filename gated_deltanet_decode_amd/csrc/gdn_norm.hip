@@ -59,6 +59,32 @@ struct Unit<float, 4> {
         __builtin_nontemporal_store(raw{f[0], f[1], f[2], f[3]}, reinterpret_cast<raw*>(p));
     }
 };
+// Element c of a row.  The row is the same for a whole wave where a workgroup shares
+// it, and an offset of 32 bits then needs no address of its own in registers.
+template <typename T>
+__device__ __forceinline__ T* spot(T* row, uint32_t c) {
+    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(row) + c * static_cast<uint32_t>(sizeof(T)));
+}
+
+// Keeps values as they were read: what is widened behind this is widened again, and not
+// held in twice the registers since before it.
+template <typename RAW>
+__device__ __forceinline__ void hold_raw(RAW& v) {
+#pragma unroll
+    for (unsigned k = 0; k < sizeof(RAW) / 4; ++k) {
+        auto word = v[k];
+        asm volatile("" : "+v"(word));
+        v[k] = word;
+    }
+}
+
+// A column that the compiler takes for a new one: weights that do not fit the registers
+// are read where they are used, and not all ahead of the loop over the rows.
+__device__ __forceinline__ uint32_t anew(uint32_t c) {
+    asm volatile("" : "+v"(c));
+    return c;
+}
+
 // Weights are read by every row.
 template <int U>
 __device__ __forceinline__ void load_weight(const float* p, float (&f)[U]) {
@@ -132,15 +158,15 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
         const int64_t base = row * W;
         float s[NV][U], d[NV][U], sq[1];
         bool on[NV];
-        int c[NV];
+        uint32_t c[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int u = (team.index + j * team.size) * U;
             on[j] = u < W;
             c[j] = on[j] ? u : 0;
             if (delta)
-                AU::to_float(AU::load(delta + base + c[j]), d[j]);
-            RU::to_float(RU::load(residual + base + c[j]), s[j]);
+                AU::to_float(AU::load(spot(delta + base, c[j])), d[j]);
+            RU::to_float(RU::load(spot(residual + base, c[j])), s[j]);
         }
         if (delta) {
             float p = 1.0f;
@@ -158,9 +184,9 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
             for (int j = 0; j < NV; ++j) {
                 float ws[U], wp[U];
                 if (scale)
-                    load_weight<U>(scale + c[j], ws);
+                    load_weight<U>(spot(scale, c[j]), ws);
                 if constexpr (POST)
-                    load_weight<U>(post + c[j], wp);
+                    load_weight<U>(spot(post, c[j]), wp);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     const float n = POST ? d[j][k] * p * wp[k] : d[j][k];
@@ -169,7 +195,7 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
                         s[j][k] = static_cast<float>(static_cast<__bf16>(s[j][k]));
                 }
                 if (on[j])
-                    RU::store(out + base + c[j], s[j]);
+                    RU::store(spot(out + base, c[j]), s[j]);
             }
         }
         sq[0] = 0.0f;
@@ -183,12 +209,12 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float ww[U];
-            load_weight<U>(w + c[j], ww);
+            load_weight<U>(spot(w, c[j]), ww);
 #pragma unroll
             for (int k = 0; k < U; ++k)
                 ww[k] *= s[j][k] * q;
             if (on[j])
-                AU::store(y + base + c[j], ww);
+                AU::store(spot(y + base, c[j]), ww);
         }
     }
 }
@@ -239,89 +265,151 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kerne
     Team<LPR> team(mem);
     using RU = Unit<Res, U>;
     using AU = Unit<Act, U>;
+    // of wide rows the weights do not fit the registers; of the widest the next row and
+    // the sums for scale and w_post do not either, which then lie in LDS, each lane's own
+    // (3,161 rows of 8,680 in bf16: 338 us for the training step with them in registers)
+    constexpr bool KEEP = NV == 1, AHEAD = NV <= 2, APART = NV > 2;
+    __shared__ float4 apart[2][APART ? NV * 1024 : 1];
     float sw[NV][U] = {}, ss[NV][U] = {}, sp[NV][U] = {}, ww[NV][U], ws[NV][U], wp[NV][U];
     bool on[NV];
-    int c[NV];
+    uint32_t c[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int u = (team.index + j * team.size) * U;
         on[j] = u < W;
         c[j] = on[j] ? u : 0;
-        load_weight<U>(w + c[j], ww[j]);
+    }
+    if constexpr (APART)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            apart[0][team.index + j * team.size] = apart[1][team.index + j * team.size] = make_float4(0, 0, 0, 0);
+    auto weigh_norm = [&](int j) { load_weight<U>(spot(w, KEEP ? c[j] : anew(c[j])), ww[j]); };
+    auto weigh_delta = [&](int j) {
+        const uint32_t at = KEEP ? c[j] : anew(c[j]);
         if (scale)
-            load_weight<U>(scale + c[j], ws[j]);
+            load_weight<U>(spot(scale, at), ws[j]);
         else
 #pragma unroll
             for (int k = 0; k < U; ++k)
                 ws[j][k] = 1.0f;
         if constexpr (POST)
-            load_weight<U>(post + c[j], wp[j]);
+            load_weight<U>(spot(post, at), wp[j]);
+    };
+    if constexpr (KEEP) {
+        weigh_norm(0);
+        weigh_delta(0);
     }
     typename RU::raw rs[NV], rt[NV] = {};
     typename AU::raw rg[NV], rd[NV] = {};
     auto ask = [&](int64_t row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            rs[j] = RU::load(stream + row * W + c[j]);
-            rg[j] = AU::load(dy + row * W + c[j]);
+            rs[j] = RU::load(spot(stream + row * W, c[j]));
+            rg[j] = AU::load(spot(dy + row * W, c[j]));
             if (delta)
-                rd[j] = AU::load(delta + row * W + c[j]);
+                rd[j] = AU::load(spot(delta + row * W, c[j]));
             if (ds)
-                rt[j] = RU::load(ds + row * W + c[j]);
+                rt[j] = RU::load(spot(ds + row * W, c[j]));
         }
     };
     const int64_t step = static_cast<int64_t>(gridDim.x) * team.teams;
     int64_t row = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot;
-    if (row < rows)
+    if (AHEAD && row < rows)
         ask(row);
     for (; row < rows; row += step) {
         const int64_t base = row * W;
-        float s[NV][U], g[NV][U], d[NV][U], t[NV][U], sums[POST ? 3 : 2] = {};
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            RU::to_float(rs[j], s[j]);
-            AU::to_float(rg[j], g[j]);
-            AU::to_float(rd[j], d[j]);
-            RU::to_float(rt[j], t[j]);
-        }
-        if (row + step < rows)
-            ask(row + step);
+        float sums[POST ? 3 : 2] = {};
+        typename RU::raw cs[NV], ct[NV];
+        typename AU::raw cg[NV], cd[NV];
+        if constexpr (!AHEAD)
+            ask(row);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
+            cs[j] = rs[j], cg[j] = rg[j], cd[j] = rd[j], ct[j] = rt[j];
+        if (AHEAD && row + step < rows)
+            ask(row + step);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (!KEEP)
+                weigh_norm(j);
+            float s[U], g[U], d[U];
+            RU::to_float(cs[j], s);
+            AU::to_float(cg[j], g);
+            AU::to_float(cd[j], d);
             if (on[j])
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    sums[0] = __builtin_fmaf(s[j][k], s[j][k], sums[0]);
-                    sums[1] = __builtin_fmaf(g[j][k] * ww[j][k], s[j][k], sums[1]);
+                    sums[0] = __builtin_fmaf(s[k], s[k], sums[0]);
+                    sums[1] = __builtin_fmaf(g[k] * ww[j][k], s[k], sums[1]);
                     if constexpr (POST)
-                        sums[2] = __builtin_fmaf(d[j][k], d[j][k], sums[2]);
+                        sums[2] = __builtin_fmaf(d[k], d[k], sums[2]);
                 }
+            if constexpr (!KEEP) {
+                hold_raw(cs[j]);
+                hold_raw(cg[j]);
+                hold_raw(cd[j]);
+            }
+        }
         team.sum(sums);
         const float q = inv_rms(sums[0], inv_n, eps);
         const float back = q * q * (sums[1] * inv_n);
         const float p = POST ? inv_rms(sums[POST ? 2 : 0], inv_n, eps) : 1.0f;
-        float dot[1] = {0.0f};
+        float t[NV][U], dot[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
+            if constexpr (!KEEP) {
+                weigh_norm(j);
+                weigh_delta(j);
+            }
+            float s[U], g[U], d[U];
+            RU::to_float(cs[j], s);
+            AU::to_float(cg[j], g);
+            AU::to_float(cd[j], d);
+            RU::to_float(ct[j], t[j]);
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                sw[j][k] = __builtin_fmaf(g[j][k], s[j][k] * q, sw[j][k]);
-                t[j][k] = __builtin_fmaf(q, g[j][k] * ww[j][k] - s[j][k] * back, t[j][k]);
+                sw[j][k] = __builtin_fmaf(g[k], s[k] * q, sw[j][k]);
+                t[j][k] = __builtin_fmaf(q, g[k] * ww[j][k] - s[k] * back, t[j][k]);
             }
             if (on[j])
-                RU::store(dres + base + c[j], t[j]);
+                RU::store(spot(dres + base, c[j]), t[j]);
+            float as[U], ap[U];   // the sums' values of this unit
+            auto fetch = [&](int which, float (&own)[U], float (&v)[U]) {
+                if constexpr (APART)
+                    load_weight<U>(reinterpret_cast<const float*>(&apart[which][team.index + j * team.size]), v);
+                else
+#pragma unroll
+                    for (int k = 0; k < U; ++k)
+                        v[k] = own[k];
+            };
+            auto keep = [&](int which, float (&own)[U], const float (&v)[U]) {
+                if constexpr (APART)
+                    apart[which][team.index + j * team.size] = make_float4(v[0], v[1], v[2], v[3]);
+                else
+#pragma unroll
+                    for (int k = 0; k < U; ++k)
+                        own[k] = v[k];
+            };
+            fetch(0, ss[j], as);
+            if constexpr (POST)
+                fetch(1, sp[j], ap);
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                const float dn = d[j][k] * p;
-                ss[j][k] = __builtin_fmaf(t[j][k], POST ? dn * wp[j][k] : dn, ss[j][k]);
+                const float dn = d[k] * p;
+                as[k] = __builtin_fmaf(t[j][k], POST ? dn * wp[j][k] : dn, as[k]);
                 t[j][k] *= ws[j][k];
                 if constexpr (POST) {
-                    sp[j][k] = __builtin_fmaf(t[j][k], dn, sp[j][k]);
+                    ap[k] = __builtin_fmaf(t[j][k], dn, ap[k]);
                     t[j][k] *= wp[j][k];
                     if (on[j])
-                        dot[0] = __builtin_fmaf(t[j][k], d[j][k], dot[0]);
+                        dot[0] = __builtin_fmaf(t[j][k], d[k], dot[0]);
                 }
             }
+            keep(0, ss[j], as);
+            if constexpr (POST)
+                keep(1, sp[j], ap);
+            if constexpr (!KEEP)
+                hold_raw(cd[j]);
         }
         if (!delta)
             continue;
@@ -329,18 +417,27 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kerne
             team.sum(dot);
             const float back2 = p * p * (dot[0] * inv_n);
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j) {
+                float d[U];
+                    AU::to_float(cd[j], d);
 #pragma unroll
                 for (int k = 0; k < U; ++k)
-                    t[j][k] = p * (t[j][k] - d[j][k] * back2);
+                    t[j][k] = p * (t[j][k] - d[k] * back2);
+            }
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (on[j])
-                AU::store(ddelta + base + c[j], t[j]);
+                AU::store(spot(ddelta + base, c[j]), t[j]);
     }
     const int64_t plane = static_cast<int64_t>(gridDim.x) * W;
     float* part = parts + static_cast<int64_t>(blockIdx.x) * W;
+    if constexpr (APART)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            load_weight<U>(reinterpret_cast<const float*>(&apart[0][team.index + j * team.size]), ss[j]);
+            load_weight<U>(reinterpret_cast<const float*>(&apart[1][team.index + j * team.size]), sp[j]);
+        }
     write_part<LPR, U, NV>(team, sw, W, lds, part);
     if (delta && scale)
         write_part<LPR, U, NV>(team, ss, W, lds, part + plane);
@@ -390,15 +487,15 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
         const int h = static_cast<int>(item - row * H);
         float v[NV][U], gate[NV][U];
         bool on[NV];
-        int c[NV];
+        uint32_t c[NV];
         float sq[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int u = (team.index + j * team.size) * U;
             on[j] = u < D;
             c[j] = on[j] ? u : 0;
-            Unit<O, U>::to_float(Unit<O, U>::load(o + item * D + c[j]), v[j]);
-            Unit<Act, U>::to_float(Unit<Act, U>::load(z + row * z_pitch + static_cast<int64_t>(h) * D + c[j]), gate[j]);
+            Unit<O, U>::to_float(Unit<O, U>::load(spot(o + item * D, c[j])), v[j]);
+            Unit<Act, U>::to_float(Unit<Act, U>::load(spot(z + row * z_pitch + static_cast<int64_t>(h) * D, c[j])), gate[j]);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -414,7 +511,7 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float ww[U];
-            load_weight<U>(w + static_cast<int64_t>(h) * w_step + c[j], ww);
+            load_weight<U>(spot(w + static_cast<int64_t>(h) * w_step, c[j]), ww);
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 ww[k] *= v[j][k] * q;
@@ -422,7 +519,7 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
                     ww[k] *= gate[j][k];
             }
             if (on[j])
-                Unit<Act, U>::store(y + item * D + c[j], ww);
+                Unit<Act, U>::store(spot(y + item * D, c[j]), ww);
         }
     }
 }
@@ -442,58 +539,88 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
     const int64_t id = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot;
     const int h = static_cast<int>(id % H);
     const int64_t first = id / H;
+    constexpr bool KEEP = NV == 1;   // of wider rows the gates are taken twice and the weights read again
     float sw[NV][U] = {}, ww[NV][U];
     bool on[NV];
-    int c[NV];
+    uint32_t c[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int u = (team.index + j * team.size) * U;
         on[j] = u < D;
         c[j] = on[j] ? u : 0;
-        load_weight<U>(w + static_cast<int64_t>(h) * w_step + c[j], ww[j]);
     }
+    auto weigh = [&](int j) {
+        load_weight<U>(spot(w + static_cast<int64_t>(h) * w_step, KEEP ? c[j] : anew(c[j])), ww[j]);
+    };
+    if constexpr (KEEP)
+        weigh(0);
     if (first < step)
         for (int64_t row = first; row < rows; row += step) {
             const int64_t base = (row * H + h) * D;
-            float v[NV][U], gate[NV][U], slope[NV][U], g[NV][U];
-            float sums[2] = {};
+            typename Unit<O, U>::raw ro[NV];
+            typename Unit<Act, U>::raw rz[NV], rg[NV];
+            float gate[NV][U], slope[NV][U], sums[2] = {};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                Unit<O, U>::to_float(Unit<O, U>::load(o + base + c[j]), v[j]);
-                Unit<Act, U>::to_float(Unit<Act, U>::load(z + row * z_pitch + static_cast<int64_t>(h) * D + c[j]), gate[j]);
-                Unit<Act, U>::to_float(Unit<Act, U>::load(dy + base + c[j]), g[j]);
+                ro[j] = Unit<O, U>::load(spot(o + base, c[j]));
+                rz[j] = Unit<Act, U>::load(spot(z + row * z_pitch + static_cast<int64_t>(h) * D, c[j]));
+                rg[j] = Unit<Act, U>::load(spot(dy + base, c[j]));
             }
+            auto open = [&](int j) {
+                float v[U];
+                Unit<Act, U>::to_float(rz[j], v);
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+                for (int k = 0; k < U; ++k)
+                    silu_slope(v[k], gate[j][k], slope[j][k]);
+            };
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if constexpr (!KEEP)
+                    weigh(j);
+                open(j);
+                float v[U], g[U];
+                Unit<O, U>::to_float(ro[j], v);
+                Unit<Act, U>::to_float(rg[j], g);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    silu_slope(gate[j][k], gate[j][k], slope[j][k]);
-                    const float u = FIRST ? v[j][k] * gate[j][k] : v[j][k];
-                    const float dn = (FIRST ? g[j][k] : g[j][k] * gate[j][k]) * ww[j][k];
+                    const float u = FIRST ? v[k] * gate[j][k] : v[k];
+                    const float dn = (FIRST ? g[k] : g[k] * gate[j][k]) * ww[j][k];
                     if (on[j]) {
                         sums[0] = __builtin_fmaf(u, u, sums[0]);
                         sums[1] = __builtin_fmaf(dn, u, sums[1]);
                     }
                 }
+                if constexpr (!KEEP) {
+                    hold_raw(ro[j]);
+                    hold_raw(rz[j]);
+                    hold_raw(rg[j]);
+                }
+            }
             team.sum(sums);
             const float q = inv_rms(sums[0], inv_n, eps);
             const float back = q * q * (sums[1] * inv_n);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                float a[U], b[U];
+                if constexpr (!KEEP) {
+                    weigh(j);
+                    open(j);
+                }
+                float v[U], g[U], a[U], b[U];
+                Unit<O, U>::to_float(ro[j], v);
+                Unit<Act, U>::to_float(rg[j], g);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    const float u = FIRST ? v[j][k] * gate[j][k] : v[j][k];
-                    const float dn = FIRST ? g[j][k] : g[j][k] * gate[j][k];
+                    const float u = FIRST ? v[k] * gate[j][k] : v[k];
+                    const float dn = FIRST ? g[k] : g[k] * gate[j][k];
                     const float n = u * q;
                     sw[j][k] = __builtin_fmaf(dn, n, sw[j][k]);
                     const float du = q * (dn * ww[j][k] - u * back);
                     a[k] = FIRST ? du * gate[j][k] : du;
-                    b[k] = (FIRST ? du * v[j][k] : g[j][k] * n * ww[j][k]) * slope[j][k];
+                    b[k] = (FIRST ? du * v[k] : g[k] * n * ww[j][k]) * slope[j][k];
                 }
                 if (on[j]) {
-                    Unit<O, U>::store(dov + base + c[j], a);
-                    Unit<Act, U>::store(dz + row * dz_pitch + static_cast<int64_t>(h) * D + c[j], b);
+                    Unit<O, U>::store(spot(dov + base, c[j]), a);
+                    Unit<Act, U>::store(spot(dz + row * dz_pitch + static_cast<int64_t>(h) * D, c[j]), b);
                 }
             }
         }
@@ -530,7 +657,7 @@ inline Shape shape_of(int n) {
     return {0, nv, (per + 63) / 64 * 64};
 }
 
-template <typename F>
+template <int U, typename F>
 static hipError_t with_shape(const Shape& s, F f) {
     switch (s.lpr) {
         case 4: return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
@@ -540,10 +667,14 @@ static hipError_t with_shape(const Shape& s, F f) {
         case 64: return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
         default: break;
     }
-    switch (s.nv) {
-        case 1: return f(std::integral_constant<int, 0>(), std::integral_constant<int, 1>());
-        case 2: return f(std::integral_constant<int, 0>(), std::integral_constant<int, 2>());
-        default: return f(std::integral_constant<int, 0>(), std::integral_constant<int, 4>());
+    if (s.nv == 1)
+        return f(std::integral_constant<int, 0>(), std::integral_constant<int, 1>());
+    if constexpr (U == 8) {   // 1,024 lanes of 2 units of 8 hold the widest row
+        return f(std::integral_constant<int, 0>(), std::integral_constant<int, 2>());
+    } else {
+        if (s.nv == 2)
+            return f(std::integral_constant<int, 0>(), std::integral_constant<int, 2>());
+        return f(std::integral_constant<int, 0>(), std::integral_constant<int, 4>());
     }
 }
 
@@ -568,7 +699,7 @@ static hipError_t residual_cfg(const ResidualNorm& a, hipStream_t s) {
     const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
     const int64_t need = (a.rows + teams - 1) / teams;
     const dim3 grid(static_cast<unsigned>(need < kBlocks ? need : kBlocks)), block(sh.threads);
-    return with_shape(sh, [&](auto lpr, auto nv) {
+    return with_shape<U>(sh, [&](auto lpr, auto nv) {
         auto go = [&](auto post) {
             hipLaunchKernelGGL((residual_norm_kernel<Act, Res, U, lpr(), nv(), post()>), grid, block, 0, s,
                                static_cast<const Res*>(a.residual), static_cast<const Act*>(a.delta), a.scale, a.post,
@@ -585,7 +716,7 @@ static hipError_t residual_back_cfg(const ResidualNormGrad& a, void* ws, hipStre
     const Shape sh = shape_of(a.W / U);
     const int64_t blocks = back_blocks(a.rows, sh);
     float* parts = static_cast<float*>(ws);
-    hipError_t e = with_shape(sh, [&](auto lpr, auto nv) {
+    hipError_t e = with_shape<U>(sh, [&](auto lpr, auto nv) {
         auto go = [&](auto post) {
             hipLaunchKernelGGL((residual_norm_backward_kernel<Act, Res, U, lpr(), nv(), post()>),
                                dim3(static_cast<unsigned>(blocks)), dim3(sh.threads), 0, s,
@@ -612,7 +743,7 @@ static hipError_t gated_cfg(const GatedNorm& a, hipStream_t s) {
     const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
     const int64_t items = a.rows * a.H, need = (items + teams - 1) / teams;
     const dim3 grid(static_cast<unsigned>(need < kBlocks ? need : kBlocks)), block(sh.threads);
-    return with_shape(sh, [&](auto lpr, auto nv) {
+    return with_shape<U>(sh, [&](auto lpr, auto nv) {
         auto go = [&](auto first) {
             hipLaunchKernelGGL((gated_norm_kernel<O, Act, U, lpr(), nv(), first()>), grid, block, 0, s,
                                static_cast<const O*>(a.o), static_cast<const Act*>(a.z), a.w, static_cast<Act*>(a.y),
@@ -640,7 +771,7 @@ static hipError_t gated_back_cfg(const GatedNorm& a, const GatedNormGrad& g, voi
     const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
     const GatedPlan plan = gated_plan(a.rows, a.H, teams);
     float* parts = static_cast<float*>(ws);
-    hipError_t e = with_shape(sh, [&](auto lpr, auto nv) {
+    hipError_t e = with_shape<U>(sh, [&](auto lpr, auto nv) {
         auto go = [&](auto first) {
             hipLaunchKernelGGL((gated_norm_backward_kernel<O, Act, U, lpr(), nv(), first()>),
                                dim3(static_cast<unsigned>(plan.blocks)), dim3(sh.threads), 0, s,
