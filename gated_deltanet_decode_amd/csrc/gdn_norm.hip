@@ -265,10 +265,11 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kerne
     Team<LPR> team(mem);
     using RU = Unit<Res, U>;
     using AU = Unit<Act, U>;
-    // of wide rows the weights do not fit the registers; of the widest the next row and
-    // the sums for scale and w_post do not either, which then lie in LDS, each lane's own
-    // (3,161 rows of 8,680 in bf16: 338 us for the training step with them in registers)
-    constexpr bool KEEP = NV == 1, AHEAD = NV <= 2, APART = NV > 2;
+    // of wide rows neither the weights nor the sums for scale and w_post fit the registers,
+    // of the widest not the next row either; the sums then lie in LDS, each lane's own
+    // (training step of 3,161 rows of 8,680 in bf16 200 us, 338 with them in registers;
+    // 8,192 of 5,120 in fp32 336 and 373)
+    constexpr bool KEEP = NV == 1, AHEAD = NV <= 2, APART = NV > 1;
     __shared__ float4 apart[2][APART ? NV * 1024 : 1];
     float sw[NV][U] = {}, ss[NV][U] = {}, sp[NV][U] = {}, ww[NV][U], ws[NV][U], wp[NV][U];
     bool on[NV];
@@ -639,18 +640,20 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
 
 // ------------------------------------------------------------ launches
 
-// Lanes of a team and units per lane for rows of n units: the smallest part of a
-// wave that holds a row, or a workgroup of as many lanes as the row has units, up to
-// 1,024 (units per lane beyond that cost registers: 32,768 rows of 5,120 take 388 us
-// at 320 lanes of 4 units, 378 at 640 of 2, with the next row asked for ahead).
+// Lanes of a team and units per lane for rows of n units of U values: the smallest part
+// of a wave that holds a row, or a workgroup.  Units of 4 take a lane each up to 1,024
+// (8,192 rows of 5,120, fp32 stream: 94 us at 640 lanes of 2, 109 at 320 of 4); units of
+// 8 two to a lane above 512, which leaves more rows to a CU (bf16 stream: 74 us at 320
+// lanes of 2, 76-85 at 640 of 1), but not in a gradient, whose sums are per lane (gated
+// norm, training step of 8,192 rows of 5,120 in bf16: 167 us with two, 157 with one).
 struct Shape {
     int lpr, nv, threads;
 };
-inline Shape shape_of(int n) {
+inline Shape shape_of(int n, bool pairs) {
     for (int lpr = 4; lpr <= 64; lpr *= 2)
         if (n <= lpr)
             return {lpr, 1, 256};
-    int nv = 1;
+    int nv = pairs && n > 512 ? 2 : 1;
     while (n > 1024 * nv)
         nv *= 2;
     const int per = (n + nv - 1) / nv;
@@ -695,7 +698,7 @@ inline int64_t back_blocks(int64_t rows, const Shape& sh) {
 template <typename Act, typename Res>
 static hipError_t residual_cfg(const ResidualNorm& a, hipStream_t s) {
     constexpr int U = unit_of<Act, Res>();
-    const Shape sh = shape_of(a.W / U);
+    const Shape sh = shape_of(a.W / U, U == 8);
     const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
     const int64_t need = (a.rows + teams - 1) / teams;
     const dim3 grid(static_cast<unsigned>(need < kBlocks ? need : kBlocks)), block(sh.threads);
@@ -713,7 +716,7 @@ static hipError_t residual_cfg(const ResidualNorm& a, hipStream_t s) {
 template <typename Act, typename Res>
 static hipError_t residual_back_cfg(const ResidualNormGrad& a, void* ws, hipStream_t s) {
     constexpr int U = kBackUnit;
-    const Shape sh = shape_of(a.W / U);
+    const Shape sh = shape_of(a.W / U, false);
     const int64_t blocks = back_blocks(a.rows, sh);
     float* parts = static_cast<float*>(ws);
     hipError_t e = with_shape<U>(sh, [&](auto lpr, auto nv) {
@@ -739,7 +742,7 @@ static hipError_t residual_back_cfg(const ResidualNormGrad& a, void* ws, hipStre
 template <typename O, typename Act>
 static hipError_t gated_cfg(const GatedNorm& a, hipStream_t s) {
     constexpr int U = unit_of<O, Act>();
-    const Shape sh = shape_of(a.D / U);
+    const Shape sh = shape_of(a.D / U, U == 8);
     const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
     const int64_t items = a.rows * a.H, need = (items + teams - 1) / teams;
     const dim3 grid(static_cast<unsigned>(need < kBlocks ? need : kBlocks)), block(sh.threads);
@@ -767,7 +770,7 @@ inline GatedPlan gated_plan(int64_t rows, int H, int teams) {
 template <typename O, typename Act>
 static hipError_t gated_back_cfg(const GatedNorm& a, const GatedNormGrad& g, void* ws, hipStream_t s) {
     constexpr int U = unit_of<O, Act>();
-    const Shape sh = shape_of(a.D / U);
+    const Shape sh = shape_of(a.D / U, false);
     const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
     const GatedPlan plan = gated_plan(a.rows, a.H, teams);
     float* parts = static_cast<float*>(ws);
@@ -794,7 +797,7 @@ static hipError_t gated_back_cfg(const GatedNorm& a, const GatedNormGrad& g, voi
 }  // namespace norm
 
 size_t residual_norm_back_ws_bytes(int64_t rows, int W) {
-    return static_cast<size_t>(norm::kMaxSums) * norm::back_blocks(rows, norm::shape_of(W / norm::kBackUnit)) * W *
+    return static_cast<size_t>(norm::kMaxSums) * norm::back_blocks(rows, norm::shape_of(W / norm::kBackUnit, false)) * W *
            sizeof(float);
 }
 
@@ -802,7 +805,7 @@ size_t residual_norm_back_ws_bytes(int64_t rows, int W) {
 size_t gated_norm_back_ws_bytes(int64_t rows, int H, int D) {
     size_t most = 0;
     for (int U = 4; U <= 8; U += 4) {
-        const norm::Shape sh = norm::shape_of(D / U);
+        const norm::Shape sh = norm::shape_of(D / U, false);
         const norm::GatedPlan plan = norm::gated_plan(rows, H, sh.lpr ? sh.threads / sh.lpr : 1);
         const size_t shared = static_cast<size_t>(plan.blocks) * D, each = static_cast<size_t>(plan.step) * H * D;
         most = most > shared ? most : shared;
