@@ -660,7 +660,8 @@ gdn_status gdn_lru_decode_token(const gdn_lru_dims* d, const gdn_lru_pitches* pi
  *           length is out of range (that sequence is untouched)
  *   workspace  device bytes >= gdn_lru_prefill_workspace_bytes(d, T), which is 0
  *           for short calls (then it may be NULL), 256-byte aligned; a size
- *           serves every call of no more sequences, tokens and channels of its type
+ *           serves every call of no more sequences, tokens and channels of its type.
+ *           Calls that may run at the same time need a workspace each.
  * State and fp32 outputs agree with the token-by-token call to fp32 rounding of
  * the terms they are sums of; bf16 outputs add their own rounding.  A NaN or
  * infinity in a token's inputs reaches its own channel from that token on.

@@ -387,3 +387,31 @@ def test_more_sequences_than_a_grid_is_high():
     f = lr.run({**i, "B": 3, **{k: i[k][-3:] for k in ("x", "r", "i", "z", "dy", "state", "dstate")}})
     near(n.state[-3:], f["state"], f["es"], "state")
     near(m.y[-3:], f["y"], f["ey"], "y")
+
+
+def test_device_operands_that_do_not_fit():
+    """Wrong types, sizes, strides, devices and workspaces raise before anything is launched."""
+    i = lr.make(91, 2, 300, 64, True)
+    m = Layer(i)
+    g, T = m.gdn, 300
+    w = m.ws(g.lru_backward_workspace_bytes(m.d, T))
+    saved = m.ws(g.lru_saved_bytes(m.d, T))
+    ok = dict(x=m.x, r=m.r, i=m.i_, A=m.A, y=m.y, state=m.state, z=m.z, saved=saved, workspace=w, lengths=None)
+    before = {k: v.clone() for k, v in ok.items() if v is not None}
+
+    def call(**kw):
+        a = {**ok, **kw}
+        g.lru_prefill(m.d, a["state"], a["x"], a["r"], a["i"], a["A"], a["y"], a["workspace"], z=a["z"], lengths=a["lengths"],
+                      saved=a["saved"])
+    wide = torch.zeros(2, T, 128, dtype=torch.bfloat16, device="cuda")
+    for kw, err in ((dict(r=m.r.float()), ValueError), (dict(r=m.r[:, :100]), ValueError), (dict(r=m.r.cpu()), ValueError),
+                    (dict(r=wide[..., ::2]), ValueError), (dict(i=wide[..., 4:68]), g.GdnError), (dict(A=m.A[:32]), ValueError),
+                    (dict(state=m.state.double()), ValueError), (dict(z=m.z.float()), ValueError), (dict(saved=saved[:-4]), ValueError),
+                    (dict(workspace=None), g.GdnError), (dict(workspace=w[:256]), g.GdnError), (dict(workspace=w[16:]), g.GdnError),
+                    (dict(workspace=w.cpu()), ValueError), (dict(lengths=torch.zeros(2, device="cuda")), ValueError),
+                    (dict(y=m.x), g.GdnError), (dict(y=None), TypeError)):
+        with pytest.raises(err):
+            call(**kw)
+    torch.cuda.synchronize()
+    for k, v in before.items():
+        assert torch.equal(v, ok[k]), k
