@@ -64,19 +64,20 @@ __global__ __launch_bounds__(256) void lru_token_kernel(float* __restrict__ stat
 // A tile is a block of channels by some tokens, and one workgroup's work.  The tiles
 // of a sequence's channels form a chain along the tokens.  Every tile reads its
 // inputs once and keeps a and v in registers; it announces its own map as soon as
-// that is known, then gathers the maps of the tiles before it, back to one whose
-// leaving state is known already, as many at a time as it has waves, and announces
-// its own leaving state.  So the chain costs one word of 8 bytes per channel and
-// tile, and inputs are not read a second time.
+// that is known, looks at as many tiles before it as it has waves until one of them
+// shows the state that leaves it, applies the maps from there, and announces its own
+// leaving state.  So the chain costs one word of 8 bytes per channel and tile, and
+// inputs are not read a second time.
 //
 // A workgroup takes its tile from a counter, in the order of the chains' tokens:
-// whoever holds a tile, all tiles before it are held by workgroups that already
-// run and that announce their maps without waiting for anyone.  So every wait
-// ends.  An announcement is one relaxed atomic word that is its own flag, so that
-// it orders no other memory; the words are filled with ones, which no announcement
-// is, before the kernel starts.  (Workgroups that stay and take one tile after the
-// other hold a tile back while they finish another, and its chain with it: 388
-// against 260 us at 32,768 tokens of 4,096 channels.)
+// whoever holds a tile, all tiles before it are held by workgroups that already run.
+// Maps are announced without waiting, and the first tile of a chain waits for nobody,
+// so one after the other shows its state and every wait ends.  An announcement is one
+// relaxed atomic word that is its own flag, so that it orders no other memory; the
+// words are filled with ones, which no announcement is, before the kernel starts.
+// (Workgroups that stay and take one tile after the other hold a tile back while they
+// finish another, and its chain with it: 388 against 260 us at 32,768 tokens of 4,096
+// channels.)
 //
 // What bounds it is how HBM takes a tile's rows: a kernel that only moves the same
 // pieces of rows takes 268 us where they are 128 bytes, 229 at 256 bytes and 225 at

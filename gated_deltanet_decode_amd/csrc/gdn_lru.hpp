@@ -19,7 +19,6 @@ struct Tile {
     static constexpr int kChannels = 4 * LPC;
     static constexpr int kPerWave = kWave / LPC;
     static constexpr int kTokens = N * kPerWave * WAVES;
-    static constexpr int kThreads = WAVES * kWave;
     static constexpr int kWords = kChannels / kWave;   // waves that hold a tile's channels, one to a lane
 };
 
