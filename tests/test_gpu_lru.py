@@ -415,3 +415,30 @@ def test_device_operands_that_do_not_fit():
     torch.cuda.synchronize()
     for k, v in before.items():
         assert torch.equal(v, ok[k]), k
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_ragged_lengths_of_wide_tiles(bf16):
+    """The same where the batch is large enough for the wide tiles (32 and 128 tokens), with ends on and beside their edges."""
+    lengths = np.array([0, 1, 31, 32, 33, 63, 64, 96, 127, 128, 129, 255, 256, 512, 599, 600], np.int32)
+    i = lr.make(92, 16, 600, 2056, bf16, gate=bf16)
+    m = Layer(i)
+    for b, n in enumerate(lengths):
+        for a in (m.x, m.r, m.i_, m.z):
+            if a is not None:
+                a[b, n:] = float("nan")
+    ld = torch.from_numpy(lengths).cuda()
+    m.prefill(ld, saved=True)
+    f = m.check(lengths)
+    m.backward(ld)
+    m.check_grads(f, lengths)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_a_long_narrow_sequence(bf16):
+    """One sequence of few channels: chains of 157 and 313 tiles, each link waited for."""
+    m = Layer(lr.make(93, 1, 20011, 8, bf16))
+    m.prefill(saved=True)
+    f = m.check()
+    m.backward()
+    m.check_grads(f)
