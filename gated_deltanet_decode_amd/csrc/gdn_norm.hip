@@ -644,11 +644,13 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
 // of a wave that holds a row, or a workgroup.  Units of 4 take a lane each up to 1,024
 // (8,192 rows of 5,120, fp32 stream: 94 us at 640 lanes of 2, 109 at 320 of 4); units of
 // 8 two to a lane above 512, which leaves more rows to a CU (bf16 stream: 74 us at 320
-// lanes of 2, 76-85 at 640 of 1), but not in a gradient, whose sums are per lane (gated
+// lanes of 2, 76-85 at 640 of 1), but not where the rows are too few to fill the chip
+// (64 rows: 4.2 us with two, 3.6 with one) and not in a gradient, whose sums are per lane (gated
 // norm, training step of 8,192 rows of 5,120 in bf16: 167 us with two, 157 with one).
 struct Shape {
     int lpr, nv, threads;
 };
+constexpr int64_t kManyRows = 1024;
 inline Shape shape_of(int n, bool pairs) {
     for (int lpr = 4; lpr <= 64; lpr *= 2)
         if (n <= lpr)
@@ -698,7 +700,7 @@ inline int64_t back_blocks(int64_t rows, const Shape& sh) {
 template <typename Act, typename Res>
 static hipError_t residual_cfg(const ResidualNorm& a, hipStream_t s) {
     constexpr int U = unit_of<Act, Res>();
-    const Shape sh = shape_of(a.W / U, U == 8);
+    const Shape sh = shape_of(a.W / U, U == 8 && a.rows >= kManyRows);
     const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
     const int64_t need = (a.rows + teams - 1) / teams;
     const dim3 grid(static_cast<unsigned>(need < kBlocks ? need : kBlocks)), block(sh.threads);
@@ -742,7 +744,7 @@ static hipError_t residual_back_cfg(const ResidualNormGrad& a, void* ws, hipStre
 template <typename O, typename Act>
 static hipError_t gated_cfg(const GatedNorm& a, hipStream_t s) {
     constexpr int U = unit_of<O, Act>();
-    const Shape sh = shape_of(a.D / U, U == 8);
+    const Shape sh = shape_of(a.D / U, U == 8 && a.rows * a.H >= kManyRows);
     const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
     const int64_t items = a.rows * a.H, need = (items + teams - 1) / teams;
     const dim3 grid(static_cast<unsigned>(need < kBlocks ? need : kBlocks)), block(sh.threads);

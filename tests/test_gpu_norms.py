@@ -266,3 +266,14 @@ def test_elements_beyond_32_bits():
     n = (last.reshape(1, 128, 128), y[-1:].float().cpu().numpy().reshape(1, 128, 128), wh.cpu().numpy())
     gdn.gated_norm(o, z, wh, out)
     near(out[-1:], *rounded(*lr.gated_norm(*n), True), "last heads")
+
+
+@pytest.mark.parametrize("W", [4104, 5120, 8200])
+def test_many_wide_rows(W):
+    """bf16 rows of more than 512 units of 8, enough of them that a lane takes two units."""
+    m = Residual(21, 1030, W, "bf16", "bf16")
+    m.forward()
+    m.check()
+    g = Gated(22, 520, 2, W, "bf16", "bf16", W == 5120, False, pitch=8)
+    g.run()
+    g.check()
