@@ -673,7 +673,9 @@ def beam_reorder(d, state, tail, parent, status=None, stream=None) -> None:
 
 def _rows(t, name, dtype, lead, W, dev):
     """(address, pitch) of rows of W contiguous values that follow each other at one pitch, lead of
-    them in all; pitch 0 for a contiguous tensor.  A slice of a wider projection's output is one."""
+    them in all; pitch 0 for a contiguous tensor alone, since the library takes 0 for "rows next to
+    each other": one row many times over (a stride of 0) has no pitch.  A slice of a wider
+    projection's output is one."""
     try:
         if t.get_device() == dev and t.dtype is dtype and t.numel() == lead * W:
             if t.is_contiguous():
@@ -681,19 +683,22 @@ def _rows(t, name, dtype, lead, W, dev):
             shape, strides = t.shape, t.stride()
             n = len(shape)
             if shape[-1] == W and strides[-1] == 1:
+                pitch = 0
                 if n == 2 or (n == 3 and shape[0] == 1):
-                    return t.data_ptr(), strides[-2]
-                if n == 3 and shape[1] > 1 and strides[0] == shape[1] * strides[1]:
-                    return t.data_ptr(), strides[1]
-                pitch, span = 0, 1          # span: rows of the dimensions behind this one
-                for m, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
-                    if m == 1:
-                        continue
-                    pitch = pitch or s
-                    if s != pitch * span:
-                        break
-                    span *= m
+                    pitch = strides[-2]
+                elif n == 3 and shape[1] > 1:
+                    pitch = strides[1] if strides[0] == shape[1] * strides[1] else 0
                 else:
+                    span = 1                # rows of the dimensions behind this one
+                    for m, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+                        if m == 1:
+                            continue
+                        pitch = pitch or s
+                        if not s or s != pitch * span:
+                            pitch = 0
+                            break
+                        span *= m
+                if pitch:
                     return t.data_ptr(), pitch
             raise ValueError(f"{name} must have contiguous rows of {W} at one pitch")
     except AttributeError:
@@ -758,10 +763,10 @@ def _room(buf, name, need, dev):
 def lru_prefill(d: LruDims, state, x, r, i, A, y, workspace, z=None, lengths=None, saved=None, status=None,
                 stream=None) -> None:
     """Prompts of a gated linear recurrent layer, or a training step's forward pass: x, r, i, y and z
-    [B][T][W] (slices of wider rows are taken as they are), state [B][W] in place.  lengths [B]
-    (int32, device): tokens of each sequence, None for T.  saved: a device byte tensor of at least
-    lru_saved_bytes(d, T) bytes for lru_backward.  workspace: one of at least
-    lru_prefill_workspace_bytes(d, T) bytes (None where that is 0)."""
+    [B][T][W] (slices of wider rows are taken as they are; rows that `expand` repeats are refused),
+    state [B][W] in place.  lengths [B] (int32, device): tokens of each sequence, None for T.  saved:
+    a device byte tensor of at least lru_saved_bytes(d, T) bytes for lru_backward.  workspace: one of
+    at least lru_prefill_workspace_bytes(d, T) bytes (None where that is 0)."""
     T = _lru_tokens(d, x, "gdn_lru_prefill")
     B, W, f32 = d.batch, d.width, torch.float32
     act = torch.bfloat16 if d.act_dtype == BF16 else f32
@@ -885,7 +890,7 @@ def _head_rows(t, name, dtype, rows, H, D, dev):
     shape, strides = t.shape, t.stride()
     if len(shape) < 2 or shape[-2:] != (H, D) or strides[-1] != 1 or (H > 1 and strides[-2] != D):
         raise ValueError(f"{name} must be [rows][H][D] with contiguous rows at one pitch")
-    if len(shape) == 3 and t.get_device() == dev and t.dtype is dtype and shape[0] == rows:
+    if len(shape) == 3 and t.get_device() == dev and t.dtype is dtype and shape[0] == rows and strides[0]:
         return t.data_ptr(), strides[0]
     return _rows(t.flatten(-2), name, dtype, rows, H * D, dev)
 
