@@ -169,7 +169,8 @@ gdn_status check_lru(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, int64_
     if (d->batch < 1 || d->width < 8 || d->width % 8 != 0 || d->width > GDN_LRU_MAX_WIDTH || T < 1 ||
         T > GDN_LRU_MAX_TOKENS)
         return GDN_ERR_SHAPE;
-    // a launch counts 2^32 threads, and workgroups of 512 take 64 channels and at least 64 tokens
+    // a launch counts 2^32 threads, and narrow tiles of 512 take 64 channels and at least 64 tokens (fewer
+    // channels or tokens only where all of a sequence's are in it); wide tiles are taken where they are no more
     if (static_cast<int64_t>(d->batch) * ((d->width + 63) / 64) * ((T + 63) / 64) >= (1ll << 23))
         return GDN_ERR_SHAPE;
     g.B = d->batch;

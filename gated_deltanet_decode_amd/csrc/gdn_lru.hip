@@ -596,12 +596,23 @@ inline Shape scan_shape(const LruGeo& g, int T) {
 // half as long: 16 x 64 tokens of 4,096 channels (1,024 wide tiles) 30 us wide, 22
 // narrow; 1 x 8,192 of 512 (1,024) 67 and 43; 3 x 1,003 of 1,544 (1,248) 44 and 49;
 // 1 x 4,096 of 2,560 (2,560) 66 both; 16 x 1,024 of 4,096 (16,384) 283 and 288, 4 x
-// 4,096 of 4,096 in fp32 403 and 476.
-inline Shape back_shape(const LruGeo& g, int T) {
+// 4,096 of 4,096 in fp32 403 and 476.  At most 64 channels leave half of a wide tile's
+// lanes off: 512 x 512 of 64 165 wide, 95 narrow; 4,096 x 512 of 8 1,129 and 609.
+inline bool wide_back(const LruGeo& g, int T) {
     const Shape s = shape_of(g, T, kWide, kBackTokens);
-    if (s.segs > 1 && s.tiles >= 2048)
-        return s;
-    return shape_of(g, T, 64, T <= 32 ? 32 : 64);
+    return g.W > 64 && s.segs > 1 && s.tiles >= 2048;
+}
+// The shape whose workspace a call needs: never less than a smaller call's.
+inline Shape back_room(const LruGeo& g, int T) {
+    return wide_back(g, T) ? shape_of(g, T, kWide, kBackTokens) : shape_of(g, T, 64, T <= 32 ? 32 : 64);
+}
+// A wide tile covers as much as a narrow one where the channels fill it, and less of 136
+// channels, say: two blocks of 128 for three of 64.  A launch counts 2^32 threads, so the
+// largest calls of such widths take the narrow tiles, by which sizes are accepted.
+constexpr int64_t kMostTiles = 1ll << 23;   // of 512 threads
+inline Shape back_shape(const LruGeo& g, int T) {
+    const Shape s = back_room(g, T);
+    return s.tiles < kMostTiles ? s : shape_of(g, T, 64, T <= 32 ? 32 : 64);
 }
 
 // The workspace of a chained call: 256 bytes with the counter, then a word of 8
@@ -717,7 +728,7 @@ hipError_t launch_lru_prefill(const LruGeo& g, const LruArgs& a, int T, const in
 }
 
 size_t lru_backward_ws_bytes(const LruGeo& g, int T) {
-    const lru::Shape sh = lru::back_shape(g, T);
+    const lru::Shape sh = lru::back_room(g, T);
     return lru::parts_bytes(g, sh) + lru::chain_bytes(sh);
 }
 
