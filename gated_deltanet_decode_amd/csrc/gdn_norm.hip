@@ -450,28 +450,39 @@ struct Sums {
     float* out[kMaxSums];
 };
 
-// Column sums of the workgroups' parts, in a fixed order.  blockIdx.y: which.
+// Column sums of the workgroups' parts, in a fixed order, 64 columns at a time.
+// blockIdx.y: which.
 __global__ __launch_bounds__(1024) void part_sum_kernel(const float* __restrict__ parts, Sums sums, int rows, int W) {
     __shared__ float mem[16][64];
     float* out = sums.out[blockIdx.y];
     if (!out)
         return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
-    const float* p = parts + static_cast<int64_t>(blockIdx.y) * rows * W + c;
-    float s = 0.0f;
-    if (c < W)
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * 64; first < W; first += static_cast<int64_t>(gridDim.x) * 64) {
+        const int64_t c = first + lane;
+        const float* p = parts + static_cast<int64_t>(blockIdx.y) * rows * W + c;
+        float s = 0.0f;
+        if (c < W)
 #pragma unroll 8
-        for (int row = wave; row < rows; row += 16)
-            s += p[static_cast<int64_t>(row) * W];
-    mem[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && c < W) {
-        float t = 0.0f;
-        for (int w = 0; w < 16; ++w)
-            t += mem[w][lane];
-        out[c] = t;
+            for (int row = wave; row < rows; row += 16)
+                s += p[static_cast<int64_t>(row) * W];
+        mem[wave][lane] = s;
+        __syncthreads();
+        if (wave == 0 && c < W) {
+            float t = 0.0f;
+            for (int w = 0; w < 16; ++w)
+                t += mem[w][lane];
+            out[c] = t;
+        }
+        __syncthreads();
     }
+}
+// Workgroups of 1,024 for so many columns; a launch counts 2^32 threads, and the weights
+// of 65,536 heads of 4,096 would be as many.
+constexpr int64_t kSumBlocks = 1 << 20;
+inline unsigned sum_blocks(int64_t columns) {
+    const int64_t need = (columns + 63) / 64;
+    return static_cast<unsigned>(need < kSumBlocks ? need : kSumBlocks);
 }
 
 // ------------------------------------------------------------ norm and gate
@@ -736,7 +747,7 @@ static hipError_t residual_back_cfg(const ResidualNormGrad& a, void* ws, hipStre
     if (e != hipSuccess)
         return e;
     const Sums sums{{a.dw, a.dscale, a.dpost}};
-    hipLaunchKernelGGL(part_sum_kernel, dim3((a.W + 63) / 64, a.dpost ? 3 : a.dscale ? 2 : 1), dim3(1024), 0, s, parts,
+    hipLaunchKernelGGL(part_sum_kernel, dim3(sum_blocks(a.W), a.dpost ? 3 : a.dscale ? 2 : 1), dim3(1024), 0, s, parts,
                        sums, static_cast<int>(blocks), a.W);
     return hipGetLastError();
 }
@@ -791,7 +802,7 @@ static hipError_t gated_back_cfg(const GatedNorm& a, const GatedNormGrad& g, voi
     if (e != hipSuccess)
         return e;
     const int cols = a.per_head ? a.H * a.D : a.D;
-    hipLaunchKernelGGL(part_sum_kernel, dim3((cols + 63) / 64, 1), dim3(1024), 0, s, parts, Sums{{g.dw, nullptr, nullptr}},
+    hipLaunchKernelGGL(part_sum_kernel, dim3(sum_blocks(cols), 1), dim3(1024), 0, s, parts, Sums{{g.dw, nullptr, nullptr}},
                        static_cast<int>(a.per_head ? plan.step : plan.blocks), cols);
     return hipGetLastError();
 }

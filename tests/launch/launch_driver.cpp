@@ -35,7 +35,7 @@ void expect_launched(gdn_status got) {
 }
 
 // Operands far apart, never dereferenced.
-void* at(int k) { return reinterpret_cast<void*>(static_cast<uintptr_t>(k + 1) << 44); }
+void* at(int k) { return reinterpret_cast<void*>(static_cast<uintptr_t>(k + 1) << 48); }
 float* fa(int k) { return static_cast<float*>(at(k)); }
 int32_t* ia(int k) { return static_cast<int32_t*>(at(k)); }
 
@@ -70,6 +70,40 @@ int lru() {
                 }
     return cases;
 }
+
+int norms() {
+    int cases = 0;
+    struct Types {
+        int act, other;
+    };
+    for (const Types t : {Types{GDN_F32, GDN_F32}, Types{GDN_BF16, GDN_F32}, Types{GDN_BF16, GDN_BF16}})
+        for (int64_t rows : {INT64_C(1), INT64_C(2), INT64_C(1000), INT64_C(1) << 20, INT64_C(0x7FFFFFFF)})
+            for (int D : {8, 64, 72, 256, 264, 1024, 4096, 8192, GDN_NORM_MAX_WIDTH}) {
+                ++cases;
+                std::snprintf(what, sizeof what, "residual norm, %lld rows of %d, types %d and %d", static_cast<long long>(rows), D,
+                              t.act, t.other);
+                launches = 0;
+                expect_launched(gdn_residual_norm(rows, D, t.act, t.other, 1e-6f, at(0), at(1), fa(2), fa(3), fa(4), at(5), at(6),
+                                                  nullptr));
+                launches = 0;
+                expect_launched(gdn_residual_norm_backward(rows, D, t.act, t.other, 1e-6f, at(0), at(1), fa(2), fa(3), fa(4), at(5),
+                                                           at(6), at(7), at(8), fa(9), fa(10), fa(11), at(12), SIZE_MAX, nullptr));
+                for (int H : {1, 3, 64, 1000, 32767, 65535, 65536})
+                    for (int flags : {0, GDN_WEIGHT_PER_HEAD}) {
+                        if (rows * H >= 1ll << 31 || static_cast<int64_t>(H) * D >= 1ll << 30)
+                            continue;
+                        std::snprintf(what, sizeof what, "gated norm, %lld rows of %d x %d, types %d and %d, flags %d",
+                                      static_cast<long long>(rows), H, D, t.act, t.other, flags);
+                        launches = 0;
+                        expect_launched(gdn_gated_norm(rows, H, D, t.other, t.act, flags, 1e-6f, at(0), at(1), 0, fa(2), at(3),
+                                                       nullptr));
+                        launches = 0;
+                        expect_launched(gdn_gated_norm_backward(rows, H, D, t.other, t.act, flags, 1e-6f, at(0), at(1), 0, fa(2),
+                                                                at(3), at(4), at(5), 0, fa(6), at(7), SIZE_MAX, nullptr));
+                    }
+            }
+    return cases;
+}
 }  // namespace
 
 extern "C" {
@@ -97,7 +131,7 @@ int hipGetLastError() { return 0; }
 
 int main(int argc, char** argv) {
     const char* which = argc > 1 ? argv[1] : "";
-    const int cases = !std::strcmp(which, "lru") ? lru() : 0;
+    const int cases = !std::strcmp(which, "lru") ? lru() : !std::strcmp(which, "norms") ? norms() : 0;
     std::printf("%d cases, at most %llu threads\n", cases, static_cast<unsigned long long>(largest));
     if (cases && !failures)
         std::puts("every launch fits");

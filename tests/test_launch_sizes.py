@@ -31,6 +31,10 @@ def test_recurrent_layer(driver):
     fits(driver, "lru")
 
 
+def test_norms(driver):
+    fits(driver, "norms")
+
+
 def test_the_largest_workspaces_serve_smaller_calls():
     """Where the gradient goes from one tile to another near the limit, its workspace's size still does not fall."""
     lib = C.CDLL(os.path.join(LIB, "libgdn.so"))
