@@ -138,9 +138,31 @@ struct Team {
     }
 };
 
-__device__ __forceinline__ float inv_rms(float sum, float inv_n, float eps) {
-    return __builtin_amdgcn_rsqf(__builtin_fmaf(sum, inv_n, eps));
-}
+// What a kernel needs of a row's length n.  The squares of a row are summed as those of
+// its values times `unit`, a power of two of at most n^-1/2: the sum then stays within
+// fp32 wherever the mean does (16,384 values of 2e17 have a mean square of 4e34 and a sum
+// of 6.6e38), and has the same digits, since nothing rounds in a product with it.  What a
+// square loses below fp32's least value is 2^-148 n of the mean square at most, which an eps
+// from 2^-100 on does not feel; beside a smaller one `unit` is 1.
+struct Mean {
+    float inv_n, unit, inv_square, eps;   // inv_square = 1 / (n unit^2)
+    Mean(int n, float e) : inv_n(1.0f / n), unit(1.0f), inv_square(inv_n), eps(e) {
+        if (e >= 0x1p-100f)
+            for (int covered = 1; covered < n; covered *= 4) {
+                unit *= 0.5f;
+                inv_square *= 4.0f;
+            }
+    }
+    // sum + (v unit)^2
+    __device__ float add_square(float v, float sum) const {
+        const float u = v * unit;
+        return __builtin_fmaf(u, u, sum);
+    }
+    // 1 / sqrt(mean square + eps) from such a sum
+    __device__ float inv_rms(float squares) const {
+        return __builtin_amdgcn_rsqf(__builtin_fmaf(squares, inv_square, eps));
+    }
+};
 
 // ------------------------------------------------------------ residual and norm
 
@@ -148,7 +170,7 @@ template <typename Act, typename Res, int U, int LPR, int NV, bool POST>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
     const Res* residual, const Act* __restrict__ delta, const float* __restrict__ scale,
     const float* __restrict__ post, const float* __restrict__ w, Res* out, Act* __restrict__ y, int64_t rows, int W,
-    float inv_n, float eps) {
+    Mean mean) {
     __shared__ float mem[96];
     Team<LPR> team(mem);
     using RU = Unit<Res, U>;
@@ -176,9 +198,9 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
                 for (int j = 0; j < NV; ++j)
 #pragma unroll
                     for (int k = 0; k < U; ++k)
-                        sq[0] = on[j] ? __builtin_fmaf(d[j][k], d[j][k], sq[0]) : sq[0];
+                        sq[0] = on[j] ? mean.add_square(d[j][k], sq[0]) : sq[0];
                 team.sum(sq);
-                p = inv_rms(sq[0], inv_n, eps);
+                p = mean.inv_rms(sq[0]);
             }
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -203,9 +225,9 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                sq[0] = on[j] ? __builtin_fmaf(s[j][k], s[j][k], sq[0]) : sq[0];
+                sq[0] = on[j] ? mean.add_square(s[j][k], sq[0]) : sq[0];
         team.sum(sq);
-        const float q = inv_rms(sq[0], inv_n, eps);
+        const float q = mean.inv_rms(sq[0]);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float ww[U];
@@ -259,7 +281,7 @@ template <typename Act, typename Res, int U, int LPR, int NV, bool POST>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kernel(
     const Res* __restrict__ stream, const Act* __restrict__ delta, const float* __restrict__ scale,
     const float* __restrict__ post, const float* __restrict__ w, const Act* __restrict__ dy, const Res* ds,
-    Res* dres, Act* __restrict__ ddelta, float* __restrict__ parts, int64_t rows, int W, float inv_n, float eps) {
+    Res* dres, Act* __restrict__ ddelta, float* __restrict__ parts, int64_t rows, int W, Mean mean) {
     __shared__ float mem[96];
     __shared__ float lds[LPR ? 256 * NV * U : 1];
     Team<LPR> team(mem);
@@ -340,10 +362,10 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kerne
             if (on[j])
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    sums[0] = __builtin_fmaf(s[k], s[k], sums[0]);
+                    sums[0] = mean.add_square(s[k], sums[0]);
                     sums[1] = __builtin_fmaf(g[k] * ww[j][k], s[k], sums[1]);
                     if constexpr (POST)
-                        sums[2] = __builtin_fmaf(d[k], d[k], sums[2]);
+                        sums[2] = mean.add_square(d[k], sums[2]);
                 }
             if constexpr (!KEEP) {
                 hold_raw(cs[j]);
@@ -352,9 +374,9 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kerne
             }
         }
         team.sum(sums);
-        const float q = inv_rms(sums[0], inv_n, eps);
-        const float back = q * q * (sums[1] * inv_n);
-        const float p = POST ? inv_rms(sums[POST ? 2 : 0], inv_n, eps) : 1.0f;
+        const float q = mean.inv_rms(sums[0]);
+        const float back = q * q * (sums[1] * mean.inv_n);
+        const float p = POST ? mean.inv_rms(sums[POST ? 2 : 0]) : 1.0f;
         float t[NV][U], dot[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -416,7 +438,7 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kerne
             continue;
         if constexpr (POST) {
             team.sum(dot);
-            const float back2 = p * p * (dot[0] * inv_n);
+            const float back2 = p * p * (dot[0] * mean.inv_n);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 float d[U];
@@ -490,7 +512,7 @@ inline unsigned sum_blocks(int64_t columns) {
 template <typename O, typename Act, int U, int LPR, int NV, bool FIRST>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
     const O* __restrict__ o, const Act* __restrict__ z, const float* __restrict__ w, Act* __restrict__ y,
-    int64_t items, int H, int D, int64_t z_pitch, int w_step, float inv_n, float eps) {
+    int64_t items, int H, int D, int64_t z_pitch, int w_step, Mean mean) {
     __shared__ float mem[96];
     Team<LPR> team(mem);
     for (int64_t item = static_cast<int64_t>(blockIdx.x) * team.teams + team.slot; item < items;
@@ -516,10 +538,10 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
                 gate[j][k] = silu(gate[j][k]);
                 if constexpr (FIRST)
                     v[j][k] *= gate[j][k];
-                sq[0] = on[j] ? __builtin_fmaf(v[j][k], v[j][k], sq[0]) : sq[0];
+                sq[0] = on[j] ? mean.add_square(v[j][k], sq[0]) : sq[0];
             }
         team.sum(sq);
-        const float q = inv_rms(sq[0], inv_n, eps);
+        const float q = mean.inv_rms(sq[0]);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float ww[U];
@@ -544,7 +566,7 @@ template <typename O, typename Act, int U, int LPR, int NV, bool FIRST>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
     const O* __restrict__ o, const Act* __restrict__ z, const float* __restrict__ w, const Act* __restrict__ dy,
     O* __restrict__ dov, Act* __restrict__ dz, float* __restrict__ parts, int64_t rows, int H, int D, int64_t step,
-    int64_t z_pitch, int64_t dz_pitch, int w_step, float inv_n, float eps) {
+    int64_t z_pitch, int64_t dz_pitch, int w_step, Mean mean) {
     __shared__ float mem[96];
     __shared__ float lds[LPR ? 256 * NV * U : 1];
     Team<LPR> team(mem);
@@ -598,7 +620,7 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
                     const float u = FIRST ? v[k] * gate[j][k] : v[k];
                     const float dn = (FIRST ? g[k] : g[k] * gate[j][k]) * ww[j][k];
                     if (on[j]) {
-                        sums[0] = __builtin_fmaf(u, u, sums[0]);
+                        sums[0] = mean.add_square(u, sums[0]);
                         sums[1] = __builtin_fmaf(dn, u, sums[1]);
                     }
                 }
@@ -609,8 +631,8 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
                 }
             }
             team.sum(sums);
-            const float q = inv_rms(sums[0], inv_n, eps);
-            const float back = q * q * (sums[1] * inv_n);
+            const float q = mean.inv_rms(sums[0]);
+            const float back = q * q * (sums[1] * mean.inv_n);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 if constexpr (!KEEP) {
@@ -719,7 +741,7 @@ static hipError_t residual_cfg(const ResidualNorm& a, hipStream_t s) {
         auto go = [&](auto post) {
             hipLaunchKernelGGL((residual_norm_kernel<Act, Res, U, lpr(), nv(), post()>), grid, block, 0, s,
                                static_cast<const Res*>(a.residual), static_cast<const Act*>(a.delta), a.scale, a.post,
-                               a.w, static_cast<Res*>(a.out), static_cast<Act*>(a.y), a.rows, a.W, 1.0f / a.W, a.eps);
+                               a.w, static_cast<Res*>(a.out), static_cast<Act*>(a.y), a.rows, a.W, Mean(a.W, a.eps));
             return hipGetLastError();
         };
         return a.post ? go(std::true_type()) : go(std::false_type());
@@ -739,7 +761,7 @@ static hipError_t residual_back_cfg(const ResidualNormGrad& a, void* ws, hipStre
                                static_cast<const Res*>(a.stream), static_cast<const Act*>(a.delta), a.scale, a.post,
                                a.w, static_cast<const Act*>(a.dy), static_cast<const Res*>(a.ds),
                                static_cast<Res*>(a.dres), static_cast<Act*>(a.ddelta), parts, a.rows, a.W,
-                               1.0f / a.W, a.eps);
+                               Mean(a.W, a.eps));
             return hipGetLastError();
         };
         return a.post ? go(std::true_type()) : go(std::false_type());
@@ -763,7 +785,7 @@ static hipError_t gated_cfg(const GatedNorm& a, hipStream_t s) {
         auto go = [&](auto first) {
             hipLaunchKernelGGL((gated_norm_kernel<O, Act, U, lpr(), nv(), first()>), grid, block, 0, s,
                                static_cast<const O*>(a.o), static_cast<const Act*>(a.z), a.w, static_cast<Act*>(a.y),
-                               items, a.H, a.D, a.z_pitch, a.per_head ? a.D : 0, 1.0f / a.D, a.eps);
+                               items, a.H, a.D, a.z_pitch, a.per_head ? a.D : 0, Mean(a.D, a.eps));
             return hipGetLastError();
         };
         return a.first ? go(std::true_type()) : go(std::false_type());
@@ -793,8 +815,8 @@ static hipError_t gated_back_cfg(const GatedNorm& a, const GatedNormGrad& g, voi
                                dim3(static_cast<unsigned>(plan.blocks)), dim3(sh.threads), 0, s,
                                static_cast<const O*>(a.o), static_cast<const Act*>(a.z), a.w,
                                static_cast<const Act*>(g.dy), static_cast<O*>(g.dov), static_cast<Act*>(g.dz), parts,
-                               a.rows, a.H, a.D, plan.step, a.z_pitch, g.dz_pitch, a.per_head ? a.D : 0, 1.0f / a.D,
-                               a.eps);
+                               a.rows, a.H, a.D, plan.step, a.z_pitch, g.dz_pitch, a.per_head ? a.D : 0,
+                               Mean(a.D, a.eps));
             return hipGetLastError();
         };
         return a.first ? go(std::true_type()) : go(std::false_type());
