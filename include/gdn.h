@@ -610,7 +610,8 @@ gdn_status gdn_ssm_beam_reorder(const gdn_ssm_dims* d, int32_t beams, float* sta
  *   decay  la = min(A, 0) * sigmoid(r), a = exp(la)
  *   state  h <- a*h + sqrt(1 - a^2) * sigmoid(i) * x
  *   output y = h, times SiLU(z) where z is given
- * A gate or 1 - a^2 below 2^-126 (fp32's smallest normal number) may count as 0.
+ * A gate, 1 - a^2, or a product of the decays of several tokens of a prompt, below
+ * 2^-126 (fp32's smallest normal number) may count as 0.
  * Types: state, A and their gradients are fp32; x, r, i, z, y and their
  * gradients have the activation type and are rounded once, on output.
  * Supported shapes: width a multiple of 8, at most GDN_LRU_MAX_WIDTH;
@@ -664,7 +665,8 @@ gdn_status gdn_lru_decode_token(const gdn_lru_dims* d, const gdn_lru_pitches* pi
  *           Calls that may run at the same time need a workspace each.
  * State and fp32 outputs agree with the token-by-token call to fp32 rounding of
  * the terms they are sums of; bf16 outputs add their own rounding.  A NaN or
- * infinity in a token's inputs reaches its own channel from that token on.
+ * infinity in a token's inputs reaches its own channel from that token on, an
+ * infinity as such or as a NaN.
  */
 size_t gdn_lru_prefill_workspace_bytes(const gdn_lru_dims* d, int32_t T);
 size_t gdn_lru_saved_bytes(const gdn_lru_dims* d, int32_t T);
