@@ -8,7 +8,7 @@
 //
 // HBM sets the time of long calls, the launch that of a few rows (64 rows of 5,120:
 // 3.5 us; 64 x 48 heads of 128: 2.5 us).  Measured, where a copy of 1 GiB runs at
-// 5.2 TB/s: 32,768 rows of 5,120 with an fp32 stream, scale and w_post 362 us, 5.6
+// 5.2 TB/s: 32,768 rows of 5,120 with an fp32 stream, scale and w_post 362-368 us, 5.5
 // TB/s; 8,192 x 48 heads of 128 from fp32 with gate 70 us forward, 120 us backward,
 // 5.8 TB/s.  Non-temporal loads and stores are worth 383 -> 367 and 212 -> 202 us.
 #include "gdn.h"
@@ -276,7 +276,7 @@ __device__ __forceinline__ void write_part(const Team<LPR>& team, float (&sums)[
 // A workgroup walks rows, so that the weights' gradients stay in its registers (and
 // the weights with them).  Two sums to wait for per row (three values, then with
 // `post` one), the next row asked for before them: 8,192 rows of 4,096 bf16 from 195
-// to 90 us (403 MB, and 25 MB of parts), with the sums one by one and no row ahead.
+// to 98 us (403 MB, and 25 MB of parts), with the sums one by one and no row ahead.
 template <typename Act, typename Res, int U, int LPR, int NV, bool POST>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kernel(
     const Res* __restrict__ stream, const Act* __restrict__ delta, const float* __restrict__ scale,
@@ -678,7 +678,10 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
 // (8,192 rows of 5,120, fp32 stream: 94 us at 640 lanes of 2, 109 at 320 of 4); units of
 // 8 two to a lane above 512, which leaves more rows to a CU (bf16 stream: 74 us at 320
 // lanes of 2, 76-85 at 640 of 1), but not where the rows are too few to fill the chip
-// (64 rows: 4.2 us with two, 3.6 with one) and not in a gradient, whose sums are per lane (gated
+// (one unit and two, rows of 5,120: 64 rows 3.9 and 4.6 us, 512 6.2 and 6.6, 768 9.0 and
+// 8.0, 1,024 10.8 and 8.6, 8,192 64 and 58; of 4,608: 768 6.7 and 8.0, 1,024 9.1 and 8.5,
+// 8,192 52 and 54; gated norm of one head, 1,024 and 8,192 of 4,608: 7.5 and 6.3, 40 and
+// 38; more than 8,192 values need two anyway) and not in a gradient, whose sums are per lane (gated
 // norm, training step of 8,192 rows of 5,120 in bf16: 167 us with two, 157 with one).
 struct Shape {
     int lpr, nv, threads;
@@ -718,15 +721,22 @@ static hipError_t with_shape(const Shape& s, F f) {
 
 constexpr int64_t kBlocks = 1 << 16;         // forward workgroups; longer calls loop
 
-constexpr int kBackUnit = 4;                 // half the registers of 8 and twice the lanes to a row: 164 against 176 us there
+// Values to a unit in a residual norm's gradient, of bf16 too: half the registers of 8 and
+// twice the lanes to a row.  bf16 stream with w_post, 4 against 8: 8,192 rows of 2,048 48
+// and 56 us, 3,161 of 8,680 153 and 352, 2,000 of 12,000 130 and 270 (units of 8 spill
+// there); where one unit of 8 to a lane holds a row, units of 8 are the faster ones: 8,192
+// of 4,096 98 and 88, of 5,120 154 and 110.
+constexpr int kBackUnit = 4;
 constexpr int64_t kGatedBlocks = 768;        // workgroups of a gated norm's gradient, each with its own weight sums
 
-// Workgroups of a residual norm's gradient: what the chip holds at about 80 registers
-// to a lane, since each leaves its own weight sums behind (8,192 rows of 4,096, 1,024
-// lanes: 164 us for the training step with 256 workgroups, 169 with 512).
+// Workgroups of a residual norm's gradient: what the chip holds, since each leaves its own
+// weight sums behind.  At about 80 registers to a lane that is 20 waves to a CU; of rows
+// with several units to a lane one workgroup, for the 64 or 128 KB of sums in its LDS
+// (8,192 rows of 4,096, 1,024 lanes: 98 us with 256 workgroups, 103 with 512; 3,161 of
+// 8,680: 153 and 165).
 inline int64_t back_blocks(int64_t rows, const Shape& sh) {
     const int teams = sh.lpr ? sh.threads / sh.lpr : 1;
-    const int64_t need = (rows + teams - 1) / teams, most = 256 * (sh.nv == 1 && sh.threads < 1280 ? 1280 / sh.threads : 1);
+    const int64_t need = (rows + teams - 1) / teams, most = 256 * (sh.nv == 1 ? 1280 / sh.threads : 1);
     return need < most ? need : most;
 }
 
@@ -836,7 +846,7 @@ size_t residual_norm_back_ws_bytes(int64_t rows, int W) {
            sizeof(float);
 }
 
-// The larger of the two layouts, for the unit that makes the most teams.
+// The larger of the two layouts over the units of either type of o.
 size_t gated_norm_back_ws_bytes(int64_t rows, int H, int D) {
     size_t most = 0;
     for (int U = 4; U <= 8; U += 4) {

@@ -610,6 +610,9 @@ gdn_status gdn_ssm_beam_reorder(const gdn_ssm_dims* d, int32_t beams, float* sta
  *   decay  la = min(A, 0) * sigmoid(r), a = exp(la)
  *   state  h <- a*h + sqrt(1 - a^2) * sigmoid(i) * x
  *   output y = h, times SiLU(z) where z is given
+ * SiLU is the one output gate and sqrt(1 - a^2) the input's factor at every token:
+ * nothing resets the state inside a sequence (documents of one batch row are
+ * sequences of their own).
  * A gate, 1 - a^2, or a product of the decays of several tokens of a prompt, below
  * 2^-126 (fp32's smallest normal number) may count as 0.
  * Types: state, A and their gradients are fp32; x, r, i, z, y and their
@@ -662,7 +665,9 @@ gdn_status gdn_lru_decode_token(const gdn_lru_dims* d, const gdn_lru_pitches* pi
  *   workspace  device bytes >= gdn_lru_prefill_workspace_bytes(d, T), which is 0
  *           for short calls (then it may be NULL), 256-byte aligned; a size
  *           serves every call of no more sequences, tokens and channels of its type.
- *           Calls that may run at the same time need a workspace each.
+ *           Calls that may run at the same time need a workspace each; where two
+ *           use one all the same, what they compute is undefined, NaN among it, and
+ *           status does not tell.
  * State and fp32 outputs agree with the token-by-token call to fp32 rounding of
  * the terms they are sums of; bf16 outputs add their own rounding.  A NaN or
  * infinity in a token's inputs reaches its own channel from that token on, an
@@ -690,7 +695,7 @@ gdn_status gdn_lru_prefill(const gdn_lru_dims* d, const gdn_lru_pitches* pitch, 
  *          nothing to dA and its gradients are not written
  *   workspace  device bytes >= gdn_lru_backward_workspace_bytes(d, T), 256-byte
  *          aligned; a size serves every call of no more sequences, tokens and channels
- *          of its type
+ *          of its type; one for each of two calls at once, as in gdn_lru_prefill
  * Where sqrt(1 - a^2) is 0 (a gate shut to the last bit, a rate of 0) its
  * derivative is taken as 0.  Sums have a fixed order: equal inputs give equal bits.
  */

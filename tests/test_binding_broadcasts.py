@@ -103,3 +103,30 @@ def test_no_call_takes_repeated_rows(which, monkeypatch):
                 call({**operands, n: one.expand(t.shape)})
         with pytest.raises(ValueError):
             call({**operands, n: zeros(t.shape[-1]).expand(t.shape)})
+
+
+@pytest.mark.gpu
+def test_device_operands_that_repeat():
+    """The same on a device: nothing is written; a constant gate as rows of its own is taken."""
+    d = gdn.lru_dims(B, W, "f32")
+    full = lambda *s: torch.randn(*s, device="cuda")
+    x, r, i, z, A, state = full(B, T, W), full(B, T, W), full(B, T, W), full(B, T, W), -torch.rand(W, device="cuda"), full(B, W)
+    y, before = torch.full_like(x, 7.0), state.clone()
+    for kw in (dict(r=full(W).expand(B, T, W)), dict(i=full(B, 1, W).expand(B, T, W)), dict(z=full(1, T, W).expand(B, T, W)),
+               dict(x=full(1, 1, W).expand(B, T, W)), dict(y=full(W).expand(B, T, W))):
+        a = {**dict(x=x, r=r, i=i, z=z, y=y), **kw}
+        with pytest.raises(ValueError, match="one pitch"):
+            gdn.lru_prefill(d, state, a["x"], a["r"], a["i"], A, a["y"], None, z=a["z"])
+    o, w, out = full(B, H, 16), full(16), torch.full((B, H, 16), 7.0, device="cuda")
+    with pytest.raises(ValueError, match="one pitch"):
+        gdn.gated_norm(o, full(H, 16).expand(B, H, 16), w, out)
+    torch.cuda.synchronize()
+    assert torch.equal(state, before) and (y == 7.0).all() and (out == 7.0).all()
+    gate = full(W)
+    gdn.lru_prefill(d, state, x, gate.expand(B, T, W).contiguous(), i, A, y, None, z=z)
+    s2 = before.clone()
+    y2 = torch.empty(B, W, device="cuda")
+    for t in range(T):
+        gdn.lru_decode_token(d, s2, x[:, t], gate.expand(B, W).contiguous(), i[:, t], A, y2, z=z[:, t])
+        # sums of at most 7 terms of magnitude below 8 each, gates within 10 half steps
+        assert (y2 - y[:, t]).abs().max() < 7 * 8 * 20 * 2.0 ** -24 * z.abs().max()
