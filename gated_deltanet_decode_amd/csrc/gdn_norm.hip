@@ -28,7 +28,7 @@ template <typename T, int U>
 struct Unit;
 template <int U>
 struct Unit<uint16_t, U> {
-    static constexpr int WORDS = U / 2;
+    static constexpr int WORDS = U / 2, VALUES = U;
     typedef uint32_t raw __attribute__((ext_vector_type(WORDS)));
     __device__ static raw load(const uint16_t* p) { return __builtin_nontemporal_load(reinterpret_cast<const raw*>(p)); }
     __device__ static void to_float(raw v, float (&f)[U]) {
@@ -52,6 +52,7 @@ struct Unit<uint16_t, U> {
 };
 template <>
 struct Unit<float, 4> {
+    static constexpr int VALUES = 4;
     typedef float raw __attribute__((ext_vector_type(4)));
     __device__ static raw load(const float* p) { return __builtin_nontemporal_load(reinterpret_cast<const raw*>(p)); }
     __device__ static void to_float(raw v, float (&f)[4]) { f[0] = v[0], f[1] = v[1], f[2] = v[2], f[3] = v[3]; }
@@ -138,31 +139,60 @@ struct Team {
     }
 };
 
-// What a kernel needs of a row's length n.  The squares of a row are summed as those of
-// its values times `unit`, a power of two of at most n^-1/2: the sum then stays within
-// fp32 wherever the mean does (16,384 values of 2e17 have a mean square of 4e34 and a sum
-// of 6.6e38), and has the same digits, since nothing rounds in a product with it.  What a
-// square loses below fp32's least value is 2^-148 n of the mean square at most, which an eps
-// from 2^-100 on does not feel; beside a smaller one `unit` is 1.
+// What a kernel needs of a row's length n.
 struct Mean {
-    float inv_n, unit, inv_square, eps;   // inv_square = 1 / (n unit^2)
-    Mean(int n, float e) : inv_n(1.0f / n), unit(1.0f), inv_square(inv_n), eps(e) {
-        if (e >= 0x1p-100f)
-            for (int covered = 1; covered < n; covered *= 4) {
-                unit *= 0.5f;
-                inv_square *= 4.0f;
-            }
-    }
-    // sum + (v unit)^2
-    __device__ float add_square(float v, float sum) const {
-        const float u = v * unit;
-        return __builtin_fmaf(u, u, sum);
-    }
-    // 1 / sqrt(mean square + eps) from such a sum
-    __device__ float inv_rms(float squares) const {
-        return __builtin_amdgcn_rsqf(__builtin_fmaf(squares, inv_square, eps));
+    float inv_n, eps;
+    float unit, inv_square;   // a power of two of at most n^-1/2; 1 / (n unit^2)
+    Mean(int n, float e) : inv_n(1.0f / n), eps(e), unit(1.0f), inv_square(inv_n) {
+        for (int covered = 1; covered < n; covered *= 4) {
+            unit *= 0.5f;
+            inv_square *= 4.0f;
+        }
     }
 };
+
+// 1 / sqrt(mean square + eps) from the sum of a row's squares, in all lanes of its team.
+// The sum may be beyond fp32 where the mean is not (16,384 values of 2e17: 6.6e38 and
+// 4e34); such a row's squares are summed again, as those of its values times `unit`,
+// which stay below their mean.  values(f) calls f with each of the lane's values.
+template <int LPR, typename F>
+__device__ __forceinline__ float inv_rms(Team<LPR>& team, const Mean& mean, float squares, F values) {
+    float inv = mean.inv_n;
+    if (__builtin_expect(squares == __builtin_inff(), 0)) {
+        float again[1] = {0.0f};
+        values([&](float v) {
+            const float u = v * mean.unit;
+            again[0] = __builtin_fmaf(u, u, again[0]);
+        });
+        team.sum(again);
+        squares = again[0];
+        inv = mean.inv_square;
+    }
+    return __builtin_amdgcn_rsqf(__builtin_fmaf(squares, inv, mean.eps));
+}
+
+// A lane's values of a row, as numbers and as they were read.
+template <int NV, int U, typename F>
+__device__ __forceinline__ void each(const bool (&on)[NV], const float (&v)[NV][U], F f) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (on[j])
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                f(v[j][k]);
+}
+template <typename UNIT, int NV, typename F>
+__device__ __forceinline__ void each_raw(const bool (&on)[NV], const typename UNIT::raw (&raw)[NV], F f) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        float v[UNIT::VALUES];
+        UNIT::to_float(raw[j], v);
+        if (on[j])
+#pragma unroll
+            for (int k = 0; k < UNIT::VALUES; ++k)
+                f(v[k]);
+    }
+}
 
 // ------------------------------------------------------------ residual and norm
 
@@ -198,9 +228,9 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
                 for (int j = 0; j < NV; ++j)
 #pragma unroll
                     for (int k = 0; k < U; ++k)
-                        sq[0] = on[j] ? mean.add_square(d[j][k], sq[0]) : sq[0];
+                        sq[0] = on[j] ? __builtin_fmaf(d[j][k], d[j][k], sq[0]) : sq[0];
                 team.sum(sq);
-                p = mean.inv_rms(sq[0]);
+                p = inv_rms(team, mean, sq[0], [&](auto f) { each(on, d, f); });
             }
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -225,9 +255,9 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_kernel(
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                sq[0] = on[j] ? mean.add_square(s[j][k], sq[0]) : sq[0];
+                sq[0] = on[j] ? __builtin_fmaf(s[j][k], s[j][k], sq[0]) : sq[0];
         team.sum(sq);
-        const float q = mean.inv_rms(sq[0]);
+        const float q = inv_rms(team, mean, sq[0], [&](auto f) { each(on, s, f); });
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float ww[U];
@@ -362,10 +392,10 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kerne
             if (on[j])
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    sums[0] = mean.add_square(s[k], sums[0]);
+                    sums[0] = __builtin_fmaf(s[k], s[k], sums[0]);
                     sums[1] = __builtin_fmaf(g[k] * ww[j][k], s[k], sums[1]);
                     if constexpr (POST)
-                        sums[2] = mean.add_square(d[k], sums[2]);
+                        sums[2] = __builtin_fmaf(d[k], d[k], sums[2]);
                 }
             if constexpr (!KEEP) {
                 hold_raw(cs[j]);
@@ -374,9 +404,9 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void residual_norm_backward_kerne
             }
         }
         team.sum(sums);
-        const float q = mean.inv_rms(sums[0]);
+        const float q = inv_rms(team, mean, sums[0], [&](auto f) { each_raw<RU>(on, cs, f); });
         const float back = q * q * (sums[1] * mean.inv_n);
-        const float p = POST ? mean.inv_rms(sums[POST ? 2 : 0]) : 1.0f;
+        const float p = POST ? inv_rms(team, mean, sums[POST ? 2 : 0], [&](auto f) { each_raw<AU>(on, cd, f); }) : 1.0f;
         float t[NV][U], dot[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -538,22 +568,31 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_kernel(
                 gate[j][k] = silu(gate[j][k]);
                 if constexpr (FIRST)
                     v[j][k] *= gate[j][k];
-                sq[0] = on[j] ? mean.add_square(v[j][k], sq[0]) : sq[0];
+                sq[0] = on[j] ? __builtin_fmaf(v[j][k], v[j][k], sq[0]) : sq[0];
             }
+        // a head in part of a wave asks for its weights before it waits for the sum: 68.5 us against
+        // 71.5 behind it; of wider rows they would only hold registers (8,192 of 5,120: 44.7 and 42.9)
+        constexpr bool EARLY = LPR != 0;
+        float ww[NV][U];
+        auto weigh = [&](int j) { load_weight<U>(spot(w + static_cast<int64_t>(h) * w_step, c[j]), ww[j]); };
+        if constexpr (EARLY)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                weigh(j);
         team.sum(sq);
-        const float q = mean.inv_rms(sq[0]);
+        const float q = inv_rms(team, mean, sq[0], [&](auto f) { each(on, v, f); });
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float ww[U];
-            load_weight<U>(spot(w + static_cast<int64_t>(h) * w_step, c[j]), ww);
+            if constexpr (!EARLY)
+                weigh(j);
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                ww[k] *= v[j][k] * q;
+                ww[j][k] *= v[j][k] * q;
                 if constexpr (!FIRST)
-                    ww[k] *= gate[j][k];
+                    ww[j][k] *= gate[j][k];
             }
             if (on[j])
-                Unit<Act, U>::store(spot(y + item * D, c[j]), ww);
+                Unit<Act, U>::store(spot(y + item * D, c[j]), ww[j]);
         }
     }
 }
@@ -620,7 +659,7 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
                     const float u = FIRST ? v[k] * gate[j][k] : v[k];
                     const float dn = (FIRST ? g[k] : g[k] * gate[j][k]) * ww[j][k];
                     if (on[j]) {
-                        sums[0] = mean.add_square(u, sums[0]);
+                        sums[0] = __builtin_fmaf(u, u, sums[0]);
                         sums[1] = __builtin_fmaf(dn, u, sums[1]);
                     }
                 }
@@ -631,7 +670,19 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
                 }
             }
             team.sum(sums);
-            const float q = mean.inv_rms(sums[0]);
+            const float q = inv_rms(team, mean, sums[0], [&](auto f) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    if constexpr (FIRST && !KEEP)
+                        open(j);
+                    float v[U];
+                    Unit<O, U>::to_float(ro[j], v);
+                    if (on[j])
+#pragma unroll
+                        for (int k = 0; k < U; ++k)
+                            f(FIRST ? v[k] * gate[j][k] : v[k]);
+                }
+            });
             const float back = q * q * (sums[1] * mean.inv_n);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {

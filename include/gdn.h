@@ -720,7 +720,7 @@ gdn_status gdn_lru_backward(const gdn_lru_dims* d, const gdn_lru_pitches* pitch,
  * res_dtype is GDN_F32 or act_dtype.  Supported shapes: W a multiple of 8, at
  * most GDN_NORM_MAX_WIDTH; 1 <= rows < 2^31; eps a normal positive
  * number (GDN_ERR_SHAPE otherwise).  Sums are fp32: rows whose mean square is beyond
- * fp32 have a norm of 0 (beside an eps below 2^-100, rows whose sum of squares is).
+ * fp32 have a norm of 0.
  */
 #define GDN_NORM_MAX_WIDTH 16384
 gdn_status gdn_residual_norm(int64_t rows, int32_t W, int32_t act_dtype, int32_t res_dtype, float eps,

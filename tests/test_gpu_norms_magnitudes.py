@@ -1,4 +1,4 @@
-"""GPU: rows of large values.  A row's norm is right for every mean square that fp32 holds, however many values
+"""GPU: rows of large values, and of small ones beside a small eps.  A row's norm is right for every mean square that fp32 holds, however many values
 the row has: the sum of the squares, up to 16,384 times the mean, may be beyond fp32."""
 import numpy as np
 import pytest
@@ -56,3 +56,32 @@ def test_small_rows_beside_a_small_eps(eps, W):
     # the root, beside an eps of at least 2^-126
     tol = (lr.norm_error(0) + 3 * lr.U + 0.5 * 2.0 ** -150 / eps) * np.abs(want) + lr.TINY
     assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+
+
+@pytest.mark.parametrize("W", [8, 64, 128, 256, 1024, 8200])
+def test_large_rows_beside_ordinary_ones(W):
+    """A row that is summed again changes nothing of its neighbours', which share its wave or follow in its workgroup;
+    infinite and NaN values reach their own row alone."""
+    a, b = (Residual(W, 300, W, "bf16", "bf16") for _ in range(2))
+    huge = torch.arange(300) % 7 == 3
+    for k in ("residual", "delta"):
+        b.t[k][huge] *= 2.0 ** 60
+    b.t["residual"][5, 3], b.t["residual"][12, W - 1] = float("inf"), float("nan")
+    ga, gb = (Gated(W, 300, 2, W, "bf16", "f32", True, False) for _ in range(2))
+    gb.t["o"][huge] *= 2.0 ** 61
+    gb.t["o"][5, 0, 3], gb.t["o"][12, 1, W - 1] = float("inf"), float("nan")
+    for m in (a, b):
+        m.forward()
+        m.backward()
+    for m in (ga, gb):
+        m.run()
+    torch.cuda.synchronize()
+    rest = ~huge
+    rest[5] = rest[12] = False
+    for k in ("out", "y", "dres", "ddelta"):
+        assert torch.equal(getattr(a, k)[rest], getattr(b, k)[rest]), k
+    for k in ("y", "do", "dz"):
+        assert torch.equal(getattr(ga, k)[rest], getattr(gb, k)[rest]), k
+    assert (b.y[huge].float().abs().amax(1) > 0.1).all() and (gb.y[huge].float().abs().amax((1, 2)) > 1e-3).all()
+    assert torch.isnan(b.y[12]).all() and torch.isnan(gb.y[12, 1]).all() and torch.isfinite(gb.y[12, 0]).all()
+    assert torch.isfinite(gb.y[5, 1]).all()
