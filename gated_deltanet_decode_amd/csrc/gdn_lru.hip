@@ -597,8 +597,9 @@ inline Shape scan_shape(const LruGeo& g, int T) {
 // narrow; 1 x 8,192 of 512 (1,024) 68 and 44; 8 x 300 of 2,048 in fp32 (1,280) 42 both;
 // 1 x 4,096 of 2,560 (2,560) 67 and 66; 16 x 1,024 of 4,096 (16,384) 278 and 283, 4 x
 // 4,096 of 4,096 in fp32 402 and 443.  Between them the count does not tell: 3 x 1,003 of
-// 1,544 (1,248) take narrow tiles and 45 us wide, 52 narrow, in fp32 without z 47 and 49.  At most 64 channels leave half of a wide tile's
-// lanes off: 512 x 512 of 64 165 wide, 95 narrow; 4,096 x 512 of 8 1,129 and 609.
+// 1,544 (1,248) take narrow tiles and 45 us wide, 52 narrow, in fp32 without z 47 and 49.
+// At most 64 channels leave half of a wide tile's lanes off: 512 x 512 of 64 165 wide, 95
+// narrow; 4,096 x 512 of 8 1,129 and 609.
 inline bool wide_back(const LruGeo& g, int T) {
     const Shape s = shape_of(g, T, kWide, kBackTokens);
     return g.W > 64 && s.segs > 1 && s.tiles >= 2048;

@@ -39,7 +39,8 @@ __device__ __forceinline__ float rate2(float A) { return rate_of(A) * kLog2e; }
 
 // 1 / (1 + e^-v) with the hardware exp2 and reciprocal (about one ulp each).  v log2 e is
 // rounded before exp2 and its constant before that, so e^-v is off by 1.25 |v| half steps
-// more: some 25 at v = -20, where the gate is 2e-9.  e^-v overflowing gives 0 and underflowing 1, the limits.
+// more: some 25 at v = -20, where the gate is 2e-9.  e^-v overflowing gives 0 and
+// underflowing 1, the limits.
 __device__ __forceinline__ float sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2e));
 }

@@ -7,7 +7,7 @@
 // once and written once.  All of it is fp32 but for what is stored.
 //
 // HBM sets the time of long calls, the launch that of a few rows (64 rows of 5,120:
-// 3.5 us; 64 x 48 heads of 128: 2.5 us).  Measured, where a copy of 1 GiB runs at
+// 3.5 us; 64 x 48 heads of 128: 2.8 us).  Measured, where a copy of 1 GiB runs at
 // 5.2 TB/s: 32,768 rows of 5,120 with an fp32 stream, scale and w_post 362-368 us, 5.5
 // TB/s; 8,192 x 48 heads of 128 from fp32 with gate 70 us forward, 120 us backward,
 // 5.8 TB/s.  Non-temporal loads and stores are worth 383 -> 367 and 212 -> 202 us.
@@ -732,8 +732,9 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void gated_norm_backward_kernel(
 // (one unit and two, rows of 5,120: 64 rows 3.9 and 4.6 us, 512 6.2 and 6.6, 768 9.0 and
 // 8.0, 1,024 10.8 and 8.6, 8,192 64 and 58; of 4,608: 768 6.7 and 8.0, 1,024 9.1 and 8.5,
 // 8,192 52 and 54; gated norm of one head, 1,024 and 8,192 of 4,608: 7.5 and 6.3, 40 and
-// 38; more than 8,192 values need two anyway) and not in a gradient, whose sums are per lane (gated
-// norm, training step of 8,192 rows of 5,120 in bf16: 167 us with two, 157 with one).
+// 38; more than 8,192 values need two anyway) and not in a gradient, whose sums are per
+// lane (gated norm, training step of 8,192 rows of 5,120 in bf16: 167 us with two, 157
+// with one).
 struct Shape {
     int lpr, nv, threads;
 };
